@@ -18,7 +18,7 @@ V41, V41_FP4 = 1, 2
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
 FLAG_ROPE, FLAG_NORM = 1, 2
-DEVERR_SLOT, DEVERR_POS, DEVERR_PAGE, DEVERR_LOC, DEVERR_STATE = 1, 2, 4, 8, 32
+DEVERR_SLOT, DEVERR_POS, DEVERR_PAGE, DEVERR_LOC, DEVERR_STATE, DEVERR_LEN = 1, 2, 4, 8, 32, 64
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_LAUNCH = 0, 1, 2, 3, 4
 HEAD_DIM = 512
 
@@ -51,6 +51,18 @@ _SIGS = {
                                       C.c_int64, C.c_void_p, C.c_void_p]),
     "kvq_dequant_slots": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int,
                                     C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
+    "kvq_attend_workspace": (C.c_size_t, [C.c_int64]),
+    "kvq_attend": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                             C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                             C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
+                             C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "kvq_attend_slots": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                   C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
+                                   C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_void_p,
+                                   C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "kvq_norm_quant": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                                 C.c_void_p, C.c_int64, C.c_void_p, C.c_float, C.c_void_p, C.c_int64,
+                                 C.c_void_p, C.c_int64, C.c_void_p]),
     "kvq_dequant": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
                               C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
 }
@@ -128,6 +140,30 @@ def _idx_dtype(t, name):
 def _contig1d(t, name):
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D tensor")
+
+
+def _same_device(first, *others):
+    """The device of `first`; raises when another tensor lives elsewhere."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"every tensor must be on {dev}, got one on {t.device}")
+    return dev
+
+
+def _err_word(err):
+    if err is not None:
+        _cuda(err, "err", (torch.int32,))
+        if err.numel() < 1:
+            raise ValueError("err must hold one int32")
+
+
+def _on(dev, stream, call):
+    """status = call(stream pointer) with `dev` current; the default stream is that device's current one."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
 
 
 # ------------------------------------------------------------------ entry points
@@ -302,3 +338,125 @@ def kvq_compress_decode(layout, page_bits, ratio, flags, values, scores, state, 
                                    rows, _ptr(group_pos), _ptr(loc), _ptr(pool), int(pool_slots),
                                    _ptr(err), _stream(stream))
     _check(st, "kvq_compress_decode")
+
+
+def attend_workspace(rows):
+    """Bytes of workspace for kvq_attend (rows = q_len * heads) or kvq_attend_slots (rows = heads)."""
+    return int(lib().kvq_attend_workspace(int(rows)))
+
+
+def _attend_rows(q, out, lse, workspace, err):
+    """Checks what both attention calls share; returns (tokens, heads, device, out dtype)."""
+    _cuda(q, "q", (torch.bfloat16,))
+    _cuda(out, "out", (torch.bfloat16, torch.float32))
+    _cuda(workspace, "workspace", (torch.uint8,))
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1:
+        raise ValueError("q must be [tokens, heads, 512] with unit inner stride")
+    if out.shape != q.shape or out.stride(2) != 1:
+        raise ValueError("out must have q's shape and unit inner stride")
+    n, h = q.shape[0], q.shape[1]
+    if n and h:
+        lo, hi = sorted(((out.stride(0), n), (out.stride(1), h)))
+        if (lo[1] > 1 and lo[0] < HEAD_DIM) or (hi[1] > 1 and hi[0] < (lo[1] - 1) * lo[0] + HEAD_DIM):
+            raise ValueError("rows of out must not overlap")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if lse is not None:
+        _cuda(lse, "lse", (torch.float32,))
+        if lse.shape != q.shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous [tokens, heads]")
+    _err_word(err)
+    return n, h, _same_device(q, out, lse, workspace, err), BF16 if out.dtype == torch.bfloat16 else F32
+
+
+def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, workspace, *, scale, q_len=1,
+               req=None, lse=None, err=None, stream=None):
+    """Latent attention of q [n_seq * q_len, heads, 512] bf16 over the paged pool: out (bf16 or fp32) of q's
+    shape and, if lse [n_seq * q_len, heads] fp32 is given, the natural-log sums.  page_table [rows, width]
+    int32, row req[i] (req None: row i) for sequence i; kv_len [n_seq] int32 cached tokens; query token j of a
+    sequence sees the first kv_len - (q_len - 1 - j).  workspace: attend_workspace(q_len * heads) bytes."""
+    n, heads, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+    _cuda(pool, "pool", (torch.uint8,))
+    _cuda(page_table, "page_table", (torch.int32,))
+    _cuda(kv_len, "kv_len", (torch.int32,))
+    if page_table.dim() != 2 or (page_table.numel() and page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise ValueError("page_table must be [rows, width] with unit inner stride")
+    _contig1d(kv_len, "kv_len")
+    n_seq = kv_len.numel()
+    if q_len < 1 or n != n_seq * q_len:
+        raise ValueError("q must hold q_len rows per entry of kv_len")
+    if req is not None:
+        _cuda(req, "req", (torch.int32,))
+        _contig1d(req, "req")
+        if req.numel() != n_seq:
+            raise ValueError("req must hold one table row per sequence")
+    elif page_table.shape[0] < n_seq:
+        raise ValueError("page_table must hold one row per sequence")
+    if not pool.is_contiguous() or pool.numel() < pool_pages * page_bytes(layout, page_bits):
+        raise ValueError("pool must be contiguous and hold pool_pages pages")
+    _same_device(q, pool, page_table, kv_len, req)
+    rows, width = page_table.shape
+    st = _on(dev, stream, lambda s: lib().kvq_attend(
+        layout, page_bits, _ptr(q), q.stride(0), q.stride(1), n_seq, q_len, heads, _ptr(pool), int(pool_pages),
+        _ptr(page_table), rows, width, page_table.stride(0) if rows > 1 else width, _ptr(req), _ptr(kv_len),
+        float(scale), _ptr(out), out_dtype, out.stride(0), out.stride(1), _ptr(lse), _ptr(workspace),
+        workspace.numel(), _ptr(err), s))
+    _check(st, "kvq_attend")
+    return out
+
+
+def kvq_attend_slots(layout, page_bits, q, pool, pool_slots, slots, out, workspace, *, scale, lse=None, err=None,
+                     stream=None):
+    """kvq_attend of query token i over the tokens in slots[i] ([tokens, n_sel] int32 / int64; -1 is padding).
+    workspace: attend_workspace(heads) bytes."""
+    n, heads, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+    _cuda(pool, "pool", (torch.uint8,))
+    _cuda(slots, "slots")
+    dt = _idx_dtype(slots, "slots")
+    if slots.dim() != 2 or slots.shape[0] != n or (slots.numel() and slots.stride(1) != 1 and slots.shape[1] > 1):
+        raise ValueError("slots must be [tokens, n_sel] with unit inner stride")
+    if not pool.is_contiguous() or pool.numel() < pool_slots * bytes_per_token(layout):
+        raise ValueError("pool must be contiguous and hold pool_slots tokens")
+    _same_device(q, pool, slots)
+    st = _on(dev, stream, lambda s: lib().kvq_attend_slots(
+        layout, page_bits, _ptr(q), q.stride(0), q.stride(1), n, heads, _ptr(pool), int(pool_slots), _ptr(slots),
+        dt, slots.shape[1], slots.stride(0), float(scale), _ptr(out), out_dtype, out.stride(0), out.stride(1),
+        _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err), s))
+    _check(st, "kvq_attend_slots")
+    return out
+
+
+def _rows2d(t, name, n, width):
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{n}, >={width}] with unit inner stride")
+
+
+def kvq_norm_quant(x, weight, codes, scales, *, eps=1e-6, residual=None, residual_out=None, stream=None):
+    """codes [n, dim] e4m3 bytes and scales [n, dim / 32] ue8m0 bytes of RMSNorm(x + residual) * weight;
+    residual_out (which may be residual or x) gets the sum in x's type.  dim is weight.numel()."""
+    _cuda(x, "x", (torch.float32, torch.bfloat16))
+    _cuda(weight, "weight", (torch.float32,))
+    _cuda(codes, "codes", (torch.uint8,))
+    _cuda(scales, "scales", (torch.uint8,))
+    _contig1d(weight, "weight")
+    dim = weight.numel()
+    if x.dim() != 2:
+        raise ValueError("x must be [n, >=dim]")
+    n = x.shape[0]
+    _rows2d(x, "x", n, dim)
+    _rows2d(codes, "codes", n, dim)
+    _rows2d(scales, "scales", n, dim // 32)
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out come together")
+    if residual is not None:
+        _cuda(residual, "residual", (x.dtype,))
+        _cuda(residual_out, "residual_out", (x.dtype,))
+        _rows2d(residual, "residual", n, dim)
+        _rows2d(residual_out, "residual_out", n, dim)
+    dev = _same_device(x, weight, codes, scales, residual, residual_out)
+    st = _on(dev, stream, lambda s: lib().kvq_norm_quant(
+        _ptr(x), BF16 if x.dtype == torch.bfloat16 else F32, n, dim, x.stride(0), _ptr(residual),
+        residual.stride(0) if residual is not None else 0, _ptr(residual_out),
+        residual_out.stride(0) if residual is not None else 0, _ptr(weight), float(eps), _ptr(codes),
+        codes.stride(0), _ptr(scales), scales.stride(0), s))
+    _check(st, "kvq_norm_quant")

@@ -71,8 +71,11 @@ enum {
     KVQ_DEVERR_PAGE = 4,  /* a page-table entry outside [0, pool_pages) (skipped)*/
     KVQ_DEVERR_LOC = 8,   /* a full slot outside the translation table (-> -1)   */
                           /* (bit 16 is unused: no kernel has a bounded wait)    */
-    KVQ_DEVERR_STATE = 32    /* a request index outside [0, n_state) or a count   */
-                             /* outside [0, ratio): that request is skipped       */
+    KVQ_DEVERR_STATE = 32,   /* a request index outside [0, n_state) or a count   */
+                             /* outside [0, ratio): that request is skipped; in   */
+                             /* kvq_attend a table row outside [0, table_rows)    */
+    KVQ_DEVERR_LEN = 64      /* a kv_len outside [0, table_width pages] (the      */
+                             /* sequence counts as empty)                         */
 };
 
 /* Bytes one token occupies: 528 (V41) or 288 (V41_FP4); 0 for a bad layout.
@@ -195,6 +198,93 @@ kvq_status kvq_dequant_slots(kvq_layout layout, int page_bits,
                              const void *slots, kvq_index_dtype slot_dtype, int64_t n,
                              void *out_bf16, int64_t out_row_stride,
                              int32_t *err, struct CUstream_st *stream);
+
+/* Bytes of workspace a kvq_attend / kvq_attend_slots call needs whose rows
+ * per sequence (q_len * heads; for kvq_attend_slots heads) are `rows`: the
+ * partial results of work that is split over CTAs.  It depends on nothing
+ * else; 0 when rows is not positive.  The contents need no initialisation
+ * and mean nothing after the call; calls that may run at the same time need
+ * workspaces of their own (captured graphs too, unless they run in turn). */
+size_t kvq_attend_workspace(int64_t rows);
+
+/* Latent attention over a paged pool: the reader of the rows that kvq_store
+ * and kvq_compress write.  Every head of a query token attends over the same
+ * row k[t] (512 values) of a cached token, as key and as value:
+ *   s[t] = scale * sum_d q[d] * k[t][d],  p = softmax(s) over the visible t,
+ *   out[d] = sum_t p[t] * k[t][d],        lse = log(sum_t exp(s[t])).
+ * Sequence i has q_len query tokens, rows i*q_len .. i*q_len + q_len - 1 of
+ * q, and kv_len[i] cached tokens, its own query tokens among them; query
+ * token j sees the first kv_len[i] - (q_len - 1 - j) of them (causal).  A
+ * query token that sees none gets a zero row and lse = -inf.
+ *   q            bf16, element (token, head, d) at token * q_token_stride +
+ *                head * q_head_stride + d; 16-B aligned rows.  A stride of 0
+ *                repeats a row.
+ *   page_table   [table_rows, table_stride] int32, the first table_width of
+ *                a row used: physical page of each logical page.
+ *   req          [n_seq] int32: table row of sequence i (NULL: row i, and
+ *                n_seq <= table_rows).
+ *   kv_len       [n_seq] int32, 0 .. table_width * 2^page_bits.
+ *   scale        finite.
+ *   out          bf16 or fp32 (out_dtype), strides like q's (16-B aligned
+ *                rows that do not overlap).
+ *   lse          [n_seq * q_len, heads] fp32, natural log, or NULL.
+ *   workspace    kvq_attend_workspace(q_len * heads) bytes, 16-B aligned.
+ * Scores, softmax statistics and sums are fp32; a softmax weight is rounded
+ * to the products' 16-bit type (V41: bf16; V41_FP4: fp16, where every decoded
+ * row is exact and a query row is first scaled by a power of two).  The
+ * result does not depend on anything but the arguments (no atomics on data).
+ * A visible token whose row holds a NaN or an infinity makes the rows that
+ * see it NaN, and no others; what masked tokens hold does not matter.
+ * A bad kv_len (KVQ_DEVERR_LEN) or req (KVQ_DEVERR_STATE) makes the sequence
+ * an empty one; a table entry outside [0, pool_pages) (KVQ_DEVERR_PAGE) masks
+ * its tokens.  Entries past a sequence's kv_len are not read. */
+kvq_status kvq_attend(kvq_layout layout, int page_bits,
+                      const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                      int64_t n_seq, int64_t q_len, int64_t heads,
+                      const uint8_t *pool, int64_t pool_pages,
+                      const int32_t *page_table, int64_t table_rows, int64_t table_width,
+                      int64_t table_stride, const int32_t *req, const int32_t *kv_len, float scale,
+                      void *out, kvq_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride,
+                      float *lse, void *workspace, size_t workspace_bytes,
+                      int32_t *err, struct CUstream_st *stream);
+
+/* kvq_attend over selected tokens: query token i attends over the tokens in
+ * slots slots[i * slots_stride + 0 .. n_sel - 1] (int32 or int64), the ones
+ * kvq_dequant_slots would gather.  Slot -1 is padding, anywhere in the list;
+ * any other slot outside [0, pool_slots) sets KVQ_DEVERR_SLOT and is masked.
+ * A slot that is listed twice counts twice.  workspace:
+ * kvq_attend_workspace(heads) bytes. */
+kvq_status kvq_attend_slots(kvq_layout layout, int page_bits,
+                            const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                            int64_t n_tokens, int64_t heads,
+                            const uint8_t *pool, int64_t pool_slots,
+                            const void *slots, kvq_index_dtype slot_dtype, int64_t n_sel,
+                            int64_t slots_stride, float scale,
+                            void *out, kvq_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride,
+                            float *lse, void *workspace, size_t workspace_bytes,
+                            int32_t *err, struct CUstream_st *stream);
+
+/* RMS norm of a row plus its residual, quantised like a V41 row: the input
+ * of the projections whose K rows kvq_store takes.
+ *   z = x + residual (fp32; residual NULL: z = x), residual_out = z rounded
+ *   to x_dtype, y = z * rsqrt(mean(z^2) + eps) * weight (fp32), then per 32
+ *   values scale byte = (amax exponent field - 8) clamped at 0 and code =
+ *   e4m3_satfinite(y * 2^(127 - byte)), as V41 blocks are written.
+ *   x, residual   [n, stride] fp32 or bf16 (x_dtype), the first dim elements
+ *                 of a row used; 16-B aligned rows.
+ *   dim           a multiple of 32, at most 16384.
+ *   weight        [dim] fp32, 16-B aligned.
+ *   residual_out  rows like x's; given exactly when residual is; it may be
+ *                 residual itself, or x.
+ *   codes         [n, codes_stride] bytes, codes_stride a multiple of 8,
+ *                 8-B aligned.
+ *   scales        [n, scales_stride] bytes, dim / 32 used a row. */
+kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n, int64_t dim, int64_t x_row_stride,
+                          const void *residual, int64_t residual_row_stride,
+                          void *residual_out, int64_t residual_out_row_stride,
+                          const float *weight, float eps,
+                          uint8_t *codes, int64_t codes_stride, uint8_t *scales, int64_t scales_stride,
+                          struct CUstream_st *stream);
 
 /* Human-readable name of a status. */
 const char *kvq_status_string(kvq_status status);
