@@ -1,146 +1,13 @@
-// kvq_attend.cu -- latent attention over the paged V41 / V41_FP4 pool, by
-// page table (kvq_attend) or by selected slots (kvq_attend_slots).
-//
-// One warp per query row.  Lane l owns dims 16l .. 16l+15 (half a quant
-// block) of the row, of every decoded token and of the output; a token's score
-// is a warp sum, and the softmax is online (running max and sum).
-#include <math.h>
-
+// kvq_attend.cu -- C entry points of the latent attention over the paged V41 /
+// V41_FP4 pool, by page table (kvq_attend) or by selected slots
+// (kvq_attend_slots).
 #include "kvq_attend.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kAtWarps = 8;
-
-template <Layout L>
-__device__ __forceinline__ void decode16(const uint8_t *pool, int64_t slot, int page_bits, int lane, float (&k)[16]) {
-    using T = LayoutTraits<L>;
-    const int64_t page = slot >> page_bits, row = slot & ((int64_t(1) << page_bits) - 1);
-    const uint8_t *base = pool + page * (int64_t(kTokenBytes<L>) << page_bits);
-    const uint8_t *codes = base + row * T::kCodeBytes;
-    const uint32_t sb = __ldg(base + (int64_t(T::kCodeBytes) << page_bits) + row * T::kScaleBytes + lane / 2);
-    if constexpr (L == Layout::V41) {
-        const uint4 c = __ldg(reinterpret_cast<const uint4 *>(codes) + lane);
-        const float s = ue8m0_to_f32(sb);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = e4m3x2_to_f32x2((w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
-            k[2 * i] = f.x * s;
-            k[2 * i + 1] = f.y * s;
-        }
-    } else {
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes) + lane);
-        const float s = e4m3x2_to_f32x2(sb).x;
-        const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = e2m1x2_to_f32x2((w[i / 4] >> (8 * (i & 3))) & 0xFFu);
-            k[2 * i] = f.x * s;
-            k[2 * i + 1] = f.y * s;
-        }
-    }
-}
-
-template <Layout L, bool kSlots>
-__global__ void __launch_bounds__(kAtWarps * 32) attend_row_kernel(const AttendArgs a, bool slots64, bool out_bf16) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * kAtWarps + (threadIdx.x >> 5);
-    const int64_t per = int64_t(a.q_len) * a.heads;
-    if (row >= a.n_seq * per) return;
-    const int64_t seq = row / per;
-    const int j = int((row % per) / a.heads), head = int(row % a.heads);
-    const int64_t tok = seq * a.q_len + j;
-    pdl_wait();
-
-    int64_t visible = a.max_len, trow = seq;
-    if constexpr (!kSlots) {
-        if (a.req) trow = a.req[seq];
-        int64_t len = a.kv_len[seq];
-        if (trow < 0 || trow >= a.table_rows) {
-            if (lane == 0) raise_err(a.err, KVQ_DEVERR_STATE);
-            len = 0;
-        } else if (len < 0 || len > a.max_len) {
-            if (lane == 0) raise_err(a.err, KVQ_DEVERR_LEN);
-            len = 0;
-        }
-        visible = len - (a.q_len - 1 - j);
-    }
-    float q[16], acc[16];
-    {
-        const uint4 *p = reinterpret_cast<const uint4 *>(a.q + tok * a.q_tok + head * a.q_head + lane * 16);
-        const uint4 u[2] = {__ldg(p), __ldg(p + 1)};
-        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            q[2 * i] = bf16_lo(w[i]);
-            q[2 * i + 1] = bf16_hi(w[i]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    const float c = a.scale * kLog2e;
-    for (int64_t t = 0; t < visible; ++t) {
-        int64_t slot;
-        if constexpr (kSlots) {
-            slot = slots64 ? static_cast<const int64_t *>(a.slots)[seq * a.slots_stride + t]
-                           : int64_t(static_cast<const int32_t *>(a.slots)[seq * a.slots_stride + t]);
-            if (slot < 0 || slot >= a.pool_limit) {
-                if (slot != -1 && lane == 0) raise_err(a.err, KVQ_DEVERR_SLOT);
-                continue;
-            }
-        } else {
-            const int64_t page = a.table[trow * a.table_stride + (t >> a.page_bits)];
-            if (page < 0 || page >= a.pool_limit) {
-                if (lane == 0) raise_err(a.err, KVQ_DEVERR_PAGE);
-                continue;
-            }
-            slot = (page << a.page_bits) + (t & ((int64_t(1) << a.page_bits) - 1));
-        }
-        float k[16];
-        decode16<L>(a.pool, slot, a.page_bits, lane, k);
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        s *= c;
-        const float mn = fmaxf(m, s);
-        const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float p = mn == -INFINITY ? s * 0.f : exp2f(s - mn);
-        l = l * al + p;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = fmaf(p, k[i], acc[i] * al);
-        m = mn;
-    }
-    const float r = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = tok * a.out_tok + head * a.out_head + lane * 16;
-    if (out_bf16) {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            o[i] = make_uint4(pack_bf16x2(acc[8 * i] * r, acc[8 * i + 1] * r), pack_bf16x2(acc[8 * i + 2] * r, acc[8 * i + 3] * r),
-                              pack_bf16x2(acc[8 * i + 4] * r, acc[8 * i + 5] * r), pack_bf16x2(acc[8 * i + 6] * r, acc[8 * i + 7] * r));
-    } else {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = make_float4(acc[4 * i] * r, acc[4 * i + 1] * r, acc[4 * i + 2] * r, acc[4 * i + 3] * r);
-    }
-    if (a.lse && lane == 0) a.lse[tok * a.heads + head] = (m + log2f(l)) * 0.6931471805599453f;
-}
-
-template <bool kSlots>
-kvq_status launch_attend(int layout, const AttendArgs &a, bool slots64, bool out_bf16, cudaStream_t s) {
-    const int64_t rows = a.n_seq * a.q_len * a.heads;
-    const int64_t blocks = (rows + kAtWarps - 1) / kAtWarps;
-    if (blocks > 0x7FFFFFFF) return KVQ_ERR_INVALID_ARG;
-    return with_layout(layout, [&](auto Lc) {
-        return launch_pdl(attend_row_kernel<decltype(Lc)::value, kSlots>, dim3(unsigned(blocks)), dim3(kAtWarps * 32),
-                          s, a, slots64, out_bf16);
-    });
+kvq_status launch_attend(int layout, const AttendArgs &a, bool slots, cudaStream_t s) {
+    return layout == KVQ_LAYOUT_V41 ? launch_attend_v41(a, slots, s) : launch_attend_fp4(a, slots, s);
 }
 
 // What both entry points share: layout, pool, query, output and workspace.
@@ -175,7 +42,10 @@ kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok,
 
 using namespace kvq;
 
-extern "C" size_t kvq_attend_workspace(int64_t rows) { return rows > 0 ? 16 : 0; }
+extern "C" size_t kvq_attend_workspace(int64_t rows) {
+    if (rows <= 0) return 0;
+    return kMaxAttendCtas * (sizeof(int2) + 2 * size_t(attend_rows(rows)) * kPartRow * sizeof(float));
+}
 
 extern "C" kvq_status kvq_attend(kvq_layout layout, int page_bits, const void *q_bf16, int64_t q_token_stride,
                                  int64_t q_head_stride, int64_t n_seq, int64_t q_len, int64_t heads,
@@ -219,7 +89,8 @@ extern "C" kvq_status kvq_attend(kvq_layout layout, int page_bits, const void *q
     a.lse = lse;
     a.ws = static_cast<uint8_t *>(workspace);
     a.err = err;
-    return launch_attend<false>(layout, a, false, out_dtype == KVQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+    a.out_bf16 = out_dtype == KVQ_BF16;
+    return launch_attend(layout, a, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" kvq_status kvq_attend_slots(kvq_layout layout, int page_bits, const void *q_bf16, int64_t q_token_stride,
@@ -259,6 +130,7 @@ extern "C" kvq_status kvq_attend_slots(kvq_layout layout, int page_bits, const v
     a.lse = lse;
     a.ws = static_cast<uint8_t *>(workspace);
     a.err = err;
-    return launch_attend<true>(layout, a, slot_dtype == KVQ_I64, out_dtype == KVQ_BF16,
-                               reinterpret_cast<cudaStream_t>(stream));
+    a.slots64 = slot_dtype == KVQ_I64;
+    a.out_bf16 = out_dtype == KVQ_BF16;
+    return launch_attend(layout, a, true, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -28,6 +28,24 @@ struct AttendArgs {
     float *lse;
     uint8_t *ws;
     int32_t *err;
+    bool slots64, out_bf16;
+    // set at the launch
+    int row_tiles;  // tiles of query rows a sequence
+    int2 *join;     // workspace, one a CTA: the tile it began and another CTA went on with (or -1), that tile's last CTA
+    float *part;    // workspace, two a CTA: a tile it went on with, a tile it began; kPartRow floats a query row
 };
+
+// A partial result of a query row: 512 sums, the running maximum (log2), the
+// weights' sum, padding to 16 bytes.
+constexpr int kPartRow = kD + 4;
+constexpr int kMaxAttendCtas = 160;
+
+// Query rows a tile holds, by the rows of a sequence.
+constexpr int attend_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+__device__ __forceinline__ float attend_lse(float m, float sum) { return (m + log2f(sum)) * 0.6931471805599453f; }
+
+kvq_status launch_attend_v41(const AttendArgs &a, bool slots, cudaStream_t s);
+kvq_status launch_attend_fp4(const AttendArgs &a, bool slots, cudaStream_t s);
 
 }  // namespace kvq

@@ -299,6 +299,13 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
     return r;
 }
 
+__device__ __forceinline__ void sts_u4(uint32_t a, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ void sts_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // ---------------------------------------------------------------- scales
 // V41: scale byte = exponent field of amax - 8, clamped at 0 (OCP MX shared
 // exponent floor(log2 amax) - emax(E4M3)); the values are then multiplied by
