@@ -9,47 +9,57 @@
 namespace kvq {
 namespace {
 
-constexpr int kTile = 128;          // cached tokens a block
-constexpr int kSoftWarps = 4;       // one thread a token of the block
-constexpr int kDeqWarps = 8;
-constexpr int kAttendThreads = (kSoftWarps + kDeqWarps + 1) * 32;
-constexpr int kChunk = 128;         // dims a step of decoding
+constexpr int kTile = 128;   // cached tokens a block
+constexpr int kChunk = 128;  // dims a step of decoding
 constexpr int kChunks = kD / kChunk;
-constexpr int kSubBytes = kTile * 128;  // 64 dims of a block, 128 B a token
-constexpr float kStaleMax = 8.f;    // how far (log2) a score may pass the running maximum before it moves
+constexpr int kSubBytes = kTile * 128;         // 64 dims of a block, 128 B a token
+constexpr int kChunkSmem = 2 * kSubBytes;
+// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-15 decode, 16 products, 17-19 only
+// complete the warpgroup.
+constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = kSoftWarps + kDeqWarps;
+constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
+// Registers a thread: the launch gives 640 threads 96 each; the warpgroups' shares 2 * 104 + 2 * 104 + 64 = 480 stay
+// within its 5 * 96 = 480.
+constexpr int kSoftRegs = 104, kDeqRegs = 104, kMmaRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kDeqRegs + kMmaRegs <= 5 * 96, "a larger sum would wait for ever");
+constexpr float kStaleMax = 8.f;  // how far (log2) a score may pass the running maximum before it moves
+
+// Decoded chunks that fit beside N query rows and their weights: a block is four.
+template <int N>
+constexpr int kRing = N == 16 ? 6 : N == 32 ? 5 : 4;
 
 template <int N>
 struct AttendShared {
-    uint64_t full[kChunks], oblk[kChunks], kfree[2], sdone, pready, qready, drain;
+    uint64_t full[kRing<N>], oblk[kRing<N>], kfree[2], sdone, pready, qready, drain;
     int64_t scan[kAttendThreads / 32];
-    int64_t u0, u1, total;
-    int start_tile, start_kb;
+    int64_t total, u0;
+    int units, start_tile, start_kb;
     uint32_t tmem;
     int abort, soft_abort;
     alignas(16) float sc[N], nm[N], m[N], alpha[N], inv[N];
-    float red[kSoftWarps][N];
+    float red[4][N];
     alignas(16) int vis[N];
     int64_t row[N];
-    uint8_t valid[2][kTile];
+    int texp[2][kTile];  // a token's power of two, or kNoToken
 };
+constexpr int kNoToken = 0x7FFFFFFF;
 
 template <int N>
-constexpr size_t kAttendSmem = 1024 + size_t(kTile) * kD * 2 + size_t(N) * kD * 2 + size_t(kTile) * N * 2 +
+constexpr size_t kAttendSmem = 1024 + size_t(kRing<N>) * kChunkSmem + size_t(N) * kD * 2 + size_t(kTile) * N * 2 +
                                sizeof(AttendShared<N>);
+static_assert(kAttendSmem<16> <= 232448 && kAttendSmem<32> <= 232448 && kAttendSmem<64> <= 232448, "227 KB a CTA");
 
 // Tiles are N query rows of a sequence (row = query token * heads + head);
 // a tile's blocks are the 128-token pieces of what its last query token sees.
 struct TileInfo {
-    int64_t seq;
-    int rt, len, seen, nb;  // cached tokens, tokens the last row sees, blocks (at least one)
-    int64_t trow;
-    int err;
+    int seq, rt, len, seen, nb;  // cached tokens, tokens the last row sees, blocks (at least one)
+    int trow, err;
 };
 
 template <int N, bool kSlots>
-__device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int64_t tile) {
+__device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int tile) {
     TileInfo t;
-    t.seq = uint32_t(tile) / uint32_t(a.row_tiles);
+    t.seq = int(uint32_t(tile) / uint32_t(a.row_tiles));
     t.rt = int(uint32_t(tile) % uint32_t(a.row_tiles));
     t.err = 0;
     t.trow = t.seq;
@@ -68,8 +78,8 @@ __device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int64_t tile)
         t.seen = t.len;
         if (a.q_len > 1) {
             const int64_t per = int64_t(a.q_len) * a.heads;
-            const int64_t last = min(int64_t(t.rt + 1) * N, per) - 1;
-            t.seen = max(0, t.len - (a.q_len - 1 - int(last / a.heads)));
+            const int last = int(min(int64_t(t.rt + 1) * N, per) - 1);
+            t.seen = max(0, t.len - (a.q_len - 1 - last / a.heads));
         }
     }
     t.nb = max(1, (t.seen + kTile - 1) / kTile);
@@ -79,12 +89,10 @@ __device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int64_t tile)
 // Walks a CTA's blocks in order.
 template <int N, bool kSlots>
 struct Cursor {
-    int64_t tile;
-    int kb;
-    int64_t left;
+    int tile, kb, left;
     TileInfo t;
     __device__ __forceinline__ Cursor(const AttendArgs &a, const AttendShared<N> &sh)
-        : tile(sh.start_tile), kb(sh.start_kb), left(sh.u1 - sh.u0), t(tile_info<N, kSlots>(a, tile)) {}
+        : tile(sh.start_tile), kb(sh.start_kb), left(sh.units), t(tile_info<N, kSlots>(a, tile)) {}
     __device__ __forceinline__ void next(const AttendArgs &a) {
         --left;
         if (++kb >= t.nb) {
@@ -95,58 +103,60 @@ struct Cursor {
     }
 };
 
-// Where chunk and word of the decoded rows lie.  A dequant thread holds
-// tokens r and r + 8 (r = lane / 4) and, of each chunk of 128 dims, 32 dims
-// of each: V41 the 16-dim pieces q and q + 4 (q = lane % 4), FP4 the 32 dims
-// from 32q.  It makes four 8-dim vectors ci = 0..3 of them; vector ci of FP4
-// is piece ci ^ (q & 2), which lets the eight lanes of a shared-memory phase
-// (two tokens, four q) store to eight different banks groups.
-//
-// In TMEM (the A operand of the scores' product) vector ci of thread q fills
-// columns 16 ci + 4 e + q, e = 0..3, two dims a column, so the contraction
-// runs over the dims in another order; q_word() puts a query's dims in the
-// same order.
-
-template <Layout L>
-struct Raw;  // one token's 32 codes of a chunk
-template <>
-struct Raw<Layout::V41> {
-    uint4 p[2];
-};
-template <>
-struct Raw<Layout::FP4> {
-    uint4 p[1];
+// The ring of decoded chunks, walked by every role in the same order.
+template <int R>
+struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == R) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
 };
 
+// Where a decoded row lies.  A decode thread holds, of tokens r and r + 8
+// (r = lane / 4) and of each chunk of 128 dims, the 16 dims from
+// 64 s + 16 q (q = lane % 4, s = 0, 1), as two vectors e = 0, 1 of eight.  In shared memory a chunk is two 128-byte-swizzled tiles of 64 dims;
+// the eight lanes of a store's phase (two tokens, four q) hit different
+// banks.  In TMEM (the A operand of the scores' product) vector e fills the
+// columns 16 (2 s + e) + 4 i + q, i = 0..3, two dims a column: the
+// contraction runs over the dims in another order, and q_word() puts a
+// query's dims in the same one.
 template <Layout L>
-__device__ __forceinline__ void load_raw(Raw<L> &r, const uint8_t *row, int chunk, int q) {
-    constexpr int kChunkBytes = LayoutTraits<L>::kCodeBytes / kChunks;
-#pragma unroll
-    for (int h = 0; h < int(sizeof(Raw<L>) / 16); ++h)
-        r.p[h] = row ? __ldg(reinterpret_cast<const uint4 *>(row + chunk * kChunkBytes + h * 64) + q)
-                     : make_uint4(0u, 0u, 0u, 0u);
+struct Raw {  // 16 codes
+    uint32_t w[L == Layout::V41 ? 4 : 2];
+};
+
+template <Layout L>
+__device__ __forceinline__ Raw<L> load_raw(const uint8_t *row, int chunk, int s, int q) {
+    Raw<L> r = {};
+    if (row) {
+        if constexpr (L == Layout::V41) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + chunk * 128 + s * 64) + q);
+            r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + chunk * 64 + s * 32) + q);
+            r.w[0] = v.x, r.w[1] = v.y;
+        }
+    }
+    return r;
 }
 
-// Vector ci of a token's 32 dims: 8 values as four packed 16-bit pairs.
+// Vector e of a token's 16 dims: codes times `mul` (fp16 twice) as fp16 pairs.
 template <Layout L>
-__device__ __forceinline__ void decode8(const Raw<L> &r, int ci, int q, uint32_t scales, uint32_t (&o)[4]) {
+__device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, uint32_t (&o)[4]) {
     if constexpr (L == Layout::V41) {
-        const uint4 &p = r.p[ci >> 1];
-        const uint32_t w[2] = {(ci & 1) ? p.z : p.x, (ci & 1) ? p.w : p.y};
-        const float s = ue8m0_to_f32((scales >> (8 * (2 * (ci >> 1) + (q >> 1)))) & 0xFFu);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = fmul2(e4m3x2_to_f32x2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), make_float2(s, s));
-            o[i] = pack_bf16x2(f.x, f.y);
-        }
+        for (int i = 0; i < 2; ++i)
+            asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t;\n\t"
+                "mov.b32 {lo, hi}, %2;\n\t"
+                "cvt.rn.f16x2.e4m3x2 t, lo;\n\tmul.rn.f16x2 %0, t, %3;\n\t"
+                "cvt.rn.f16x2.e4m3x2 t, hi;\n\tmul.rn.f16x2 %1, t, %3;\n\t}"
+                : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+                : "r"(r.w[2 * e + i]), "r"(mul));
     } else {
-        const uint4 &p = r.p[0];
-        const bool swap = q & 2;
-        const uint32_t w = ci == 0 ? (swap ? p.z : p.x) : ci == 1 ? (swap ? p.w : p.y) : ci == 2 ? (swap ? p.x : p.z)
-                                                                                              : (swap ? p.y : p.w);
-        const uint32_t sb = (scales >> (8 * q)) & 0xFFu;
-        uint32_t s2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(uint16_t(sb * 0x101u)));
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 t;\n\t"
             "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
             "cvt.rn.f16x2.e2m1x2 t, b0;\n\tmul.rn.f16x2 %0, t, %5;\n\t"
@@ -154,47 +164,90 @@ __device__ __forceinline__ void decode8(const Raw<L> &r, int ci, int q, uint32_t
             "cvt.rn.f16x2.e2m1x2 t, b2;\n\tmul.rn.f16x2 %2, t, %5;\n\t"
             "cvt.rn.f16x2.e2m1x2 t, b3;\n\tmul.rn.f16x2 %3, t, %5;\n\t}"
             : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-            : "r"(w), "r"(s2));
+            : "r"(r.w[e]), "r"(mul));
     }
 }
 
-// Byte offset, in a query tile's shared memory, of word e (dims 8g + 2e,
-// 8g + 2e + 1) of piece g = 0..63 of row r.
-template <Layout L, int N>
-__device__ __forceinline__ uint32_t q_word(int r, int g, int e) {
-    const int b = g >> 4, gi = g & 15;
-    int ci, q;
-    if constexpr (L == Layout::V41) {
-        ci = 2 * (gi >> 3) + (gi & 1);
-        q = (gi >> 1) & 3;
-    } else {
-        q = gi >> 2;
-        ci = (gi & 3) ^ (q & 2);
+// A token's scales for a decode thread: two bytes a chunk (the blocks its 2 *
+// 16 dims lie in).  FP4: code * e4m3 scale is exact in fp16 as it is.  V41: the
+// ue8m0 scales of a row span more than fp16 does, so a row is decoded times
+// 2^-texp, which brings its largest scale to 2^7 (448 * 2^7 < 65504); the
+// softmax warps put 2^texp back into the scores and the weights.  Blocks
+// whose scale is 2^-31 of the row's largest or less vanish, values 2^-22 of
+// it or less are rounded to multiples of 2^-40 of it; both are far below
+// what fp32 sums resolve.  A row whose largest scale is below 2^-40 counts as
+// if it were 2^-40, which keeps the weights of tiny rows apart from zero.
+constexpr int kMinScaleByte = 127 - 40;
+
+template <Layout L>
+struct RowScale {
+    uint32_t bytes[2];  // chunks 0 and 1, 2 and 3
+    int texp;
+    __device__ __forceinline__ void set(uint32_t v, int lane) {  // lanes 4 r .. 4 r + 3 bring a row's four words
+        uint32_t w[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) w[b] = __shfl_sync(0xFFFFFFFFu, v, (lane & ~3) + b);
+        const uint32_t pick = lane & 2 ? 0x7531u : 0x6420u;  // bytes q / 2 and 2 + q / 2 of two words
+        bytes[0] = __byte_perm(w[0], w[1], pick);
+        bytes[1] = __byte_perm(w[2], w[3], pick);
+        texp = 0;
+        if constexpr (L == Layout::V41) {
+            // largest byte: even and odd bytes as 16-bit lanes
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                hi = __vmaxu2(hi, (w[b] >> 8) & 0x00FF00FFu);
+                lo = __vmaxu2(lo, w[b] & 0x00FF00FFu);
+            }
+            lo = __vmaxu2(lo, hi);
+            texp = max(max(int(lo >> 16), int(lo & 0xFFFFu)), kMinScaleByte) - 134;
+        }
     }
-    return uint32_t((2 * b + (ci >> 1)) * N * 128 + r * 128 + (((4 * (ci & 1) + e) ^ (r & 7)) << 4) + q * 4);
+    // The multiplier of half s of chunk b, fp16 twice.
+    __device__ __forceinline__ uint32_t mul(int b, int s) const {
+        uint32_t r;
+        const uint32_t byte = (bytes[b >> 1] >> (16 * (b & 1) + 8 * s)) & 0xFFu;
+        if constexpr (L == Layout::V41) {
+            // 2^(byte - 127 - texp): through bf16, which holds every ue8m0 value and NaN
+            uint32_t h;
+            asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(h) : "h"(uint16_t(byte)));
+            const float f = bf16_lo(h) * __uint_as_float(uint32_t(127 - texp) << 23);
+            asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(f));
+        } else {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(byte * 0x101u)));
+        }
+        return r;
+    }
+};
+
+// Byte offset, in a query tile's shared memory, of word i (dims 8g + 2i,
+// 8g + 2i + 1) of piece g = 0..63 of row r.
+template <int N>
+__device__ __forceinline__ uint32_t q_word(int r, int g, int i) {
+    const int b = g >> 4, s = (g >> 3) & 1, q = (g >> 1) & 3, e = g & 1;
+    return uint32_t((2 * b + s) * N * 128 + r * 128 + (((4 * e + i) ^ (r & 7)) << 4) + q * 4);
 }
 
 // Swizzled byte offset of 16-byte vector j of row t of the weights' tile
 // (rows of N 16-bit values).
 template <int N>
 __device__ __forceinline__ uint32_t p_vec(int t, int j) {
-    constexpr int kVecs = N / 8;
     const int x = N == 64 ? (t & 7) : N == 32 ? ((t >> 1) & 3) : ((t >> 2) & 1);
-    return uint32_t(t * N * 2 + ((j ^ (x & (kVecs - 1))) << 4));
+    return uint32_t(t * N * 2 + ((j ^ x) << 4));
 }
 
-// Lane-transposing reductions: from N values a thread to the warp's total of
-// column col, i = 0 .. max(1, N / 32) - 1, in v[i].
-template <int N>
-__device__ __forceinline__ int warp_columns_sum(float (&v)[N], int lane) {
+// Sums NC values a thread over the warp, lane-transposing; v[0] becomes the
+// total of the returned column (each column in 32 / NC lanes).
+template <int NC>
+__device__ __forceinline__ int warp_columns_sum(float (&v)[NC], int lane) {
     int col = 0;
-    int half = N / 2;
+    int half = NC / 2;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         if (half >= 1) {
             const bool up = lane & o;
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i)
+            for (int i = 0; i < NC / 2; ++i)
                 if (i < half) {
                     const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
                     v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
@@ -214,51 +267,56 @@ __device__ __forceinline__ float redux_max(float v) {
     return r;
 }
 
-// Barrier of the four softmax warps; the second form returns whether any of
+// Barrier of the softmax warps; the second form returns whether any of
 // their threads brought true.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool p) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
-        "bar.red.or.pred b, 1, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+        "bar.red.or.pred b, 1, 256, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
         : "=r"(r)
         : "r"(uint32_t(p))
         : "memory");
     return r != 0;
 }
 
+__device__ __forceinline__ float2 pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+
 template <Layout L, int N, bool kSlots>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using T = LayoutTraits<L>;
-    constexpr bool kBf16 = L == Layout::V41;
+    constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
+    constexpr int R = kRing<N>;
     constexpr uint32_t kTmemS = 4 * N, kTmemK = 5 * N;
     constexpr uint32_t kTmemCols = 5 * N + 128 <= 256 ? 256 : 512;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
-    uint8_t *const sK = base, *const sQ = sK + kTile * kD * 2, *const sP = sQ + N * kD * 2;
+    uint8_t *const sK = base, *const sQ = sK + R * kChunkSmem, *const sP = sQ + N * kD * 2;
     auto &sh = *reinterpret_cast<AttendShared<N> *>(sP + kTile * N * 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_wait();
 
-    // ---- this CTA's share: block units [u0, u1) of the tiles in order
-    const int64_t tiles = a.n_seq * a.row_tiles;
+    // ---- this CTA's share: blocks [u0, u1) of all tiles' blocks in order
+    const int tiles = int(a.n_seq * a.row_tiles);
     if constexpr (kSlots) {
         if (tid == 0) {
             const int64_t nb = max(int64_t(1), (a.max_len + kTile - 1) / kTile);
-            sh.total = tiles * nb;
-            const int64_t g = min(int64_t(gridDim.x), sh.total);
-            sh.u0 = blockIdx.x < g ? int64_t(blockIdx.x) * sh.total / g : 0;
-            sh.u1 = blockIdx.x < g ? int64_t(blockIdx.x + 1) * sh.total / g : 0;
-            sh.start_tile = int(sh.u0 / nb);
-            sh.start_kb = int(sh.u0 % nb);
+            const int64_t total = tiles * nb, g = min(int64_t(gridDim.x), total);
+            const int64_t u0 = blockIdx.x < g ? int64_t(blockIdx.x) * total / g : 0;
+            const int64_t u1 = blockIdx.x < g ? int64_t(blockIdx.x + 1) * total / g : 0;
+            sh.total = total;
+            sh.u0 = u0;
+            sh.units = int(u1 - u0);
+            sh.start_tile = int(u0 / nb);
+            sh.start_kb = int(u0 % nb);
         }
     } else {
-        const int64_t per = (tiles + kAttendThreads - 1) / kAttendThreads;
-        const int64_t t0 = min(tiles, tid * per), t1 = min(tiles, t0 + per);
+        const int per = (tiles + kAttendThreads - 1) / kAttendThreads;
+        const int t0 = int(min(int64_t(tiles), int64_t(tid) * per)), t1 = int(min(int64_t(tiles), int64_t(t0) + per));
         int64_t mine = 0;
-        for (int64_t t = t0; t < t1; ++t) mine += tile_info<N, kSlots>(a, t).nb;
+        for (int t = t0; t < t1; ++t) mine += tile_info<N, kSlots>(a, t).nb;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -276,16 +334,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int64_t u0 = blockIdx.x < g ? int64_t(blockIdx.x) * total / g : 0;
         const int64_t u1 = blockIdx.x < g ? int64_t(blockIdx.x + 1) * total / g : 0;
         if (tid == 0) {
-            sh.u0 = u0;
-            sh.u1 = u1;
             sh.total = total;
+            sh.u0 = u0;
+            sh.units = int(u1 - u0);
         }
         int64_t at = before + incl - mine;
         if (u0 >= at && u0 < at + mine)
-            for (int64_t t = t0; t < t1; ++t) {
+            for (int t = t0; t < t1; ++t) {
                 const int nb = tile_info<N, kSlots>(a, t).nb;
                 if (u0 < at + nb) {
-                    sh.start_tile = int(t);
+                    sh.start_tile = t;
                     sh.start_kb = int(u0 - at);
                     break;
                 }
@@ -293,7 +351,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
     }
     if (tid == 0) {
-        for (int i = 0; i < kChunks; ++i) {
+        for (int i = 0; i < R; ++i) {
             mbar_init(smem_addr(&sh.full[i]), kDeqWarps);
             mbar_init(smem_addr(&sh.oblk[i]), 1);
         }
@@ -307,37 +365,39 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    const int64_t units = sh.u1 - sh.u0;
+    const int units = sh.units;
     if (units == 0) {  // the same for every thread
         if (tid == 0) a.join[blockIdx.x] = make_int2(-1, 0);
         pdl_trigger();
         return;
     }
-    if (warp == kSoftWarps + kDeqWarps) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
-    if (warp >= kSoftWarps && warp < kSoftWarps + kDeqWarps) {
+    if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
         const int w = warp - kSoftWarps, q = lane & 3, r8 = lane >> 2;
         const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
         const uint32_t krow = smem_addr(sK) + tok0 * 128;
-        const uint32_t kxor = (L == Layout::V41 ? 2 * q : ((q & 1) * 4) ^ (q & 2)) ^ r8;
+        const uint32_t at0 = krow + (((2 * q) ^ r8) << 4), at1 = krow + (((2 * q + 1) ^ r8) << 4);
         const uint32_t tlane = tmem + kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
         const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits;
         const int in_page = (1 << a.page_bits) - 1;
 
         Cursor<N, kSlots> cur(a, sh);
-        int64_t idx[2];   // page or slot, -1: no token
-        int in[2];        // row in the page (paged)
+        using Index = std::conditional_t<kSlots, int64_t, int>;
+        Index idx[2];  // page or slot, -1: no token
+        int row0 = 0;  // token tok0's place in its page (paged)
         auto fetch = [&]() {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t t = int64_t(cur.kb) * kTile + tok0 + 8 * h;
                 idx[h] = -1;
-                in[h] = int(t) & in_page;
+                if (h == 0) row0 = int(t) & in_page;
                 if (cur.left > 0 && t < cur.t.seen) {
                     if constexpr (kSlots) {
                         const int64_t at = cur.t.seq * a.slots_stride + t;
@@ -351,99 +411,106 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
         };
         const uint8_t *code[2];
-        uint4 sc[2];
+        uint32_t sc[2];  // word q of the token's 16 scale bytes
         auto resolve = [&]() {  // row pointers and scales of the fetched block
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 code[h] = nullptr;
-                sc[h] = make_uint4(0u, 0u, 0u, 0u);
+                sc[h] = 0;
                 if (idx[h] >= 0 && idx[h] < a.pool_limit) {
                     const int64_t page = kSlots ? idx[h] >> a.page_bits : idx[h];
-                    const int row = kSlots ? int(idx[h]) & in_page : in[h];
+                    const int row = kSlots ? int(idx[h]) & in_page : (row0 + 8 * h) & in_page;
                     const uint8_t *p = a.pool + page * page_bytes;
                     code[h] = p + row * T::kCodeBytes;
-                    sc[h] = __ldg(reinterpret_cast<const uint4 *>(p + (int64_t(T::kCodeBytes) << a.page_bits) +
-                                                                  row * T::kScaleBytes));
+                    sc[h] = __ldg(reinterpret_cast<const uint32_t *>(p + (int64_t(T::kCodeBytes) << a.page_bits) +
+                                                                     row * T::kScaleBytes) + q);
                 } else if (idx[h] != -1 && q == 0) {
                     raise_err(a.err, kSlots ? KVQ_DEVERR_SLOT : KVQ_DEVERR_PAGE);
                 }
             }
         };
 
-        Raw<L> raw[kChunks][2];
+        Raw<L> raw[kChunks][2][2];  // chunk, token, half
+        auto load = [&](int b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) raw[b][h][s] = load_raw<L>(code[h], b, s, q);
+        };
+        RowScale<L> rs[2];
+        bool ok[2];
+        auto adopt = [&]() {  // the resolved block becomes the current one
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ok[h] = code[h] != nullptr;
+                rs[h].set(sc[h], lane);
+            }
+        };
         fetch();
         resolve();
 #pragma unroll
-        for (int b = 0; b < kChunks; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) load_raw<L>(raw[b][h], code[h], b, q);
-        bool ok[2] = {code[0] != nullptr, code[1] != nullptr};
-        uint4 now[2] = {sc[0], sc[1]};
+        for (int b = 0; b < kChunks; ++b) load(b);
         cur.next(a);
         fetch();
-        for (int64_t i = 0; i < units; ++i) {
-            resolve();   // the next block; its indexes came a block ago
+        adopt();
+        Ring<R> ring;
+        bool live = true;
+        for (int i = 0; i < units && live; ++i) {
+            resolve();  // the next block; its indexes came a block ago
             if (cur.left > 0) cur.next(a);
             fetch();
-            const uint32_t phase = uint32_t(i) & 1;
-            bool live = true;
 #pragma unroll
             for (int b = 0; b < kChunks; ++b) {
-                // shared memory is free when the last block's product over these dims is done; the TMEM slot
-                // when the scores' product two chunks ago is
-                if (i > 0) live = live && mbar_wait(smem_addr(&sh.oblk[b]), phase ^ 1);
+                // the slot is free when the product over the dims that it held is done, a TMEM slot when the
+                // scores' product two chunks ago is
+                if (i * kChunks + b >= R) live = live && mbar_wait(smem_addr(&sh.oblk[ring.slot]), ring.parity ^ 1);
                 if (i > 0 || b >= 2) live = live && mbar_wait(smem_addr(&sh.kfree[b & 1]), b >= 2 ? 0 : 1);
                 tc_fence_after();
                 if (b == 0 && q == 0) {
-                    sh.valid[phase][tok0] = ok[0];
-                    sh.valid[phase][tok0 + 8] = ok[1];
+                    sh.texp[i & 1][tok0] = ok[0] ? rs[0].texp : kNoToken;
+                    sh.texp[i & 1][tok0 + 8] = ok[1] ? rs[1].texp : kNoToken;
                 }
-                const uint32_t s0 = b == 0 ? now[0].x : b == 1 ? now[0].y : b == 2 ? now[0].z : now[0].w;
-                const uint32_t s1 = b == 0 ? now[1].x : b == 1 ? now[1].y : b == 2 ? now[1].z : now[1].w;
+                const uint32_t off = ring.slot * kChunkSmem;
 #pragma unroll
-                for (int ci = 0; ci < 4; ++ci) {
-                    uint32_t v0[4], v1[4];
-                    decode8<L>(raw[b][0], ci, q, s0, v0);
-                    decode8<L>(raw[b][1], ci, q, s1, v1);
-                    const int sub = 2 * b + (L == Layout::V41 ? ci >> 1 : 0);
-                    const uint32_t at = krow + sub * kSubBytes + (L == Layout::V41 ? 0 : (q >> 1) * kSubBytes) +
-                                        ((kxor ^ (L == Layout::V41 ? (ci & 1) : ci)) << 4);
-                    sts_u4(at, v0);
-                    sts_u4(at + 8 * 128, v1);
-                    tmem_st_16x128b_x4(tlane + (b & 1) * 64 + 16 * ci, v0, v1);
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t m0 = rs[0].mul(b, s), m1 = rs[1].mul(b, s);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t v0[4], v1[4];
+                        decode8<L>(raw[b][0][s], e, m0, v0);
+                        decode8<L>(raw[b][1][s], e, m1, v1);
+                        const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
+                        sts_u4(at, v0);
+                        sts_u4(at + 8 * 128, v1);
+                        tmem_st_16x128b_x4(tlane + (b & 1) * 64 + 32 * s + 16 * e, v0, v1);
+                    }
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) load_raw<L>(raw[b][h], code[h], b, q);
+                load(b);
                 tc_wait_st();
                 tc_fence_before();
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.full[b]));
+                if (lane == 0) mbar_arrive(smem_addr(&sh.full[ring.slot]));
+                ring.next();
             }
-            if (!live) {
-                sh.abort = 1;
-                break;
-            }
-            ok[0] = code[0] != nullptr;
-            ok[1] = code[1] != nullptr;
-            now[0] = sc[0];
-            now[1] = sc[1];
+            adopt();
         }
-    } else if (warp == kSoftWarps + kDeqWarps) {
+        if (!live) sh.abort = 1;
+    } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = mma_idesc(kTile, N, kBf16, false, false);
-            constexpr uint32_t kIdescO = mma_idesc(kTile, N, kBf16, true, true);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (warp == kMmaWarp) {
+            constexpr uint32_t kIdescS = mma_idesc(kTile, N, false, false);
+            constexpr uint32_t kIdescO = mma_idesc(kTile, N, true, true);
             constexpr uint64_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
             const uint64_t qd = smem_desc(smem_addr(sQ), 16, 1024, kSwizzle128);
             const uint64_t vd = smem_desc(smem_addr(sK), kSubBytes, 1024, kSwizzle128);
             const uint64_t pd = smem_desc(smem_addr(sP), 16, 16 * N, kPSwizzle);
-            int64_t left_tile = 0;
+            int left_tile = 0, tile = sh.start_tile, kb = sh.start_kb;
             uint32_t seg = 0;
-            int64_t tile = sh.start_tile;
-            int kb = sh.start_kb;
             bool live = true;
-            for (int64_t i = 0; i < units && live; ++i) {
+            Ring<R> sr, vr;
+            for (int i = 0; i < units && live; ++i) {
                 const uint32_t phase = uint32_t(i) & 1;
                 bool first = false;
                 if (left_tile == 0) {  // a new tile: its queries, a fresh accumulator
@@ -455,86 +522,99 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     ++seg;
                 }
                 --left_tile;
-                for (int b = 0; b < kChunks && live; ++b) {
-                    live = live && mbar_wait(smem_addr(&sh.full[b]), phase);
-                    tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + kTmemS, tmem + kTmemK + (b & 1) * 64 + 8 * k,
-                               qd + ((((2 * b + (k >> 2)) * N * 128) + (k & 3) * 32) >> 4), kIdescS, b + k > 0);
-                    mma_commit(smem_addr(&sh.kfree[b & 1]));
+                for (int b = 0; b < kChunks; ++b) {
+                    live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
+                    tc_fence_after();
+                    if (live && elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(tmem + kTmemS, tmem + kTmemK + (b & 1) * 64 + 8 * k,
+                                   qd + ((((2 * b + (k >> 2)) * N * 128) + (k & 3) * 32) >> 4), kIdescS, b + k > 0);
+                        mma_commit(smem_addr(&sh.kfree[b & 1]));
+                        if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
+                    }
+                    __syncwarp();
+                    sr.next();
                 }
-                mma_commit(smem_addr(&sh.sdone));
                 live = live && mbar_wait(smem_addr(&sh.pready), phase);
                 tc_fence_after();
-                for (int b = 0; b < kChunks; ++b) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ss(tmem + b * N, vd + ((2 * b * kSubBytes + k * 2048) >> 4), pd + ((k * 32 * N) >> 4),
-                               kIdescO, !first || k > 0);
-                    mma_commit(smem_addr(&sh.oblk[b]));
+                for (int b = 0; b < kChunks; ++b) {
+                    if (live && elect_one()) {
+                        const uint64_t at = vd + ((vr.slot * kChunkSmem) >> 4);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ss(tmem + b * N, at + ((k * 2048) >> 4), pd + ((k * 32 * N) >> 4), kIdescO,
+                                   !first || k > 0);
+                        mma_commit(smem_addr(&sh.oblk[vr.slot]));
+                    }
+                    __syncwarp();
+                    vr.next();
                 }
             }
             if (!live) {
                 sh.abort = 1;
-                mma_commit(smem_addr(&sh.drain));   // nothing may write TMEM once it is freed
+                if (elect_one()) mma_commit(smem_addr(&sh.drain));  // nothing may write TMEM once it is freed
                 mbar_wait(smem_addr(&sh.drain), 0);
             }
         }
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        constexpr int NC = N / 2;  // columns a thread: those from c0
+        const int t_row = tid & 127, quarter = warp & 3, half = warp >> 2, c0 = half * NC;
         const float c = a.scale * kLog2e;
-        const int64_t per = int64_t(a.q_len) * a.heads;
-        const uint32_t trow = tmem + (uint32_t(warp * 32) << 16);
+        const int per = a.q_len * a.heads;
+        const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
         Cursor<N, kSlots> cur(a, sh);
-        float l[N];
-        // A warp that gives up a wait says so before the four warps' next barrier, so that all leave together.
+        Ring<R> ring;
+        float l[NC];
+        // A warp that gives up a wait says so before the softmax warps' next barrier, so that all leave together.
         volatile int &gone = sh.soft_abort;
         bool unset = false, live = true;
         int kb0 = 0;
-        for (int64_t i = 0; i < units && live; ++i, cur.next(a)) {
+        for (int i = 0; i < units && live; ++i, cur.next(a)) {
             const uint32_t phase = uint32_t(i) & 1;
             const bool first = i == 0 || cur.kb == 0;
             if (first) {
                 // the scores' products of the last tile are done (their result was waited for)
                 kb0 = cur.kb;
                 if (tid == 0 && cur.kb == 0 && cur.t.rt == 0 && cur.t.err) raise_err(a.err, cur.t.err);
-                const int64_t row0 = int64_t(cur.t.rt) * N;
+                const int row0 = cur.t.rt * N;
                 const uint32_t sq = smem_addr(sQ);
-#pragma unroll 4
+#pragma unroll 2
                 for (int r = warp; r < N; r += kSoftWarps) {
-                    const int64_t R = row0 + r;
+                    const int row = row0 + r;
                     uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                    if (R < per) {
-                        const uint16_t *p = a.q + (cur.t.seq * a.q_len + R / a.heads) * a.q_tok + (R % a.heads) * a.q_head;
+                    const int rc = min(row, per - 1);
+                    const int64_t tok = int64_t(cur.t.seq) * a.q_len + rc / a.heads;
+                    const int head = rc % a.heads;
+                    if (row < per) {
+                        const uint16_t *p = a.q + tok * a.q_tok + head * a.q_head;
                         u[0] = ld_stream_u4(p + lane * 8);
                         u[1] = ld_stream_u4(p + (lane + 32) * 8);
                     }
-                    float back = 1.f;
                     uint32_t v[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-                    if constexpr (!kBf16) {
-                        // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
-                        uint32_t big = 0;
+                    // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
+                    uint32_t big = 0;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) big = max(big, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
-                        big = __reduce_max_sync(0xFFFFFFFFu, big);
-                        const uint32_t up = min(268u - (big >> 23), 254u);
-                        const float f = __uint_as_float(up << 23);
-                        back = ue8m0_to_f32(254u - up);
+                    for (int e = 0; e < 8; ++e) big = max(big, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+                    big = __reduce_max_sync(0xFFFFFFFFu, big);
+                    const uint32_t up = min(268u - (big >> 23), 254u);
+                    const float f = __uint_as_float(up << 23);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[e]) : "f"(bf16_hi(v[e]) * f), "f"(bf16_lo(v[e]) * f));
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t h;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[e]) * f), "f"(bf16_lo(v[e]) * f));
+                        sts_u32(sq + q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
                     }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sts_u32(sq + q_word<L, N>(r, lane + 32 * (e >> 2), e & 3), v[e]);
                     if (lane == 0) {
-                        const int64_t Rc = min(R, per - 1);
-                        const int64_t tok = cur.t.seq * a.q_len + Rc / a.heads;
-                        sh.sc[r] = c * back;
+                        sh.sc[r] = c * ue8m0_to_f32(254u - up);
                         sh.m[r] = -INFINITY;
-                        sh.vis[r] = kSlots || R >= per ? cur.t.seen : max(0, cur.t.len - (a.q_len - 1 - int(Rc / a.heads)));
-                        sh.row[r] = R < per ? tok * a.out_tok + (Rc % a.heads) * a.out_head : -1;
+                        sh.nm[r] = 0.f;
+                        sh.vis[r] = kSlots || row >= per ? cur.t.seen : max(0, cur.t.len - (a.q_len - 1 - rc / a.heads));
+                        sh.row[r] = row < per ? tok * a.out_tok + head * a.out_head : -1;
                     }
                 }
                 fence_proxy_async();
@@ -542,163 +622,148 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if (lane == 0) mbar_arrive(smem_addr(&sh.qready));
                 soft_sync();
 #pragma unroll
-                for (int j = 0; j < N; ++j) l[j] = 0.f;
+                for (int j = 0; j < NC; ++j) l[j] = 0.f;
                 unset = true;
             }
-            // full[0] orders this thread's read of `valid`
-            if (!mbar_wait(smem_addr(&sh.full[0]), phase) || !mbar_wait(smem_addr(&sh.sdone), phase)) gone = 1;
+            // the full barrier of the block's first chunk orders this thread's read of `texp`
+            if (!mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity) || !mbar_wait(smem_addr(&sh.sdone), phase)) gone = 1;
             tc_fence_after();
-            const int64_t t64 = int64_t(cur.kb) * kTile + tid;
-            const bool have = sh.valid[phase][tid];
-            const int t_at = have ? int(t64) : 0x7FFFFFFF;
+            const int te = sh.texp[i & 1][t_row];
+            const bool have = te != kNoToken;
+            const int t_at = have ? cur.kb * kTile + t_row : 0x7FFFFFFF;
             // whether some of the block is masked for some row (the first row of a tile sees least)
-            const bool masked = !__all_sync(0xFFFFFFFFu, have) || (int64_t(cur.kb) + 1) * kTile > sh.vis[0];
+            const bool masked = !__all_sync(0xFFFFFFFFu, have) || int64_t(cur.kb + 1) * kTile > sh.vis[0];
+            const float et = kExp && have ? float(te) : 0.f;
+            const float e_up = kExp && have ? __uint_as_float(uint32_t(127 + te) << 23) : 1.f;
+            const float e_down = kExp && have ? __uint_as_float(uint32_t(127 - te) << 23) : 1.f;
 
-            auto scores = [&](int j0, uint32_t (&s)[1][16]) {
-                tmem_ld16(trow + kTmemS + j0, s[0]);
-                tmem_ld_done(s);
-            };
+            // x = score in log2 units, plus the row's power of two; -inf where it is masked
+            float x[NC];
+            bool odd = false;  // a score that is not finite, where some rows do not see the token
+            {
+                uint32_t sraw[NC];
+                tmem_ld<NC>(trow + kTmemS + c0, sraw);
+#pragma unroll
+                for (int j = 0; j < NC; j += 2) {
+                    float2 v = make_float2(__uint_as_float(sraw[j]), __uint_as_float(sraw[j + 1]));
+                    if (masked) odd = odd || !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
+                    if constexpr (kExp)
+                        v = ffma2(fmul2(v, make_float2(e_up, e_up)), pair(&sh.sc[c0 + j]), make_float2(et, et));
+                    else
+                        v = fmul2(v, pair(&sh.sc[c0 + j]));
+                    x[j] = v.x;
+                    x[j + 1] = v.y;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+                        if (!(t_at < sh.vis[c0 + j])) x[j] = -INFINITY;
+                }
+            }
             bool move = unset;
             if (!move) {
                 float top = -INFINITY;
 #pragma unroll
-                for (int j0 = 0; j0 < N; j0 += 16) {
-                    uint32_t s[1][16];
-                    scores(j0, s);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 x = ffma2(make_float2(__uint_as_float(s[0][j]), __uint_as_float(s[0][j + 1])),
-                                               *reinterpret_cast<const float2 *>(&sh.sc[j0 + j]),
-                                               *reinterpret_cast<const float2 *>(&sh.nm[j0 + j]));
-                        if (masked) {
-                            if (t_at < sh.vis[j0 + j]) top = fmaxf(top, x.x);
-                            if (t_at < sh.vis[j0 + j + 1]) top = fmaxf(top, x.y);
-                        } else {
-                            top = fmax3(top, x.x, x.y);
-                        }
-                    }
+                for (int j = 0; j < NC; j += 2) {
+                    const float2 v = fadd2(make_float2(x[j], x[j + 1]), pair(&sh.nm[c0 + j]));
+                    top = fmax3(top, v.x, v.y);
                 }
                 move = soft_any(top > kStaleMax);
             }
             if (move) {
                 // the columns' new maxima, and what is summed so far in their terms
-                float mine[(N + 31) / 32];
+                float mine = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < (N + 31) / 32; ++k) mine[k] = -INFINITY;
-#pragma unroll
-                for (int j0 = 0; j0 < N; j0 += 16) {
-                    uint32_t s[1][16];
-                    scores(j0, s);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float x = __uint_as_float(s[0][j]) * sh.sc[j0 + j];
-                        if (!(t_at < sh.vis[j0 + j])) x = -INFINITY;
-                        x = redux_max(x);
-                        if (lane == ((j0 + j) & 31)) mine[(j0 + j) >> 5] = x;
-                    }
+                for (int j = 0; j < NC; ++j) {
+                    const float v = redux_max(x[j]);
+                    if (lane == j) mine = v;
                 }
-#pragma unroll
-                for (int k = 0; k < (N + 31) / 32; ++k)
-                    if (lane + 32 * k < N) sh.red[warp][lane + 32 * k] = mine[k];
+                if (lane < NC) sh.red[quarter][c0 + lane] = mine;
                 soft_sync();
                 bool none = false;
                 if (tid < N) {
                     const float m0 = sh.m[tid];
                     const float m1 = fmaxf(fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid])), m0);
-                    sh.m[tid] = m1;
-                    sh.nm[tid] = m1 == -INFINITY ? 0.f : -m1;
-                    sh.alpha[tid] = m1 == -INFINITY ? 1.f : ex2_approx(m0 - m1);
                     none = m1 == -INFINITY;
+                    sh.m[tid] = m1;
+                    sh.nm[tid] = none ? 0.f : -m1;
+                    sh.alpha[tid] = none ? 1.f : ex2_approx(m0 - m1);
                 }
                 unset = soft_any(none);
 #pragma unroll
-                for (int j = 0; j < N; ++j) l[j] *= sh.alpha[j];
+                for (int j = 0; j < NC; ++j) l[j] *= sh.alpha[c0 + j];
                 if (!first) {
 #pragma unroll 1
-                    for (int b = 0; b < kChunks; ++b)
-#pragma unroll
+                    for (int b = 2 * half; b < 2 * half + 2; ++b)
+#pragma unroll 1
                         for (int j0 = 0; j0 < N; j0 += 16) {
-                            uint32_t o[1][16];
-                            tmem_ld16(trow + b * N + j0, o[0]);
-                            tmem_ld_done(o);
+                            uint32_t o[16];
+                            tmem_ld<16>(trow + b * N + j0, o);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                o[0][j] = __float_as_uint(__uint_as_float(o[0][j]) * sh.alpha[j0 + j]);
-                            tmem_st16(trow + b * N + j0, o[0]);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.alpha[j0 + j]);
+                            tmem_st16(trow + b * N + j0, o);
                         }
                     tc_wait_st();
                 }
             }
-            if (gone) {   // a barrier lies between any warp's wait and here
+            if (gone) {  // a barrier lies between any warp's wait and here
                 live = false;
                 break;
             }
-            bool odd = false;   // a score that is not finite, where some rows do not see the token
+            const uint32_t sp = smem_addr(sP);
 #pragma unroll
-            for (int j0 = 0; j0 < N; j0 += 16) {
-                uint32_t s[1][16];
-                scores(j0, s);
-                float p[16];
+            for (int j0 = 0; j0 < NC; j0 += 8) {
+                uint32_t h[4];
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    float2 x = ffma2(make_float2(__uint_as_float(s[0][j]), __uint_as_float(s[0][j + 1])),
-                                     *reinterpret_cast<const float2 *>(&sh.sc[j0 + j]),
-                                     *reinterpret_cast<const float2 *>(&sh.nm[j0 + j]));
-                    if (masked) {
-                        odd = odd || !(fabsf(__uint_as_float(s[0][j])) < INFINITY) ||
-                              !(fabsf(__uint_as_float(s[0][j + 1])) < INFINITY);
-                        if (!(t_at < sh.vis[j0 + j])) x.x = -INFINITY;
-                        if (!(t_at < sh.vis[j0 + j + 1])) x.y = -INFINITY;
-                    }
-                    p[j] = ex2_approx(x.x);
-                    p[j + 1] = ex2_approx(x.y);
-                    l[j0 + j] += p[j];
-                    l[j0 + j + 1] += p[j + 1];
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 v = fadd2(make_float2(x[j0 + j], x[j0 + j + 1]), pair(&sh.nm[c0 + j0 + j]));
+                    const float2 p = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+                    float2 sum = make_float2(l[j0 + j], l[j0 + j + 1]);
+                    if constexpr (kExp) sum = ffma2(p, make_float2(e_down, e_down), sum);
+                    else sum = fadd2(sum, p);
+                    l[j0 + j] = sum.x;
+                    l[j0 + j + 1] = sum.y;
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j / 2]) : "f"(p.y), "f"(p.x));
                 }
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (kBf16)
-                            w[e] = pack_bf16x2(p[8 * v + 2 * e], p[8 * v + 2 * e + 1]);
-                        else
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p[8 * v + 2 * e + 1]), "f"(p[8 * v + 2 * e]));
-                    }
-                    sts_u4(smem_addr(sP) + p_vec<N>(tid, j0 / 8 + v), w);
-                }
+                sts_u4(sp + p_vec<N>(t_row, (c0 + j0) / 8), h);
             }
-            if (masked && odd && have) {
+            if (masked && odd && have && half == 0) {
                 // a weight of 0 does not silence a NaN: if the token's row itself is not finite, the rows that see
                 // it are NaN by their weights already, and the others must meet zeros
-                const uint32_t row = smem_addr(sK) + tid * 128;
                 bool bad = false;
-                for (int v = 0; v < 64; ++v) {
-                    const uint4 u = lds_u4(row + (v >> 3) * kSubBytes + (v & 7) * 16);
-                    constexpr uint32_t kInf = kBf16 ? 0x7F80u : 0x7C00u;
-                    const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
-                    for (int e = 0; e < 4; ++e)
-                        bad = bad || (ws[e] & kInf) == kInf || ((ws[e] >> 16) & kInf) == kInf;
-                }
-                if (bad)
-                    for (int v = 0; v < 64; ++v) {
-                        const uint32_t z[4] = {0u, 0u, 0u, 0u};
-                        sts_u4(row + (v >> 3) * kSubBytes + (v & 7) * 16, z);
+                for (int pass = 0; pass < 2; ++pass) {
+                    Ring<R> at = ring;
+                    for (int v = 0; v < 64 && (pass == 0 || bad); ++v) {
+                        const uint32_t p = smem_addr(sK) + at.slot * kChunkSmem + ((v >> 3) & 1) * kSubBytes + t_row * 128 + (v & 7) * 16;
+                        if (pass == 0) {
+                            const uint4 u = lds_u4(p);
+                            const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+                            for (int e = 0; e < 4; ++e)
+                                bad = bad || (ws[e] & 0x7C00u) == 0x7C00u || (ws[e] & 0x7C000000u) == 0x7C000000u;
+                        } else {
+                            const uint32_t z[4] = {0u, 0u, 0u, 0u};
+                            sts_u4(p, z);
+                        }
+                        if ((v & 15) == 15) at.next();
                     }
+                }
             }
             tc_fence_before();
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.pready));
+            // the ring moves on by a block; the last chunk's slot tells when the block's outputs are summed
+            Ring<R> end = ring;
+            for (int b = 0; b < kChunks; ++b) {
+                end = ring;
+                ring.next();
+            }
 
-            const bool last = i + 1 == units || cur.kb + 1 == cur.t.nb;
-            if (last) {
+            if (i + 1 == units || cur.kb + 1 == cur.t.nb) {
                 // ---- this CTA's part of the tile is done
                 const bool whole = kb0 == 0 && cur.kb + 1 == cur.t.nb;
-                const int col = warp_columns_sum<N>(l, lane);
-#pragma unroll
-                for (int k = 0; k < (N + 31) / 32; ++k)
-                    if (N >= 32 || (lane & 1) == 0) sh.red[warp][col + k] = l[k];
+                const int col = c0 + warp_columns_sum<NC>(l, lane);
+                if ((lane & (32 / NC - 1)) == 0) sh.red[quarter][col] = l[0];
                 soft_sync();
                 float *part = nullptr;
                 if (!whole) part = a.part + (2 * int64_t(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * N * kPartRow;
@@ -706,48 +771,47 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     const float sum = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
                     const float m = sh.m[tid];
                     sh.inv[tid] = whole ? (m == -INFINITY && sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                    const int64_t R = int64_t(cur.t.rt) * N + tid;
+                    const int row = cur.t.rt * N + tid;
                     if (!whole) {
                         part[tid * kPartRow + kD] = m;
                         part[tid * kPartRow + kD + 1] = sum;
-                    } else if (a.lse && R < per) {
-                        a.lse[cur.t.seq * per + R] = attend_lse(m, sum);
+                    } else if (a.lse && row < per) {
+                        a.lse[int64_t(cur.t.seq) * per + row] = attend_lse(m, sum);
                     }
                 }
-                if (tid == 0 && (i + 1 == units)) {
+                if (tid == 0 && i + 1 == units) {
                     int2 join = make_int2(-1, 0);
                     if (kb0 == 0 && !whole) {  // later CTAs hold the rest of this tile
-                        const int64_t end = sh.u1 + (cur.t.nb - 1 - cur.kb) - 1;   // its last unit
-                        const int64_t g = min(int64_t(gridDim.x), int64_t(sh.total));
-                        join = make_int2(int(cur.tile), int(((end + 1) * g - 1) / sh.total));
+                        const int64_t end_unit = sh.u0 + units - 1 + (cur.t.nb - 1 - cur.kb);
+                        const int64_t g = min(int64_t(gridDim.x), sh.total);
+                        join = make_int2(cur.tile, int(((end_unit + 1) * g - 1) / sh.total));
                     }
                     a.join[blockIdx.x] = join;
                 }
                 soft_sync();
-                const bool done = mbar_wait(smem_addr(&sh.oblk[kChunks - 1]), phase);
+                const bool done = mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity);
                 if (!done) gone = 1;
                 tc_fence_after();
                 if (done) {
 #pragma unroll 1
-                    for (int b = 0; b < kChunks; ++b) {
-                        const int d = b * kChunk + tid;
+                    for (int b = 2 * half; b < 2 * half + 2; ++b) {
+                        const int d = b * kChunk + t_row;
 #pragma unroll 1
                         for (int j0 = 0; j0 < N; j0 += 16) {
-                            uint32_t o[1][16];
-                            tmem_ld16(trow + b * N + j0, o[0]);
-                            tmem_ld_done(o);
+                            uint32_t o[16];
+                            tmem_ld<16>(trow + b * N + j0, o);
                             if (!whole) {
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) part[(j0 + j) * kPartRow + d] = __uint_as_float(o[0][j]);
+                                for (int j = 0; j < 16; ++j) part[(j0 + j) * kPartRow + d] = __uint_as_float(o[j]);
                             } else if (a.out_bf16) {
                                 // neighbouring lanes swap columns, so that a store is two dims of one row
 #pragma unroll
                                 for (int j = 0; j < 16; j += 2) {
-                                    const float x = __uint_as_float(o[0][j]) * sh.inv[j0 + j];
-                                    const float y = __uint_as_float(o[0][j + 1]) * sh.inv[j0 + j + 1];
-                                    const float z = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? x : y, 1);
+                                    const float u = __uint_as_float(o[j]) * sh.inv[j0 + j];
+                                    const float v = __uint_as_float(o[j + 1]) * sh.inv[j0 + j + 1];
+                                    const float z = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? u : v, 1);
                                     const int64_t row = sh.row[j0 + j + (lane & 1)];
-                                    const uint32_t two = (lane & 1) ? pack_bf16x2(z, y) : pack_bf16x2(x, z);
+                                    const uint32_t two = (lane & 1) ? pack_bf16x2(z, v) : pack_bf16x2(u, z);
                                     if (row >= 0)
                                         *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row + (d & ~1)) = two;
                                 }
@@ -755,19 +819,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) {
                                     const int64_t row = sh.row[j0 + j];
-                                    if (row >= 0) static_cast<float *>(a.out)[row + d] = __uint_as_float(o[0][j]) * sh.inv[j0 + j];
+                                    if (row >= 0) static_cast<float *>(a.out)[row + d] = __uint_as_float(o[j]) * sh.inv[j0 + j];
                                 }
                             }
                         }
                     }
                 }
                 tc_fence_before();
-                soft_sync();   // the tile's arrays are free for the next one
+                soft_sync();  // the tile's arrays are free for the next one
                 live = !gone;
             }
         }
         if (!live) {
-            if (lane == 0) raise_err(a.err, KVQ_DEVERR_WAIT);
             sh.abort = 1;
             if (tid == 0) a.join[blockIdx.x] = make_int2(-1, 0);
         }
@@ -778,7 +841,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && sh.abort) raise_err(a.err, KVQ_DEVERR_WAIT);
-    if (warp == kSoftWarps + kDeqWarps) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the tiles that CTAs split: CTA (x, y) takes rows 4y .. 4y+3 of the
@@ -839,12 +902,13 @@ kvq_status launch_attend_n(AttendArgs a, cudaStream_t s) {
     const int64_t per = int64_t(a.q_len) * a.heads;
     a.row_tiles = int((per + N - 1) / N);
     const int64_t tiles = a.n_seq * a.row_tiles;
-    if (tiles > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
     int64_t grid = 0;
     kvq_status st = resident_grid<attend_kernel<L, N, kSlots>, kAttendThreads>(kAttendSmem<N>, &grid);
     if (st != KVQ_OK) return st;
     if (grid > kMaxAttendCtas) grid = kMaxAttendCtas;
-    const int64_t most = (a.max_len + kTile - 1) / kTile;   // blocks of the longest tile there can be
+    const int64_t most = (a.max_len + kTile - 1) / kTile;  // blocks of the longest tile there can be
+    if (tiles > 0x7FFFFFFF || per > 0x7FFFFFFF || tiles * (most ? most : 1) / grid >= 0x7FFFFFFF / kChunks)
+        return KVQ_ERR_UNSUPPORTED;
     if (most <= 1 && tiles < grid) grid = tiles;
     a.join = reinterpret_cast<int2 *>(a.ws);
     a.part = reinterpret_cast<float *>(a.ws + kMaxAttendCtas * sizeof(int2));
