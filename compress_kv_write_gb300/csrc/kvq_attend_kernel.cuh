@@ -203,10 +203,10 @@ struct RowScale {
             texp = max(max(int(lo >> 16), int(lo & 0xFFFFu)), kMinScaleByte) - 134;
         }
     }
-    // The multiplier of half s of chunk b, fp16 twice.
-    __device__ __forceinline__ uint32_t mul(int b, int s) const {
+    // The multiplier of half s of chunk 2 b2 + u, fp16 twice.
+    __device__ __forceinline__ uint32_t mul(int b2, int u, int s) const {
         uint32_t r;
-        const uint32_t byte = (bytes[b >> 1] >> (16 * (b & 1) + 8 * s)) & 0xFFu;
+        const uint32_t byte = ((b2 ? bytes[1] : bytes[0]) >> (16 * u + 8 * s)) & 0xFFu;
         if constexpr (L == Layout::V41) {
             // 2^(byte - 127 - texp): through bf16, which holds every ue8m0 value and NaN
             uint32_t h;
@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
     constexpr int R = kRing<N>;
     constexpr uint32_t kTmemS = 4 * N, kTmemK = 5 * N;
-    constexpr uint32_t kTmemCols = 5 * N + 128 <= 256 ? 256 : 512;
+    constexpr uint32_t kTmemCols = 512;  // all of them, which begin at column 0
+    static_assert(5 * N + 128 <= 512, "outputs, scores, two chunks of rows");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
     uint8_t *const sK = base, *const sQ = sK + R * kChunkSmem, *const sP = sQ + N * kD * 2;
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int per = (tiles + kAttendThreads - 1) / kAttendThreads;
         const int t0 = int(min(int64_t(tiles), int64_t(tid) * per)), t1 = int(min(int64_t(tiles), int64_t(t0) + per));
         int64_t mine = 0;
+#pragma unroll 1
         for (int t = t0; t < t1; ++t) mine += tile_info<N, kSlots>(a, t).nb;
         int64_t incl = mine;
 #pragma unroll
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (lane == 31) sh.scan[warp] = incl;
         __syncthreads();
         int64_t before = 0, total = 0;
+#pragma unroll 1
         for (int i = 0; i < kAttendThreads / 32; ++i) {
             if (i < warp) before += sh.scan[i];
             total += sh.scan[i];
@@ -340,6 +343,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
         int64_t at = before + incl - mine;
         if (u0 >= at && u0 < at + mine)
+#pragma unroll 1
             for (int t = t0; t < t1; ++t) {
                 const int nb = tile_info<N, kSlots>(a, t).nb;
                 if (u0 < at + nb) {
@@ -375,7 +379,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
         const uint32_t krow = smem_addr(sK) + tok0 * 128;
         const uint32_t at0 = krow + (((2 * q) ^ r8) << 4), at1 = krow + (((2 * q + 1) ^ r8) << 4);
-        const uint32_t tlane = tmem + kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
+        const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
         const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits;
         const int in_page = (1 << a.page_bits) - 1;
 
@@ -422,6 +425,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     const int row = kSlots ? int(idx[h]) & in_page : (row0 + 8 * h) & in_page;
                     const uint8_t *p = a.pool + page * page_bytes;
                     code[h] = p + row * T::kCodeBytes;
+                    if (q == 0) prefetch_l2_bulk(code[h], T::kCodeBytes);
                     sc[h] = __ldg(reinterpret_cast<const uint32_t *>(p + (int64_t(T::kCodeBytes) << a.page_bits) +
                                                                      row * T::kScaleBytes) + q);
                 } else if (idx[h] != -1 && q == 0) {
@@ -430,68 +434,75 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
         };
 
-        Raw<L> raw[kChunks][2][2];  // chunk, token, half
-        auto load = [&](int b) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) raw[b][h][s] = load_raw<L>(code[h], b, s, q);
-        };
+        // Codes are loaded two chunks ahead, from L2: a block's rows are sent for a whole block ahead.
+        Raw<L> raw[2][2][2];  // chunk & 1, token, half
+        const uint8_t *now[2];
         RowScale<L> rs[2];
-        bool ok[2];
         auto adopt = [&]() {  // the resolved block becomes the current one
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                ok[h] = code[h] != nullptr;
+                now[h] = code[h];
                 rs[h].set(sc[h], lane);
             }
         };
         fetch();
         resolve();
 #pragma unroll
-        for (int b = 0; b < kChunks; ++b) load(b);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) raw[u][h][s] = load_raw<L>(code[h], u, s, q);
         cur.next(a);
         fetch();
         adopt();
         Ring<R> ring;
         bool live = true;
+#pragma unroll 1
         for (int i = 0; i < units && live; ++i) {
             resolve();  // the next block; its indexes came a block ago
             if (cur.left > 0) cur.next(a);
             fetch();
+#pragma unroll 1
+            for (int b2 = 0; b2 < kChunks / 2; ++b2) {
+                const uint8_t *from[2] = {b2 ? code[0] : now[0], b2 ? code[1] : now[1]};
 #pragma unroll
-            for (int b = 0; b < kChunks; ++b) {
-                // the slot is free when the product over the dims that it held is done, a TMEM slot when the
-                // scores' product two chunks ago is
-                if (i * kChunks + b >= R) live = live && mbar_wait(smem_addr(&sh.oblk[ring.slot]), ring.parity ^ 1);
-                if (i > 0 || b >= 2) live = live && mbar_wait(smem_addr(&sh.kfree[b & 1]), b >= 2 ? 0 : 1);
-                tc_fence_after();
-                if (b == 0 && q == 0) {
-                    sh.texp[i & 1][tok0] = ok[0] ? rs[0].texp : kNoToken;
-                    sh.texp[i & 1][tok0 + 8] = ok[1] ? rs[1].texp : kNoToken;
-                }
-                const uint32_t off = ring.slot * kChunkSmem;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t m0 = rs[0].mul(b, s), m1 = rs[1].mul(b, s);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t v0[4], v1[4];
-                        decode8<L>(raw[b][0][s], e, m0, v0);
-                        decode8<L>(raw[b][1][s], e, m1, v1);
-                        const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
-                        sts_u4(at, v0);
-                        sts_u4(at + 8 * 128, v1);
-                        tmem_st_16x128b_x4(tlane + (b & 1) * 64 + 32 * s + 16 * e, v0, v1);
+                for (int u = 0; u < 2; ++u) {
+                    // the slot is free when the product over the dims that it held is done, a TMEM slot when the
+                    // scores' product two chunks ago is
+                    if (i * kChunks + 2 * b2 + u >= R) live = live && mbar_wait(smem_addr(&sh.oblk[ring.slot]), ring.parity ^ 1);
+                    if (i + b2 > 0) live = live && mbar_wait(smem_addr(&sh.kfree[u]), b2 ^ 1);
+                    tc_fence_after();
+                    if (b2 + u == 0 && q == 0) {
+                        sh.texp[i & 1][tok0] = now[0] ? rs[0].texp : kNoToken;
+                        sh.texp[i & 1][tok0 + 8] = now[1] ? rs[1].texp : kNoToken;
                     }
+                    const uint32_t off = ring.slot * kChunkSmem;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t m0 = rs[0].mul(b2, u, s), m1 = rs[1].mul(b2, u, s);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t v0[4], v1[4];
+                            decode8<L>(raw[u][0][s], e, m0, v0);
+                            decode8<L>(raw[u][1][s], e, m1, v1);
+                            const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
+                            sts_u4(at, v0);
+                            sts_u4(at + 8 * 128, v1);
+                            tmem_st_16x128b_x4(tlane + u * 64 + 32 * s + 16 * e, v0, v1);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) raw[u][h][s] = load_raw<L>(from[h], (b2 ^ 1) * 2 + u, s, q);
+                    tc_wait_st();
+                    tc_fence_before();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.full[ring.slot]));
+                    ring.next();
                 }
-                load(b);
-                tc_wait_st();
-                tc_fence_before();
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.full[ring.slot]));
-                ring.next();
             }
             adopt();
         }
@@ -502,14 +513,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (warp == kMmaWarp) {
             constexpr uint32_t kIdescS = mma_idesc(kTile, N, false, false);
             constexpr uint32_t kIdescO = mma_idesc(kTile, N, true, true);
-            constexpr uint64_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
-            const uint64_t qd = smem_desc(smem_addr(sQ), 16, 1024, kSwizzle128);
-            const uint64_t vd = smem_desc(smem_addr(sK), kSubBytes, 1024, kSwizzle128);
-            const uint64_t pd = smem_desc(smem_addr(sP), 16, 16 * N, kPSwizzle);
+            constexpr uint32_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
+            const uint32_t qd = desc_lo(smem_addr(sQ), 16), vd = desc_lo(smem_addr(sK), kSubBytes), pd = desc_lo(smem_addr(sP), 16);
+            constexpr uint32_t kQHi = desc_hi(1024, kSwizzle128), kVHi = kQHi, kPHi = desc_hi(16 * N, kPSwizzle);
             int left_tile = 0, tile = sh.start_tile, kb = sh.start_kb;
             uint32_t seg = 0;
             bool live = true;
             Ring<R> sr, vr;
+#pragma unroll 1
             for (int i = 0; i < units && live; ++i) {
                 const uint32_t phase = uint32_t(i) & 1;
                 bool first = false;
@@ -522,15 +533,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     ++seg;
                 }
                 --left_tile;
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
                     live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
                     tc_fence_after();
                     if (live && elect_one()) {
+                        const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + (b & 1) * 64;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_ts(tmem + kTmemS, tmem + kTmemK + (b & 1) * 64 + 8 * k,
-                                   qd + ((((2 * b + (k >> 2)) * N * 128) + (k & 3) * 32) >> 4), kIdescS, b + k > 0);
+                            mma_ts(kTmemS, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS,
+                                   b + k > 0);
                         mma_commit(smem_addr(&sh.kfree[b & 1]));
                         if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
                     }
@@ -539,13 +551,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
                 live = live && mbar_wait(smem_addr(&sh.pready), phase);
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
                     if (live && elect_one()) {
-                        const uint64_t at = vd + ((vr.slot * kChunkSmem) >> 4);
+                        const uint32_t at = vd + ((vr.slot * kChunkSmem) >> 4);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_ss(tmem + b * N, at + ((k * 2048) >> 4), pd + ((k * 32 * N) >> 4), kIdescO,
+                            mma_ss(b * N, at + ((k * 2048) >> 4), kVHi, pd + ((k * 32 * N) >> 4), kPHi, kIdescO,
                                    !first || k > 0);
                         mma_commit(smem_addr(&sh.oblk[vr.slot]));
                     }
@@ -566,7 +578,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int t_row = tid & 127, quarter = warp & 3, half = warp >> 2, c0 = half * NC;
         const float c = a.scale * kLog2e;
         const int per = a.q_len * a.heads;
-        const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
+        const uint32_t trow = (uint32_t(quarter * 32) << 16);
         Cursor<N, kSlots> cur(a, sh);
         Ring<R> ring;
         float l[NC];
@@ -574,6 +586,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         volatile int &gone = sh.soft_abort;
         bool unset = false, live = true;
         int kb0 = 0;
+#pragma unroll 1
         for (int i = 0; i < units && live; ++i, cur.next(a)) {
             const uint32_t phase = uint32_t(i) & 1;
             const bool first = i == 0 || cur.kb == 0;
@@ -731,8 +744,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 // a weight of 0 does not silence a NaN: if the token's row itself is not finite, the rows that see
                 // it are NaN by their weights already, and the others must meet zeros
                 bool bad = false;
+#pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
                     Ring<R> at = ring;
+#pragma unroll 1
                     for (int v = 0; v < 64 && (pass == 0 || bad); ++v) {
                         const uint32_t p = smem_addr(sK) + at.slot * kChunkSmem + ((v >> 3) & 1) * kSubBytes + t_row * 128 + (v & 7) * 16;
                         if (pass == 0) {
@@ -841,7 +856,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && sh.abort) raise_err(a.err, KVQ_DEVERR_WAIT);
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }
 
 // Joins the tiles that CTAs split: CTA (x, y) takes rows 4y .. 4y+3 of the
