@@ -14,19 +14,24 @@ constexpr int kChunk = 128;  // dims a step of decoding
 constexpr int kChunks = kD / kChunk;
 constexpr int kSubBytes = kTile * 128;         // 64 dims of a block, 128 B a token
 constexpr int kChunkSmem = 2 * kSubBytes;
-// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-15 decode, 16 products, 17-19 only
-// complete the warpgroup.
-constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = kSoftWarps + kDeqWarps;
+// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-23 decode, 24 products, 25 and 26 wait for
+// the products on behalf of the decode and the softmax warps, 27 looks up where the rows of coming blocks lie.  A warp
+// that polls an mbarrier takes issue slots from the others, so the many wait at named barriers, which take none.
+constexpr int kSoftWarps = 8, kDeqWarps = 16, kMmaWarp = kSoftWarps + kDeqWarps;
 constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
-// Registers a thread: the launch gives 640 threads 96 each; the warpgroups' shares 2 * 104 + 2 * 104 + 64 = 480 stay
-// within its 5 * 96 = 480.
-constexpr int kSoftRegs = 104, kDeqRegs = 104, kMmaRegs = 64;
-static_assert(2 * kSoftRegs + 2 * kDeqRegs + kMmaRegs <= 5 * 96, "a larger sum would wait for ever");
-constexpr float kStaleMax = 8.f;  // how far (log2) a score may pass the running maximum before it moves
+// Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
+constexpr int kSoftRegs = 104, kDeqRegs = 56, kMmaRegs = 72;
+static_assert(2 * kSoftRegs + 4 * kDeqRegs + kMmaRegs <= 7 * 72, "a larger sum would wait for ever");
+// How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
+// (which rescales the outputs in TMEM) is rare after a tile's first block.
+constexpr float kStaleMax = 14.f;
 
 // Decoded chunks that fit beside N query rows and their weights: a block is four.
 template <int N>
-constexpr int kRing = N == 16 ? 6 : N == 32 ? 5 : 4;
+constexpr int kRing = N == 64 ? 4 : 5;
+
+constexpr int kNoToken = 0x7FFFFFFF;
+constexpr int kLookups = 4;
 
 template <int N>
 struct AttendShared {
@@ -35,14 +40,17 @@ struct AttendShared {
     int64_t total, u0;
     int units, start_tile, start_kb;
     uint32_t tmem;
-    int abort, soft_abort;
+    int abort, progress;
     alignas(16) float sc[N], nm[N], m[N], alpha[N], inv[N];
     float red[4][N];
     alignas(16) int vis[N];
     int64_t row[N];
-    int texp[2][kTile];  // a token's power of two, or kNoToken
+    // What the lookup warp found for a block's tokens, four blocks in turn.
+    uint64_t addr[kLookups];                   // full
+    alignas(16) uint4 scale[kLookups][kTile];  // a row's scale bytes
+    const uint8_t *code[kLookups][kTile];      // a row's codes
+    int texp[kLookups][kTile];                 // a row's power of two, or kNoToken
 };
-constexpr int kNoToken = 0x7FFFFFFF;
 
 template <int N>
 constexpr size_t kAttendSmem = 1024 + size_t(kRing<N>) * kChunkSmem + size_t(N) * kD * 2 + size_t(kTile) * N * 2 +
@@ -118,7 +126,8 @@ struct Ring {
 
 // Where a decoded row lies.  A decode thread holds, of tokens r and r + 8
 // (r = lane / 4) and of each chunk of 128 dims, the 16 dims from
-// 64 s + 16 q (q = lane % 4, s = 0, 1), as two vectors e = 0, 1 of eight.  In shared memory a chunk is two 128-byte-swizzled tiles of 64 dims;
+// 64 s + 16 q (q = lane % 4, s the warp's half), as two vectors e = 0, 1 of
+// eight.  In shared memory a chunk is two 128-byte-swizzled tiles of 64 dims;
 // the eight lanes of a store's phase (two tokens, four q) hit different
 // banks.  In TMEM (the A operand of the scores' product) vector e fills the
 // columns 16 (2 s + e) + 4 i + q, i = 0..3, two dims a column: the
@@ -129,17 +138,17 @@ struct Raw {  // 16 codes
     uint32_t w[L == Layout::V41 ? 4 : 2];
 };
 
+// p: the thread's first code of the row.
 template <Layout L>
-__device__ __forceinline__ Raw<L> load_raw(const uint8_t *row, int chunk, int s, int q) {
-    Raw<L> r = {};
-    if (row) {
-        if constexpr (L == Layout::V41) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + chunk * 128 + s * 64) + q);
-            r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
-        } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + chunk * 64 + s * 32) + q);
-            r.w[0] = v.x, r.w[1] = v.y;
-        }
+__device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int chunk) {
+    Raw<L> r;
+    if constexpr (L == Layout::V41) {
+        // volatile: a load stays where it is issued, two chunks before its use
+        asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                     : "l"(p + chunk * 128));
+    } else {
+        asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p + chunk * 64));
     }
     return r;
 }
@@ -168,8 +177,7 @@ __device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, ui
     }
 }
 
-// A token's scales for a decode thread: two bytes a chunk (the blocks its 2 *
-// 16 dims lie in).  FP4: code * e4m3 scale is exact in fp16 as it is.  V41: the
+// A row's scales.  FP4: code * e4m3 scale is exact in fp16 as it is.  V41: the
 // ue8m0 scales of a row span more than fp16 does, so a row is decoded times
 // 2^-texp, which brings its largest scale to 2^7 (448 * 2^7 < 65504); the
 // softmax warps put 2^texp back into the scores and the weights.  Blocks
@@ -180,45 +188,35 @@ __device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, ui
 constexpr int kMinScaleByte = 127 - 40;
 
 template <Layout L>
-struct RowScale {
-    uint32_t bytes[2];  // chunks 0 and 1, 2 and 3
-    int texp;
-    __device__ __forceinline__ void set(uint32_t v, int lane) {  // lanes 4 r .. 4 r + 3 bring a row's four words
-        uint32_t w[4];
+__device__ __forceinline__ int row_texp(const uint4 &v) {
+    if constexpr (L == Layout::FP4) return 0;
+    // largest byte: even and odd bytes as 16-bit lanes
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi = 0, lo = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) w[b] = __shfl_sync(0xFFFFFFFFu, v, (lane & ~3) + b);
-        const uint32_t pick = lane & 2 ? 0x7531u : 0x6420u;  // bytes q / 2 and 2 + q / 2 of two words
-        bytes[0] = __byte_perm(w[0], w[1], pick);
-        bytes[1] = __byte_perm(w[2], w[3], pick);
-        texp = 0;
-        if constexpr (L == Layout::V41) {
-            // largest byte: even and odd bytes as 16-bit lanes
-            uint32_t hi = 0, lo = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                hi = __vmaxu2(hi, (w[b] >> 8) & 0x00FF00FFu);
-                lo = __vmaxu2(lo, w[b] & 0x00FF00FFu);
-            }
-            lo = __vmaxu2(lo, hi);
-            texp = max(max(int(lo >> 16), int(lo & 0xFFFFu)), kMinScaleByte) - 134;
-        }
+    for (int b = 0; b < 4; ++b) {
+        hi = __vmaxu2(hi, (w[b] >> 8) & 0x00FF00FFu);
+        lo = __vmaxu2(lo, w[b] & 0x00FF00FFu);
     }
-    // The multiplier of half s of chunk 2 b2 + u, fp16 twice.
-    __device__ __forceinline__ uint32_t mul(int b2, int u, int s) const {
-        uint32_t r;
-        const uint32_t byte = ((b2 ? bytes[1] : bytes[0]) >> (16 * u + 8 * s)) & 0xFFu;
-        if constexpr (L == Layout::V41) {
-            // 2^(byte - 127 - texp): through bf16, which holds every ue8m0 value and NaN
-            uint32_t h;
-            asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(h) : "h"(uint16_t(byte)));
-            const float f = bf16_lo(h) * __uint_as_float(uint32_t(127 - texp) << 23);
-            asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(f));
-        } else {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(byte * 0x101u)));
-        }
-        return r;
+    lo = __vmaxu2(lo, hi);
+    return max(max(int(lo >> 16), int(lo & 0xFFFFu)), kMinScaleByte) - 134;
+}
+
+// A block's multiplier, fp16 twice.
+template <Layout L>
+__device__ __forceinline__ uint32_t block_mul(uint32_t byte, int texp) {
+    uint32_t r;
+    if constexpr (L == Layout::V41) {
+        // 2^(byte - 127 - texp): through bf16, which holds every ue8m0 value and NaN
+        uint32_t h;
+        asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(h) : "h"(uint16_t(byte)));
+        const float f = bf16_lo(h) * __uint_as_float(uint32_t(127 - texp) << 23);
+        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(r) : "f"(f));
+    } else {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(byte * 0x101u)));
     }
-};
+    return r;
+}
 
 // Byte offset, in a query tile's shared memory, of word i (dims 8g + 2i,
 // 8g + 2i + 1) of piece g = 0..63 of row r.
@@ -267,6 +265,11 @@ __device__ __forceinline__ float redux_max(float v) {
     return r;
 }
 
+// Barriers with the warps that wait for the products.
+__device__ __forceinline__ void decode_sync() { asm volatile("bar.sync 2, 544;" ::: "memory"); }
+__device__ __forceinline__ void scores_sync() { asm volatile("bar.sync 3, 288;" ::: "memory"); }
+static_assert(kDeqWarps * 32 + 32 == 544 && kSoftWarps * 32 + 32 == 288, "participants");
+
 // Barrier of the softmax warps; the second form returns whether any of
 // their threads brought true.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -280,8 +283,6 @@ __device__ __forceinline__ bool soft_any(bool p) {
         : "memory");
     return r != 0;
 }
-
-__device__ __forceinline__ float2 pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
 template <Layout L, int N, bool kSlots>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
@@ -354,7 +355,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 at += nb;
             }
     }
+    for (int i = tid; i < kLookups * kTile; i += kAttendThreads) sh.code[0][i] = a.pool;
     if (tid == 0) {
+        for (int i = 0; i < kLookups; ++i) mbar_init(smem_addr(&sh.addr[i]), 1);
         for (int i = 0; i < R; ++i) {
             mbar_init(smem_addr(&sh.full[i]), kDeqWarps);
             mbar_init(smem_addr(&sh.oblk[i]), 1);
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         mbar_init(smem_addr(&sh.pready), kSoftWarps);
         mbar_init(smem_addr(&sh.qready), kSoftWarps);
         mbar_init(smem_addr(&sh.drain), 1);
-        sh.abort = sh.soft_abort = 0;
+        sh.abort = sh.progress = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -382,131 +385,93 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
-        const int w = warp - kSoftWarps, q = lane & 3, r8 = lane >> 2;
-        const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
-        const uint32_t krow = smem_addr(sK) + tok0 * 128;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
+        const int w = warp - kSoftWarps, q = lane & 3, r8 = lane >> 2, s = w >> 3;
+        const int tok0 = 32 * (w & 3) + 16 * ((w >> 2) & 1) + r8;  // and tok0 + 8
+        const uint32_t krow = smem_addr(sK) + s * kSubBytes + tok0 * 128;
         const uint32_t at0 = krow + (((2 * q) ^ r8) << 4), at1 = krow + (((2 * q + 1) ^ r8) << 4);
-        const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
-        const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits;
-        const int in_page = (1 << a.page_bits) - 1;
+        const uint32_t tlane = kTmemK + 32 * s + ((32 * (w & 3) + 16 * ((w >> 2) & 1)) << 16);
+        constexpr int kLaneBytes = T::kCodeBytes / 32;  // of a chunk
+        const uint32_t lane_at = (4 * s + q) * kLaneBytes;
+        const int block_at = 2 * s + (q >> 1);  // the scale byte of a chunk's four
 
-        Cursor<N, kSlots> cur(a, sh);
-        using Index = std::conditional_t<kSlots, int64_t, int>;
-        Index idx[2];  // page or slot, -1: no token
-        int row0 = 0;  // token tok0's place in its page (paged)
-        auto fetch = [&]() {
+        // Codes are loaded two chunks ahead, from L2, where the lookup warp has sent for them.  A chunk is decoded
+        // before its slot is free, so that only the stores wait for that.
+        Raw<L> raw[2][2];  // chunk & 1, token
+        const uint8_t *now[2], *next[2];
+        int texp[2];
+        bool all_ok;
+        uint32_t v[2][2][4];  // token, vector
+        auto look = [&](const uint8_t *(&to)[2], int k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) to[h] = sh.code[k][tok0 + 8 * h] + lane_at;
+        };
+        auto adopt = [&](int k) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) texp[h] = sh.texp[k][tok0 + 8 * h];
+            all_ok = __all_sync(0xFFFFFFFFu, texp[0] != kNoToken && texp[1] != kNoToken);
+        };
+        auto decode = [&](Raw<L> (&r)[2], int k, int b) {
+            if (!all_ok) {  // a token that is not there has the pool's first row: its codes are cleared
+                asm volatile("");
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < int(sizeof(Raw<L>) / 4); ++i) r[h].w[i] = texp[h] != kNoToken ? r[h].w[i] : 0u;
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t t = int64_t(cur.kb) * kTile + tok0 + 8 * h;
-                idx[h] = -1;
-                if (h == 0) row0 = int(t) & in_page;
-                if (cur.left > 0 && t < cur.t.seen) {
-                    if constexpr (kSlots) {
-                        const int64_t at = cur.t.seq * a.slots_stride + t;
-                        idx[h] = a.slots64 ? __ldg(static_cast<const int64_t *>(a.slots) + at)
-                                           : int64_t(__ldg(static_cast<const int32_t *>(a.slots) + at));
-                    } else {
-                        idx[h] = __ldg(a.table + cur.t.trow * a.table_stride + (t >> a.page_bits));
-                        if (idx[h] < 0) idx[h] = -2;
-                    }
-                }
+                const uint32_t byte = reinterpret_cast<const uint8_t *>(&sh.scale[k][tok0 + 8 * h])[4 * b + block_at];
+                const uint32_t m = block_mul<L>(byte, texp[h]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) decode8<L>(r[h], e, m, v[h][e]);
             }
         };
-        const uint8_t *code[2];
-        uint32_t sc[2];  // word q of the token's 16 scale bytes
-        auto resolve = [&]() {  // row pointers and scales of the fetched block
+        auto load = [&](Raw<L> (&r)[2], const uint8_t *const (&from)[2], int b) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                code[h] = nullptr;
-                sc[h] = 0;
-                if (idx[h] >= 0 && idx[h] < a.pool_limit) {
-                    const int64_t page = kSlots ? idx[h] >> a.page_bits : idx[h];
-                    const int row = kSlots ? int(idx[h]) & in_page : (row0 + 8 * h) & in_page;
-                    const uint8_t *p = a.pool + page * page_bytes;
-                    code[h] = p + row * T::kCodeBytes;
-                    if (q == 0) prefetch_l2_bulk(code[h], T::kCodeBytes);
-                    sc[h] = __ldg(reinterpret_cast<const uint32_t *>(p + (int64_t(T::kCodeBytes) << a.page_bits) +
-                                                                     row * T::kScaleBytes) + q);
-                } else if (idx[h] != -1 && q == 0) {
-                    raise_err(a.err, kSlots ? KVQ_DEVERR_SLOT : KVQ_DEVERR_PAGE);
-                }
-            }
+            for (int h = 0; h < 2; ++h) r[h] = load_raw<L>(from[h], b);
         };
-
-        // Codes are loaded two chunks ahead, from L2: a block's rows are sent for a whole block ahead.
-        Raw<L> raw[2][2][2];  // chunk & 1, token, half
-        const uint8_t *now[2];
-        RowScale<L> rs[2];
-        auto adopt = [&]() {  // the resolved block becomes the current one
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                now[h] = code[h];
-                rs[h].set(sc[h], lane);
-            }
-        };
-        fetch();
-        resolve();
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) raw[u][h][s] = load_raw<L>(code[h], u, s, q);
-        cur.next(a);
-        fetch();
-        adopt();
-        Ring<R> ring;
-        bool live = true;
+        decode_sync();  // the first block is looked up
+        look(now, 0);
+        load(raw[0], now, 0);
+        load(raw[1], now, 1);
+        adopt(0);
+        decode(raw[0], 0, 0);
+        load(raw[0], now, 2);
+        int slot = 0;
 #pragma unroll 1
-        for (int i = 0; i < units && live; ++i) {
-            resolve();  // the next block; its indexes came a block ago
-            if (cur.left > 0) cur.next(a);
-            fetch();
-#pragma unroll 1
-            for (int b2 = 0; b2 < kChunks / 2; ++b2) {
-                const uint8_t *from[2] = {b2 ? code[0] : now[0], b2 ? code[1] : now[1]};
+        for (int i = 0; i < units; ++i) {
+            const int k = i & (kLookups - 1), kn = i + 1 < units ? (i + 1) & (kLookups - 1) : k;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    // the slot is free when the product over the dims that it held is done, a TMEM slot when the
-                    // scores' product two chunks ago is
-                    if (i * kChunks + 2 * b2 + u >= R) live = live && mbar_wait(smem_addr(&sh.oblk[ring.slot]), ring.parity ^ 1);
-                    if (i + b2 > 0) live = live && mbar_wait(smem_addr(&sh.kfree[u]), b2 ^ 1);
-                    tc_fence_after();
-                    if (b2 + u == 0 && q == 0) {
-                        sh.texp[i & 1][tok0] = now[0] ? rs[0].texp : kNoToken;
-                        sh.texp[i & 1][tok0 + 8] = now[1] ? rs[1].texp : kNoToken;
-                    }
-                    const uint32_t off = ring.slot * kChunkSmem;
+            for (int b = 0; b < kChunks; ++b) {
+                decode_sync();  // the slot is free (b = 0: and the next block is looked up)
+                tc_fence_after();
+                const uint32_t off = slot * kChunkSmem;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint32_t m0 = rs[0].mul(b2, u, s), m1 = rs[1].mul(b2, u, s);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t v0[4], v1[4];
-                            decode8<L>(raw[u][0][s], e, m0, v0);
-                            decode8<L>(raw[u][1][s], e, m1, v1);
-                            const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
-                            sts_u4(at, v0);
-                            sts_u4(at + 8 * 128, v1);
-                            tmem_st_16x128b_x4(tlane + u * 64 + 32 * s + 16 * e, v0, v1);
-                        }
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) raw[u][h][s] = load_raw<L>(from[h], (b2 ^ 1) * 2 + u, s, q);
-                    tc_wait_st();
-                    tc_fence_before();
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.full[ring.slot]));
-                    ring.next();
+                for (int e = 0; e < 2; ++e) {
+                    sts_u4((e ? at1 : at0) + off, v[0][e]);
+                    sts_u4((e ? at1 : at0) + off + 8 * 128, v[1][e]);
+                    tmem_st_16x128b_x4(tlane + (b & 1) * 64 + 16 * e, v[0][e], v[1][e]);
                 }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
+                if (++slot == R) slot = 0;
+                // the next chunk's values, and codes for the one that is two further on
+                if (b == 0) look(next, kn);
+                if (b == kChunks - 1) {
+                    adopt(kn);
+                    now[0] = next[0];
+                    now[1] = next[1];
+                }
+                decode(raw[(b + 1) & 1], b == kChunks - 1 ? kn : k, (b + 1) % kChunks);
+                if (b == 0) load(raw[1], now, 3);
+                if (b == 1) load(raw[0], next, 0);
+                if (b == 2) load(raw[1], next, 1);
+                if (b == 3) load(raw[0], now, 2);
             }
-            adopt();
         }
-        if (!live) sh.abort = 1;
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
@@ -535,7 +500,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 --left_tile;
 #pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
+                    // The writers only arrive: the fence between their stores and the tensor core's reads is made
+                    // here, where no load is in flight (in a decode warp it would wait for the next codes).
                     live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
+                    fence_proxy_async();
                     tc_fence_after();
                     if (live && elect_one()) {
                         const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + (b & 1) * 64;
@@ -550,6 +518,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     sr.next();
                 }
                 live = live && mbar_wait(smem_addr(&sh.pready), phase);
+                fence_proxy_async();
                 tc_fence_after();
 #pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
@@ -570,6 +539,112 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if (elect_one()) mma_commit(smem_addr(&sh.drain));  // nothing may write TMEM once it is freed
                 mbar_wait(smem_addr(&sh.drain), 0);
             }
+        } else if (warp == kMmaWarp + 1) {
+            // A chunk's slot is free when the product over the dims that it held is done; that product comes after
+            // the scores of its block, and so frees the TMEM slot of a chunk too, unless the ring is longer than a
+            // block or the block itself has used the slot.  A wait that is given up ends all further ones: every
+            // role then runs through its blocks, and the call reports it.
+            Ring<R> ring;
+            bool live = mbar_wait(smem_addr(&sh.addr[0]), 0);
+            decode_sync();
+#pragma unroll 1
+            for (int i = 0; i < units; ++i) {
+                if (lane == 0) *const_cast<volatile int *>(&sh.progress) = i;
+                if (i + 1 < units)
+                    live = live && mbar_wait(smem_addr(&sh.addr[(i + 1) & (kLookups - 1)]), ((i + 1) / kLookups) & 1);
+#pragma unroll 1
+                for (int b = 0; b < kChunks; ++b) {
+                    if (i * kChunks + b >= R) live = live && mbar_wait(smem_addr(&sh.oblk[ring.slot]), ring.parity ^ 1);
+                    if (b >= 2 || (R > kChunks && i > 0)) live = live && mbar_wait(smem_addr(&sh.kfree[b & 1]), b >= 2 ? 0 : 1);
+                    decode_sync();
+                    ring.next();
+                }
+            }
+            if (lane == 0) *const_cast<volatile int *>(&sh.progress) = units;
+            if (!live) sh.abort = 1;
+        } else if (warp == kMmaWarp + 2) {
+            // scores are there; `full` of the block's first chunk orders the softmax warps' reads of texp
+            Ring<R> ring;
+            bool live = true;
+#pragma unroll 1
+            for (int i = 0; i < units; ++i) {
+                live = live && mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity) && mbar_wait(smem_addr(&sh.sdone), i & 1);
+                scores_sync();
+                for (int b = 0; b < kChunks; ++b) ring.next();
+            }
+            if (!live) sh.abort = 1;
+        } else {
+            // Looks up where a block's rows lie and fetches their scales, up to two blocks ahead of the decode warps.
+            // A load of a row's first bytes (V41: of either half) asks for 256 bytes in L2, and so for the row.  Lane
+            // l has tokens l, l + 32, l + 64, l + 96.  Three blocks are under way: the indexes of one, the scales of
+            // one, and one that is written down.
+            constexpr int K = kTile / 32;
+            using Index = std::conditional_t<kSlots, int64_t, int>;
+            const uint32_t page_bytes = uint32_t(kTokenBytes<L>) << a.page_bits, in_page = (1u << a.page_bits) - 1;
+            const uint32_t scale_at = uint32_t(T::kCodeBytes) << a.page_bits;
+            volatile int &progress = sh.progress;
+            Cursor<N, kSlots> cur(a, sh);
+            Index idx[K];
+            int t0 = 0, seen = 0;
+            auto fetch = [&]() {
+                t0 = cur.kb * kTile + lane;
+                seen = cur.left > 0 ? cur.t.seen : 0;
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    const int t = t0 + 32 * j;
+                    idx[j] = -1;
+                    if (t >= seen) continue;
+                    if constexpr (kSlots) {
+                        const int64_t at = cur.t.seq * a.slots_stride + t;
+                        idx[j] = a.slots64 ? __ldg(static_cast<const int64_t *>(a.slots) + at)
+                                           : int64_t(__ldg(static_cast<const int32_t *>(a.slots) + at));
+                    } else {
+                        idx[j] = __ldg(a.table + cur.t.trow * a.table_stride + (t >> a.page_bits));
+                    }
+                }
+            };
+            const uint8_t *row[K];
+            uint4 sc[K];
+            uint32_t good = 0;
+            fetch();
+#pragma unroll 1
+            for (int i = 0; i <= units; ++i) {
+                if (i > 0) {
+                    // block i - 1: wait until its entries are free (every reader of block i - 5 is done)
+                    for (int tries = 0; progress < i - 3 && tries < (1 << 22); ++tries) __nanosleep(64);
+                    const int k = (i - 1) & (kLookups - 1);
+#pragma unroll
+                    for (int j = 0; j < K; ++j) {
+                        const bool g = (good >> j) & 1;
+                        sh.scale[k][lane + 32 * j] = sc[j];
+                        sh.code[k][lane + 32 * j] = row[j];
+                        sh.texp[k][lane + 32 * j] = g ? row_texp<L>(sc[j]) : kNoToken;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.addr[k]));
+                }
+                if (i == units) break;
+                good = 0;
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    const int t = t0 + 32 * j;
+                    const bool g = t < seen && idx[j] >= 0 && idx[j] < a.pool_limit;
+                    if (t < seen && !g && !(kSlots && idx[j] == -1)) raise_err(a.err, kSlots ? KVQ_DEVERR_SLOT : KVQ_DEVERR_PAGE);
+                    // a token that is not there has the pool's first row, which always exists
+                    const uint32_t page = !g ? 0 : kSlots ? uint32_t(idx[j] >> a.page_bits) : uint32_t(idx[j]);
+                    const uint32_t r = !g ? 0 : (kSlots ? uint32_t(idx[j]) : uint32_t(t)) & in_page;
+                    const uint8_t *p = a.pool + uint64_t(page) * page_bytes;
+                    good |= uint32_t(g) << j;
+                    row[j] = p + r * T::kCodeBytes;
+                    sc[j] = __ldg(reinterpret_cast<const uint4 *>(p + (scale_at + r * T::kScaleBytes)));
+                    uint32_t sink;
+                    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(sink) : "l"(row[j]));
+                    if constexpr (L == Layout::V41)
+                        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(sink) : "l"(row[j] + 256));
+                }
+                cur.next(a);
+                fetch();
+            }
         }
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
@@ -582,13 +657,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         Cursor<N, kSlots> cur(a, sh);
         Ring<R> ring;
         float l[NC];
-        // A warp that gives up a wait says so before the softmax warps' next barrier, so that all leave together.
-        volatile int &gone = sh.soft_abort;
         bool unset = false, live = true;
         int kb0 = 0;
 #pragma unroll 1
-        for (int i = 0; i < units && live; ++i, cur.next(a)) {
-            const uint32_t phase = uint32_t(i) & 1;
+        for (int i = 0; i < units; ++i, cur.next(a)) {
             const bool first = i == 0 || cur.kb == 0;
             if (first) {
                 // the scores' products of the last tile are done (their result was waited for)
@@ -630,7 +702,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         sh.row[r] = row < per ? tok * a.out_tok + head * a.out_head : -1;
                     }
                 }
-                fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.qready));
                 soft_sync();
@@ -638,10 +709,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 for (int j = 0; j < NC; ++j) l[j] = 0.f;
                 unset = true;
             }
-            // the full barrier of the block's first chunk orders this thread's read of `texp`
-            if (!mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity) || !mbar_wait(smem_addr(&sh.sdone), phase)) gone = 1;
+            scores_sync();
             tc_fence_after();
-            const int te = sh.texp[i & 1][t_row];
+            const int te = sh.texp[i & (kLookups - 1)][t_row];
             const bool have = te != kNoToken;
             const int t_at = have ? cur.kb * kTile + t_row : 0x7FFFFFFF;
             // whether some of the block is masked for some row (the first row of a tile sees least)
@@ -652,34 +722,42 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
             // x = score in log2 units, plus the row's power of two; -inf where it is masked
             float x[NC];
-            bool odd = false;  // a score that is not finite, where some rows do not see the token
             {
                 uint32_t sraw[NC];
                 tmem_ld<NC>(trow + kTmemS + c0, sraw);
 #pragma unroll
-                for (int j = 0; j < NC; j += 2) {
-                    float2 v = make_float2(__uint_as_float(sraw[j]), __uint_as_float(sraw[j + 1]));
-                    if (masked) odd = odd || !(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY);
-                    if constexpr (kExp)
-                        v = ffma2(fmul2(v, make_float2(e_up, e_up)), pair(&sh.sc[c0 + j]), make_float2(et, et));
-                    else
-                        v = fmul2(v, pair(&sh.sc[c0 + j]));
-                    x[j] = v.x;
-                    x[j + 1] = v.y;
+                for (int j = 0; j < NC; j += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(&sh.sc[c0 + j]);
+                    float2 u = make_float2(__uint_as_float(sraw[j]), __uint_as_float(sraw[j + 1]));
+                    float2 w = make_float2(__uint_as_float(sraw[j + 2]), __uint_as_float(sraw[j + 3]));
+                    if constexpr (kExp) {
+                        u = ffma2(fmul2(u, make_float2(e_up, e_up)), make_float2(k.x, k.y), make_float2(et, et));
+                        w = ffma2(fmul2(w, make_float2(e_up, e_up)), make_float2(k.z, k.w), make_float2(et, et));
+                    } else {
+                        u = fmul2(u, make_float2(k.x, k.y));
+                        w = fmul2(w, make_float2(k.z, k.w));
+                    }
+                    x[j] = u.x, x[j + 1] = u.y, x[j + 2] = w.x, x[j + 3] = w.y;
                 }
-                if (masked) {
+            }
+            bool odd = false;  // a score that is not finite, where some rows do not see the token
+            if (masked) {
+                asm volatile("");  // a branch, not 2 NC selects in every block
 #pragma unroll
-                    for (int j = 0; j < NC; ++j)
-                        if (!(t_at < sh.vis[c0 + j])) x[j] = -INFINITY;
+                for (int j = 0; j < NC; ++j) {
+                    odd = odd || !(fabsf(x[j]) < INFINITY);
+                    if (!(t_at < sh.vis[c0 + j])) x[j] = -INFINITY;
                 }
             }
             bool move = unset;
             if (!move) {
                 float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < NC; j += 2) {
-                    const float2 v = fadd2(make_float2(x[j], x[j + 1]), pair(&sh.nm[c0 + j]));
-                    top = fmax3(top, v.x, v.y);
+                for (int j = 0; j < NC; j += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(&sh.nm[c0 + j]);
+                    const float2 u = fadd2(make_float2(x[j], x[j + 1]), make_float2(k.x, k.y));
+                    const float2 w = fadd2(make_float2(x[j + 2], x[j + 3]), make_float2(k.z, k.w));
+                    top = fmax3(top, fmax3(u.x, u.y, w.x), w.y);
                 }
                 move = soft_any(top > kStaleMax);
             }
@@ -719,24 +797,26 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     tc_wait_st();
                 }
             }
-            if (gone) {  // a barrier lies between any warp's wait and here
-                live = false;
-                break;
-            }
             const uint32_t sp = smem_addr(sP);
 #pragma unroll
             for (int j0 = 0; j0 < NC; j0 += 8) {
                 uint32_t h[4];
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float2 v = fadd2(make_float2(x[j0 + j], x[j0 + j + 1]), pair(&sh.nm[c0 + j0 + j]));
-                    const float2 p = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-                    float2 sum = make_float2(l[j0 + j], l[j0 + j + 1]);
-                    if constexpr (kExp) sum = ffma2(p, make_float2(e_down, e_down), sum);
-                    else sum = fadd2(sum, p);
-                    l[j0 + j] = sum.x;
-                    l[j0 + j + 1] = sum.y;
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j / 2]) : "f"(p.y), "f"(p.x));
+                for (int g = 0; g < 2; ++g) {
+                    const float4 k = *reinterpret_cast<const float4 *>(&sh.nm[c0 + j0 + 4 * g]);
+                    const float add[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                    for (int d = 0; d < 4; d += 2) {
+                        const int j = j0 + 4 * g + d;
+                        const float2 z = fadd2(make_float2(x[j], x[j + 1]), make_float2(add[d], add[d + 1]));
+                        const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                        float2 sum = make_float2(l[j], l[j + 1]);
+                        if constexpr (kExp) sum = ffma2(p, make_float2(e_down, e_down), sum);
+                        else sum = fadd2(sum, p);
+                        l[j] = sum.x;
+                        l[j + 1] = sum.y;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[2 * g + d / 2]) : "f"(p.y), "f"(p.x));
+                    }
                 }
                 sts_u4(sp + p_vec<N>(t_row, (c0 + j0) / 8), h);
             }
@@ -764,7 +844,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
             }
             tc_fence_before();
-            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.pready));
             // the ring moves on by a block; the last chunk's slot tells when the block's outputs are summed
@@ -804,10 +883,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     a.join[blockIdx.x] = join;
                 }
                 soft_sync();
-                const bool done = mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity);
-                if (!done) gone = 1;
+                live = live && mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity);
                 tc_fence_after();
-                if (done) {
+                if (live) {
 #pragma unroll 1
                     for (int b = 2 * half; b < 2 * half + 2; ++b) {
                         const int d = b * kChunk + t_row;
@@ -842,20 +920,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
                 tc_fence_before();
                 soft_sync();  // the tile's arrays are free for the next one
-                live = !gone;
             }
         }
-        if (!live) {
-            sh.abort = 1;
-            if (tid == 0) a.join[blockIdx.x] = make_int2(-1, 0);
-        }
+        if (!live) sh.abort = 1;
     }
     __syncwarp();
     if (tid == 0) pdl_trigger();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && sh.abort) raise_err(a.err, KVQ_DEVERR_WAIT);
+    if (tid == 0 && sh.abort) {
+        raise_err(a.err, KVQ_DEVERR_WAIT);
+        a.join[blockIdx.x] = make_int2(-1, 0);
+    }
     if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }
 

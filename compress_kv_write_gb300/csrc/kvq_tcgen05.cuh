@@ -15,15 +15,16 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 
 // Waits until the phase of the given parity has completed.  The wait is
-// bounded: 2^22 tries that suspend for a microsecond at most.  Returns false
-// when it gave up.
+// bounded: 2^24 tries, each of which the hardware may suspend for a while (a
+// time-limit operand would make it a sleeping loop, which wakes up late and
+// takes issue slots).  Returns false when it gave up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
-    for (int i = 0; i < (1 << 22); ++i) {
+    for (int i = 0; i < (1 << 24); ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(bar), "r"(parity)
