@@ -24,7 +24,7 @@ kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok,
         n_seq * q_len > (int64_t(1) << 24))
         return KVQ_ERR_UNSUPPORTED;
     if (!(scale - scale == 0.f)) return KVQ_ERR_INVALID_ARG;  // NaN or infinite
-    if (!pool || !aligned(pool, 16) || pool_limit <= 0) return KVQ_ERR_INVALID_ARG;
+    if (!pool || !aligned(pool, 32) || pool_limit <= 0) return KVQ_ERR_INVALID_ARG;
     if (err && !aligned(err, 4)) return KVQ_ERR_INVALID_ARG;
     if (n_seq == 0) return KVQ_OK;
     // the stride of an axis of one element is never used

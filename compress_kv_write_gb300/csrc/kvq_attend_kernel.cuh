@@ -14,13 +14,13 @@ constexpr int kChunk = 128;  // dims a step of decoding
 constexpr int kChunks = kD / kChunk;
 constexpr int kSubBytes = kTile * 128;         // 64 dims of a block, 128 B a token
 constexpr int kChunkSmem = 2 * kSubBytes;
-// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-23 decode, 24 products, 25 and 26 wait for
-// the products on behalf of the decode and the softmax warps, 27 looks up where the rows of coming blocks lie.  A warp
-// that polls an mbarrier takes issue slots from the others, so the many wait at named barriers, which take none.
+// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-23 decode (8-15 the even chunks, 16-23 the
+// odd ones, so that one half's stores overlap the other's waits), 24 products, 25 looks up where the rows of coming
+// blocks lie, 26 and 27 complete the warpgroup.
 constexpr int kSoftWarps = 8, kDeqWarps = 16, kMmaWarp = kSoftWarps + kDeqWarps;
 constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
 // Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
-constexpr int kSoftRegs = 104, kDeqRegs = 56, kMmaRegs = 72;
+constexpr int kSoftRegs = 104, kDeqRegs = 64, kMmaRegs = 40;
 static_assert(2 * kSoftRegs + 4 * kDeqRegs + kMmaRegs <= 7 * 72, "a larger sum would wait for ever");
 // How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
 // (which rescales the outputs in TMEM) is rare after a tile's first block.
@@ -29,13 +29,16 @@ constexpr float kStaleMax = 14.f;
 // Decoded chunks that fit beside N query rows and their weights: a block is four.
 template <int N>
 constexpr int kRing = N == 64 ? 4 : 5;
+// Chunks that TMEM holds for the scores' products, beside the outputs (4 N columns) and the scores (N).
+template <int N>
+constexpr int kTmemRing = N == 64 ? 3 : 4;
 
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kLookups = 4;
 
 template <int N>
 struct AttendShared {
-    uint64_t full[kRing<N>], oblk[kRing<N>], kfree[2], sdone, pready, qready, drain;
+    uint64_t full[kRing<N>], oblk[kRing<N>], kfree, sdone, pready, qready, drain;
     int64_t scan[kAttendThreads / 32];
     int64_t total, u0;
     int units, start_tile, start_kb;
@@ -44,7 +47,7 @@ struct AttendShared {
     alignas(16) float sc[N], nm[N], m[N], alpha[N], inv[N];
     float red[4][N];
     alignas(16) int vis[N];
-    int64_t row[N];
+    int64_t q[N], row[N];  // a query row's element offsets, -1: none
     // What the lookup warp found for a block's tokens, four blocks in turn.
     uint64_t addr[kLookups];                   // full
     alignas(16) uint4 scale[kLookups][kTile];  // a row's scale bytes
@@ -125,14 +128,15 @@ struct Ring {
 };
 
 // Where a decoded row lies.  A decode thread holds, of tokens r and r + 8
-// (r = lane / 4) and of each chunk of 128 dims, the 16 dims from
-// 64 s + 16 q (q = lane % 4, s the warp's half), as two vectors e = 0, 1 of
-// eight.  In shared memory a chunk is two 128-byte-swizzled tiles of 64 dims;
-// the eight lanes of a store's phase (two tokens, four q) hit different
-// banks.  In TMEM (the A operand of the scores' product) vector e fills the
-// columns 16 (2 s + e) + 4 i + q, i = 0..3, two dims a column: the
-// contraction runs over the dims in another order, and q_word() puts a
-// query's dims in the same one.
+// (r = lane / 4) and of a chunk of 128 dims, the 16 dims from 64 s + 16 q
+// (q = lane % 4, s = 0, 1), as two vectors e = 0, 1 of eight: a warp's load
+// touches eight rows, where a thread a token would touch 32 (and take 1.4
+// times as long in all).  In shared memory a chunk is two 128-byte-swizzled
+// tiles of 64 dims; the eight lanes of a store's phase (two tokens, four q)
+// hit different banks.  In TMEM (the A operand of the scores' product) vector
+// e of half s fills the columns 32 s + 16 e + 4 i + q, i = 0..3, two dims a
+// column: the contraction runs over the dims in another order, and q_word()
+// puts a query's dims in the same one.
 template <Layout L>
 struct Raw {  // 16 codes
     uint32_t w[L == Layout::V41 ? 4 : 2];
@@ -140,20 +144,20 @@ struct Raw {  // 16 codes
 
 // p: the thread's first code of the row.
 template <Layout L>
-__device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int chunk) {
+__device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int chunk, int s) {
     Raw<L> r;
+    // volatile: a load stays where it is issued, a block before its use
     if constexpr (L == Layout::V41) {
-        // volatile: a load stays where it is issued, two chunks before its use
         asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-                     : "l"(p + chunk * 128));
+                     : "l"(p + chunk * 128 + s * 64));
     } else {
-        asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p + chunk * 64));
+        asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p + chunk * 64 + s * 32));
     }
     return r;
 }
 
-// Vector e of a token's 16 dims: codes times `mul` (fp16 twice) as fp16 pairs.
+// Vector e of 16 codes: codes times `mul` (fp16 twice) as fp16 pairs.
 template <Layout L>
 __device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, uint32_t (&o)[4]) {
     if constexpr (L == Layout::V41) {
@@ -265,11 +269,6 @@ __device__ __forceinline__ float redux_max(float v) {
     return r;
 }
 
-// Barriers with the warps that wait for the products.
-__device__ __forceinline__ void decode_sync() { asm volatile("bar.sync 2, 544;" ::: "memory"); }
-__device__ __forceinline__ void scores_sync() { asm volatile("bar.sync 3, 288;" ::: "memory"); }
-static_assert(kDeqWarps * 32 + 32 == 544 && kSoftWarps * 32 + 32 == 288, "participants");
-
 // Barrier of the softmax warps; the second form returns whether any of
 // their threads brought true.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -284,6 +283,20 @@ __device__ __forceinline__ bool soft_any(bool p) {
     return r != 0;
 }
 
+// This CTA's share [u0, u1) of `total` blocks: as equal as can be, none past the first `total` CTAs.
+__device__ __forceinline__ void share(int64_t total, int64_t &u0, int64_t &u1) {
+    const int64_t g = min(int64_t(gridDim.x), total), x = blockIdx.x;
+    if (x >= g) {
+        u0 = u1 = 0;
+    } else if (total <= 0xFFFFFFFFll / (kMaxAttendCtas + 1)) {  // short divisions
+        u0 = uint32_t(x) * uint32_t(total) / uint32_t(g);
+        u1 = uint32_t(x + 1) * uint32_t(total) / uint32_t(g);
+    } else {
+        u0 = x * total / g;
+        u1 = (x + 1) * total / g;
+    }
+}
+
 template <Layout L, int N, bool kSlots>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using T = LayoutTraits<L>;
@@ -291,13 +304,31 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     constexpr int R = kRing<N>;
     constexpr uint32_t kTmemS = 4 * N, kTmemK = 5 * N;
     constexpr uint32_t kTmemCols = 512;  // all of them, which begin at column 0
-    static_assert(5 * N + 128 <= 512, "outputs, scores, two chunks of rows");
+    constexpr int KR = kTmemRing<N>;
+    static_assert(5 * N + 64 * KR <= 512, "outputs, scores, chunks of rows");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
     uint8_t *const sK = base, *const sQ = sK + R * kChunkSmem, *const sP = sQ + N * kD * 2;
     auto &sh = *reinterpret_cast<AttendShared<N> *>(sP + kTile * N * 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    // ---- what needs nothing of the grid before
+    for (int i = tid; i < kLookups * kTile; i += kAttendThreads) sh.code[0][i] = a.pool;
+    if (tid == 0) {
+        for (int i = 0; i < kLookups; ++i) mbar_init(smem_addr(&sh.addr[i]), 1);
+        for (int i = 0; i < R; ++i) {
+            mbar_init(smem_addr(&sh.full[i]), kDeqWarps / 2);
+            mbar_init(smem_addr(&sh.oblk[i]), 1);
+        }
+        mbar_init(smem_addr(&sh.kfree), 1);
+        mbar_init(smem_addr(&sh.sdone), 1);
+        mbar_init(smem_addr(&sh.pready), kSoftWarps);
+        mbar_init(smem_addr(&sh.qready), kSoftWarps);
+        mbar_init(smem_addr(&sh.drain), 1);
+        sh.abort = sh.progress = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
     pdl_wait();
 
     // ---- this CTA's share: blocks [u0, u1) of all tiles' blocks in order
@@ -305,9 +336,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     if constexpr (kSlots) {
         if (tid == 0) {
             const int64_t nb = max(int64_t(1), (a.max_len + kTile - 1) / kTile);
-            const int64_t total = tiles * nb, g = min(int64_t(gridDim.x), total);
-            const int64_t u0 = blockIdx.x < g ? int64_t(blockIdx.x) * total / g : 0;
-            const int64_t u1 = blockIdx.x < g ? int64_t(blockIdx.x + 1) * total / g : 0;
+            const int64_t total = tiles * nb;
+            int64_t u0, u1;
+            share(total, u0, u1);
             sh.total = total;
             sh.u0 = u0;
             sh.units = int(u1 - u0);
@@ -334,9 +365,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             if (i < warp) before += sh.scan[i];
             total += sh.scan[i];
         }
-        const int64_t g = min(int64_t(gridDim.x), total);
-        const int64_t u0 = blockIdx.x < g ? int64_t(blockIdx.x) * total / g : 0;
-        const int64_t u1 = blockIdx.x < g ? int64_t(blockIdx.x + 1) * total / g : 0;
+        int64_t u0, u1;
+        share(total, u0, u1);
         if (tid == 0) {
             sh.total = total;
             sh.u0 = u0;
@@ -355,123 +385,109 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 at += nb;
             }
     }
-    for (int i = tid; i < kLookups * kTile; i += kAttendThreads) sh.code[0][i] = a.pool;
-    if (tid == 0) {
-        for (int i = 0; i < kLookups; ++i) mbar_init(smem_addr(&sh.addr[i]), 1);
-        for (int i = 0; i < R; ++i) {
-            mbar_init(smem_addr(&sh.full[i]), kDeqWarps);
-            mbar_init(smem_addr(&sh.oblk[i]), 1);
-        }
-        mbar_init(smem_addr(&sh.kfree[0]), 1);
-        mbar_init(smem_addr(&sh.kfree[1]), 1);
-        mbar_init(smem_addr(&sh.sdone), 1);
-        mbar_init(smem_addr(&sh.pready), kSoftWarps);
-        mbar_init(smem_addr(&sh.qready), kSoftWarps);
-        mbar_init(smem_addr(&sh.drain), 1);
-        sh.abort = sh.progress = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
+    tc_fence_before();
     __syncthreads();
     const int units = sh.units;
+    tc_fence_after();
     if (units == 0) {  // the same for every thread
         if (tid == 0) a.join[blockIdx.x] = make_int2(-1, 0);
+        if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
         pdl_trigger();
         return;
     }
-    if (warp == kMmaWarp) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
-        const int w = warp - kSoftWarps, q = lane & 3, r8 = lane >> 2, s = w >> 3;
-        const int tok0 = 32 * (w & 3) + 16 * ((w >> 2) & 1) + r8;  // and tok0 + 8
-        const uint32_t krow = smem_addr(sK) + s * kSubBytes + tok0 * 128;
+        const int w = (warp - kSoftWarps) & 7, group = (warp - kSoftWarps) >> 3, q = lane & 3, r8 = lane >> 2;
+        const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
+        const uint32_t krow = smem_addr(sK) + tok0 * 128;
         const uint32_t at0 = krow + (((2 * q) ^ r8) << 4), at1 = krow + (((2 * q + 1) ^ r8) << 4);
-        const uint32_t tlane = kTmemK + 32 * s + ((32 * (w & 3) + 16 * ((w >> 2) & 1)) << 16);
-        constexpr int kLaneBytes = T::kCodeBytes / 32;  // of a chunk
-        const uint32_t lane_at = (4 * s + q) * kLaneBytes;
-        const int block_at = 2 * s + (q >> 1);  // the scale byte of a chunk's four
+        const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
+        const uint32_t lane_at = q * (T::kCodeBytes / 32);  // of a chunk's half
 
-        // Codes are loaded two chunks ahead, from L2, where the lookup warp has sent for them.  A chunk is decoded
-        // before its slot is free, so that only the stores wait for that.
-        Raw<L> raw[2][2];  // chunk & 1, token
-        const uint8_t *now[2], *next[2];
-        int texp[2];
-        bool all_ok;
-        uint32_t v[2][2][4];  // token, vector
-        auto look = [&](const uint8_t *(&to)[2], int k) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) to[h] = sh.code[k][tok0 + 8 * h] + lane_at;
-        };
-        auto adopt = [&](int k) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) texp[h] = sh.texp[k][tok0 + 8 * h];
-            all_ok = __all_sync(0xFFFFFFFFu, texp[0] != kNoToken && texp[1] != kNoToken);
-        };
-        auto decode = [&](Raw<L> (&r)[2], int k, int b) {
-            if (!all_ok) {  // a token that is not there has the pool's first row: its codes are cleared
-                asm volatile("");
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < int(sizeof(Raw<L>) / 4); ++i) r[h].w[i] = texp[h] != kNoToken ? r[h].w[i] : 0u;
-            }
+        // A chunk's codes are loaded a block before they are decoded, from L2, where the lookup warp has sent for them.
+        Raw<L> raw[2][2][2];  // which of the group's two chunks, token, half
+        auto load = [&](int k, int j) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t byte = reinterpret_cast<const uint8_t *>(&sh.scale[k][tok0 + 8 * h])[4 * b + block_at];
-                const uint32_t m = block_mul<L>(byte, texp[h]);
+                const uint8_t *p = sh.code[k][tok0 + 8 * h] + lane_at;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) decode8<L>(r[h], e, m, v[h][e]);
+                for (int s = 0; s < 2; ++s) raw[j][h][s] = load_raw<L>(p, 2 * j + group, s);
             }
         };
-        auto load = [&](Raw<L> (&r)[2], const uint8_t *const (&from)[2], int b) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) r[h] = load_raw<L>(from[h], b);
-        };
-        decode_sync();  // the first block is looked up
-        look(now, 0);
-        load(raw[0], now, 0);
-        load(raw[1], now, 1);
-        adopt(0);
-        decode(raw[0], 0, 0);
-        load(raw[0], now, 2);
-        int slot = 0;
+        bool live = mbar_wait(smem_addr(&sh.addr[0]), 0);
+        load(0, 0);
+        load(0, 1);
+        // The chunk's slots: R in shared memory, KR in TMEM.
+        int slot = group, kslot = group;
+        uint32_t parity = 0;
 #pragma unroll 1
-        for (int i = 0; i < units; ++i) {
+        for (int i = 0; i < units && live; ++i) {
             const int k = i & (kLookups - 1), kn = i + 1 < units ? (i + 1) & (kLookups - 1) : k;
+            int texp[2];
 #pragma unroll
-            for (int b = 0; b < kChunks; ++b) {
-                decode_sync();  // the slot is free (b = 0: and the next block is looked up)
+            for (int h = 0; h < 2; ++h) texp[h] = sh.texp[k][tok0 + 8 * h];
+            const bool all_ok = __all_sync(0xFFFFFFFFu, texp[0] != kNoToken && texp[1] != kNoToken);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int b = 2 * j + group;
+                // A slot in shared memory is free when the product over the dims that it held is done.  The chunk that
+                // had the TMEM slot before belongs to the block before, whose scores were done before any of those
+                // products began; except that with three TMEM slots the last chunk follows the block's own first
+                // one, and with a longer ring the first chunk need not wait for a product of the block before.  Both
+                // then wait for the scores over a first chunk.
+                static_assert((R == 4 && KR == 3) || (R == 5 && KR == 4), "what the rings imply");
+                if (i * kChunks + b >= R) live = live && mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1);
+                if (KR == 3 && b == 3) live = live && mbar_wait(smem_addr(&sh.kfree), i & 1);
+                if (KR == 4 && b == 0 && i > 0) live = live && mbar_wait(smem_addr(&sh.kfree), (i - 1) & 1);
                 tc_fence_after();
+                if (!all_ok) {  // a token that is not there has the pool's first row: its codes are cleared
+                    asm volatile("");
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+#pragma unroll
+                            for (int x = 0; x < int(sizeof(Raw<L>) / 4); ++x)
+                                raw[j][h][s].w[x] = texp[h] != kNoToken ? raw[j][h][s].w[x] : 0u;
+                }
                 const uint32_t off = slot * kChunkSmem;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sts_u4((e ? at1 : at0) + off, v[0][e]);
-                    sts_u4((e ? at1 : at0) + off + 8 * 128, v[1][e]);
-                    tmem_st_16x128b_x4(tlane + (b & 1) * 64 + 16 * e, v[0][e], v[1][e]);
+                for (int s = 0; s < 2; ++s) {
+                    uint32_t m[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        m[h] = block_mul<L>(reinterpret_cast<const uint8_t *>(&sh.scale[k][tok0 + 8 * h])[4 * b + 2 * s + (q >> 1)], texp[h]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t v0[4], v1[4];
+                        decode8<L>(raw[j][0][s], e, m[0], v0);
+                        decode8<L>(raw[j][1][s], e, m[1], v1);
+                        const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
+                        sts_u4(at, v0);
+                        sts_u4(at + 8 * 128, v1);
+                        tmem_st_16x128b_x4(tlane + kslot * 64 + 32 * s + 16 * e, v0, v1);
+                    }
                 }
+                fence_proxy_async();
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
-                if (++slot == R) slot = 0;
-                // the next chunk's values, and codes for the one that is two further on
-                if (b == 0) look(next, kn);
-                if (b == kChunks - 1) {
-                    adopt(kn);
-                    now[0] = next[0];
-                    now[1] = next[1];
+                if (j == 0 && i + 1 < units) live = live && mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1);
+                load(kn, j);
+                slot += 2;
+                if (slot >= R) {
+                    slot -= R;
+                    parity ^= 1;
                 }
-                decode(raw[(b + 1) & 1], b == kChunks - 1 ? kn : k, (b + 1) % kChunks);
-                if (b == 0) load(raw[1], now, 3);
-                if (b == 1) load(raw[0], next, 0);
-                if (b == 2) load(raw[1], next, 1);
-                if (b == 3) load(raw[0], now, 2);
+                kslot += 2;
+                if (kslot >= KR) kslot -= KR;
             }
+            if (warp == kSoftWarps && lane == 0) *const_cast<volatile int *>(&sh.progress) = i + 1;
         }
+        if (!live) sh.abort = 1;
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
@@ -483,6 +499,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             constexpr uint32_t kQHi = desc_hi(1024, kSwizzle128), kVHi = kQHi, kPHi = desc_hi(16 * N, kPSwizzle);
             int left_tile = 0, tile = sh.start_tile, kb = sh.start_kb;
             uint32_t seg = 0;
+            int kslot = 0;
             bool live = true;
             Ring<R> sr, vr;
 #pragma unroll 1
@@ -500,25 +517,22 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 --left_tile;
 #pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
-                    // The writers only arrive: the fence between their stores and the tensor core's reads is made
-                    // here, where no load is in flight (in a decode warp it would wait for the next codes).
                     live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
-                    fence_proxy_async();
                     tc_fence_after();
                     if (live && elect_one()) {
-                        const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + (b & 1) * 64;
+                        const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_ts(kTmemS, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS,
                                    b + k > 0);
-                        mma_commit(smem_addr(&sh.kfree[b & 1]));
+                        if (b == 0) mma_commit(smem_addr(&sh.kfree));
                         if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
                     }
                     __syncwarp();
                     sr.next();
+                    if (++kslot == KR) kslot = 0;
                 }
                 live = live && mbar_wait(smem_addr(&sh.pready), phase);
-                fence_proxy_async();
                 tc_fence_after();
 #pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
@@ -540,40 +554,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 mbar_wait(smem_addr(&sh.drain), 0);
             }
         } else if (warp == kMmaWarp + 1) {
-            // A chunk's slot is free when the product over the dims that it held is done; that product comes after
-            // the scores of its block, and so frees the TMEM slot of a chunk too, unless the ring is longer than a
-            // block or the block itself has used the slot.  A wait that is given up ends all further ones: every
-            // role then runs through its blocks, and the call reports it.
-            Ring<R> ring;
-            bool live = mbar_wait(smem_addr(&sh.addr[0]), 0);
-            decode_sync();
-#pragma unroll 1
-            for (int i = 0; i < units; ++i) {
-                if (lane == 0) *const_cast<volatile int *>(&sh.progress) = i;
-                if (i + 1 < units)
-                    live = live && mbar_wait(smem_addr(&sh.addr[(i + 1) & (kLookups - 1)]), ((i + 1) / kLookups) & 1);
-#pragma unroll 1
-                for (int b = 0; b < kChunks; ++b) {
-                    if (i * kChunks + b >= R) live = live && mbar_wait(smem_addr(&sh.oblk[ring.slot]), ring.parity ^ 1);
-                    if (b >= 2 || (R > kChunks && i > 0)) live = live && mbar_wait(smem_addr(&sh.kfree[b & 1]), b >= 2 ? 0 : 1);
-                    decode_sync();
-                    ring.next();
-                }
-            }
-            if (lane == 0) *const_cast<volatile int *>(&sh.progress) = units;
-            if (!live) sh.abort = 1;
-        } else if (warp == kMmaWarp + 2) {
-            // scores are there; `full` of the block's first chunk orders the softmax warps' reads of texp
-            Ring<R> ring;
-            bool live = true;
-#pragma unroll 1
-            for (int i = 0; i < units; ++i) {
-                live = live && mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity) && mbar_wait(smem_addr(&sh.sdone), i & 1);
-                scores_sync();
-                for (int b = 0; b < kChunks; ++b) ring.next();
-            }
-            if (!live) sh.abort = 1;
-        } else {
             // Looks up where a block's rows lie and fetches their scales, up to two blocks ahead of the decode warps.
             // A load of a row's first bytes (V41: of either half) asks for 256 bytes in L2, and so for the row.  Lane
             // l has tokens l, l + 32, l + 64, l + 96.  Three blocks are under way: the indexes of one, the scales of
@@ -666,42 +646,52 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 // the scores' products of the last tile are done (their result was waited for)
                 kb0 = cur.kb;
                 if (tid == 0 && cur.kb == 0 && cur.t.rt == 0 && cur.t.err) raise_err(a.err, cur.t.err);
-                const int row0 = cur.t.rt * N;
+                if (tid < N) {
+                    const int row = cur.t.rt * N + tid, rc = min(row, per - 1);
+                    const int j = rc / a.heads, head = rc - j * a.heads;
+                    const int64_t tok = int64_t(cur.t.seq) * a.q_len + j;
+                    sh.q[tid] = row < per ? tok * a.q_tok + head * a.q_head : -1;
+                    sh.row[tid] = row < per ? tok * a.out_tok + head * a.out_head : -1;
+                    sh.vis[tid] = kSlots || row >= per ? cur.t.seen : max(0, cur.t.len - (a.q_len - 1 - j));
+                    sh.m[tid] = -INFINITY;
+                    sh.nm[tid] = 0.f;
+                }
+                soft_sync();
                 const uint32_t sq = smem_addr(sQ);
-#pragma unroll 2
-                for (int r = warp; r < N; r += kSoftWarps) {
-                    const int row = row0 + r;
-                    uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                    const int rc = min(row, per - 1);
-                    const int64_t tok = int64_t(cur.t.seq) * a.q_len + rc / a.heads;
-                    const int head = rc % a.heads;
-                    if (row < per) {
-                        const uint16_t *p = a.q + tok * a.q_tok + head * a.q_head;
-                        u[0] = ld_stream_u4(p + lane * 8);
-                        u[1] = ld_stream_u4(p + (lane + 32) * 8);
-                    }
-                    uint32_t v[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-                    // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
-                    uint32_t big = 0;
+                constexpr int kBatch = N / kSoftWarps < 4 ? N / kSoftWarps : 4;  // rows whose loads are in flight
+#pragma unroll 1
+                for (int r0 = warp; r0 < N; r0 += kBatch * kSoftWarps) {
+                    uint32_t v[kBatch][8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) big = max(big, max((v[e] << 16) & 0x7FFF0000u, v[e] & 0x7FFF0000u));
-                    big = __reduce_max_sync(0xFFFFFFFFu, big);
-                    const uint32_t up = min(268u - (big >> 23), 254u);
-                    const float f = __uint_as_float(up << 23);
+                    for (int t = 0; t < kBatch; ++t) {
+                        const int64_t at = sh.q[r0 + t * kSoftWarps];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t h;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[e]) * f), "f"(bf16_lo(v[e]) * f));
-                        sts_u32(sq + q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
+                        for (int h = 0; h < 2; ++h) {
+                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                            if (at >= 0) u = ld_stream_u4(a.q + at + (lane + 32 * h) * 8);
+                            v[t][4 * h] = u.x, v[t][4 * h + 1] = u.y, v[t][4 * h + 2] = u.z, v[t][4 * h + 3] = u.w;
+                        }
                     }
-                    if (lane == 0) {
-                        sh.sc[r] = c * ue8m0_to_f32(254u - up);
-                        sh.m[r] = -INFINITY;
-                        sh.nm[r] = 0.f;
-                        sh.vis[r] = kSlots || row >= per ? cur.t.seen : max(0, cur.t.len - (a.q_len - 1 - rc / a.heads));
-                        sh.row[r] = row < per ? tok * a.out_tok + head * a.out_head : -1;
+#pragma unroll
+                    for (int t = 0; t < kBatch; ++t) {
+                        const int r = r0 + t * kSoftWarps;
+                        // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
+                        uint32_t big = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) big = max(big, max((v[t][e] << 16) & 0x7FFF0000u, v[t][e] & 0x7FFF0000u));
+                        big = __reduce_max_sync(0xFFFFFFFFu, big);
+                        const uint32_t up = min(268u - (big >> 23), 254u);
+                        const float f = __uint_as_float(up << 23);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t h;
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[t][e]) * f), "f"(bf16_lo(v[t][e]) * f));
+                            sts_u32(sq + q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
+                        }
+                        if (lane == 0) sh.sc[r] = c * ue8m0_to_f32(254u - up);
                     }
                 }
+                fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.qready));
                 soft_sync();
@@ -709,7 +699,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 for (int j = 0; j < NC; ++j) l[j] = 0.f;
                 unset = true;
             }
-            scores_sync();
+            // `full` of the block's first chunk orders this thread's read of texp
+            live = live && mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity) && mbar_wait(smem_addr(&sh.sdone), i & 1);
             tc_fence_after();
             const int te = sh.texp[i & (kLookups - 1)][t_row];
             const bool have = te != kNoToken;
@@ -722,7 +713,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
             // x = score in log2 units, plus the row's power of two; -inf where it is masked
             float x[NC];
-            {
+            bool odd = false;  // a score that is not finite, where some rows do not see the token
+            auto scores = [&]() {
                 uint32_t sraw[NC];
                 tmem_ld<NC>(trow + kTmemS + c0, sraw);
 #pragma unroll
@@ -739,30 +731,44 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     }
                     x[j] = u.x, x[j + 1] = u.y, x[j + 2] = w.x, x[j + 3] = w.y;
                 }
-            }
-            bool odd = false;  // a score that is not finite, where some rows do not see the token
-            if (masked) {
-                asm volatile("");  // a branch, not 2 NC selects in every block
+                if (masked) {
+                    asm volatile("");  // a branch, not 2 NC selects in every block
 #pragma unroll
-                for (int j = 0; j < NC; ++j) {
-                    odd = odd || !(fabsf(x[j]) < INFINITY);
-                    if (!(t_at < sh.vis[c0 + j])) x[j] = -INFINITY;
+                    for (int j = 0; j < NC; ++j) {
+                        odd = odd || !(fabsf(x[j]) < INFINITY);
+                        if (!(t_at < sh.vis[c0 + j])) x[j] = -INFINITY;
+                    }
                 }
-            }
-            bool move = unset;
-            if (!move) {
+            };
+            // x becomes the weights 2^(x - maximum), which go to shared memory as fp16; returns the largest exponent
+            auto weights = [&]() {
                 float top = -INFINITY;
+                const uint32_t sp = smem_addr(sP);
 #pragma unroll
-                for (int j = 0; j < NC; j += 4) {
-                    const float4 k = *reinterpret_cast<const float4 *>(&sh.nm[c0 + j]);
-                    const float2 u = fadd2(make_float2(x[j], x[j + 1]), make_float2(k.x, k.y));
-                    const float2 w = fadd2(make_float2(x[j + 2], x[j + 3]), make_float2(k.z, k.w));
-                    top = fmax3(top, fmax3(u.x, u.y, w.x), w.y);
+                for (int j0 = 0; j0 < NC; j0 += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int j = j0 + 4 * g;
+                        const float4 k = *reinterpret_cast<const float4 *>(&sh.nm[c0 + j]);
+                        const float2 u = fadd2(make_float2(x[j], x[j + 1]), make_float2(k.x, k.y));
+                        const float2 w = fadd2(make_float2(x[j + 2], x[j + 3]), make_float2(k.z, k.w));
+                        top = fmax3(top, fmax3(u.x, u.y, w.x), w.y);
+                        x[j] = ex2_approx(u.x), x[j + 1] = ex2_approx(u.y);
+                        x[j + 2] = ex2_approx(w.x), x[j + 3] = ex2_approx(w.y);
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[2 * g]) : "f"(x[j + 1]), "f"(x[j]));
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[2 * g + 1]) : "f"(x[j + 3]), "f"(x[j + 2]));
+                    }
+                    sts_u4(sp + p_vec<N>(t_row, (c0 + j0) / 8), h);
                 }
-                move = soft_any(top > kStaleMax);
-            }
+                return top;
+            };
+            scores();
+            bool move = unset;
+            if (!unset) move = soft_any(weights() > kStaleMax);
             if (move) {
                 // the columns' new maxima, and what is summed so far in their terms
+                if (!unset) scores();
                 float mine = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < NC; ++j) {
@@ -796,29 +802,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         }
                     tc_wait_st();
                 }
+                weights();
             }
-            const uint32_t sp = smem_addr(sP);
 #pragma unroll
-            for (int j0 = 0; j0 < NC; j0 += 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 k = *reinterpret_cast<const float4 *>(&sh.nm[c0 + j0 + 4 * g]);
-                    const float add[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-                    for (int d = 0; d < 4; d += 2) {
-                        const int j = j0 + 4 * g + d;
-                        const float2 z = fadd2(make_float2(x[j], x[j + 1]), make_float2(add[d], add[d + 1]));
-                        const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-                        float2 sum = make_float2(l[j], l[j + 1]);
-                        if constexpr (kExp) sum = ffma2(p, make_float2(e_down, e_down), sum);
-                        else sum = fadd2(sum, p);
-                        l[j] = sum.x;
-                        l[j + 1] = sum.y;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[2 * g + d / 2]) : "f"(p.y), "f"(p.x));
-                    }
-                }
-                sts_u4(sp + p_vec<N>(t_row, (c0 + j0) / 8), h);
+            for (int j = 0; j < NC; j += 2) {
+                float2 sum = make_float2(l[j], l[j + 1]);
+                if constexpr (kExp) sum = ffma2(make_float2(x[j], x[j + 1]), make_float2(e_down, e_down), sum);
+                else sum = fadd2(sum, make_float2(x[j], x[j + 1]));
+                l[j] = sum.x;
+                l[j + 1] = sum.y;
             }
             if (masked && odd && have && half == 0) {
                 // a weight of 0 does not silence a NaN: if the token's row itself is not finite, the rows that see
@@ -844,6 +836,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
             }
             tc_fence_before();
+            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.pready));
             // the ring moves on by a block; the last chunk's slot tells when the block's outputs are summed

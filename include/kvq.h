@@ -220,6 +220,7 @@ size_t kvq_attend_workspace(int64_t rows);
  *   q            bf16, element (token, head, d) at token * q_token_stride +
  *                head * q_head_stride + d; 16-B aligned rows.  A stride of 0
  *                repeats a row.
+ *   pool         32-B aligned.
  *   page_table   [table_rows, table_stride] int32, the first table_width of
  *                a row used: physical page of each logical page.
  *   req          [n_seq] int32: table row of sequence i (NULL: row i, and
