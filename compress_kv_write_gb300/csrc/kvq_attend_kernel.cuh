@@ -15,13 +15,16 @@ constexpr int kChunks = kD / kChunk;
 constexpr int kSubBytes = kTile * 128;         // 64 dims of a block, 128 B a token
 constexpr int kChunkSmem = 2 * kSubBytes;
 // Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-23 decode (8-15 the even chunks, 16-23 the
-// odd ones, so that one half's stores overlap the other's waits), 24 products, 25 looks up where the rows of coming
-// blocks lie, 26 and 27 complete the warpgroup.
+// odd ones, so that one half's stores overlap the other's waits), 24 products, 25 and 26 look up where the rows of
+// coming blocks lie, 27 completes the warpgroup.
 constexpr int kSoftWarps = 8, kDeqWarps = 16, kMmaWarp = kSoftWarps + kDeqWarps;
 constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
 // Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
-constexpr int kSoftRegs = 104, kDeqRegs = 64, kMmaRegs = 40;
-static_assert(2 * kSoftRegs + 4 * kDeqRegs + kMmaRegs <= 7 * 72, "a larger sum would wait for ever");
+template <Layout L, int N>
+struct Regs {
+    static constexpr int kSoft = N == 64 ? 112 : 88, kDeq = N == 64 ? 56 : 64, kMma = N == 64 ? 56 : 72;
+    static_assert(2 * kSoft + 4 * kDeq + kMma <= 7 * 72, "a larger sum would wait for ever");
+};
 // How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
 // (which rescales the outputs in TMEM) is rare after a tile's first block.
 constexpr float kStaleMax = 14.f;
@@ -34,7 +37,7 @@ template <int N>
 constexpr int kTmemRing = N == 64 ? 3 : 4;
 
 constexpr int kNoToken = 0x7FFFFFFF;
-constexpr int kLookups = 4;
+constexpr int kLookups = 4, kLookupWarps = 2;
 
 template <int N>
 struct AttendShared {
@@ -146,7 +149,7 @@ struct Raw {  // 16 codes
 template <Layout L>
 __device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int chunk, int s) {
     Raw<L> r;
-    // volatile: a load stays where it is issued, a block before its use
+    // volatile: a load stays where it is issued, half a block before its use
     if constexpr (L == Layout::V41) {
         asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     // ---- what needs nothing of the grid before
     for (int i = tid; i < kLookups * kTile; i += kAttendThreads) sh.code[0][i] = a.pool;
     if (tid == 0) {
-        for (int i = 0; i < kLookups; ++i) mbar_init(smem_addr(&sh.addr[i]), 1);
+        for (int i = 0; i < kLookups; ++i) mbar_init(smem_addr(&sh.addr[i]), kLookupWarps);
         for (int i = 0; i < R; ++i) {
             mbar_init(smem_addr(&sh.full[i]), kDeqWarps / 2);
             mbar_init(smem_addr(&sh.oblk[i]), 1);
@@ -359,11 +362,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
         if (lane == 31) sh.scan[warp] = incl;
         __syncthreads();
-        int64_t before = 0, total = 0;
-#pragma unroll 1
-        for (int i = 0; i < kAttendThreads / 32; ++i) {
-            if (i < warp) before += sh.scan[i];
-            total += sh.scan[i];
+        // every warp sums the warps' totals: lane w has that of warp w
+        const int64_t of_warp = lane < kAttendThreads / 32 ? sh.scan[lane] : 0;
+        int64_t before = lane < warp ? of_warp : 0, total = of_warp;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            before += __shfl_xor_sync(0xFFFFFFFFu, (long long)before, o);
+            total += __shfl_xor_sync(0xFFFFFFFFu, (long long)total, o);
         }
         int64_t u0, u1;
         share(total, u0, u1);
@@ -373,17 +378,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             sh.units = int(u1 - u0);
         }
         int64_t at = before + incl - mine;
-        if (u0 >= at && u0 < at + mine)
+        if (u0 >= at && u0 < at + mine) {  // one thread
+            int t = t0;
 #pragma unroll 1
-            for (int t = t0; t < t1; ++t) {
+            for (; t + 1 < t1; ++t) {
                 const int nb = tile_info<N, kSlots>(a, t).nb;
-                if (u0 < at + nb) {
-                    sh.start_tile = t;
-                    sh.start_kb = int(u0 - at);
-                    break;
-                }
+                if (u0 < at + nb) break;
                 at += nb;
             }
+            sh.start_tile = t;
+            sh.start_kb = int(u0 - at);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
+        if constexpr (Regs<L, N>::kDeq < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kDeq));
         const int w = (warp - kSoftWarps) & 7, group = (warp - kSoftWarps) >> 3, q = lane & 3, r8 = lane >> 2;
         const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
         const uint32_t krow = smem_addr(sK) + tok0 * 128;
@@ -406,19 +411,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
         const uint32_t lane_at = q * (T::kCodeBytes / 32);  // of a chunk's half
 
-        // A chunk's codes are loaded a block before they are decoded, from L2, where the lookup warp has sent for them.
-        Raw<L> raw[2][2][2];  // which of the group's two chunks, token, half
+        // A chunk's codes are loaded while the other half's chunk is stored, from L2, where the lookup warps have sent
+        // for them.
+        Raw<L> raw[2][2];  // token, half
         auto load = [&](int k, int j) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint8_t *p = sh.code[k][tok0 + 8 * h] + lane_at;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) raw[j][h][s] = load_raw<L>(p, 2 * j + group, s);
+                for (int s = 0; s < 2; ++s) raw[h][s] = load_raw<L>(p, 2 * j + group, s);
             }
         };
         bool live = mbar_wait(smem_addr(&sh.addr[0]), 0);
         load(0, 0);
-        load(0, 1);
         // The chunk's slots: R in shared memory, KR in TMEM.
         int slot = group, kslot = group;
         uint32_t parity = 0;
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         for (int s = 0; s < 2; ++s)
 #pragma unroll
                             for (int x = 0; x < int(sizeof(Raw<L>) / 4); ++x)
-                                raw[j][h][s].w[x] = texp[h] != kNoToken ? raw[j][h][s].w[x] : 0u;
+                                raw[h][s].w[x] = texp[h] != kNoToken ? raw[h][s].w[x] : 0u;
                 }
                 const uint32_t off = slot * kChunkSmem;
 #pragma unroll
@@ -462,8 +467,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         uint32_t v0[4], v1[4];
-                        decode8<L>(raw[j][0][s], e, m[0], v0);
-                        decode8<L>(raw[j][1][s], e, m[1], v1);
+                        decode8<L>(raw[0][s], e, m[0], v0);
+                        decode8<L>(raw[1][s], e, m[1], v1);
                         const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
                         sts_u4(at, v0);
                         sts_u4(at + 8 * 128, v1);
@@ -475,8 +480,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
-                if (j == 0 && i + 1 < units) live = live && mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1);
-                load(kn, j);
+                if (j == 0) {
+                    load(k, 1);
+                } else {
+                    if (i + 1 < units) live = live && mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1);
+                    load(kn, 0);
+                }
                 slot += 2;
                 if (slot >= R) {
                     slot -= R;
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (!live) sh.abort = 1;
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if constexpr (Regs<L, N>::kMma < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kMma));
         if (warp == kMmaWarp) {
             constexpr uint32_t kIdescS = mma_idesc(kTile, N, false, false);
             constexpr uint32_t kIdescO = mma_idesc(kTile, N, true, true);
@@ -502,9 +511,37 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             int kslot = 0;
             bool live = true;
             Ring<R> sr, vr;
+            // scores over chunk b of a block
+            auto scores = [&](int b) {
+                live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
+                tc_fence_after();
+                if (live && elect_one()) {
+                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(kTmemS, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS, b + k > 0);
+                    if (b == 0) mma_commit(smem_addr(&sh.kfree));
+                    if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
+                }
+                __syncwarp();
+                sr.next();
+                if (++kslot == KR) kslot = 0;
+            };
+            // outputs of dims 128 b .. 128 b + 127
+            auto outputs = [&](int b, bool add) {
+                if (live && elect_one()) {
+                    const uint32_t at = vd + ((vr.slot * kChunkSmem) >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ss(b * N, at + ((k * 2048) >> 4), kVHi, pd + ((k * 32 * N) >> 4), kPHi, kIdescO, add || k > 0);
+                    mma_commit(smem_addr(&sh.oblk[vr.slot]));
+                }
+                __syncwarp();
+                vr.next();
+            };
+            bool begun = false;  // whether the block's scores over its first chunk are under way
 #pragma unroll 1
             for (int i = 0; i < units && live; ++i) {
-                const uint32_t phase = uint32_t(i) & 1;
                 bool first = false;
                 if (left_tile == 0) {  // a new tile: its queries, a fresh accumulator
                     left_tile = tile_info<N, kSlots>(a, tile).nb - kb;
@@ -516,36 +553,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
                 --left_tile;
 #pragma unroll 1
-                for (int b = 0; b < kChunks; ++b) {
-                    live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
-                    tc_fence_after();
-                    if (live && elect_one()) {
-                        const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ts(kTmemS, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS,
-                                   b + k > 0);
-                        if (b == 0) mma_commit(smem_addr(&sh.kfree));
-                        if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
-                    }
-                    __syncwarp();
-                    sr.next();
-                    if (++kslot == KR) kslot = 0;
-                }
-                live = live && mbar_wait(smem_addr(&sh.pready), phase);
+                for (int b = begun ? 1 : 0; b < kChunks; ++b) scores(b);
+                live = live && mbar_wait(smem_addr(&sh.pready), i & 1);
                 tc_fence_after();
+                // The next block's scores over its first chunk go before the last outputs: they free a chunk's place
+                // in TMEM sooner.  (Of another tile they wait for its queries, which wait for these outputs.)
+                begun = left_tile > 0 && i + 1 < units;
 #pragma unroll 1
                 for (int b = 0; b < kChunks; ++b) {
-                    if (live && elect_one()) {
-                        const uint32_t at = vd + ((vr.slot * kChunkSmem) >> 4);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ss(b * N, at + ((k * 2048) >> 4), kVHi, pd + ((k * 32 * N) >> 4), kPHi, kIdescO,
-                                   !first || k > 0);
-                        mma_commit(smem_addr(&sh.oblk[vr.slot]));
-                    }
-                    __syncwarp();
-                    vr.next();
+                    if (b == kChunks - 1 && begun) scores(0);
+                    outputs(b, !first);
                 }
             }
             if (!live) {
@@ -553,12 +570,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if (elect_one()) mma_commit(smem_addr(&sh.drain));  // nothing may write TMEM once it is freed
                 mbar_wait(smem_addr(&sh.drain), 0);
             }
-        } else if (warp == kMmaWarp + 1) {
+        } else if (warp <= kMmaWarp + kLookupWarps) {
             // Looks up where a block's rows lie and fetches their scales, up to two blocks ahead of the decode warps.
             // A load of a row's first bytes (V41: of either half) asks for 256 bytes in L2, and so for the row.  Lane
-            // l has tokens l, l + 32, l + 64, l + 96.  Three blocks are under way: the indexes of one, the scales of
-            // one, and one that is written down.
-            constexpr int K = kTile / 32;
+            // l of a warp has two tokens.
+            constexpr int K = kTile / 32 / kLookupWarps;
+            const int mine = (warp - kMmaWarp - 1) * 32 * K + lane;  // the first of the lane's tokens
             using Index = std::conditional_t<kSlots, int64_t, int>;
             const uint32_t page_bytes = uint32_t(kTokenBytes<L>) << a.page_bits, in_page = (1u << a.page_bits) - 1;
             const uint32_t scale_at = uint32_t(T::kCodeBytes) << a.page_bits;
@@ -567,7 +584,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             Index idx[K];
             int t0 = 0, seen = 0;
             auto fetch = [&]() {
-                t0 = cur.kb * kTile + lane;
+                t0 = cur.kb * kTile + mine;
                 seen = cur.left > 0 ? cur.t.seen : 0;
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
@@ -583,28 +600,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     }
                 }
             };
-            const uint8_t *row[K];
-            uint4 sc[K];
-            uint32_t good = 0;
-            fetch();
 #pragma unroll 1
-            for (int i = 0; i <= units; ++i) {
-                if (i > 0) {
-                    // block i - 1: wait until its entries are free (every reader of block i - 5 is done)
-                    for (int tries = 0; progress < i - 3 && tries < (1 << 22); ++tries) __nanosleep(64);
-                    const int k = (i - 1) & (kLookups - 1);
-#pragma unroll
-                    for (int j = 0; j < K; ++j) {
-                        const bool g = (good >> j) & 1;
-                        sh.scale[k][lane + 32 * j] = sc[j];
-                        sh.code[k][lane + 32 * j] = row[j];
-                        sh.texp[k][lane + 32 * j] = g ? row_texp<L>(sc[j]) : kNoToken;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.addr[k]));
-                }
-                if (i == units) break;
-                good = 0;
+            for (int i = 0; i < units; ++i) {
+                fetch();
+                const uint8_t *row[K];
+                uint4 sc[K];
+                uint32_t good = 0;
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
                     const int t = t0 + 32 * j;
@@ -622,13 +623,23 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     if constexpr (L == Layout::V41)
                         asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(sink) : "l"(row[j] + 256));
                 }
+                // wait until the entries are free (every reader of block i - 4 is done)
+                for (int tries = 0; progress < i - 2 && tries < (1 << 22); ++tries) __nanosleep(64);
+                const int k = i & (kLookups - 1);
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    sh.scale[k][mine + 32 * j] = sc[j];
+                    sh.code[k][mine + 32 * j] = row[j];
+                    sh.texp[k][mine + 32 * j] = (good >> j) & 1 ? row_texp<L>(sc[j]) : kNoToken;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.addr[k]));
                 cur.next(a);
-                fetch();
             }
         }
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kSoft));
         constexpr int NC = N / 2;  // columns a thread: those from c0
         const int t_row = tid & 127, quarter = warp & 3, half = warp >> 2, c0 = half * NC;
         const float c = a.scale * kLog2e;
