@@ -313,7 +313,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
     uint8_t *const sK = base, *const sQ = sK + R * kChunkSmem, *const sP = sQ + N * kD * 2;
     auto &sh = *reinterpret_cast<AttendShared<N> *>(sP + kTile * N * 2);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // shuffled, so that the compiler knows it to be the same for a warp's lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
     // ---- what needs nothing of the grid before
     for (int i = tid; i < kLookups * kTile; i += kAttendThreads) sh.code[0][i] = a.pool;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     }
     tc_fence_before();
     __syncthreads();
-    const int units = sh.units;
+    const int units = __shfl_sync(0xFFFFFFFFu, sh.units, 0);
     tc_fence_after();
     if (units == 0) {  // the same for every thread
         if (tid == 0) a.join[blockIdx.x] = make_int2(-1, 0);
@@ -422,13 +423,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 for (int s = 0; s < 2; ++s) raw[h][s] = load_raw<L>(p, 2 * j + group, s);
             }
         };
-        bool live = mbar_wait(smem_addr(&sh.addr[0]), 0);
+        uint32_t tries = kWaitTries;
+        mbar_wait(smem_addr(&sh.addr[0]), 0, tries);
         load(0, 0);
         // The chunk's slots: R in shared memory, KR in TMEM.
         int slot = group, kslot = group;
         uint32_t parity = 0;
 #pragma unroll 1
-        for (int i = 0; i < units && live; ++i) {
+        for (int i = 0; i < units; ++i) {
             const int k = i & (kLookups - 1), kn = i + 1 < units ? (i + 1) & (kLookups - 1) : k;
             int texp[2];
 #pragma unroll
@@ -443,9 +445,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 // one, and with a longer ring the first chunk need not wait for a product of the block before.  Both
                 // then wait for the scores over a first chunk.
                 static_assert((R == 4 && KR == 3) || (R == 5 && KR == 4), "what the rings imply");
-                if (i * kChunks + b >= R) live = live && mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1);
-                if (KR == 3 && b == 3) live = live && mbar_wait(smem_addr(&sh.kfree), i & 1);
-                if (KR == 4 && b == 0 && i > 0) live = live && mbar_wait(smem_addr(&sh.kfree), (i - 1) & 1);
+                if (i * kChunks + b >= R) mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1, tries);
+                if (KR == 3 && b == 3) mbar_wait(smem_addr(&sh.kfree), i & 1, tries);
+                if (KR == 4 && b == 0 && i > 0) mbar_wait(smem_addr(&sh.kfree), (i - 1) & 1, tries);
                 tc_fence_after();
                 if (!all_ok) {  // a token that is not there has the pool's first row: its codes are cleared
                     asm volatile("");
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if (j == 0) {
                     load(k, 1);
                 } else {
-                    if (i + 1 < units) live = live && mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1);
+                    if (i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1, tries);
                     load(kn, 0);
                 }
                 slot += 2;
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
             if (warp == kSoftWarps && lane == 0) *const_cast<volatile int *>(&sh.progress) = i + 1;
         }
-        if (!live) sh.abort = 1;
+        if (!tries) sh.abort = 1;
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
         if constexpr (Regs<L, N>::kMma < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kMma));
@@ -506,16 +508,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             constexpr uint32_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
             const uint32_t qd = desc_lo(smem_addr(sQ), 16), vd = desc_lo(smem_addr(sK), kSubBytes), pd = desc_lo(smem_addr(sP), 16);
             constexpr uint32_t kQHi = desc_hi(1024, kSwizzle128), kVHi = kQHi, kPHi = desc_hi(16 * N, kPSwizzle);
-            int left_tile = 0, tile = sh.start_tile, kb = sh.start_kb;
+            int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
             uint32_t seg = 0;
             int kslot = 0;
-            bool live = true;
+            uint32_t tries = kWaitTries;
             Ring<R> sr, vr;
             // scores over chunk b of a block
             auto scores = [&](int b) {
-                live = live && mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity);
+                mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity, tries);
                 tc_fence_after();
-                if (live && elect_one()) {
+                if (elect_one()) {
                     const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             };
             // outputs of dims 128 b .. 128 b + 127
             auto outputs = [&](int b, bool add) {
-                if (live && elect_one()) {
+                if (elect_one()) {
                     const uint32_t at = vd + ((vr.slot * kChunkSmem) >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -541,34 +543,36 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             };
             bool begun = false;  // whether the block's scores over its first chunk are under way
 #pragma unroll 1
-            for (int i = 0; i < units && live; ++i) {
+            for (int i = 0; i < units; ++i) {
                 bool first = false;
                 if (left_tile == 0) {  // a new tile: its queries, a fresh accumulator
-                    left_tile = tile_info<N, kSlots>(a, tile).nb - kb;
+                    left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kSlots>(a, tile).nb, 0) - kb;
                     ++tile;
                     kb = 0;
                     first = true;
-                    live = live && mbar_wait(smem_addr(&sh.qready), seg & 1);
+                    mbar_wait(smem_addr(&sh.qready), seg & 1, tries);
                     ++seg;
                 }
                 --left_tile;
-#pragma unroll 1
-                for (int b = begun ? 1 : 0; b < kChunks; ++b) scores(b);
-                live = live && mbar_wait(smem_addr(&sh.pready), i & 1);
+                if (!begun) scores(0);
+#pragma unroll
+                for (int b = 1; b < kChunks; ++b) scores(b);
+                mbar_wait(smem_addr(&sh.pready), i & 1, tries);
                 tc_fence_after();
                 // The next block's scores over its first chunk go before the last outputs: they free a chunk's place
                 // in TMEM sooner.  (Of another tile they wait for its queries, which wait for these outputs.)
                 begun = left_tile > 0 && i + 1 < units;
-#pragma unroll 1
+#pragma unroll
                 for (int b = 0; b < kChunks; ++b) {
                     if (b == kChunks - 1 && begun) scores(0);
                     outputs(b, !first);
                 }
             }
-            if (!live) {
+            if (!tries) {
                 sh.abort = 1;
+                tries = kWaitTries;
                 if (elect_one()) mma_commit(smem_addr(&sh.drain));  // nothing may write TMEM once it is freed
-                mbar_wait(smem_addr(&sh.drain), 0);
+                mbar_wait(smem_addr(&sh.drain), 0, tries);
             }
         } else if (warp <= kMmaWarp + kLookupWarps) {
             // Looks up where a block's rows lie and fetches their scales, up to two blocks ahead of the decode warps.
@@ -648,7 +652,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         Cursor<N, kSlots> cur(a, sh);
         Ring<R> ring;
         float l[NC];
-        bool unset = false, live = true;
+        bool unset = false;
+        uint32_t tries = kWaitTries;
         int kb0 = 0;
 #pragma unroll 1
         for (int i = 0; i < units; ++i, cur.next(a)) {
@@ -711,7 +716,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 unset = true;
             }
             // `full` of the block's first chunk orders this thread's read of texp
-            live = live && mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity) && mbar_wait(smem_addr(&sh.sdone), i & 1);
+            mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
+            mbar_wait(smem_addr(&sh.sdone), i & 1, tries);
             tc_fence_after();
             const int te = sh.texp[i & (kLookups - 1)][t_row];
             const bool have = te != kNoToken;
@@ -887,9 +893,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     a.join[blockIdx.x] = join;
                 }
                 soft_sync();
-                live = live && mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity);
+                mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity, tries);
                 tc_fence_after();
-                if (live) {
+                if (tries) {
 #pragma unroll 1
                     for (int b = 2 * half; b < 2 * half + 2; ++b) {
                         const int d = b * kChunk + t_row;
@@ -926,7 +932,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 soft_sync();  // the tile's arrays are free for the next one
             }
         }
-        if (!live) sh.abort = 1;
+        if (!tries) sh.abort = 1;
     }
     __syncwarp();
     if (tid == 0) pdl_trigger();

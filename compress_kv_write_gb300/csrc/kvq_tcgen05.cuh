@@ -14,24 +14,31 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Waits until the phase of the given parity has completed.  The wait is
-// bounded: 2^24 tries, each of which the hardware may suspend for a while (a
-// time-limit operand would make it a sleeping loop, which wakes up late and
-// takes issue slots).  Returns false when it gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < (1 << 24); ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (done) return true;
-    }
-    return false;
+// Waits until the phase of the given parity has completed, with a bound:
+// `tries` tries (2^24 at first), each of which the hardware may suspend for a
+// while.  (A time-limit operand would make it a sleeping loop, which wakes up
+// late.)  A wait that gives up sets `tries` to 0: the caller's further waits
+// then return at once, its loops run through, and the call is reported as
+// failed.  The loop is inside the statement so that the compiler sees no
+// branch, and what follows stays warp-uniform.
+constexpr uint32_t kWaitTries = 1u << 24;
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, uint32_t &tries) {
+    asm volatile(
+        "{\n\t.reg .pred p, z;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %0;\n\t"
+        "WAIT:\n\t"
+        "setp.eq.u32 z, n, 0;\n\t"
+        "@z bra GIVE_UP;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "@!p bra WAIT;\n\t"
+        "bra DONE;\n\t"
+        "GIVE_UP:\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "DONE:\n\t}"
+        : "+r"(tries)
+        : "r"(bar), "r"(parity)
+        : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
