@@ -22,7 +22,9 @@ constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
 // Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
 template <Layout L, int N>
 struct Regs {
-    static constexpr int kSoft = N == 64 ? 112 : 88, kDeq = N == 64 ? 56 : 64, kMma = N == 64 ? 56 : 72;
+    static constexpr int kSoft = N == 64 ? 112 : 88, kDeq = N == 64 ? 56 : L == Layout::V41 ? 72 : 64,
+                         kMma = N == 64 ? 56 : L == Layout::V41 ? 40 : 72;
+    static constexpr int kBufs = L == Layout::V41 && N == 64 ? 1 : 2;  // code buffers a decode thread has room for
     static_assert(2 * kSoft + 4 * kDeq + kMma <= 7 * 72, "a larger sum would wait for ever");
 };
 // How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
@@ -149,7 +151,7 @@ struct Raw {  // 16 codes
 template <Layout L>
 __device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int chunk, int s) {
     Raw<L> r;
-    // volatile: a load stays where it is issued, half a block before its use
+    // volatile: a load stays where it is issued
     if constexpr (L == Layout::V41) {
         asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
@@ -412,10 +414,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
         const uint32_t lane_at = q * (T::kCodeBytes / 32);  // of a chunk's half
 
-        // A chunk's codes are loaded while the other half's chunk is stored, from L2, where the lookup warps have sent
-        // for them.
-        Raw<L> raw[2][2];  // token, half
+        // A chunk's codes are loaded a block ahead (with one buffer: half a block), from L2, where the lookup warps have
+        // sent for them.
+        constexpr int kBufs = Regs<L, N>::kBufs;
+        Raw<L> raws[kBufs][2][2];  // token, half
         auto load = [&](int k, int j) {
+            auto &raw = raws[j % kBufs];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint8_t *p = sh.code[k][tok0 + 8 * h] + lane_at;
@@ -426,6 +430,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         uint32_t tries = kWaitTries;
         mbar_wait(smem_addr(&sh.addr[0]), 0, tries);
         load(0, 0);
+        if (kBufs == 2) load(0, 1);
         // The chunk's slots: R in shared memory, KR in TMEM.
         int slot = group, kslot = group;
         uint32_t parity = 0;
@@ -439,6 +444,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int b = 2 * j + group;
+                auto &raw = raws[j % kBufs];
                 // A slot in shared memory is free when the product over the dims that it held is done.  The chunk that
                 // had the TMEM slot before belongs to the block before, whose scores were done before any of those
                 // products began; except that with three TMEM slots the last chunk follows the block's own first
@@ -482,12 +488,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
-                if (j == 0) {
-                    load(k, 1);
-                } else {
-                    if (i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1, tries);
-                    load(kn, 0);
-                }
+                if (j == kBufs % 2 && i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), ((i + 1) / kLookups) & 1, tries);
+                if (kBufs == 2) load(kn, j);
+                else load(j == 0 ? k : kn, 1 - j);
                 slot += 2;
                 if (slot >= R) {
                     slot -= R;
