@@ -34,13 +34,16 @@ constexpr float kStaleMax = 14.f;
 // Decoded chunks that fit beside N query rows and their weights: a block is four, and what is more lets the next
 // block's first chunks be decoded and multiplied while this one's softmax runs.
 template <int N>
-constexpr int kRing = N == 16 ? 6 : N == 32 ? 5 : 4;
+constexpr int kRing = N == 64 ? 4 : 5;
+// Chunks that TMEM holds for the scores' products, beside the outputs (4 N columns) and one or two blocks' scores.
+template <int N>
+constexpr int kTmemRing = N == 64 ? 3 : kRing<N>;
 constexpr int kNoToken = 0x7FFFFFFF;
-constexpr int kLookups = 3, kLookupWarps = 2;
+constexpr int kLookups = 4, kLookupWarps = 2;
 
 template <int N>
 struct AttendShared {
-    uint64_t full[kRing<N>], oblk[kRing<N>], sdone, pready, qready, drain;
+    uint64_t full[kRing<N>], oblk[kRing<N>], kfree, sdone, pready, qready, drain;
     int64_t scan[kAttendThreads / 32];
     int64_t total, u0;
     int units, start_tile, start_kb;
@@ -134,9 +137,11 @@ struct Ring {
 // (q = lane % 4, s = 0, 1), as two vectors e = 0, 1 of eight: a warp's load
 // touches eight rows, where a thread a token would touch 32 (and take 1.4
 // times as long in all).  In shared memory a chunk is two 128-byte-swizzled
-// tiles of 64 dims, which the scores' product reads as rows of tokens and the
-// outputs' product as rows of dims; the eight lanes of a store's phase (two
-// tokens, four q) hit different banks.
+// tiles of 64 dims; the eight lanes of a store's phase (two tokens, four q)
+// hit different banks.  In TMEM (the A operand of the scores' product) vector
+// e of half s fills the columns 32 s + 16 e + 4 i + q, i = 0..3, two dims a
+// column: the contraction runs over the dims in another order, and q_word()
+// puts a query's dims in the same one.
 template <Layout L>
 struct Raw {  // 16 codes
     uint32_t w[L == Layout::V41 ? 4 : 2];
@@ -222,11 +227,12 @@ __device__ __forceinline__ uint32_t block_mul(uint32_t byte, int texp) {
     return r;
 }
 
-// Byte offset, in a query tile's shared memory, of the 16-byte vector g = 0 ..
-// 63 (eight dims) of row r.
+// Byte offset, in a query tile's shared memory, of word i (dims 8g + 2i,
+// 8g + 2i + 1) of piece g = 0..63 of row r.
 template <int N>
-__device__ __forceinline__ uint32_t q_vec(int r, int g) {
-    return uint32_t((g >> 3) * N * 128 + r * 128 + (((g & 7) ^ (r & 7)) << 4));
+__device__ __forceinline__ uint32_t q_word(int r, int g, int i) {
+    const int b = g >> 4, s = (g >> 3) & 1, q = (g >> 1) & 3, e = g & 1;
+    return uint32_t((2 * b + s) * N * 128 + r * 128 + (((4 * e + i) ^ (r & 7)) << 4) + q * 4);
 }
 
 // Swizzled byte offset of 16-byte vector j of row t of the weights' tile
@@ -301,9 +307,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     using T = LayoutTraits<L>;
     constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
     constexpr int R = kRing<N>;
-    constexpr uint32_t kTmemS = 4 * N;      // outputs before, two blocks' scores from here
-    constexpr uint32_t kTmemCols = 512;     // all of them, which begin at column 0
-    static_assert(6 * N <= 512, "outputs and scores");
+    constexpr int KR = kTmemRing<N>, kScoreBufs = N == 64 ? 1 : 2;
+    // TMEM columns: outputs, scores, chunks of rows
+    constexpr uint32_t kTmemS = 4 * N, kTmemK = (4 + kScoreBufs) * N;
+    constexpr uint32_t kTmemCols = 512;  // all of them, which begin at column 0
+    static_assert(kTmemK + 64 * KR <= kTmemCols, "they fit");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
     uint8_t *const sK = base, *const sQ = sK + R * kChunkSmem, *const sP = sQ + N * kD * 2;
@@ -319,6 +327,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             mbar_init(smem_addr(&sh.full[i]), kDeqWarps / 2);
             mbar_init(smem_addr(&sh.oblk[i]), 1);
         }
+        mbar_init(smem_addr(&sh.kfree), 1);
         mbar_init(smem_addr(&sh.sdone), 1);
         mbar_init(smem_addr(&sh.pready), kSoftWarps);
         mbar_init(smem_addr(&sh.qready), kSoftWarps);
@@ -403,6 +412,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
         const uint32_t krow = smem_addr(sK) + tok0 * 128;
         const uint32_t at0 = krow + (((2 * q) ^ r8) << 4), at1 = krow + (((2 * q + 1) ^ r8) << 4);
+        const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
         const uint32_t lane_at = q * (T::kCodeBytes / 32);  // of a chunk's half
 
         // A chunk's codes are loaded a block ahead (with one buffer: half a block), from L2, where the lookup warps have
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         mbar_wait(smem_addr(&sh.addr[0]), 0, tries);
         load(0, 0);
         if (kBufs == 2) load(0, 1);
-        int slot = group, k = 0;
+        int slot = group, kslot = group, k = 0;
         uint32_t parity = 0, looked = 0;  // `looked`: the phase of the next block's lookup
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
@@ -437,8 +447,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             for (int j = 0; j < 2; ++j) {
                 const int b = 2 * j + group;
                 auto &raw = raws[j % kBufs];
-                // the slot is free when the product over the dims that it held is done
+                // The slot in shared memory is free when the product over the dims that it held is done.  That comes
+                // after the scores over what the TMEM slot held, except that with three of them a block's last chunk
+                // follows its own first one.
+                static_assert(KR == R || (R == kChunks && KR == 3), "what the rings imply");
                 if (i * kChunks + b >= R) mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1, tries);
+                if (KR == 3 && b == 3) mbar_wait(smem_addr(&sh.kfree), i & 1, tries);
+                tc_fence_after();
                 if (!all_ok) {  // a token that is not there has the pool's first row: its codes are cleared
                     asm volatile("");
 #pragma unroll
@@ -464,9 +479,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
                         sts_u4(at, v0);
                         sts_u4(at + 8 * 128, v1);
+                        tmem_st_16x128b_x4(tlane + kslot * 64 + 32 * s + 16 * e, v0, v1);
                     }
                 }
                 fence_proxy_async();
+                tc_wait_st();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
                 if (j == kBufs % 2 && i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), looked, tries);
@@ -477,6 +495,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     slot -= R;
                     parity ^= 1;
                 }
+                kslot += 2;
+                if (kslot >= KR) kslot -= KR;
             }
             if (warp == kSoftWarps && lane == 0) *const_cast<volatile int *>(&sh.progress) = i + 1;
             k = kn;
@@ -489,25 +509,29 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             constexpr uint32_t kIdescS = mma_idesc(kTile, N, false, false);
             constexpr uint32_t kIdescO = mma_idesc(kTile, N, true, true);
             constexpr uint32_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
-            const uint32_t qd = desc_lo(smem_addr(sQ), 16), vd = desc_lo(smem_addr(sK), kSubBytes), kd = desc_lo(smem_addr(sK), 16), pd = desc_lo(smem_addr(sP), 16);
+            const uint32_t qd = desc_lo(smem_addr(sQ), 16), vd = desc_lo(smem_addr(sK), kSubBytes),  pd = desc_lo(smem_addr(sP), 16);
             constexpr uint32_t kQHi = desc_hi(1024, kSwizzle128), kVHi = kQHi, kPHi = desc_hi(16 * N, kPSwizzle);
             int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
             uint32_t seg = 0;
+            int kslot = 0;
             uint32_t tries = kWaitTries;
             Ring<R> sr, vr;
             // scores over chunk b of block i
             auto scores = [&](int i, int b) {
                 mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity, tries);
+                tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kd + ((sr.slot * kChunkSmem) >> 4);
+                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), to = kTmemS + (kScoreBufs == 2 ? (i & 1) * N : 0),
+                                   from = kTmemK + kslot * 64;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ss(kTmemS + (i & 1) * N, from + (((k >> 2) * kSubBytes + (k & 3) * 32) >> 4), kQHi,
-                               at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS, b + k > 0);
+                        mma_ts(to, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS, b + k > 0);
+                    if (KR == 3 && b == 0) mma_commit(smem_addr(&sh.kfree));
                     if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
                 }
                 __syncwarp();
                 sr.next();
+                if (++kslot == KR) kslot = 0;
             };
             // outputs of dims 128 b .. 128 b + 127
             auto outputs = [&](int b, bool add) {
@@ -521,8 +545,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 __syncwarp();
                 vr.next();
             };
-            constexpr int kEarly = R - kChunks;
-            bool begun = false;  // whether the block's scores over its first kEarly chunks are under way
+            // The next block's scores over its first chunks are begun early, if it is of the same tile (another tile's
+            // wait for its queries, and those for this block's outputs): with two score buffers while the softmax
+            // runs, over as many chunks as the ring is longer than a block; with one, over one chunk before the last
+            // outputs, which frees that chunk's place in TMEM sooner.
+            constexpr int kEarly = kScoreBufs == 2 ? R - kChunks : 1;
+            bool begun = false;
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
                 bool first = false;
@@ -541,16 +569,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     for (int b = 0; b < kEarly; ++b) scores(i, b);
 #pragma unroll
                 for (int b = kEarly; b < kChunks; ++b) scores(i, b);
-                // While the softmax runs: the next block's first scores, if it is of the same tile (another tile's wait
-                // for its queries, and those for this block's outputs).
-                begun = kEarly > 0 && left_tile > 0 && i + 1 < units;
-                if (begun)
+                begun = left_tile > 0 && i + 1 < units;
+                if (kScoreBufs == 2 && begun)
 #pragma unroll
                     for (int b = 0; b < kEarly; ++b) scores(i + 1, b);
                 mbar_wait(smem_addr(&sh.pready), i & 1, tries);
                 tc_fence_after();
 #pragma unroll
-                for (int b = 0; b < kChunks; ++b) outputs(b, !first);
+                for (int b = 0; b < kChunks; ++b) {
+                    if (kScoreBufs == 1 && b == kChunks - 1 && begun) scores(i + 1, 0);
+                    outputs(b, !first);
+                }
             }
             if (!tries) {
                 sh.abort = 1;
@@ -683,12 +712,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         const uint32_t up = min(268u - (big >> 23), 254u);
                         const float f = __uint_as_float(up << 23);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v[t][e]) : "f"(bf16_hi(v[t][e]) * f), "f"(bf16_lo(v[t][e]) * f));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t four[4] = {v[t][4 * h], v[t][4 * h + 1], v[t][4 * h + 2], v[t][4 * h + 3]};
-                            sts_u4(sq + q_vec<N>(r, lane + 32 * h), four);
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t h;
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[t][e]) * f), "f"(bf16_lo(v[t][e]) * f));
+                            sts_u32(sq + q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
                         }
                         if (lane == 0) sh.sc[r] = c * ue8m0_to_f32(254u - up);
                     }
@@ -719,7 +746,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             bool odd = false;  // a score that is not finite, where some rows do not see the token
             auto scores = [&]() {
                 uint32_t sraw[NC];
-                tmem_ld<NC>(trow + kTmemS + (i & 1) * N + c0, sraw);
+                tmem_ld<NC>(trow + kTmemS + (kScoreBufs == 2 ? (i & 1) * N : 0) + c0, sraw);
 #pragma unroll
                 for (int j = 0; j < NC; j += 4) {
                     const float4 k = *reinterpret_cast<const float4 *>(&sh.sc[c0 + j]);
@@ -932,78 +959,81 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }
 
-// Joins the tiles that CTAs split: CTA (x, y) takes rows 4y .. 4y + 3 of the
-// tile whose first part CTA x made, four warps a row.  The parts go round the
-// row's warps, each weighted by 2^(its maximum - the largest), and the warps'
-// sums are added in order.
-constexpr int kJoinRows = 4, kJoinWays = 4, kJoinThreads = kJoinRows * kJoinWays * 32;
+// Joins the tiles that CTAs split.  Every CTA lists the `ctas` shares' split
+// tiles, and the warps of the grid go round (tile, query row, quarter of the
+// dims): a warp adds the parts of 128 dims in order, each weighted by 2^(its
+// maximum - the largest so far), with eight parts' loads in flight.
+constexpr int kJoinThreads = 512, kJoinBatch = 8;
 
 template <int N>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-    __shared__ __align__(16) float sums[kJoinRows][kJoinWays][kD];
-    __shared__ float weights[kJoinRows][kJoinWays];
+__global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const __grid_constant__ AttendArgs a, int ctas) {
+    __shared__ int3 split[kMaxAttendCtas];  // first CTA, its tile, last CTA
+    __shared__ int counts[kJoinThreads / 32];
+    static_assert(kMaxAttendCtas <= kJoinThreads, "a thread a share");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
-    const int2 join = a.join[blockIdx.x];
-    if (join.x < 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r4 = warp / kJoinWays, way = warp % kJoinWays;
-    const int r = blockIdx.y * kJoinRows + r4;
-    const int per = a.q_len * a.heads;
-    const int seq = join.x / a.row_tiles, R = join.x % a.row_tiles * N + r;
-    const int parts = join.y - int(blockIdx.x) + 1;
-    auto at = [&](int i) {
-        return a.part + ((i == 0 ? 2 * int64_t(blockIdx.x) + 1 : 2 * (int64_t(blockIdx.x) + i)) * N + r) * kPartRow;
-    };
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldg(at(i) + kD));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float zero = top == -INFINITY ? 0.f : top;
-    float acc[16], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = way; i < parts; i += kJoinWays) {
-        const float *p = at(i);
-        const float2 ml = __ldg(reinterpret_cast<const float2 *>(p + kD));
-        float4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __ldg(reinterpret_cast<const float4 *>(p + 128 * k + 4 * lane));
-        const float w = ex2_approx(ml.x - zero);
-        sum = fmaf(w, ml.y, sum);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            acc[4 * k] = fmaf(w, v[k].x, acc[4 * k]);
-            acc[4 * k + 1] = fmaf(w, v[k].y, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(w, v[k].z, acc[4 * k + 2]);
-            acc[4 * k + 3] = fmaf(w, v[k].w, acc[4 * k + 3]);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<float4 *>(&sums[r4][way][128 * k + 4 * lane]) =
-            make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
-    if (lane == 0) weights[r4][way] = sum;
+    const int2 join = tid < ctas ? a.join[tid] : make_int2(-1, 0);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, join.x >= 0);
+    if (lane == 0) counts[warp] = __popc(some);
     __syncthreads();
-    if (R >= per) return;
-    // warp `way` of a row finishes dims 128 way ..
-    static_assert(kJoinWays * 128 == kD, "a warp finishes 128 dims");
-    float4 v = *reinterpret_cast<const float4 *>(&sums[r4][0][128 * way + 4 * lane]);
-    sum = weights[r4][0];
+    int before = 0, n = 0;
 #pragma unroll
-    for (int w = 1; w < kJoinWays; ++w) {
-        const float4 u = *reinterpret_cast<const float4 *>(&sums[r4][w][128 * way + 4 * lane]);
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        sum += weights[r4][w];
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        if (w < warp) before += counts[w];
+        n += counts[w];
     }
-    const float inv = top == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
-    const int j = R / a.heads;
-    const int64_t row = (int64_t(seq) * a.q_len + j) * a.out_tok + (R - j * a.heads) * a.out_head + 128 * way + 4 * lane;
-    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-    if (a.out_bf16)
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    else
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row) = v;
-    if (a.lse && way == 0 && lane == 0) a.lse[int64_t(seq) * per + R] = attend_lse(top, sum);
+    if (join.x >= 0) split[before + __popc(some & ((1u << lane) - 1))] = make_int3(tid, join.x, join.y);
+    __syncthreads();
+    const int per = a.q_len * a.heads;
+    const int warps = gridDim.x * (kJoinThreads / 32);
+    for (int item = blockIdx.x * (kJoinThreads / 32) + warp; item < n * N * 4; item += warps) {
+        const int3 s = split[item / (4 * N)];
+        const int r = item / 4 % N, d = item % 4 * 128 + 4 * lane;
+        const int seq = s.y / a.row_tiles, row = s.y % a.row_tiles * N + r;
+        if (row >= per) continue;
+        const int parts = s.z - s.x + 1;
+        auto at = [&](int i) {
+            return a.part + ((i == 0 ? 2 * int64_t(s.x) + 1 : 2 * (int64_t(s.x) + i)) * N + r) * kPartRow;
+        };
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < parts; i0 += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 v[kJoinBatch];
+            float to = top;
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + k < parts) {
+                    ml[k] = __ldg(reinterpret_cast<const float2 *>(at(i0 + k) + kD));
+                    v[k] = __ldg(reinterpret_cast<const float4 *>(at(i0 + k) + d));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) to = fmaxf(to, ml[k].x);
+            const float zero = to == -INFINITY ? 0.f : to;
+            const float keep = ex2_approx(top - zero);   // of nothing: 0
+            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep, sum *= keep;
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                const float w = ex2_approx(ml[k].x - zero);
+                sum = fmaf(w, ml[k].y, sum);
+                acc.x = fmaf(w, v[k].x, acc.x), acc.y = fmaf(w, v[k].y, acc.y);
+                acc.z = fmaf(w, v[k].z, acc.z), acc.w = fmaf(w, v[k].w, acc.w);
+            }
+            top = to;
+        }
+        const float inv = top == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
+        const int j = row / a.heads;
+        const int64_t to = (int64_t(seq) * a.q_len + j) * a.out_tok + (row - j * a.heads) * a.out_head + d;
+        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+        if (a.out_bf16)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to) = acc;
+        if (a.lse && item % 4 == 0 && lane == 0) a.lse[int64_t(seq) * per + row] = attend_lse(top, sum);
+    }
 }
 
 template <Layout L, int N, bool kSlots>
@@ -1023,7 +1053,7 @@ kvq_status launch_attend_n(AttendArgs a, cudaStream_t s) {
     a.part = reinterpret_cast<float *>(a.ws + kMaxAttendCtas * sizeof(int2));
     st = launch_pdl_smem(attend_kernel<L, N, kSlots>, dim3(unsigned(grid)), dim3(kAttendThreads), kAttendSmem<N>, s, a);
     if (st != KVQ_OK || most <= 1) return st;  // a tile of one block is never split
-    return launch_pdl(attend_join_kernel<N>, dim3(unsigned(grid), N / kJoinRows), dim3(kJoinThreads), s, a);
+    return launch_pdl(attend_join_kernel<N>, dim3(unsigned(2 * grid)), dim3(kJoinThreads), s, a, int(grid));
 }
 
 template <Layout L, bool kSlots>

@@ -22,7 +22,6 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // failed.  The loop is inside the statement so that the compiler sees no
 // branch, and what follows stays warp-uniform.
 constexpr uint32_t kWaitTries = 1u << 24;
-template <int kSleepNs = 0>
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, uint32_t &tries) {
     asm volatile(
         "{\n\t.reg .pred p, z;\n\t.reg .u32 n;\n\t"
@@ -32,14 +31,13 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, uint32_
         "@z bra GIVE_UP;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "sub.u32 n, n, 1;\n\t"
-        "@p bra DONE;\n\t"
-        "nanosleep.u32 %3;\n\t"
-        "bra WAIT;\n\t"
+        "@!p bra WAIT;\n\t"
+        "bra DONE;\n\t"
         "GIVE_UP:\n\t"
         "mov.u32 %0, 0;\n\t"
         "DONE:\n\t}"
         : "+r"(tries)
-        : "r"(bar), "r"(parity), "n"(kSleepNs)
+        : "r"(bar), "r"(parity)
         : "memory");
 }
 
@@ -97,6 +95,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
         : "memory");
 }
+// 16 lanes x 16 columns: thread l writes column 4i + l % 4 of lanes l / 4 (a[i]) and l / 4 + 8 (b[i]).
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t addr, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(a[0]), "r"(b[0]),
+                 "r"(a[1]), "r"(b[1]), "r"(a[2]), "r"(b[2]), "r"(a[3]), "r"(b[3]), "r"(addr)
+                 : "memory");
+}
+
 // Halves of a shared-memory matrix descriptor (addresses and strides in
 // bytes, multiples of 16).  A step along the operand adds (bytes >> 4) to the
 // low half.
@@ -128,6 +133,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
         "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
         "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+// The same with A in TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(uint32_t(accumulate))
         : "memory");
 }
 // Arrives on the mbarrier when every MMA this thread has issued so far is done.
