@@ -22,8 +22,7 @@ constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
 // Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
 template <Layout L, int N>
 struct Regs {
-    static constexpr int kSoft = N == 64 ? 112 : 88, kDeq = N == 64 ? 56 : L == Layout::V41 ? 72 : 64,
-                         kMma = N == 64 ? 56 : L == Layout::V41 ? 40 : 72;
+    static constexpr int kSoft = N == 64 ? 112 : 80, kDeq = N == 64 ? 56 : 72, kMma = 56;
     static constexpr int kBufs = L == Layout::V41 && N == 64 ? 1 : 2;  // code buffers a decode thread has room for
     static_assert(2 * kSoft + 4 * kDeq + kMma <= 7 * 72, "a larger sum would wait for ever");
 };
@@ -32,10 +31,10 @@ struct Regs {
 constexpr float kStaleMax = 14.f;
 
 // Decoded chunks that fit beside N query rows and their weights: a block is four, and what is more lets the next
-// block's first chunks be decoded and multiplied while this one's softmax runs.
+// block's first chunk be decoded while this one's softmax runs.
 template <int N>
 constexpr int kRing = N == 64 ? 4 : 5;
-// Chunks that TMEM holds for the scores' products, beside the outputs (4 N columns) and one or two blocks' scores.
+// Chunks that TMEM holds for the scores' products, beside the outputs (4 N columns) and the scores (N).
 template <int N>
 constexpr int kTmemRing = N == 64 ? 3 : kRing<N>;
 constexpr int kNoToken = 0x7FFFFFFF;
@@ -307,9 +306,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     using T = LayoutTraits<L>;
     constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
     constexpr int R = kRing<N>;
-    constexpr int KR = kTmemRing<N>, kScoreBufs = N == 64 ? 1 : 2;
+    constexpr int KR = kTmemRing<N>;
     // TMEM columns: outputs, scores, chunks of rows
-    constexpr uint32_t kTmemS = 4 * N, kTmemK = (4 + kScoreBufs) * N;
+    constexpr uint32_t kTmemS = 4 * N, kTmemK = 5 * N;
     constexpr uint32_t kTmemCols = 512;  // all of them, which begin at column 0
     static_assert(kTmemK + 64 * KR <= kTmemCols, "they fit");
     extern __shared__ uint8_t smem_raw[];
@@ -516,16 +515,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             int kslot = 0;
             uint32_t tries = kWaitTries;
             Ring<R> sr, vr;
-            // scores over chunk b of block i
-            auto scores = [&](int i, int b) {
+            // scores over chunk b of a block
+            auto scores = [&](int b) {
                 mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity, tries);
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), to = kTmemS + (kScoreBufs == 2 ? (i & 1) * N : 0),
-                                   from = kTmemK + kslot * 64;
+                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(to, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS, b + k > 0);
+                        mma_ts(kTmemS, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS, b + k > 0);
                     if (KR == 3 && b == 0) mma_commit(smem_addr(&sh.kfree));
                     if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
                 }
@@ -545,12 +543,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 __syncwarp();
                 vr.next();
             };
-            // The next block's scores over its first chunks are begun early, if it is of the same tile (another tile's
-            // wait for its queries, and those for this block's outputs): with two score buffers while the softmax
-            // runs, over as many chunks as the ring is longer than a block; with one, over one chunk before the last
-            // outputs, which frees that chunk's place in TMEM sooner.
-            constexpr int kEarly = kScoreBufs == 2 ? R - kChunks : 1;
-            bool begun = false;
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
                 bool first = false;
@@ -564,22 +556,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     ++seg;
                 }
                 --left_tile;
-                if (!begun)
 #pragma unroll
-                    for (int b = 0; b < kEarly; ++b) scores(i, b);
-#pragma unroll
-                for (int b = kEarly; b < kChunks; ++b) scores(i, b);
-                begun = left_tile > 0 && i + 1 < units;
-                if (kScoreBufs == 2 && begun)
-#pragma unroll
-                    for (int b = 0; b < kEarly; ++b) scores(i + 1, b);
+                for (int b = 0; b < kChunks; ++b) scores(b);
                 mbar_wait(smem_addr(&sh.pready), i & 1, tries);
                 tc_fence_after();
 #pragma unroll
-                for (int b = 0; b < kChunks; ++b) {
-                    if (kScoreBufs == 1 && b == kChunks - 1 && begun) scores(i + 1, 0);
-                    outputs(b, !first);
-                }
+                for (int b = 0; b < kChunks; ++b) outputs(b, !first);
             }
             if (!tries) {
                 sh.abort = 1;
@@ -617,9 +599,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     }
                 }
             };
+            fetch();
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
-                fetch();
                 const uint8_t *row[K];
                 uint4 sc[K];
                 uint32_t good = 0;
@@ -640,6 +622,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     if constexpr (L == Layout::V41)
                         asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(sink) : "l"(row[j] + 256));
                 }
+                if (i > 0) {  // the next block's indexes, while the scales come
+                    cur.next(a);
+                    fetch();
+                }
                 // wait until the entries are free (every reader of block i - kLookups is done)
                 for (int tries = 0; progress < i - (kLookups - 2) && tries < (1 << 22); ++tries) __nanosleep(64);
                 const int k = i % kLookups;
@@ -651,7 +637,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.addr[k]));
-                cur.next(a);
+                if (i == 0) {  // the first block has gone out first
+                    cur.next(a);
+                    fetch();
+                }
             }
         }
     } else {
@@ -746,7 +735,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             bool odd = false;  // a score that is not finite, where some rows do not see the token
             auto scores = [&]() {
                 uint32_t sraw[NC];
-                tmem_ld<NC>(trow + kTmemS + (kScoreBufs == 2 ? (i & 1) * N : 0) + c0, sraw);
+                tmem_ld<NC>(trow + kTmemS + c0, sraw);
 #pragma unroll
                 for (int j = 0; j < NC; j += 4) {
                     const float4 k = *reinterpret_cast<const float4 *>(&sh.sc[c0 + j]);
