@@ -9,40 +9,39 @@
 namespace kvq {
 namespace {
 
-constexpr int kTile = 128;   // cached tokens a block
+constexpr int kTile = 64;    // cached tokens a block
 constexpr int kChunk = 128;  // dims a step of decoding
 constexpr int kChunks = kD / kChunk;
 constexpr int kSubBytes = kTile * 128;         // 64 dims of a block, 128 B a token
 constexpr int kChunkSmem = 2 * kSubBytes;
-// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-23 decode (8-15 the even chunks, 16-23 the
-// odd ones, so that one half's stores overlap the other's waits), 24 products, 25 and 26 look up where the rows of
-// coming blocks lie, 27 completes the warpgroup.
+// Warps: 0-7 softmax (two a TMEM lane quarter, each half of the columns), 8-23 decode (four a chunk, so that one
+// chunk's stores overlap the others' waits), 24 the scores' products, 25 and 26 look up where the rows of coming blocks
+// lie, 27 the outputs' products.
 constexpr int kSoftWarps = 8, kDeqWarps = 16, kMmaWarp = kSoftWarps + kDeqWarps;
 constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
 // Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
 template <Layout L, int N>
 struct Regs {
-    static constexpr int kSoft = N == 64 ? 112 : 80, kDeq = N == 64 ? 56 : 72, kMma = 56;
-    static constexpr int kBufs = L == Layout::V41 && N == 64 ? 1 : 2;  // code buffers a decode thread has room for
+    static constexpr int kSoft = 104, kDeq = 64, kMma = 40;
     static_assert(2 * kSoft + 4 * kDeq + kMma <= 7 * 72, "a larger sum would wait for ever");
 };
 // How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
 // (which rescales the outputs in TMEM) is rare after a tile's first block.
 constexpr float kStaleMax = 14.f;
 
-// Decoded chunks that fit beside N query rows and their weights: a block is four, and what is more lets the next
-// block's first chunk be decoded while this one's softmax runs.
+// Decoded chunks: two blocks (a block is four), so that one is decoded while the other is multiplied.
+constexpr int kRing = 2 * kChunks;
+// Chunks that TMEM holds for the scores' products, beside the outputs (4 N columns) and one or two blocks' scores.
 template <int N>
-constexpr int kRing = N == 64 ? 4 : 5;
-// Chunks that TMEM holds for the scores' products, beside the outputs (4 N columns) and the scores (N).
+constexpr int kTmemRing = N == 64 ? 3 : N == 32 ? 5 : 6;
 template <int N>
-constexpr int kTmemRing = N == 64 ? 3 : kRing<N>;
+constexpr int kScoreBufs = N == 64 ? 1 : 2;
 constexpr int kNoToken = 0x7FFFFFFF;
-constexpr int kLookups = 4, kLookupWarps = 2;
+constexpr int kLookups = 6, kLookupWarps = 2;
 
 template <int N>
 struct AttendShared {
-    uint64_t full[kRing<N>], oblk[kRing<N>], kfree, sdone, pready, qready, drain;
+    uint64_t full[kRing], oblk[kRing], kfree[kTmemRing<N>], sdone[2], sread[2], pready[2], qready, drain[2];
     int64_t scan[kAttendThreads / 32];
     int64_t total, u0;
     int units, start_tile, start_kb;
@@ -60,12 +59,12 @@ struct AttendShared {
 };
 
 template <int N>
-constexpr size_t kAttendSmem = 1024 + size_t(kRing<N>) * kChunkSmem + size_t(N) * kD * 2 + size_t(kTile) * N * 2 +
+constexpr size_t kAttendSmem = 1024 + size_t(kRing) * kChunkSmem + size_t(N) * kD * 2 + 2 * size_t(kTile) * N * 2 +
                                sizeof(AttendShared<N>);
 static_assert(kAttendSmem<16> <= 232448 && kAttendSmem<32> <= 232448 && kAttendSmem<64> <= 232448, "227 KB a CTA");
 
 // Tiles are N query rows of a sequence (row = query token * heads + head);
-// a tile's blocks are the 128-token pieces of what its last query token sees.
+// a tile's blocks are the 64-token pieces of what its last query token sees.
 struct TileInfo {
     int seq, rt, len, seen, nb;  // cached tokens, tokens the last row sees, blocks (at least one)
     int trow, err;
@@ -132,31 +131,32 @@ struct Ring {
 };
 
 // Where a decoded row lies.  A decode thread holds, of tokens r and r + 8
-// (r = lane / 4) and of a chunk of 128 dims, the 16 dims from 64 s + 16 q
-// (q = lane % 4, s = 0, 1), as two vectors e = 0, 1 of eight: a warp's load
-// touches eight rows, where a thread a token would touch 32 (and take 1.4
-// times as long in all).  In shared memory a chunk is two 128-byte-swizzled
-// tiles of 64 dims; the eight lanes of a store's phase (two tokens, four q)
-// hit different banks.  In TMEM (the A operand of the scores' product) vector
-// e of half s fills the columns 32 s + 16 e + 4 i + q, i = 0..3, two dims a
-// column: the contraction runs over the dims in another order, and q_word()
-// puts a query's dims in the same one.
+// (r = lane / 4) of its warp's 16 and of its chunk of 128 dims, the 16 dims
+// from 64 s + 16 q (q = lane % 4, s = 0, 1), as two vectors e = 0, 1 of eight:
+// a warp's load touches eight rows, where a thread a token would touch 32 (and
+// take 1.4 times as long in all).  In shared memory a chunk is two
+// 128-byte-swizzled tiles of 64 dims; the eight lanes of a store's phase (two
+// tokens, four q) hit different banks.  In TMEM (the A operand of the scores'
+// product) a block's 64 rows are the first 16 lanes of each of the four lane
+// quarters, and vector e of half s fills the columns 32 s + 16 e + 4 i + q,
+// i = 0..3, two dims a column: the contraction runs over the dims in another
+// order, and q_word() puts a query's dims in the same one.
 template <Layout L>
 struct Raw {  // 16 codes
     uint32_t w[L == Layout::V41 ? 4 : 2];
 };
 
-// p: the thread's first code of the row.
+// p: the thread's first code of the chunk.
 template <Layout L>
-__device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int chunk, int s) {
+__device__ __forceinline__ Raw<L> load_raw(const uint8_t *p, int s) {
     Raw<L> r;
     // volatile: a load stays where it is issued
     if constexpr (L == Layout::V41) {
         asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-                     : "l"(p + chunk * 128 + s * 64));
+                     : "l"(p + s * 64));
     } else {
-        asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p + chunk * 64 + s * 32));
+        asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p + s * 32));
     }
     return r;
 }
@@ -242,35 +242,16 @@ __device__ __forceinline__ uint32_t p_vec(int t, int j) {
     return uint32_t(t * N * 2 + ((j ^ x) << 4));
 }
 
-// Sums NC values a thread over the warp, lane-transposing; v[0] becomes the
-// total of the returned column (each column in 32 / NC lanes).
-template <int NC>
-__device__ __forceinline__ int warp_columns_sum(float (&v)[NC], int lane) {
-    int col = 0;
-    int half = NC / 2;
+// Over the eight lanes that differ in lane / 4.
+__device__ __forceinline__ float rows_max(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        if (half >= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int i = 0; i < NC / 2; ++i)
-                if (i < half) {
-                    const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
-                    v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
-                }
-            if (up) col += half;
-            half >>= 1;
-        } else {
-            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
-        }
-    }
-    return col;
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
 }
-
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
+__device__ __forceinline__ float rows_sum(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
 // Barrier of the softmax warps; the second form returns whether any of
@@ -305,16 +286,16 @@ template <Layout L, int N, bool kSlots>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using T = LayoutTraits<L>;
     constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
-    constexpr int R = kRing<N>;
-    constexpr int KR = kTmemRing<N>;
+    constexpr int R = kRing;
+    constexpr int KR = kTmemRing<N>, kBufs = kScoreBufs<N>;
     // TMEM columns: outputs, scores, chunks of rows
-    constexpr uint32_t kTmemS = 4 * N, kTmemK = 5 * N;
+    constexpr uint32_t kTmemS = 4 * N, kTmemK = (4 + kBufs) * N;
     constexpr uint32_t kTmemCols = 512;  // all of them, which begin at column 0
     static_assert(kTmemK + 64 * KR <= kTmemCols, "they fit");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
     uint8_t *const sK = base, *const sQ = sK + R * kChunkSmem, *const sP = sQ + N * kD * 2;
-    auto &sh = *reinterpret_cast<AttendShared<N> *>(sP + kTile * N * 2);
+    auto &sh = *reinterpret_cast<AttendShared<N> *>(sP + 2 * kTile * N * 2);
     // shuffled, so that the compiler knows it to be the same for a warp's lanes
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
@@ -323,14 +304,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     if (tid == 0) {
         for (int i = 0; i < kLookups; ++i) mbar_init(smem_addr(&sh.addr[i]), kLookupWarps);
         for (int i = 0; i < R; ++i) {
-            mbar_init(smem_addr(&sh.full[i]), kDeqWarps / 2);
+            mbar_init(smem_addr(&sh.full[i]), kDeqWarps / kChunks);
             mbar_init(smem_addr(&sh.oblk[i]), 1);
         }
-        mbar_init(smem_addr(&sh.kfree), 1);
-        mbar_init(smem_addr(&sh.sdone), 1);
-        mbar_init(smem_addr(&sh.pready), kSoftWarps);
+        for (int i = 0; i < KR; ++i) mbar_init(smem_addr(&sh.kfree[i]), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.sread[i]), kSoftWarps);
+            mbar_init(smem_addr(&sh.sdone[i]), 1);
+            mbar_init(smem_addr(&sh.pready[i]), kSoftWarps);
+        }
         mbar_init(smem_addr(&sh.qready), kSoftWarps);
-        mbar_init(smem_addr(&sh.drain), 1);
+        mbar_init(smem_addr(&sh.drain[0]), 1);
+        mbar_init(smem_addr(&sh.drain[1]), 1);
         sh.abort = sh.progress = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -407,96 +392,92 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
         if constexpr (Regs<L, N>::kDeq < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kDeq));
-        const int w = (warp - kSoftWarps) & 7, group = (warp - kSoftWarps) >> 3, q = lane & 3, r8 = lane >> 2;
-        const int tok0 = 32 * (w & 3) + 16 * (w >> 2) + r8;  // and tok0 + 8
+        const int quarter = warp & 3, chunk = (warp - kSoftWarps) >> 2, q = lane & 3, r8 = lane >> 2;
+        const int tok0 = 16 * quarter + r8;  // and tok0 + 8
         const uint32_t krow = smem_addr(sK) + tok0 * 128;
         const uint32_t at0 = krow + (((2 * q) ^ r8) << 4), at1 = krow + (((2 * q + 1) ^ r8) << 4);
-        const uint32_t tlane = kTmemK + ((32 * (w & 3) + 16 * (w >> 2)) << 16);
-        const uint32_t lane_at = q * (T::kCodeBytes / 32);  // of a chunk's half
+        const uint32_t tlane = kTmemK + ((32 * quarter) << 16);
+        const uint32_t lane_at = q * (T::kCodeBytes / 32) + chunk * (T::kCodeBytes / kChunks);
+        const int scale_at = 4 * chunk + (q >> 1);  // and 2 further for the second half
 
-        // A chunk's codes are loaded a block ahead (with one buffer: half a block), from L2, where the lookup warps have
-        // sent for them.
-        constexpr int kBufs = Regs<L, N>::kBufs;
-        Raw<L> raws[kBufs][2][2];  // token, half
-        auto load = [&](int k, int j) {
-            auto &raw = raws[j % kBufs];
+        // A chunk's codes are loaded a block ahead, from L2, where the lookup warps have sent for them.
+        Raw<L> raw[2][2];  // token, half
+        auto load = [&](int k) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint8_t *p = sh.code[k][tok0 + 8 * h] + lane_at;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int s = 0; s < 2; ++s) raw[h][s] = load_raw<L>(p, 2 * j + group, s);
-            }
+                for (int s = 0; s < 2; ++s) raw[h][s] = load_raw<L>(sh.code[k][tok0 + 8 * h] + lane_at, s);
         };
         uint32_t tries = kWaitTries;
         mbar_wait(smem_addr(&sh.addr[0]), 0, tries);
-        load(0, 0);
-        if (kBufs == 2) load(0, 1);
-        int slot = group, kslot = group, k = 0;
-        uint32_t parity = 0, looked = 0;  // `looked`: the phase of the next block's lookup
+        load(0);
+        int slot = chunk, kslot = chunk, k = 0;
+        uint32_t parity = 0, kparity = 0, looked = 0;  // `looked`: the phase of the next block's lookup
+        if (kslot >= KR) {
+            kslot -= KR;
+            kparity = 1;
+        }
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
             // the next block's entries (of the last block: its own again)
             const int kn = i + 1 == units ? k : k + 1 == kLookups ? 0 : k + 1;
             if (kn == 0 && i > 0) looked ^= 1;
             int texp[2];
+            uint32_t m[2][2];  // token, half
 #pragma unroll
-            for (int h = 0; h < 2; ++h) texp[h] = sh.texp[k][tok0 + 8 * h];
-            const bool all_ok = __all_sync(0xFFFFFFFFu, texp[0] != kNoToken && texp[1] != kNoToken);
+            for (int h = 0; h < 2; ++h) {
+                texp[h] = sh.texp[k][tok0 + 8 * h];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int b = 2 * j + group;
-                auto &raw = raws[j % kBufs];
-                // The slot in shared memory is free when the product over the dims that it held is done.  That comes
-                // after the scores over what the TMEM slot held, except that with three of them a block's last chunk
-                // follows its own first one.
-                static_assert(KR == R || (R == kChunks && KR == 3), "what the rings imply");
-                if (i * kChunks + b >= R) mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1, tries);
-                if (KR == 3 && b == 3) mbar_wait(smem_addr(&sh.kfree), i & 1, tries);
-                tc_fence_after();
-                if (!all_ok) {  // a token that is not there has the pool's first row: its codes are cleared
-                    asm volatile("");
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-#pragma unroll
-                            for (int x = 0; x < int(sizeof(Raw<L>) / 4); ++x)
-                                raw[h][s].w[x] = texp[h] != kNoToken ? raw[h][s].w[x] : 0u;
-                }
-                const uint32_t off = slot * kChunkSmem;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    uint32_t m[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        m[h] = block_mul<L>(reinterpret_cast<const uint8_t *>(&sh.scale[k][tok0 + 8 * h])[4 * b + 2 * s + (q >> 1)], texp[h]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t v0[4], v1[4];
-                        decode8<L>(raw[0][s], e, m[0], v0);
-                        decode8<L>(raw[1][s], e, m[1], v1);
-                        const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
-                        sts_u4(at, v0);
-                        sts_u4(at + 8 * 128, v1);
-                        tmem_st_16x128b_x4(tlane + kslot * 64 + 32 * s + 16 * e, v0, v1);
-                    }
-                }
-                fence_proxy_async();
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
-                if (j == kBufs % 2 && i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), looked, tries);
-                if (kBufs == 2) load(kn, j);
-                else load(j == 0 ? k : kn, 1 - j);
-                slot += 2;
-                if (slot >= R) {
-                    slot -= R;
-                    parity ^= 1;
-                }
-                kslot += 2;
-                if (kslot >= KR) kslot -= KR;
+                for (int s = 0; s < 2; ++s)
+                    m[h][s] = block_mul<L>(reinterpret_cast<const uint8_t *>(&sh.scale[k][tok0 + 8 * h])[scale_at + 2 * s], texp[h]);
             }
+            if (!__all_sync(0xFFFFFFFFu, texp[0] != kNoToken && texp[1] != kNoToken)) {
+                asm volatile("");  // a token that is not there has the pool's first row: its codes are cleared
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int x = 0; x < int(sizeof(Raw<L>) / 4); ++x)
+                            raw[h][s].w[x] = texp[h] != kNoToken ? raw[h][s].w[x] : 0u;
+            }
+            // a slot in shared memory is free when the product over the dims that it held is done, one in TMEM when
+            // the scores over them are
+            if (i * kChunks + chunk >= R) mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1, tries);
+            if (i * kChunks + chunk >= KR) mbar_wait(smem_addr(&sh.kfree[kslot]), kparity ^ 1, tries);
+            tc_fence_after();
+            const uint32_t off = slot * kChunkSmem;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t v0[4], v1[4];
+                    decode8<L>(raw[0][s], e, m[0][s], v0);
+                    decode8<L>(raw[1][s], e, m[1][s], v1);
+                    const uint32_t at = (e ? at1 : at0) + off + s * kSubBytes;
+                    sts_u4(at, v0);
+                    sts_u4(at + 8 * 128, v1);
+                    tmem_st_16x128b_x4(tlane + kslot * 64 + 32 * s + 16 * e, v0, v1);
+                }
+            fence_proxy_async();
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
+            if (i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), looked, tries);
+            load(kn);
+            slot += kChunks;
+            if (slot >= R) {
+                slot -= R;
+                parity ^= 1;
+            }
+            kslot += kChunks;
+#pragma unroll
+            for (int wrap = 0; wrap < (kChunks + KR - 1) / KR; ++wrap)
+                if (kslot >= KR) {
+                    kslot -= KR;
+                    kparity ^= 1;
+                }
             if (warp == kSoftWarps && lane == 0) *const_cast<volatile int *>(&sh.progress) = i + 1;
             k = kn;
         }
@@ -505,70 +486,86 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         // ------------------------------------------------------ products
         if constexpr (Regs<L, N>::kMma < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kMma));
         if (warp == kMmaWarp) {
-            constexpr uint32_t kIdescS = mma_idesc(kTile, N, false, false);
-            constexpr uint32_t kIdescO = mma_idesc(kTile, N, true, true);
-            constexpr uint32_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
-            const uint32_t qd = desc_lo(smem_addr(sQ), 16), vd = desc_lo(smem_addr(sK), kSubBytes),  pd = desc_lo(smem_addr(sP), 16);
-            constexpr uint32_t kQHi = desc_hi(1024, kSwizzle128), kVHi = kQHi, kPHi = desc_hi(16 * N, kPSwizzle);
+            // Scores, block after block: over a chunk as soon as it is decoded.  They run beside the softmax and the
+            // outputs of the block before.
+            constexpr uint32_t kIdesc = mma_idesc(kTile, N, false, false), kHi = desc_hi(1024, kSwizzle128);
+            const uint32_t qd = desc_lo(smem_addr(sQ), 16);
             int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
             uint32_t seg = 0;
             int kslot = 0;
             uint32_t tries = kWaitTries;
-            Ring<R> sr, vr;
-            // scores over chunk b of a block
-            auto scores = [&](int b) {
-                mbar_wait(smem_addr(&sh.full[sr.slot]), sr.parity, tries);
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(kTmemS, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kQHi, kIdescS, b + k > 0);
-                    if (KR == 3 && b == 0) mma_commit(smem_addr(&sh.kfree));
-                    if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone));
-                }
-                __syncwarp();
-                sr.next();
-                if (++kslot == KR) kslot = 0;
-            };
-            // outputs of dims 128 b .. 128 b + 127
-            auto outputs = [&](int b, bool add) {
-                if (elect_one()) {
-                    const uint32_t at = vd + ((vr.slot * kChunkSmem) >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ss(b * N, at + ((k * 2048) >> 4), kVHi, pd + ((k * 32 * N) >> 4), kPHi, kIdescO, add || k > 0);
-                    mma_commit(smem_addr(&sh.oblk[vr.slot]));
-                }
-                __syncwarp();
-                vr.next();
-            };
+            Ring<R> ring;
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
-                bool first = false;
-                if (left_tile == 0) {  // a new tile: its queries, a fresh accumulator
+                if (left_tile == 0) {  // a new tile: its queries
                     left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kSlots>(a, tile).nb, 0) - kb;
                     ++tile;
                     kb = 0;
-                    first = true;
                     mbar_wait(smem_addr(&sh.qready), seg & 1, tries);
-                    tc_fence_after();
                     ++seg;
                 }
                 --left_tile;
+                // the score buffer is free when the softmax warps have read what it held
+                if (i >= kBufs) mbar_wait(smem_addr(&sh.sread[(i - kBufs) & 1]), ((i - kBufs) >> 1) & 1, tries);
+                const uint32_t to = kTmemS + (kBufs == 2 ? (i & 1) * N : 0);
 #pragma unroll
-                for (int b = 0; b < kChunks; ++b) scores(b);
-                mbar_wait(smem_addr(&sh.pready), i & 1, tries);
+                for (int b = 0; b < kChunks; ++b) {
+                    mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(to, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kHi, kIdesc, b + k > 0);
+                        mma_commit(smem_addr(&sh.kfree[kslot]));
+                        if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone[i & 1]));
+                    }
+                    __syncwarp();
+                    ring.next();
+                    if (++kslot == KR) kslot = 0;
+                }
+            }
+            if (!tries) sh.abort = 1;
+            tries = kWaitTries;
+            if (elect_one()) mma_commit(smem_addr(&sh.drain[0]));  // nothing may write TMEM once it is freed
+            mbar_wait(smem_addr(&sh.drain[0]), 0, tries);
+        } else if (warp == kMmaWarp + 3) {
+            // Outputs, block after block: 128 dims a product of the block's chunk with its weights.
+            constexpr uint32_t kIdesc = mma_idesc(kChunk, N, true, true);
+            constexpr uint32_t kPSwizzle = N == 64 ? kSwizzle128 : N == 32 ? kSwizzle64 : kSwizzle32;
+            constexpr uint32_t kVHi = desc_hi(1024, kSwizzle128), kPHi = desc_hi(16 * N, kPSwizzle);
+            const uint32_t vd = desc_lo(smem_addr(sK), kSubBytes), pd = desc_lo(smem_addr(sP), 16);
+            int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
+            uint32_t tries = kWaitTries;
+            static_assert(R == 2 * kChunks, "a block's slots alternate between two runs");
+#pragma unroll 1
+            for (int i = 0; i < units; ++i) {
+                const bool first = left_tile == 0;  // a new tile: a fresh accumulator
+                if (first) {
+                    left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kSlots>(a, tile).nb, 0) - kb;
+                    ++tile;
+                    kb = 0;
+                }
+                --left_tile;
+                mbar_wait(smem_addr(&sh.pready[i & 1]), (i >> 1) & 1, tries);
                 tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t v = vd + (((i & 1) * kChunks * kChunkSmem) >> 4), p = pd + (((i & 1) * kTile * N * 2) >> 4);
 #pragma unroll
-                for (int b = 0; b < kChunks; ++b) outputs(b, !first);
+                    for (int b = 0; b < kChunks; ++b) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ss(b * N, v + ((b * kChunkSmem + k * 2048) >> 4), kVHi, p + ((k * 32 * N) >> 4), kPHi, kIdesc,
+                                   !first || k > 0);
+                        mma_commit(smem_addr(&sh.oblk[(i & 1) * kChunks + b]));
+                    }
+                }
+                __syncwarp();
             }
-            if (!tries) {
-                sh.abort = 1;
-                tries = kWaitTries;
-                if (elect_one()) mma_commit(smem_addr(&sh.drain));  // nothing may write TMEM once it is freed
-                mbar_wait(smem_addr(&sh.drain), 0, tries);
-            }
+            if (!tries) sh.abort = 1;
+            tries = kWaitTries;
+            if (elect_one()) mma_commit(smem_addr(&sh.drain[1]));
+            mbar_wait(smem_addr(&sh.drain[1]), 0, tries);
         } else if (warp <= kMmaWarp + kLookupWarps) {
             // Looks up where a block's rows lie and fetches their scales, up to two blocks ahead of the decode warps.
             // A load of a row's first bytes (V41: of either half) asks for 256 bytes in L2, and so for the row.  Lane
@@ -627,7 +624,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     fetch();
                 }
                 // wait until the entries are free (every reader of block i - kLookups is done)
-                for (int tries = 0; progress < i - (kLookups - 2) && tries < (1 << 22); ++tries) __nanosleep(64);
+                for (int tries = 0; progress < i - (kLookups - 1 - (R + kChunks - 1) / kChunks) && tries < (1 << 22); ++tries) __nanosleep(64);
                 const int k = i % kLookups;
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
@@ -646,14 +643,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kSoft));
-        constexpr int NC = N / 2;  // columns a thread: those from c0
-        const int t_row = tid & 127, quarter = warp & 3, half = warp >> 2, c0 = half * NC;
+        // A warp has 16 tokens (those of its TMEM lane quarter) and NC columns (query rows) from c0; a thread of it the
+        // tokens tok and tok + 8 and of every eight columns two, 8 g + 2 (lane % 4) + {0, 1}.
+        constexpr int NC = N / 2, G = NC / 8;
+        const int quarter = warp & 3, half = warp >> 2, c0 = half * NC, tok = 16 * quarter + (lane >> 2);
+        const int col0 = c0 + 2 * (lane & 3);
+        const int t_row = tid & 127;  // lane of the outputs: a dim of 128
         const float c = a.scale * kLog2e;
         const int per = a.q_len * a.heads;
         const uint32_t trow = (uint32_t(quarter * 32) << 16);
         Cursor<N, kSlots> cur(a, sh);
         Ring<R> ring;
-        float l[NC];
+        float l[G][2], sc[G][2], nm[G][2];
+        Ring<R> end;  // the slot of the block's last chunk
         bool unset = false;
         uint32_t tries = kWaitTries;
         int kb0 = 0;
@@ -714,87 +716,93 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if (lane == 0) mbar_arrive(smem_addr(&sh.qready));
                 soft_sync();
 #pragma unroll
-                for (int j = 0; j < NC; ++j) l[j] = 0.f;
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        l[g][e] = nm[g][e] = 0.f;
+                        sc[g][e] = sh.sc[col0 + 8 * g + e];
+                    }
                 unset = true;
             }
             // `full` of the block's first chunk orders this thread's read of texp
             mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
-            mbar_wait(smem_addr(&sh.sdone), i & 1, tries);
+            mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
             tc_fence_after();
-            const int te = sh.texp[i % kLookups][t_row];
-            const bool have = te != kNoToken;
-            const int t_at = have ? cur.kb * kTile + t_row : 0x7FFFFFFF;
+            // x = score in log2 units, plus the row's power of two; -inf where it is masked.  [.][h][e]: token tok + 8 h.
+            float x[G][2][2];
+            tmem_ld_rows<G>(trow + kTmemS + (kBufs == 2 ? (i & 1) * N : 0) + c0, x);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.sread[i & 1]));
+            int t_at[2];
+            float down[2] = {1.f, 1.f};
+            bool have = true;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int te = sh.texp[i % kLookups][tok + 8 * h];
+                const bool there = te != kNoToken;
+                have = have && there;
+                t_at[h] = there ? cur.kb * kTile + tok + 8 * h : 0x7FFFFFFF;
+                float et = 0.f, up = 1.f;
+                if constexpr (kExp) {
+                    et = there ? float(te) : 0.f;
+                    up = there ? __uint_as_float(uint32_t(127 + te) << 23) : 1.f;
+                    down[h] = there ? __uint_as_float(uint32_t(127 - te) << 23) : 1.f;
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float2 u = make_float2(x[g][h][0], x[g][h][1]);
+                    const float2 k = make_float2(sc[g][0], sc[g][1]);
+                    if constexpr (kExp) u = ffma2(fmul2(u, make_float2(up, up)), k, make_float2(et, et));
+                    else u = fmul2(u, k);
+                    x[g][h][0] = u.x, x[g][h][1] = u.y;
+                }
+            }
             // whether some of the block is masked for some row (the first row of a tile sees least)
             const bool masked = !__all_sync(0xFFFFFFFFu, have) || int64_t(cur.kb + 1) * kTile > sh.vis[0];
-            const float et = kExp && have ? float(te) : 0.f;
-            const float e_up = kExp && have ? __uint_as_float(uint32_t(127 + te) << 23) : 1.f;
-            const float e_down = kExp && have ? __uint_as_float(uint32_t(127 - te) << 23) : 1.f;
-
-            // x = score in log2 units, plus the row's power of two; -inf where it is masked
-            float x[NC];
-            bool odd = false;  // a score that is not finite, where some rows do not see the token
-            auto scores = [&]() {
-                uint32_t sraw[NC];
-                tmem_ld<NC>(trow + kTmemS + c0, sraw);
+            bool odd[2] = {false, false};  // a score that is not finite, where some rows do not see the token
+            if (masked) {
+                asm volatile("");  // a branch, not selects in every block
 #pragma unroll
-                for (int j = 0; j < NC; j += 4) {
-                    const float4 k = *reinterpret_cast<const float4 *>(&sh.sc[c0 + j]);
-                    float2 u = make_float2(__uint_as_float(sraw[j]), __uint_as_float(sraw[j + 1]));
-                    float2 w = make_float2(__uint_as_float(sraw[j + 2]), __uint_as_float(sraw[j + 3]));
-                    if constexpr (kExp) {
-                        u = ffma2(fmul2(u, make_float2(e_up, e_up)), make_float2(k.x, k.y), make_float2(et, et));
-                        w = ffma2(fmul2(w, make_float2(e_up, e_up)), make_float2(k.z, k.w), make_float2(et, et));
-                    } else {
-                        u = fmul2(u, make_float2(k.x, k.y));
-                        w = fmul2(w, make_float2(k.z, k.w));
-                    }
-                    x[j] = u.x, x[j + 1] = u.y, x[j + 2] = w.x, x[j + 3] = w.y;
-                }
-                if (masked) {
-                    asm volatile("");  // a branch, not 2 NC selects in every block
+                for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int j = 0; j < NC; ++j) {
-                        odd = odd || !(fabsf(x[j]) < INFINITY);
-                        if (!(t_at < sh.vis[c0 + j])) x[j] = -INFINITY;
+                    for (int e = 0; e < 2; ++e) {
+                        const int vis = sh.vis[col0 + 8 * g + e];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            odd[h] = odd[h] || !(fabsf(x[g][h][e]) < INFINITY);
+                            if (!(t_at[h] < vis)) x[g][h][e] = -INFINITY;
+                        }
                     }
-                }
-            };
-            // x becomes the weights 2^(x - maximum), which go to shared memory as fp16; returns the largest exponent
+            }
+            // The weights 2^(x - maximum), which go to shared memory as fp16; returns the largest exponent.
+            float p[G][2][2];
+            const uint32_t sp = smem_addr(sP) + (i & 1) * kTile * N * 2 + 4 * (lane & 3);
             auto weights = [&]() {
                 float top = -INFINITY;
-                const uint32_t sp = smem_addr(sP);
 #pragma unroll
-                for (int j0 = 0; j0 < NC; j0 += 8) {
-                    uint32_t h[4];
+                for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int j = j0 + 4 * g;
-                        const float4 k = *reinterpret_cast<const float4 *>(&sh.nm[c0 + j]);
-                        const float2 u = fadd2(make_float2(x[j], x[j + 1]), make_float2(k.x, k.y));
-                        const float2 w = fadd2(make_float2(x[j + 2], x[j + 3]), make_float2(k.z, k.w));
-                        top = fmax3(top, fmax3(u.x, u.y, w.x), w.y);
-                        x[j] = ex2_approx(u.x), x[j + 1] = ex2_approx(u.y);
-                        x[j + 2] = ex2_approx(w.x), x[j + 3] = ex2_approx(w.y);
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[2 * g]) : "f"(x[j + 1]), "f"(x[j]));
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[2 * g + 1]) : "f"(x[j + 3]), "f"(x[j + 2]));
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 u = fadd2(make_float2(x[g][h][0], x[g][h][1]), make_float2(nm[g][0], nm[g][1]));
+                        top = fmax3(top, u.x, u.y);
+                        p[g][h][0] = ex2_approx(u.x), p[g][h][1] = ex2_approx(u.y);
+                        uint32_t w;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(p[g][h][1]), "f"(p[g][h][0]));
+                        sts_u32(sp + p_vec<N>(tok + 8 * h, c0 / 8 + g), w);
                     }
-                    sts_u4(sp + p_vec<N>(t_row, (c0 + j0) / 8), h);
-                }
                 return top;
             };
-            scores();
             bool move = unset;
             if (!unset) move = soft_any(weights() > kStaleMax);
             if (move) {
                 // the columns' new maxima, and what is summed so far in their terms
-                if (!unset) scores();
-                float mine = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < NC; ++j) {
-                    const float v = redux_max(x[j]);
-                    if (lane == j) mine = v;
-                }
-                if (lane < NC) sh.red[quarter][c0 + lane] = mine;
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float v = rows_max(fmaxf(x[g][0][e], x[g][1][e]));
+                        if (lane < 4) sh.red[quarter][col0 + 8 * g + e] = v;
+                    }
                 soft_sync();
                 bool none = false;
                 if (tid < N) {
@@ -807,8 +815,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
                 unset = soft_any(none);
 #pragma unroll
-                for (int j = 0; j < NC; ++j) l[j] *= sh.alpha[c0 + j];
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        l[g][e] *= sh.alpha[col0 + 8 * g + e];
+                        nm[g][e] = sh.nm[col0 + 8 * g + e];
+                    }
                 if (!first) {
+                    // the outputs so far: the last block's must be in (`end` is still its last chunk)
+                    mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity, tries);
+                    tc_fence_after();
 #pragma unroll 1
                     for (int b = 2 * half; b < 2 * half + 2; ++b)
 #pragma unroll 1
@@ -824,42 +840,48 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 weights();
             }
 #pragma unroll
-            for (int j = 0; j < NC; j += 2) {
-                float2 sum = make_float2(l[j], l[j + 1]);
-                if constexpr (kExp) sum = ffma2(make_float2(x[j], x[j + 1]), make_float2(e_down, e_down), sum);
-                else sum = fadd2(sum, make_float2(x[j], x[j + 1]));
-                l[j] = sum.x;
-                l[j + 1] = sum.y;
+            for (int g = 0; g < G; ++g) {
+                float2 sum = make_float2(l[g][0], l[g][1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (kExp) sum = ffma2(make_float2(p[g][h][0], p[g][h][1]), make_float2(down[h], down[h]), sum);
+                    else sum = fadd2(sum, make_float2(p[g][h][0], p[g][h][1]));
+                }
+                l[g][0] = sum.x, l[g][1] = sum.y;
             }
-            if (masked && odd && have && half == 0) {
-                // a weight of 0 does not silence a NaN: if the token's row itself is not finite, the rows that see
-                // it are NaN by their weights already, and the others must meet zeros
-                bool bad = false;
+            if (masked && half == 0) {
+                // A weight of 0 does not silence a NaN: if a token's row itself is not finite, the rows that see it are
+                // NaN by their weights already, and the others must meet zeros.  (Such a row's scores are odd in every
+                // column, so each of its four lanes knows; one of them looks.)
+                for (int h = 0; h < 2; ++h) {
+                    if (!odd[h] || t_at[h] == 0x7FFFFFFF || (lane & 3) != 0) continue;
+                    bool bad = false;
 #pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    Ring<R> at = ring;
+                    for (int pass = 0; pass < 2; ++pass) {
+                        Ring<R> at = ring;
 #pragma unroll 1
-                    for (int v = 0; v < 64 && (pass == 0 || bad); ++v) {
-                        const uint32_t p = smem_addr(sK) + at.slot * kChunkSmem + ((v >> 3) & 1) * kSubBytes + t_row * 128 + (v & 7) * 16;
-                        if (pass == 0) {
-                            const uint4 u = lds_u4(p);
-                            const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
-                            for (int e = 0; e < 4; ++e)
-                                bad = bad || (ws[e] & 0x7C00u) == 0x7C00u || (ws[e] & 0x7C000000u) == 0x7C000000u;
-                        } else {
-                            const uint32_t z[4] = {0u, 0u, 0u, 0u};
-                            sts_u4(p, z);
+                        for (int v = 0; v < 64 && (pass == 0 || bad); ++v) {
+                            const uint32_t where = smem_addr(sK) + at.slot * kChunkSmem + ((v >> 3) & 1) * kSubBytes +
+                                                   (tok + 8 * h) * 128 + (v & 7) * 16;
+                            if (pass == 0) {
+                                const uint4 u = lds_u4(where);
+                                const uint32_t ws[4] = {u.x, u.y, u.z, u.w};
+                                for (int e = 0; e < 4; ++e)
+                                    bad = bad || (ws[e] & 0x7C00u) == 0x7C00u || (ws[e] & 0x7C000000u) == 0x7C000000u;
+                            } else {
+                                const uint32_t z[4] = {0u, 0u, 0u, 0u};
+                                sts_u4(where, z);
+                            }
+                            if ((v & 15) == 15) at.next();
                         }
-                        if ((v & 15) == 15) at.next();
                     }
                 }
             }
             tc_fence_before();
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.pready));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.pready[i & 1]));
             // the ring moves on by a block; the last chunk's slot tells when the block's outputs are summed
-            Ring<R> end = ring;
             for (int b = 0; b < kChunks; ++b) {
                 end = ring;
                 ring.next();
@@ -868,8 +890,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             if (i + 1 == units || cur.kb + 1 == cur.t.nb) {
                 // ---- this CTA's part of the tile is done
                 const bool whole = kb0 == 0 && cur.kb + 1 == cur.t.nb;
-                const int col = c0 + warp_columns_sum<NC>(l, lane);
-                if ((lane & (32 / NC - 1)) == 0) sh.red[quarter][col] = l[0];
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float v = rows_sum(l[g][e]);
+                        if (lane < 4) sh.red[quarter][col0 + 8 * g + e] = v;
+                    }
                 soft_sync();
                 float *part = nullptr;
                 if (!whole) part = a.part + (2 * int64_t(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * N * kPartRow;

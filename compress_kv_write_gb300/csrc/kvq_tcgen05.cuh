@@ -56,6 +56,36 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
+// 16 lanes x 8 G columns: thread l has lanes l / 4 (h = 0) and l / 4 + 8, and
+// of every eight columns 2 (l % 4) + e.  Waits as tmem_ld.
+template <int G>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, float (&v)[G][2][2]) {
+    static_assert(G == 1 || G == 2 || G == 4, "compiled shapes");
+    uint32_t r[4 * G];
+    if constexpr (G == 1) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    } else if constexpr (G == 2) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(addr));
+    }
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4 * G; ++i) {
+        asm volatile("" : "+r"(r[i]));
+        v[i / 4][(i >> 1) & 1][i & 1] = __uint_as_float(r[i]);
+    }
+}
+
 // 32 lanes x C columns: thread = lane, register i = column i.  Waits for the
 // values; the compiler moves no use of them above that.
 template <int C>
