@@ -24,7 +24,7 @@ kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok,
         n_seq * q_len > (int64_t(1) << 24))
         return KVQ_ERR_UNSUPPORTED;
     if (!(scale - scale == 0.f)) return KVQ_ERR_INVALID_ARG;  // NaN or infinite
-    if (!pool || !aligned(pool, 32) || pool_limit <= 0) return KVQ_ERR_INVALID_ARG;
+    if (!pool || !aligned(pool, 16) || pool_limit <= 0) return KVQ_ERR_INVALID_ARG;
     if (err && !aligned(err, 4)) return KVQ_ERR_INVALID_ARG;
     if (n_seq == 0) return KVQ_OK;
     // the stride of an axis of one element is never used
@@ -32,6 +32,11 @@ kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok,
     if (!q || !aligned(q, 16) || !out || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
     if (n_seq * q_len > 1 && (q_tok < 0 || q_tok % 8 || out_tok < kD || out_tok % unit)) return KVQ_ERR_INVALID_ARG;
     if (heads > 1 && (q_head < 0 || q_head % 8 || out_head < kD || out_head % unit)) return KVQ_ERR_INVALID_ARG;
+    if (n_seq * q_len > 1 && heads > 1) {  // rows that do not overlap: one stride spans the other axis
+        const bool by_token = out_tok >= out_head;
+        const int64_t inner = by_token ? out_head : out_tok, outer = by_token ? out_tok : out_head;
+        if (outer - kD < inner * ((by_token ? heads : n_seq * q_len) - 1)) return KVQ_ERR_INVALID_ARG;
+    }
     if (lse && !aligned(lse, 4)) return KVQ_ERR_INVALID_ARG;
     if (!ws || !aligned(ws, 16) || ws_bytes < kvq_attend_workspace(q_len * heads)) return KVQ_ERR_INVALID_ARG;
     return KVQ_OK;

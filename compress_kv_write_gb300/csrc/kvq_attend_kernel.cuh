@@ -19,12 +19,10 @@ constexpr int kChunkSmem = 2 * kSubBytes;
 // lie, 27 the outputs' products.
 constexpr int kSoftWarps = 8, kDeqWarps = 16, kMmaWarp = kSoftWarps + kDeqWarps;
 constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
-// Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.
-template <Layout L, int N>
-struct Regs {
-    static constexpr int kSoft = 104, kDeq = 64, kMma = 40;
-    static_assert(2 * kSoft + 4 * kDeq + kMma <= 7 * 72, "a larger sum would wait for ever");
-};
+// Registers a thread: the launch gives 896 threads 72 each, and the warpgroups' shares stay within that sum.  With
+// these none spills; 88/64/72 costs the 64-row tiles 3 % (spills), 96/72/24 1 to 2 %.
+constexpr int kLaunchRegs = 72, kSoftRegs = 104, kDeqRegs = 56;
+static_assert(2 * kSoftRegs + 4 * kDeqRegs + kLaunchRegs <= 7 * kLaunchRegs, "a larger sum would wait for ever");
 // How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
 // (which rescales the outputs in TMEM) is rare after a tile's first block.
 constexpr float kStaleMax = 14.f;
@@ -188,10 +186,10 @@ __device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, ui
 // A row's scales.  FP4: code * e4m3 scale is exact in fp16 as it is.  V41: the
 // ue8m0 scales of a row span more than fp16 does, so a row is decoded times
 // 2^-texp, which brings its largest scale to 2^7 (448 * 2^7 < 65504); the
-// softmax warps put 2^texp back into the scores and the weights.  Blocks
-// whose scale is 2^-31 of the row's largest or less vanish, values 2^-22 of
-// it or less are rounded to multiples of 2^-40 of it; both are far below
-// what fp32 sums resolve.  A row whose largest scale is below 2^-40 counts as
+// softmax warps put 2^texp back into the scores and the weights.  A
+// block whose scale is 2^-32 of the row's largest or less vanishes, other
+// values are off by at most 2^-40 of the row's largest value; both are below
+// what fp32 sums of the row resolve.  A row whose largest scale is below 2^-40 counts as
 // if it were 2^-40, which keeps the weights of tiny rows apart from zero.
 constexpr int kMinScaleByte = 127 - 40;
 
@@ -391,7 +389,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------------ decode
-        if constexpr (Regs<L, N>::kDeq < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kDeq));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
         const int quarter = warp & 3, chunk = (warp - kSoftWarps) >> 2, q = lane & 3, r8 = lane >> 2;
         const int tok0 = 16 * quarter + r8;  // and tok0 + 8
         const uint32_t krow = smem_addr(sK) + tok0 * 128;
@@ -484,7 +482,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         if (!tries) sh.abort = 1;
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
-        if constexpr (Regs<L, N>::kMma < 72) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kMma));
         if (warp == kMmaWarp) {
             // Scores, block after block: over a chunk as soon as it is decoded.  They run beside the softmax and the
             // outputs of the block before.
@@ -567,7 +564,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             if (elect_one()) mma_commit(smem_addr(&sh.drain[1]));
             mbar_wait(smem_addr(&sh.drain[1]), 0, tries);
         } else if (warp <= kMmaWarp + kLookupWarps) {
-            // Looks up where a block's rows lie and fetches their scales, up to two blocks ahead of the decode warps.
+            // Looks up where a block's rows lie and fetches their scales, up to three blocks ahead of the decode warps.
             // A load of a row's first bytes (V41: of either half) asks for 256 bytes in L2, and so for the row.  Lane
             // l of a warp has two tokens.
             constexpr int K = kTile / 32 / kLookupWarps;
@@ -642,7 +639,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         }
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<L, N>::kSoft));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // A warp has 16 tokens (those of its TMEM lane quarter) and NC columns (query rows) from c0; a thread of it the
         // tokens tok and tok + 8 and of every eight columns two, 8 g + 2 (lane % 4) + {0, 1}.
         constexpr int NC = N / 2, G = NC / 8;
@@ -830,7 +827,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll 1
                         for (int j0 = 0; j0 < N; j0 += 16) {
                             uint32_t o[16];
-                            tmem_ld<16>(trow + b * N + j0, o);
+                            tmem_ld16(trow + b * N + j0, o);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.alpha[j0 + j]);
                             tmem_st16(trow + b * N + j0, o);
@@ -931,7 +928,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll 1
                         for (int j0 = 0; j0 < N; j0 += 16) {
                             uint32_t o[16];
-                            tmem_ld<16>(trow + b * N + j0, o);
+                            tmem_ld16(trow + b * N + j0, o);
                             if (!whole) {
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) part[(j0 + j) * kPartRow + d] = __uint_as_float(o[j]);

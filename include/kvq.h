@@ -87,8 +87,8 @@ size_t kvq_bytes_per_token(kvq_layout layout);
  * rows ([P1] section 2, kv_page_bytes).  0 for a bad layout / page_bits. */
 size_t kvq_page_bytes(kvq_layout layout, int page_bits);
 
-/* 1 if page_bits has a compiled instance (the layout's page size is a
- * compile-time constant of every kernel), else 0. */
+/* 1 if page_bits is supported (the page size is a compile-time constant of the
+ * store, compress and dequant kernels), else 0. */
 int kvq_page_bits_supported(int page_bits);
 
 /* Full -> SWA slot translation, hoisted to once per step ([P2] sections 1-2).
@@ -220,7 +220,7 @@ size_t kvq_attend_workspace(int64_t rows);
  *   q            bf16, element (token, head, d) at token * q_token_stride +
  *                head * q_head_stride + d; 16-B aligned rows.  A stride of 0
  *                repeats a row.
- *   pool         32-B aligned.
+ *   pool         16-B aligned.
  *   page_table   [table_rows, table_stride] int32, the first table_width of
  *                a row used: physical page of each logical page.
  *   req          [n_seq] int32: table row of sequence i (NULL: row i, and
@@ -228,13 +228,21 @@ size_t kvq_attend_workspace(int64_t rows);
  *   kv_len       [n_seq] int32, 0 .. table_width * 2^page_bits.
  *   scale        finite.
  *   out          bf16 or fp32 (out_dtype), strides like q's (16-B aligned
- *                rows that do not overlap).
+ *                rows that do not overlap each other or an input).
  *   lse          [n_seq * q_len, heads] fp32, natural log, or NULL.
  *   workspace    kvq_attend_workspace(q_len * heads) bytes, 16-B aligned.
- * Scores, softmax statistics and sums are fp32; a softmax weight is rounded
- * to the products' 16-bit type (V41: bf16; V41_FP4: fp16, where every decoded
- * row is exact and a query row is first scaled by a power of two).  The
- * result does not depend on anything but the arguments (no atomics on data).
+ * Scores, softmax statistics and sums are fp32; the products' operands are
+ * fp16.  A query row is scaled by a power of two that brings its largest value
+ * to [2^14, 2^15): exact down to 2^-28 of that value.  A V41_FP4 row is exact
+ * as it is.  A V41 row is decoded relative to a power of two of its own that
+ * brings its largest scale to 2^7 (the scores and weights take it back):
+ * values above 2^-36 of the row's largest are exact, smaller ones off by at
+ * most 2^-40 of it, and a block whose scale is 2^-32 of the row's largest or
+ * less counts as zeros.  (A row whose largest scale is below 2^-40 counts as
+ * if it were 2^-40.)  A softmax weight, for V41 times its row's power of two, is
+ * rounded to fp16: relative 2^-11, or 2^-25 of the largest where that is more.
+ * The result does not depend on anything but the arguments (no atomics on
+ * data).
  * A visible token whose row holds a NaN or an infinity makes the rows that
  * see it NaN, and no others; what masked tokens hold does not matter.
  * A bad kv_len (KVQ_DEVERR_LEN) or req (KVQ_DEVERR_STATE) makes the sequence

@@ -10,8 +10,13 @@ step:
   of a row ds;
 * a weight p = exp(s - m) is off by 2 ds relative (numerator and the sum),
   2^-21 for the exponential and the exponent's rounding at |s - m| <= 64, and
-  the rounding of the weight itself to 16 bits: 2^-8 (V41, bf16) or 2^-11
-  (V41_FP4, fp16; below 2^-14 of the largest weight 2^-25 absolute);
+  the rounding of p * t to fp16, where t is the power of two that the token's
+  row is decoded relative to (V41_FP4: 1; V41: the one that brings the row's
+  largest scale to 2^7): 2^-11, or below 2^-14 of the largest p * t of the row
+  2^-25 of that one;
+* a value of a V41 row is decoded as fp16 relative to t, whose subnormals are
+  multiples of 2^-24: off by at most 2^-25 t (where no block's scale is 2^-32 of
+  the row's largest or less, as here);
 * out is a weighted mean of the rows: off by that relative error times
   sum p |k|, 512-step-like accumulation 2^-22 * (blocks + 16) of the same sum,
   and its own rounding, 2^-8 |out| for bf16;
@@ -76,6 +81,15 @@ def queries(n, heads, seed, std=2.0):
     return (torch.randn((n, heads, 512), generator=g) * std).to(torch.bfloat16)
 
 
+def row_power(layout, rows):
+    """The power of two that each row is decoded relative to (a V41 block's largest code is 2^8 to 448)."""
+    if layout == FP4:
+        return np.ones(rows.shape[0])
+    amax = np.abs(rows).max(1)
+    top = np.where(amax > 0, np.frexp(amax)[1] - 1 - 8, -127)          # the largest scale's exponent
+    return np.ldexp(1.0, np.maximum(top, -40) - 7)
+
+
 def reference(layout, q, rows, scale):
     """q float64 [h, 512] over rows [n, 512]: (out, lse, tol_out without the output's rounding, tol_lse)."""
     h = q.shape[0]
@@ -90,11 +104,12 @@ def reference(layout, q, rows, scale):
     lse = (m + np.log(l))[:, 0]
     ds = (512 * 2.0 ** -23 * abs(scale) * (np.abs(q) @ np.abs(rows).T) + 2.0 ** -22 * np.abs(s)).max(1)
     mean = p @ np.abs(rows) / l
-    blocks = -(-rows.shape[0] // 128)
-    rel = 2 * ds + 2.0 ** -21 + 2.0 ** -22 * (blocks + 16) + (2.0 ** -8 if layout == V41 else 2.0 ** -11)
-    tol = rel[:, None] * mean
-    if layout == FP4:
-        tol = tol + 2.0 ** -25 * np.abs(rows).sum(0)[None, :] / l
+    blocks = -(-rows.shape[0] // 64)
+    rel = 2 * ds + 2.0 ** -21 + 2.0 ** -22 * (blocks + 16) + 2.0 ** -11
+    t = row_power(layout, rows)
+    tol = rel[:, None] * mean + 2.0 ** -25 * (p * t).max(1, keepdims=True) * (np.abs(rows) / t[:, None]).sum(0) / l
+    if layout == V41:
+        tol = tol + 2.0 ** -25 * (p @ t)[:, None] / l
     return out, lse, tol, ds + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)
 
 
@@ -325,6 +340,23 @@ def test_large_and_small_magnitudes(K):
         c.scale = 512 ** -0.5 * 2.0 ** -100
         out, lse = c.run(K)
         check(out, lse, c.want(), "huge queries")
+
+
+def test_rows_of_many_magnitudes(K):
+    """V41 tokens and blocks whose scales differ by large powers of two, down to none at all."""
+    from compress_kv_write_gb300 import synth
+    for span, heads in ((6, 16), (30, 16), (60, 40)):
+        c = Paged(V41, 6, [200, 67, 1], heads, q_len=2, seed=37)
+        x = synth.store_rows_bf16(c.pages * 64, "cpu", 41).float()
+        g = torch.Generator().manual_seed(43)
+        x *= torch.exp2(torch.randint(-span, span // 6 + 1, (c.pages * 64, 1), generator=g).float())
+        x *= torch.exp2(torch.randint(-20, 1, (c.pages * 64, 16), generator=g).float()).repeat_interleave(32, 1)
+        x[7], x[11, 32:] = 0, 0
+        x = x.to(torch.bfloat16)
+        assert O.store(V41, 6, 0, x.view(torch.int16).numpy().view(np.uint16), np.arange(c.pages * 64), c.pool) == O.OK
+        c.q[:, ::3] = 0                                # equal weights, so that every row counts
+        out, lse = c.run(K, out=torch.empty(c.q.shape, device=DEV))
+        check(out, lse, c.want(), span)
 
 
 def test_device_errors(K):

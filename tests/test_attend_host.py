@@ -38,7 +38,7 @@ def _attend(L, layout=1, page_bits=6, q=A, q_tok=8192, q_head=512, n_seq=4, q_le
     dict(stride=1), dict(rows=3), dict(req=A + 1), dict(kv_len=None), dict(kv_len=A + 2), dict(scale=NAN),
     dict(scale=INF), dict(scale=-INF), dict(out=None), dict(out=A + 8), dict(out_dtype=2), dict(out_tok=504),
     dict(out_tok=8196), dict(out_head=256), dict(out_head=516), dict(lse=A + 2), dict(ws=None), dict(ws=A + 8),
-    dict(err=A + 2),
+    dict(err=A + 2), dict(out_tok=512), dict(out_tok=7680), dict(out_tok=512, out_head=1536),
 ])
 def test_attend_rejects_on_host(L, bad):
     assert _attend(L, **bad) == 1, bad
