@@ -34,12 +34,18 @@ template <int N>
 constexpr int kTmemRing = N == 64 ? 3 : N == 32 ? 5 : 6;
 template <int N>
 constexpr int kScoreBufs = N == 64 ? 1 : 2;
+// Barriers that tell which chunks' scores are done, in turn.  A wait tells a phase only from its neighbours: the
+// chunk that it waits for is KR = kTmemRing chunks back, the phase after is complete only once this chunk is decoded
+// if there are KR barriers or more, and the phase before is known to be if there are kChunks or more (the warp's last
+// chunk waited for it).
+template <int N>
+constexpr int kScored = kTmemRing<N> > kChunks ? kTmemRing<N> : kChunks;
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kLookups = 6, kLookupWarps = 2;
 
 template <int N>
 struct AttendShared {
-    uint64_t full[kRing], oblk[kRing], kfree[kTmemRing<N>], sdone[2], sread[2], pready[2], qready, drain[2];
+    uint64_t full[kRing], oblk[kRing], scored[kScored<N>], sdone[2], sread[2], pready[2], qready, drain[2];
     int64_t scan[kAttendThreads / 32];
     int64_t total, u0;
     int units, start_tile, start_kb;
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             mbar_init(smem_addr(&sh.full[i]), kDeqWarps / kChunks);
             mbar_init(smem_addr(&sh.oblk[i]), 1);
         }
-        for (int i = 0; i < KR; ++i) mbar_init(smem_addr(&sh.kfree[i]), 1);
+        for (int i = 0; i < kScored<N>; ++i) mbar_init(smem_addr(&sh.scored[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.sread[i]), kSoftWarps);
             mbar_init(smem_addr(&sh.sdone[i]), 1);
@@ -409,12 +415,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         uint32_t tries = kWaitTries;
         mbar_wait(smem_addr(&sh.addr[0]), 0, tries);
         load(0);
-        int slot = chunk, kslot = chunk, k = 0;
-        uint32_t parity = 0, kparity = 0, looked = 0;  // `looked`: the phase of the next block's lookup
-        if (kslot >= KR) {
-            kslot -= KR;
-            kparity = 1;
-        }
+        int slot = chunk, kslot = chunk % KR, k = 0;
+        int before = (chunk + kScored<N> - KR) % kScored<N>;  // the barrier of the chunk that had this one's TMEM slot
+        uint32_t parity = 0, looked = 0;  // `looked`: the phase of the next block's lookup
+        uint32_t bparity = chunk + kScored<N> - KR < kScored<N> ? 1 : 0;
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
             // the next block's entries (of the last block: its own again)
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             // a slot in shared memory is free when the product over the dims that it held is done, one in TMEM when
             // the scores over them are
             if (i * kChunks + chunk >= R) mbar_wait(smem_addr(&sh.oblk[slot]), parity ^ 1, tries);
-            if (i * kChunks + chunk >= KR) mbar_wait(smem_addr(&sh.kfree[kslot]), kparity ^ 1, tries);
+            if (i * kChunks + chunk >= KR) mbar_wait(smem_addr(&sh.scored[before]), bparity, tries);
             tc_fence_after();
             const uint32_t off = slot * kChunkSmem;
 #pragma unroll
@@ -469,13 +473,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 slot -= R;
                 parity ^= 1;
             }
-            kslot += kChunks;
-#pragma unroll
-            for (int wrap = 0; wrap < (kChunks + KR - 1) / KR; ++wrap)
-                if (kslot >= KR) {
-                    kslot -= KR;
-                    kparity ^= 1;
-                }
+            kslot += kChunks % KR;
+            if (kslot >= KR) kslot -= KR;
+            before += kChunks;
+            if (before >= kScored<N>) {
+                before -= kScored<N>;
+                bparity ^= 1;
+            }
             if (warp == kSoftWarps && lane == 0) *const_cast<volatile int *>(&sh.progress) = i + 1;
             k = kn;
         }
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             const uint32_t qd = desc_lo(smem_addr(sQ), 16);
             int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
             uint32_t seg = 0;
-            int kslot = 0;
+            int kslot = 0, done = 0;
             uint32_t tries = kWaitTries;
             Ring<R> ring;
 #pragma unroll 1
@@ -514,12 +518,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_ts(to, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kHi, kIdesc, b + k > 0);
-                        mma_commit(smem_addr(&sh.kfree[kslot]));
+                        mma_commit(smem_addr(&sh.scored[done]));
                         if (b == kChunks - 1) mma_commit(smem_addr(&sh.sdone[i & 1]));
                     }
                     __syncwarp();
                     ring.next();
                     if (++kslot == KR) kslot = 0;
+                    if (++done == kScored<N>) done = 0;
                 }
             }
             if (!tries) sh.abort = 1;

@@ -228,6 +228,37 @@ def test_many_sequences(K, layout):
     check(out, lse, c.want(), "many")
 
 
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads,q_len", [(16, 1), (32, 1), (64, 1), (40, 2)])
+def test_many_blocks_a_cta(K, layout, heads, q_len):
+    """More blocks than CTAs, in long tiles and in short ones: every ring goes round several times."""
+    c = Paged(layout, 6, [64 * 152 * 12 + 5] if heads < 64 else [64 * 152 * 6 + 5, 700], heads, q_len=q_len, seed=51)
+    out, lse = c.run(K)
+    check(out, lse, c.want(), (heads, "long"))
+    lens = [64 * (1 + (7 * i) % 9) - (i % 3) for i in range(200)]
+    c = Paged(layout, 6, lens, heads, q_len=q_len, seed=53)
+    out, lse = c.run(K)
+    check(out, lse, c.want(), (heads, "short"))
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_many_blocks_a_cta_by_slots(K, layout, heads):
+    pool = make_pool(layout, 6, 2048, 57)
+    g = torch.Generator().manual_seed(59)
+    q = queries(200, heads, 61)
+    slots = torch.randint(-1, 2048, (200, 333), generator=g, dtype=torch.int32)
+    out, lse = torch.empty(q.shape, device=DEV), torch.empty(q.shape[:2], device=DEV)
+    ws = torch.empty(K.attend_workspace(heads), dtype=torch.uint8, device=DEV)
+    K.kvq_attend_slots(layout, 6, q.to(DEV), torch.from_numpy(pool).to(DEV), 2048, slots.to(DEV), out, ws, scale=512 ** -0.5, lse=lse)
+    torch.cuda.synchronize()
+    want = []
+    for i in range(200):
+        s = slots[i].numpy()
+        want.append(reference(layout, q[i].double().numpy(), decode(layout, 6, pool, s[s >= 0]), 512 ** -0.5))
+    check(out, lse, want, heads)
+
+
 def test_query_and_output_layouts(K):
     """Head-major q and out, a slice of a wider projection, and a query row
     repeated by a stride of 0 give the contiguous call's bits."""
