@@ -40,7 +40,8 @@ struct AttendArgs {
 constexpr int kPartRow = kD + 4;
 constexpr int kMaxAttendCtas = 160;
 
-// Query rows a tile holds, by the rows of a sequence.
+// Query rows a tile holds, by the rows of a sequence: the fewest that hold them, up to 64 (kvq_attend_kernel.cuh has
+// both sides' times).
 constexpr int attend_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 __device__ __forceinline__ float attend_lse(float m, float sum) { return (m + log2f(sum)) * 0.6931471805599453f; }

@@ -1,4 +1,46 @@
 // kvq_attend_kernel.cuh -- the tensor-core attention kernel and its join.
+//
+// For a tile of N query rows q and the cached rows k[t] (512 dims, key and
+// value at once), block after block of 64 tokens:
+//   S^T[t, r] = sum_d k[t, d] q[r, d]           (tokens x rows)
+//   x = scale log2(e) S,  p[t, r] = 2^(x - m_r),  l_r += sum_t p
+//   O^T[d, r] += sum_t k[t, d] p[t, r]          (dims x rows)
+// and in the end out = O / l, lse = (m + log2 l) ln 2.  Both products have the
+// cached rows on the tensor cores' wide side (M = 64 tokens, M = 128 dims) and
+// the query rows on the narrow one (N = 16, 32, 64), so few heads waste no
+// more than their tile's padding.  m_r lags: a block moves it, and rescales O
+// in TMEM, only when a score passes it by kStaleMax, as 2^14 times a weight
+// still fits fp16; after a tile's first block that is rare.
+//
+// A block is decoded once for both products: 16 bits a value into shared
+// memory (the A operand of O^T, dims contiguous) and into TMEM (the A operand
+// of S^T).  From TMEM the scores' products take 18 to 33 clocks each (N = 16 to
+// 64), from shared memory 42 to 49, since the 128 bytes a clock of shared
+// memory carry the decoded rows' stores, the outputs' operands and the weights
+// already.  Loads touch eight rows at a time (a thread a token: 1.4 times as
+// long in all).
+//
+// The tiles' blocks in order are cut into equal shares, one a CTA (one an SM),
+// whatever the lengths: a long sequence is spread over the machine and short
+// ones are packed.  Tiles that a cut passes through leave partial sums, which
+// attend_join_kernel adds in order, so the result does not depend on timing.
+//
+// Rules for N by the rows of a sequence (kvq_attend.cuh): V41, one sequence of
+// 100 tokens / 48 of 1,024 to 8,192, in us: 16 heads as 16 rows 9.7 / 39, as 32
+// 10.9 / 45, as 64 13.2 / 60; 32 heads as 32 rows 11.1 / 45, as 64 13.4 / 61;
+// 64 heads as 64 rows 13.5 / 64, as twice 32 11.2 / 77.
+//
+// What bounds it: a block of 64 tokens takes about 2,500 clocks at N = 16 and
+// 3,100 at N = 64 (0.42 PFLOP/s; tensor cores 1,240 and 1,850 of them), and no
+// unit is full.  The rest is the chain of a block: its outputs free the slots
+// that the block after the next is decoded into (wait 100, codes from L2 to
+// registers, conversions and stores 500, fences 250), then the scores (600 to
+// 1,100), the softmax (1,200 to 1,500) and the outputs (700 to 800); two blocks
+// are under way at a time, as many as shared memory holds.  Blocks of 128
+// tokens take 8 % longer where selections are short (8-bit slots decode 65
+// instead of 56 us) and are 1 to 3 % slower elsewhere; a longer ring at N = 16
+// and 32, a second code buffer in registers, two score buffers at N = 64 and
+// one wait for a block's four chunks change nothing or cost up to 10 %.
 #pragma once
 
 #include <math.h>

@@ -3,16 +3,34 @@
 // Cache: V41 and FP4 formats", section 1, the block rule; the fused K norm of
 // its store-latency table for the norm).
 //
-// A row is read once: W warps hold it in registers (pieces of 8 values, piece
-// i of thread t is t + 32 W i), so the sum of squares, the block maxima and
-// the outputs all come from one pass over memory.  A quant block is the pieces
-// of four neighbouring lanes.
+// With z = x + residual, r = 1 / sqrt(mean(z^2) + eps): y = z r weight, and per
+// block of 32 the scale byte b = exponent field of max |y| minus 8 and the
+// codes e4m3(y 2^(127 - b)).  A value costs 4 to 8 bytes of traffic and some
+// ten operations, so a large call is bound by memory and a small one by the
+// latency of a row: one load, the sum over the row, one store.
+//
+// A row is read once: W warps hold it in registers (ITER pieces of 8 values a
+// thread, piece i of thread t is t + 32 W i), so the sum of squares, the block
+// maxima and the outputs all come from one pass over memory.  A quant block is
+// the pieces of four neighbouring lanes, its maximum two shuffles.
+//
+// One piece a thread makes the shortest row (bf16 with residual, 1 row and 300
+// rows: dim 512 with 2 warps 1.7 and 2.1 us, with 1 warp 2.2 and 2.6; dim 2048
+// with 8 warps 1.7 and 2.3, with 4 warps 2.3 and 2.6; dim 4096 with 16 warps
+// 2.0 and 2.8, with 8 warps 2.4 and 3.3; dim 16384 with 32 warps 3.7 and 6.1,
+// with 8 warps 6.3 and 10.8).  Large batches agree (8192 rows: dim 1024 with 4
+// warps 10.1, with 8 warps 12.9; dim 8192 with 16 warps 75 us = 6.3 TB/s, with
+// 8 warps 82, with 32 warps 88; dim 16384 with 32 warps 155, with 8 warps
+// 195), but for dim 4096, where two pieces a thread keep more bytes in flight
+// (39.1 us = 6.0 TB/s against 40.7).
 #include "kvq_launch.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kNqThreads = 256;
+// Threads a CTA: rows of W <= 8 warps share a CTA of eight.
+template <int W>
+constexpr int kNqThreads = W > 8 ? 32 * W : 256;
 constexpr int64_t kNqMaxDim = 16384;
 
 struct NormQuantArgs {
@@ -45,10 +63,10 @@ __device__ __forceinline__ void load8(const uint8_t *p, float (&v)[8]) {
 
 // W warps a row, ITER pieces of 8 values a thread.
 template <bool kBf16, bool kRes, int W, int ITER>
-__global__ void __launch_bounds__(kNqThreads) norm_quant_kernel(const NormQuantArgs a) {
-    constexpr int kRows = kNqThreads / 32 / W;
+__global__ void __launch_bounds__(kNqThreads<W>) norm_quant_kernel(const NormQuantArgs a) {
+    constexpr int kRows = kNqThreads<W> / 32 / W;
     constexpr int kPieceBytes = kBf16 ? 16 : 32;
-    __shared__ float s_sum[kNqThreads / 32];
+    __shared__ float s_sum[kNqThreads<W> / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = (warp % W) * 32 + lane;
     const int64_t row = int64_t(blockIdx.x) * kRows + warp / W;
@@ -104,7 +122,7 @@ __global__ void __launch_bounds__(kNqThreads) norm_quant_kernel(const NormQuantA
 #pragma unroll
         for (int i = 0; i < W; ++i) sum += s_sum[warp / W * W + i];
     }
-    const float r = rsqrt_approx(__fdiv_rn(sum, float(a.dim)) + a.eps);
+    const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(a.dim)), a.eps));
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const int p = t + 32 * W * i;
@@ -137,10 +155,10 @@ __global__ void __launch_bounds__(kNqThreads) norm_quant_kernel(const NormQuantA
 
 template <bool kBf16, bool kRes, int W, int ITER>
 kvq_status launch_nq(const NormQuantArgs &a, cudaStream_t s) {
-    constexpr int kRows = kNqThreads / 32 / W;
+    constexpr int kRows = kNqThreads<W> / 32 / W;
     const int64_t blocks = (a.n + kRows - 1) / kRows;
     if (blocks > 0x7FFFFFFF) return KVQ_ERR_INVALID_ARG;
-    return launch_pdl(norm_quant_kernel<kBf16, kRes, W, ITER>, dim3(unsigned(blocks)), dim3(kNqThreads), s, a);
+    return launch_pdl(norm_quant_kernel<kBf16, kRes, W, ITER>, dim3(unsigned(blocks)), dim3(kNqThreads<W>), s, a);
 }
 
 }  // namespace
@@ -191,11 +209,12 @@ extern "C" kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n
         return with_bool(residual != nullptr, [&](auto Rc) {
             constexpr bool B = decltype(Bc)::value, R = decltype(Rc)::value;
             if (dim <= 256) return launch_nq<B, R, 1, 1>(a, s);
-            if (dim <= 512) return launch_nq<B, R, 1, 2>(a, s);
-            if (dim <= 2048) return launch_nq<B, R, 4, 2>(a, s);
-            if (dim <= 4096) return launch_nq<B, R, 8, 2>(a, s);
-            if (dim <= 8192) return launch_nq<B, R, 8, 4>(a, s);
-            return launch_nq<B, R, 8, 8>(a, s);
+            if (dim <= 512) return launch_nq<B, R, 2, 1>(a, s);
+            if (dim <= 1024) return launch_nq<B, R, 4, 1>(a, s);
+            if (dim <= 2048) return launch_nq<B, R, 8, 1>(a, s);
+            if (dim <= 4096) return n < 2048 ? launch_nq<B, R, 16, 1>(a, s) : launch_nq<B, R, 8, 2>(a, s);
+            if (dim <= 8192) return launch_nq<B, R, 16, 2>(a, s);
+            return launch_nq<B, R, 32, 2>(a, s);
         });
     });
 }

@@ -8,6 +8,7 @@ CPU path.  A missing library raises ImportError.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -92,10 +93,12 @@ def status_string(status: int) -> str:
     return lib().kvq_status_string(status).decode()
 
 
+@functools.lru_cache(maxsize=None)
 def bytes_per_token(layout: int) -> int:
     return int(lib().kvq_bytes_per_token(layout))
 
 
+@functools.lru_cache(maxsize=None)
 def page_bytes(layout: int, page_bits: int) -> int:
     return int(lib().kvq_page_bytes(layout, page_bits))
 
@@ -120,13 +123,14 @@ def _cuda(t, name, dtypes=None):
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+        # the raw handle: a Stream object costs more than the rest of a small call's binding
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _idx_dtype(t, name):
@@ -143,11 +147,11 @@ def _contig1d(t, name):
 
 
 def _same_device(first, *others):
-    """The device of `first`; raises when another tensor lives elsewhere."""
-    dev = first.device
+    """The device index of `first`; raises when another tensor lives elsewhere."""
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"every tensor must be on {dev}, got one on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on {first.device}, got one on {t.device}")
     return dev
 
 
@@ -160,7 +164,7 @@ def _err_word(err):
 
 def _on(dev, stream, call):
     """status = call(stream pointer) with `dev` current; the default stream is that device's current one."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         return call(_stream(stream))
     with torch.cuda.device(dev):
         return call(_stream(stream))
@@ -346,27 +350,28 @@ def attend_workspace(rows):
 
 
 def _attend_rows(q, out, lse, workspace, err):
-    """Checks what both attention calls share; returns (tokens, heads, device, out dtype)."""
+    """Checks what both attention calls share; returns (tokens, heads, strides of q and out, device, out dtype)."""
     _cuda(q, "q", (torch.bfloat16,))
     _cuda(out, "out", (torch.bfloat16, torch.float32))
     _cuda(workspace, "workspace", (torch.uint8,))
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1:
+    shape, qs, outs = q.shape, q.stride(), out.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or qs[2] != 1:
         raise ValueError("q must be [tokens, heads, 512] with unit inner stride")
-    if out.shape != q.shape or out.stride(2) != 1:
+    if out.shape != shape or outs[2] != 1:
         raise ValueError("out must have q's shape and unit inner stride")
-    n, h = q.shape[0], q.shape[1]
+    n, h, _ = shape
     if n and h:
-        lo, hi = sorted(((out.stride(0), n), (out.stride(1), h)))
+        lo, hi = ((outs[0], n), (outs[1], h)) if outs[0] <= outs[1] else ((outs[1], h), (outs[0], n))
         if (lo[1] > 1 and lo[0] < HEAD_DIM) or (hi[1] > 1 and hi[0] < (lo[1] - 1) * lo[0] + HEAD_DIM):
             raise ValueError("rows of out must not overlap")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if lse is not None:
         _cuda(lse, "lse", (torch.float32,))
-        if lse.shape != q.shape[:2] or not lse.is_contiguous():
+        if lse.shape != shape[:2] or not lse.is_contiguous():
             raise ValueError("lse must be contiguous [tokens, heads]")
     _err_word(err)
-    return n, h, _same_device(q, out, lse, workspace, err), BF16 if out.dtype == torch.bfloat16 else F32
+    return n, h, qs, outs, _same_device(q, out, lse, workspace, err), BF16 if out.dtype == torch.bfloat16 else F32
 
 
 def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, workspace, *, scale, q_len=1,
@@ -375,11 +380,14 @@ def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, 
     shape and, if lse [n_seq * q_len, heads] fp32 is given, the natural-log sums.  page_table [rows, width]
     int32, row req[i] (req None: row i) for sequence i; kv_len [n_seq] int32 cached tokens; query token j of a
     sequence sees the first kv_len - (q_len - 1 - j).  workspace: attend_workspace(q_len * heads) bytes."""
-    n, heads, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+    n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
     _cuda(pool, "pool", (torch.uint8,))
     _cuda(page_table, "page_table", (torch.int32,))
     _cuda(kv_len, "kv_len", (torch.int32,))
-    if page_table.dim() != 2 or (page_table.numel() and page_table.stride(1) != 1 and page_table.shape[1] > 1):
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [rows, width] with unit inner stride")
+    (rows, width), ts = page_table.shape, page_table.stride()
+    if rows and width > 1 and ts[1] != 1:
         raise ValueError("page_table must be [rows, width] with unit inner stride")
     _contig1d(kv_len, "kv_len")
     n_seq = kv_len.numel()
@@ -390,16 +398,15 @@ def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, 
         _contig1d(req, "req")
         if req.numel() != n_seq:
             raise ValueError("req must hold one table row per sequence")
-    elif page_table.shape[0] < n_seq:
+    elif rows < n_seq:
         raise ValueError("page_table must hold one row per sequence")
     if not pool.is_contiguous() or pool.numel() < pool_pages * page_bytes(layout, page_bits):
         raise ValueError("pool must be contiguous and hold pool_pages pages")
     _same_device(q, pool, page_table, kv_len, req)
-    rows, width = page_table.shape
     st = _on(dev, stream, lambda s: lib().kvq_attend(
-        layout, page_bits, _ptr(q), q.stride(0), q.stride(1), n_seq, q_len, heads, _ptr(pool), int(pool_pages),
-        _ptr(page_table), rows, width, page_table.stride(0) if rows > 1 else width, _ptr(req), _ptr(kv_len),
-        float(scale), _ptr(out), out_dtype, out.stride(0), out.stride(1), _ptr(lse), _ptr(workspace),
+        layout, page_bits, _ptr(q), qs[0], qs[1], n_seq, q_len, heads, _ptr(pool), int(pool_pages),
+        _ptr(page_table), rows, width, ts[0] if rows > 1 else width, _ptr(req), _ptr(kv_len),
+        float(scale), _ptr(out), out_dtype, outs[0], outs[1], _ptr(lse), _ptr(workspace),
         workspace.numel(), _ptr(err), s))
     _check(st, "kvq_attend")
     return out
@@ -409,7 +416,7 @@ def kvq_attend_slots(layout, page_bits, q, pool, pool_slots, slots, out, workspa
                      stream=None):
     """kvq_attend of query token i over the tokens in slots[i] ([tokens, n_sel] int32 / int64; -1 is padding).
     workspace: attend_workspace(heads) bytes."""
-    n, heads, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+    n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
     _cuda(pool, "pool", (torch.uint8,))
     _cuda(slots, "slots")
     dt = _idx_dtype(slots, "slots")
@@ -419,8 +426,8 @@ def kvq_attend_slots(layout, page_bits, q, pool, pool_slots, slots, out, workspa
         raise ValueError("pool must be contiguous and hold pool_slots tokens")
     _same_device(q, pool, slots)
     st = _on(dev, stream, lambda s: lib().kvq_attend_slots(
-        layout, page_bits, _ptr(q), q.stride(0), q.stride(1), n, heads, _ptr(pool), int(pool_slots), _ptr(slots),
-        dt, slots.shape[1], slots.stride(0), float(scale), _ptr(out), out_dtype, out.stride(0), out.stride(1),
+        layout, page_bits, _ptr(q), qs[0], qs[1], n, heads, _ptr(pool), int(pool_slots), _ptr(slots),
+        dt, slots.shape[1], slots.stride(0), float(scale), _ptr(out), out_dtype, outs[0], outs[1],
         _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err), s))
     _check(st, "kvq_attend_slots")
     return out
