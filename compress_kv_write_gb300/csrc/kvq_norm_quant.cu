@@ -18,7 +18,9 @@
 // rows: dim 512 with 2 warps 1.7 and 2.1 us, with 1 warp 2.2 and 2.6; dim 2048
 // with 8 warps 1.7 and 2.3, with 4 warps 2.3 and 2.6; dim 4096 with 16 warps
 // 2.0 and 2.8, with 8 warps 2.4 and 3.3; dim 16384 with 32 warps 3.7 and 6.1,
-// with 8 warps 6.3 and 10.8).  Large batches agree (8192 rows: dim 1024 with 4
+// with 8 warps 6.3 and 10.8), so up to dim 2048 a row has just the warps that
+// its pieces fill (1537 fp32 rows of 1056: 5 warps 3.3 us, 8 warps 4.0).  Large
+// batches agree (8192 rows: dim 1024 with 4
 // warps 10.1, with 8 warps 12.9; dim 8192 with 16 warps 75 us = 6.3 TB/s, with
 // 8 warps 82, with 32 warps 88; dim 16384 with 32 warps 155, with 8 warps
 // 195), but for dim 4096, where two pieces a thread keep more bytes in flight
@@ -28,9 +30,9 @@
 namespace kvq {
 namespace {
 
-// Threads a CTA: rows of W <= 8 warps share a CTA of eight.
+// Threads a CTA: as many rows of W warps as eight warps hold, or one.
 template <int W>
-constexpr int kNqThreads = W > 8 ? 32 * W : 256;
+constexpr int kNqThreads = W >= 8 ? 32 * W : 8 / W * W * 32;
 constexpr int64_t kNqMaxDim = 16384;
 
 struct NormQuantArgs {
@@ -208,10 +210,17 @@ extern "C" kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n
     return with_bool(x_dtype == KVQ_BF16, [&](auto Bc) {
         return with_bool(residual != nullptr, [&](auto Rc) {
             constexpr bool B = decltype(Bc)::value, R = decltype(Rc)::value;
-            if (dim <= 256) return launch_nq<B, R, 1, 1>(a, s);
-            if (dim <= 512) return launch_nq<B, R, 2, 1>(a, s);
-            if (dim <= 1024) return launch_nq<B, R, 4, 1>(a, s);
-            if (dim <= 2048) return launch_nq<B, R, 8, 1>(a, s);
+            switch ((dim + 255) / 256) {
+                case 1: return launch_nq<B, R, 1, 1>(a, s);
+                case 2: return launch_nq<B, R, 2, 1>(a, s);
+                case 3: return launch_nq<B, R, 3, 1>(a, s);
+                case 4: return launch_nq<B, R, 4, 1>(a, s);
+                case 5: return launch_nq<B, R, 5, 1>(a, s);
+                case 6: return launch_nq<B, R, 6, 1>(a, s);
+                case 7: return launch_nq<B, R, 7, 1>(a, s);
+                case 8: return launch_nq<B, R, 8, 1>(a, s);
+                default: break;
+            }
             if (dim <= 4096) return n < 2048 ? launch_nq<B, R, 16, 1>(a, s) : launch_nq<B, R, 8, 2>(a, s);
             if (dim <= 8192) return launch_nq<B, R, 16, 2>(a, s);
             return launch_nq<B, R, 32, 2>(a, s);

@@ -59,7 +59,8 @@ def bits(t):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("n,dim", [(1, 32), (3, 64), (9, 256), (5, 288), (17, 512), (2, 544), (1, 1056), (33, 2048),
-                                   (3, 2080), (7, 4096), (2, 4128), (5, 8192), (1, 8224), (3, 16384), (700, 96), (2, 992), (2050, 4000)])
+                                   (3, 2080), (7, 4096), (2, 4128), (5, 8192), (1, 8224), (3, 16384), (700, 96), (2, 992), (2050, 4000), (5, 768),
+                                   (11, 1280), (4, 1504), (6, 1792)])
 def test_norm_quant(K, dtype, residual, n, dim):
     g = torch.Generator().manual_seed(n * 131 + dim)
     x = torch.randn((n, dim), generator=g).to(dtype)
