@@ -10,6 +10,8 @@ kvq_status launch_attend(int layout, const AttendArgs &a, bool slots, cudaStream
     return layout == KVQ_LAYOUT_V41 ? launch_attend_v41(a, slots, s) : launch_attend_fp4(a, slots, s);
 }
 
+constexpr int64_t kMaxLen = int64_t(1) << 30;  // cached tokens of a sequence: positions and block sums fit an int
+
 // What both entry points share: layout, pool, query, output and workspace.
 kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok, int64_t q_head, int64_t n_seq,
                         int64_t q_len, int64_t heads, const uint8_t *pool, int64_t pool_limit, float scale,
@@ -68,8 +70,8 @@ extern "C" kvq_status kvq_attend(kvq_layout layout, int page_bits, const void *q
     if (!aligned(page_table, 4) || (req && !aligned(req, 4))) return KVQ_ERR_INVALID_ARG;
     if (!kv_len || !aligned(kv_len, 4)) return KVQ_ERR_INVALID_ARG;
     if (!req && n_seq > table_rows) return KVQ_ERR_INVALID_ARG;
-    // kv_len is int32: no sequence is longer, however wide the table
-    if (table_width > (int64_t(0x7FFFFFFF) >> page_bits)) table_width = int64_t(0x7FFFFFFF) >> page_bits;
+    // no sequence is longer than kMaxLen, however wide the table
+    if (table_width > (kMaxLen >> page_bits)) table_width = kMaxLen >> page_bits;
 
     AttendArgs a = {};
     a.q = static_cast<const uint16_t *>(q_bf16);
@@ -111,7 +113,7 @@ extern "C" kvq_status kvq_attend_slots(kvq_layout layout, int page_bits, const v
     if (st != KVQ_OK) return st;
     if ((pool_slots & ((int64_t(1) << page_bits) - 1)) != 0) return KVQ_ERR_INVALID_ARG;
     if (slot_dtype != KVQ_I32 && slot_dtype != KVQ_I64) return KVQ_ERR_INVALID_ARG;
-    if (n_sel < 0 || slots_stride < 0 || n_sel > 0x7FFFFFFF - 128) return KVQ_ERR_INVALID_ARG;
+    if (n_sel < 0 || slots_stride < 0 || n_sel > kMaxLen) return KVQ_ERR_INVALID_ARG;
     if (n_tokens == 0) return KVQ_OK;
     if (n_sel > 0 && (!slots || !aligned(slots, slot_dtype == KVQ_I64 ? 8 : 4))) return KVQ_ERR_INVALID_ARG;
 

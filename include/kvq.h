@@ -75,8 +75,8 @@ enum {
     KVQ_DEVERR_STATE = 32,   /* a request index outside [0, n_state) or a count   */
                              /* outside [0, ratio): that request is skipped; in   */
                              /* kvq_attend a table row outside [0, table_rows)    */
-    KVQ_DEVERR_LEN = 64      /* a kv_len outside [0, table_width pages] (the      */
-                             /* sequence counts as empty)                         */
+    KVQ_DEVERR_LEN = 64      /* a kv_len outside [0, table_width pages] or above  */
+                             /* 2^30 (the sequence counts as empty)               */
 };
 
 /* Bytes one token occupies: 528 (V41) or 288 (V41_FP4); 0 for a bad layout.
@@ -225,7 +225,7 @@ size_t kvq_attend_workspace(int64_t rows);
  *                a row used: physical page of each logical page.
  *   req          [n_seq] int32: table row of sequence i (NULL: row i, and
  *                n_seq <= table_rows).
- *   kv_len       [n_seq] int32, 0 .. table_width * 2^page_bits.
+ *   kv_len       [n_seq] int32, 0 .. table_width * 2^page_bits, at most 2^30.
  *   scale        finite.
  *   out          bf16 or fp32 (out_dtype), strides like q's (16-B aligned
  *                rows that do not overlap each other or an input).
@@ -262,7 +262,7 @@ kvq_status kvq_attend(kvq_layout layout, int page_bits,
  * slots slots[i * slots_stride + 0 .. n_sel - 1] (int32 or int64), the ones
  * kvq_dequant_slots would gather.  Slot -1 is padding, anywhere in the list;
  * any other slot outside [0, pool_slots) sets KVQ_DEVERR_SLOT and is masked.
- * A slot that is listed twice counts twice.  workspace:
+ * A slot that is listed twice counts twice.  n_sel: at most 2^30.  workspace:
  * kvq_attend_workspace(heads) bytes. */
 kvq_status kvq_attend_slots(kvq_layout layout, int page_bits,
                             const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,

@@ -413,6 +413,14 @@ def test_device_errors(K):
     out, lse = c.run(K, kv_len=lens, err=err)
     assert err.item() == 64
     check(out, lse, [want[0], none, none, want[3]], "bad lengths")
+    err.zero_()      # past 2^30 tokens, though the table is wide enough
+    wide = torch.zeros((4, (1 << 24) + 4), dtype=torch.int32, device=DEV)
+    wide[:, :c.width] = torch.from_numpy(c.table).to(DEV)
+    lens = torch.tensor([200, (1 << 30) + 1, 0x7FFFFFFF, 64], dtype=torch.int32, device=DEV)
+    out, lse = c.run(K, kv_len=lens, table=wide, err=err)
+    assert err.item() == 64
+    check(out, lse, [want[0], none, none, want[3]], "too long")
+    del wide
     err.zero_()
     out, lse = c.run(K, req=torch.tensor([0, 4, 2, -1], dtype=torch.int32, device=DEV), err=err)
     assert err.item() == 32

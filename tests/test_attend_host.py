@@ -70,7 +70,7 @@ def _slots(L, layout=2, page_bits=6, q=A, q_tok=8192, q_head=512, n=4, heads=16,
 @pytest.mark.parametrize("bad", [
     dict(layout=7), dict(page_bits=-1), dict(q=None), dict(q_head=511), dict(n=-1), dict(heads=0), dict(pool=A + 1),
     dict(slots_n=0), dict(slots_n=100), dict(slots=None), dict(slots=A + 2), dict(slots=A + 4, dt=1), dict(dt=2),
-    dict(n_sel=-1), dict(n_sel=0x7FFFFFFF), dict(stride=-1), dict(scale=NAN), dict(out=A + 2), dict(out_dtype=-1),
+    dict(n_sel=-1), dict(n_sel=0x7FFFFFFF), dict(n_sel=(1 << 30) + 1, stride=1 << 31), dict(stride=-1), dict(scale=NAN), dict(out=A + 2), dict(out_dtype=-1),
     dict(out_head=510), dict(ws=None), dict(ws_bytes=8), dict(lse=A + 1), dict(err=A + 3),
 ])
 def test_attend_slots_rejects_on_host(L, bad):
