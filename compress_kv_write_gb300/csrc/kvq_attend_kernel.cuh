@@ -770,15 +770,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
             // `full` of the block's first chunk orders this thread's read of texp
             mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
-            mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
-            tc_fence_after();
-            // x = score in log2 units, plus the row's power of two; -inf where it is masked.  [.][h][e]: token tok + 8 h.
-            float x[G][2][2];
-            tmem_ld_rows<G>(trow + kTmemS + (kBufs == 2 ? (i & 1) * N : 0) + c0, x);
-            tc_fence_before();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.sread[i & 1]));
             int t_at[2];
-            float down[2] = {1.f, 1.f};
+            float down[2] = {1.f, 1.f}, up[2] = {1.f, 1.f}, et[2] = {0.f, 0.f};
             bool have = true;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -786,23 +779,32 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 const bool there = te != kNoToken;
                 have = have && there;
                 t_at[h] = there ? cur.kb * kTile + tok + 8 * h : 0x7FFFFFFF;
-                float et = 0.f, up = 1.f;
                 if constexpr (kExp) {
-                    et = there ? float(te) : 0.f;
-                    up = there ? __uint_as_float(uint32_t(127 + te) << 23) : 1.f;
+                    et[h] = there ? float(te) : 0.f;
+                    up[h] = there ? __uint_as_float(uint32_t(127 + te) << 23) : 1.f;
                     down[h] = there ? __uint_as_float(uint32_t(127 - te) << 23) : 1.f;
-                }
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    float2 u = make_float2(x[g][h][0], x[g][h][1]);
-                    const float2 k = make_float2(sc[g][0], sc[g][1]);
-                    if constexpr (kExp) u = ffma2(fmul2(u, make_float2(up, up)), k, make_float2(et, et));
-                    else u = fmul2(u, k);
-                    x[g][h][0] = u.x, x[g][h][1] = u.y;
                 }
             }
             // whether some of the block is masked for some row (the first row of a tile sees least)
             const bool masked = !__all_sync(0xFFFFFFFFu, have) || int64_t(cur.kb + 1) * kTile > sh.vis[0];
+            mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
+            tc_fence_after();
+            // x = score in log2 units, plus the row's power of two; -inf where it is masked.  [.][h][e]: token tok + 8 h.
+            float x[G][2][2];
+            tmem_ld_rows<G>(trow + kTmemS + (kBufs == 2 ? (i & 1) * N : 0) + c0, x);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.sread[i & 1]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float2 u = make_float2(x[g][h][0], x[g][h][1]);
+                    const float2 k = make_float2(sc[g][0], sc[g][1]);
+                    if constexpr (kExp) u = ffma2(fmul2(u, make_float2(up[h], up[h])), k, make_float2(et[h], et[h]));
+                    else u = fmul2(u, k);
+                    x[g][h][0] = u.x, x[g][h][1] = u.y;
+                }
+            }
             bool odd[2] = {false, false};  // a score that is not finite, where some rows do not see the token
             if (masked) {
                 asm volatile("");  // a branch, not selects in every block
