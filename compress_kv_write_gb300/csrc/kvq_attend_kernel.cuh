@@ -26,11 +26,11 @@
 // attend_join_kernel adds in order, so the result does not depend on timing.
 //
 // Rules for N by the rows of a sequence (kvq_attend.cuh): V41, one sequence of
-// 100 tokens / 48 of 1,024 to 8,192, in us: 16 heads as 16 rows 9.7 / 39, as 32
+// 100 tokens / 48 of 1,024 to 8,192 (before the prefetch), in us: 16 heads as 16 rows 9.7 / 39, as 32
 // 10.9 / 45, as 64 13.2 / 60; 32 heads as 32 rows 11.1 / 45, as 64 13.4 / 61;
 // 64 heads as 64 rows 13.5 / 64, as twice 32 11.2 / 77.
 //
-// What bounds it: a block of 64 tokens takes about 2,500 clocks at N = 16 and
+// What bounds it: a block of 64 tokens takes about 2,300 clocks at N = 16 and
 // 3,100 at N = 64 (0.42 PFLOP/s; tensor cores 1,240 and 1,850 of them), and no
 // unit is full.  The rest is the chain of a block: its outputs free the slots
 // that the block after the next is decoded into (wait 100, codes from L2 to
@@ -612,8 +612,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             mbar_wait(smem_addr(&sh.drain[1]), 0, tries);
         } else if (warp <= kMmaWarp + kLookupWarps) {
             // Looks up where a block's rows lie and fetches their scales, up to three blocks ahead of the decode warps.
-            // A load of a row's first bytes (V41: of either half) asks for 256 bytes in L2, and so for the row.  Lane
-            // l of a warp has two tokens.
+            // Every 128-byte line of a row is sent for to L2 (8-bit decode 44.2 us; without 46.6, a prefetch every 32
+            // bytes 48.0, one bulk prefetch a row 51.9).  Lane l of a warp has a token.
             constexpr int K = kTile / 32 / kLookupWarps;
             const int mine = (warp - kMmaWarp - 1) * 32 * K + lane;  // the first of the lane's tokens
             using Index = std::conditional_t<kSlots, int64_t, int>;
@@ -658,10 +658,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     good |= uint32_t(g) << j;
                     row[j] = p + r * T::kCodeBytes;
                     sc[j] = __ldg(reinterpret_cast<const uint4 *>(p + (scale_at + r * T::kScaleBytes)));
-                    uint32_t sink;
-                    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(sink) : "l"(row[j]));
-                    if constexpr (L == Layout::V41)
-                        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(sink) : "l"(row[j] + 256));
+#pragma unroll
+                    for (int z = 0; z < T::kCodeBytes; z += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row[j] + z));
                 }
                 if (i > 0) {  // the next block's indexes, while the scales come
                     cur.next(a);
