@@ -36,11 +36,11 @@
 // that the block after the next is decoded into (wait 100, codes from L2 to
 // registers, conversions and stores 500, fences 250), then the scores (600 to
 // 1,100), the softmax (1,200 to 1,500) and the outputs (700 to 800); two blocks
-// are under way at a time, as many as shared memory holds.  Blocks of 128
-// tokens take 8 % longer where selections are short (8-bit slots decode 65
-// instead of 56 us) and are 1 to 3 % slower elsewhere; a longer ring at N = 16
-// and 32, a second code buffer in registers, two score buffers at N = 64 and
-// one wait for a block's four chunks change nothing or cost up to 10 %.
+// are under way at a time.  With blocks of 128 tokens 129 x 2,048 slots of 32
+// heads take 65 instead of 55 us and long calls 1 to 4 % longer (a call of two
+// blocks 8.4 instead of 9.8); a ring of three blocks at N = 16, a second code
+// buffer in registers, two score buffers at N = 64 and one wait for a block's
+// four chunks change nothing or cost up to 10 %.
 #pragma once
 
 #include <math.h>

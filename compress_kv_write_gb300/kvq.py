@@ -164,10 +164,11 @@ def _err_word(err):
 
 def _on(dev, stream, call):
     """status = call(stream pointer) with `dev` current; the default stream is that device's current one."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch.cuda.current_device():
-        return call(_stream(stream))
+        return call(s)
     with torch.cuda.device(dev):
-        return call(_stream(stream))
+        return call(s)
 
 
 # ------------------------------------------------------------------ entry points
