@@ -476,14 +476,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     m[h][s] = block_mul<L>(reinterpret_cast<const uint8_t *>(&sh.scale[k][tok0 + 8 * h])[scale_at + 2 * s], texp[h]);
             }
             if (!__all_sync(0xFFFFFFFFu, texp[0] != kNoToken && texp[1] != kNoToken)) {
-                asm volatile("");  // a token that is not there has the pool's first row: its codes are cleared
+                // a token that is not there has the pool's first row, which may hold anything: its codes are cleared, and
+                // so are its multipliers, since 0 times a NaN or an infinity would be a NaN in every output
+                asm volatile("");
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                    for (int s = 0; s < 2; ++s) {
+                        m[h][s] = texp[h] != kNoToken ? m[h][s] : 0u;
 #pragma unroll
                         for (int x = 0; x < int(sizeof(Raw<L>) / 4); ++x)
                             raw[h][s].w[x] = texp[h] != kNoToken ? raw[h][s].w[x] : 0u;
+                    }
             }
             // a slot in shared memory is free when the product over the dims that it held is done, one in TMEM when
             // the scores over them are
