@@ -240,6 +240,17 @@ __device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, ui
 // what fp32 sums of the row resolve.  A row whose largest scale is below 2^-40 counts as
 // if it were 2^-40, which keeps the weights of tiny rows apart from zero.
 constexpr int kMinScaleByte = 127 - 40;
+// A V41 score is S 2^texp c with S the product of the fp16 operands (up to 2^40), 2^texp (2^-47 to 2^121) the row's and c
+// the query row's factor (down to 2^-127 and less).  S 2^texp alone can pass fp32, so 2^kLift of the row's power is c's.
+constexpr int kLift = 32;
+
+// scale 2^(127 - up) 2^lift, within fp32's finite values (a score that is 0 stays 0, whatever its factor).
+template <Layout L>
+__device__ __forceinline__ float score_factor(float scale, uint32_t up) {
+    const int e = 127 - int(up) + (L == Layout::V41 ? kLift : 0), half = e / 2;  // -127 .. 146
+    const float f = scale * __uint_as_float(uint32_t(127 + half) << 23) * __uint_as_float(uint32_t(127 + e - half) << 23);
+    return fminf(fmaxf(f, -3.4e38f), 3.4e38f);
+}
 
 template <Layout L>
 __device__ __forceinline__ int row_texp(const uint4 &v) {
@@ -754,7 +765,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                             asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[t][e]) * f), "f"(bf16_lo(v[t][e]) * f));
                             sts_u32(sq + q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
                         }
-                        if (lane == 0) sh.sc[r] = c * ue8m0_to_f32(254u - up);
+                        if (lane == 0) sh.sc[r] = score_factor<L>(c, up);
                     }
                 }
                 fence_proxy_async();
@@ -783,7 +794,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 t_at[h] = there ? cur.kb * kTile + tok + 8 * h : 0x7FFFFFFF;
                 if constexpr (kExp) {
                     et[h] = there ? float(te) : 0.f;
-                    up[h] = there ? __uint_as_float(uint32_t(127 + te) << 23) : 1.f;
+                    up[h] = there ? __uint_as_float(uint32_t(127 + te - kLift) << 23) : 1.f;
                     down[h] = there ? __uint_as_float(uint32_t(127 - te) << 23) : 1.f;
                 }
             }
