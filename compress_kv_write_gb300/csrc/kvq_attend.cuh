@@ -44,7 +44,12 @@ constexpr int kMaxAttendCtas = 160;
 // both sides' times).
 constexpr int attend_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-__device__ __forceinline__ float attend_lse(float m, float sum) { return (m + log2f(sum)) * 0.6931471805599453f; }
+// (m + log2 sum) ln 2.  The sum's power of two is added to m, since the two may cancel (rows of large powers of two).
+__device__ __forceinline__ float attend_lse(float m, float sum) {
+    const int e = int(__float_as_uint(sum) >> 23) - 127;
+    if (e < -126 || e > 127) return (m + log2f(sum)) * 0.6931471805599453f;  // zero, infinite, NaN
+    return ((m + float(e)) + log2f(__uint_as_float((__float_as_uint(sum) & 0x7FFFFFu) | 0x3F800000u))) * 0.6931471805599453f;
+}
 
 kvq_status launch_attend_v41(const AttendArgs &a, bool slots, cudaStream_t s);
 kvq_status launch_attend_fp4(const AttendArgs &a, bool slots, cudaStream_t s);

@@ -242,6 +242,10 @@ __device__ __forceinline__ void decode8(const Raw<L> &r, int e, uint32_t mul, ui
 constexpr int kMinScaleByte = 127 - 40;
 // A V41 score is S 2^texp c with S the product of the fp16 operands (up to 2^40), 2^texp (2^-47 to 2^121) the row's and c
 // the query row's factor (down to 2^-127 and less).  S 2^texp alone can pass fp32, so 2^kLift of the row's power is c's.
+// The weights of the outputs are relative to the running maximum m of score + texp, 2^(x - m); their sum, which has no
+// row in it, takes 2^(x - m - texp).  A row of small power beside one of large power has a weight that fp32 cannot hold
+// in the first and can have as large a share of the second as any, so what is computed is E = 2^(x - m - texp + kLift):
+// the sum takes E (2^93 at most, and 2^-89 at least for the token that is the maximum), the outputs E 2^(texp - kLift).
 constexpr int kLift = 32;
 
 // scale 2^(127 - up) 2^lift, within fp32's finite values (a score that is 0 stays 0, whatever its factor).
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             // `full` of the block's first chunk orders this thread's read of texp
             mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
             int t_at[2];
-            float down[2] = {1.f, 1.f}, up[2] = {1.f, 1.f}, et[2] = {0.f, 0.f};
+            float up[2] = {1.f, 1.f}, et[2] = {0.f, 0.f}, lift[2] = {0.f, 0.f};
             bool have = true;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -795,7 +799,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if constexpr (kExp) {
                     et[h] = there ? float(te) : 0.f;
                     up[h] = there ? __uint_as_float(uint32_t(127 + te - kLift) << 23) : 1.f;
-                    down[h] = there ? __uint_as_float(uint32_t(127 - te) << 23) : 1.f;
+                    lift[h] = there ? float(kLift - te) : 0.f;
                 }
             }
             // whether some of the block is masked for some row (the first row of a tile sees least)
@@ -844,9 +848,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     for (int h = 0; h < 2; ++h) {
                         const float2 u = fadd2(make_float2(x[g][h][0], x[g][h][1]), make_float2(nm[g][0], nm[g][1]));
                         top = fmax3(top, u.x, u.y);
-                        p[g][h][0] = ex2_approx(u.x), p[g][h][1] = ex2_approx(u.y);
+                        const float2 at = kExp ? fadd2(u, make_float2(lift[h], lift[h])) : u;
+                        p[g][h][0] = ex2_approx(at.x), p[g][h][1] = ex2_approx(at.y);
+                        float2 o = make_float2(p[g][h][0], p[g][h][1]);
+                        if constexpr (kExp) o = fmul2(o, make_float2(up[h], up[h]));
                         uint32_t w;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(p[g][h][1]), "f"(p[g][h][0]));
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(o.y), "f"(o.x));
                         sts_u32(sp + p_vec<N>(tok + 8 * h, c0 / 8 + g), w);
                     }
                 return top;
@@ -870,14 +877,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     none = m1 == -INFINITY;
                     sh.m[tid] = m1;
                     sh.nm[tid] = none ? 0.f : -m1;
-                    sh.alpha[tid] = none ? 1.f : ex2_approx(m0 - m1);
+                    sh.alpha[tid] = none ? 1.f : ex2_approx(0.5f * (m0 - m1));  // twice, as the whole can pass fp32
                 }
                 unset = soft_any(none);
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        l[g][e] *= sh.alpha[col0 + 8 * g + e];
+                        const float alpha = sh.alpha[col0 + 8 * g + e];
+                        l[g][e] = l[g][e] * alpha * alpha;
                         nm[g][e] = sh.nm[col0 + 8 * g + e];
                     }
                 if (!first) {
@@ -891,7 +899,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                             uint32_t o[16];
                             tmem_ld16(trow + b * N + j0, o);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.alpha[j0 + j]);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.alpha[j0 + j] * sh.alpha[j0 + j]);
                             tmem_st16(trow + b * N + j0, o);
                         }
                     tc_wait_st();
@@ -902,10 +910,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             for (int g = 0; g < G; ++g) {
                 float2 sum = make_float2(l[g][0], l[g][1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (kExp) sum = ffma2(make_float2(p[g][h][0], p[g][h][1]), make_float2(down[h], down[h]), sum);
-                    else sum = fadd2(sum, make_float2(p[g][h][0], p[g][h][1]));
-                }
+                for (int h = 0; h < 2; ++h) sum = fadd2(sum, make_float2(p[g][h][0], p[g][h][1]));
                 l[g][0] = sum.x, l[g][1] = sum.y;
             }
             if (masked && half == 0) {
@@ -960,7 +965,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 float *part = nullptr;
                 if (!whole) part = a.part + (2 * int64_t(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * N * kPartRow;
                 if (tid < N) {
-                    const float sum = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
+                    const float sum = ((sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid])) *
+                                      (kExp ? 1.f / float(int64_t(1) << kLift) : 1.f);
                     const float m = sh.m[tid];
                     sh.inv[tid] = whole ? (m == -INFINITY && sum == 0.f ? 0.f : 1.f / sum) : 1.f;
                     const int row = cur.t.rt * N + tid;
@@ -1037,7 +1043,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 // Joins the tiles that CTAs split.  Every CTA lists the `ctas` shares' split
 // tiles, and the warps of the grid go round (tile, query row, quarter of the
 // dims): a warp adds the parts of 128 dims in order, each weighted by 2^(its
-// maximum - the largest so far), with eight parts' loads in flight.
+// maximum - the largest so far), with eight parts' loads in flight.  Of that
+// weight the root is applied twice: a V41 part's maximum contains its rows'
+// powers of two, and two of them may differ by more than fp32 holds.
 constexpr int kJoinThreads = 512, kJoinBatch = 8;
 
 template <int N>
@@ -1088,12 +1096,12 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const __gr
 #pragma unroll
             for (int k = 0; k < kJoinBatch; ++k) to = fmaxf(to, ml[k].x);
             const float zero = to == -INFINITY ? 0.f : to;
-            const float keep = ex2_approx(top - zero);   // of nothing: 0
-            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep, sum *= keep;
+            const float keep = ex2_approx(0.5f * (top - zero)), keep2 = keep * keep;   // of nothing: 0
+            acc.x *= keep2, acc.y *= keep2, acc.z *= keep2, acc.w *= keep2, sum = sum * keep * keep;
 #pragma unroll
             for (int k = 0; k < kJoinBatch; ++k) {
-                const float w = ex2_approx(ml[k].x - zero);
-                sum = fmaf(w, ml[k].y, sum);
+                const float root = ex2_approx(0.5f * (ml[k].x - zero)), w = root * root;
+                sum = fmaf(root, root * ml[k].y, sum);
                 acc.x = fmaf(w, v[k].x, acc.x), acc.y = fmaf(w, v[k].y, acc.y);
                 acc.z = fmaf(w, v[k].z, acc.z), acc.w = fmaf(w, v[k].w, acc.w);
             }
