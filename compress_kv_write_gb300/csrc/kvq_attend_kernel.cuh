@@ -65,9 +65,18 @@ constexpr int kAttendThreads = (kMmaWarp + 4) * 32;
 // these none spills; 88/64/72 costs the 64-row tiles 3 % (spills), 96/72/24 1 to 2 %.
 constexpr int kLaunchRegs = 72, kSoftRegs = 104, kDeqRegs = 56;
 static_assert(2 * kSoftRegs + 4 * kDeqRegs + kLaunchRegs <= 7 * kLaunchRegs, "a larger sum would wait for ever");
-// How far (log2) a score may pass the running maximum before it moves: weights stay below fp16's 65504, and a move
+// How large (log2) a weight may become before the running maximum moves: weights stay below fp16's 65504, and a move
 // (which rescales the outputs in TMEM) is rare after a tile's first block.
-constexpr float kStaleMax = 14.f;
+constexpr float kStaleMax = 15.f;
+// A moved maximum gives the largest weight 2^headroom, and a weight that is 2^-(25 + headroom) of it or less is fp16's
+// zero.  What a long flat tail behind one large weight can lose that way grows with the tokens summed, so the headroom
+// does too: of n tokens at most n 2^-(25 + headroom) <= 2^-13 of the largest weight is lost, up to 2^26 tokens.  Less
+// headroom means fewer moves (4-bit decode / long / chunk 99.8 / 77.3 / 774 us with none, 103 / 82 / 804 with 4, 113 /
+// 91 / 892 with 8, 137 / 112 / 1016 with 12, whatever the length), and a part of up to 64 blocks, as most are, needs none.
+constexpr int kTailBlocks = 6, kMaxHeadroom = 14, kFoldBlocks = 64;
+__device__ __forceinline__ float headroom(int blocks) {
+    return float(min(max(32 - __clz(max(blocks - 1, 0)) - kTailBlocks, 0), kMaxHeadroom));
+}
 
 // Decoded chunks: two blocks (a block is four), so that one is decoded while the other is multiplied.
 constexpr int kRing = 2 * kChunks;
@@ -94,7 +103,7 @@ struct AttendShared {
     uint32_t tmem;
     int abort, progress;
     alignas(16) float sc[N], nm[N], m[N], alpha[N], inv[N];
-    float red[4][N];
+    float red[4][N], lsum[4][N];
     alignas(16) int vis[N];
     int64_t q[N], row[N];  // a query row's element offsets, -1: none
     // What the lookup warps found for a block's tokens, kLookups blocks in turn.
@@ -720,6 +729,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         bool unset = false;
         uint32_t tries = kWaitTries;
         int kb0 = 0;
+        float room = 0.f;
 #pragma unroll 1
         for (int i = 0; i < units; ++i, cur.next(a)) {
             const bool first = i == 0 || cur.kb == 0;
@@ -727,6 +737,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 // the scores' products of the last tile are done (their result was waited for)
                 kb0 = cur.kb;
                 if (tid == 0 && cur.kb == 0 && cur.t.rt == 0 && cur.t.err) raise_err(a.err, cur.t.err);
+                room = headroom(min(cur.left, cur.t.nb - cur.kb));
                 if (tid < N) {
                     const int row = cur.t.rt * N + tid, rc = min(row, per - 1);
                     const int j = rc / a.heads, head = rc - j * a.heads;
@@ -784,6 +795,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         sc[g][e] = sh.sc[col0 + 8 * g + e];
                     }
                 unset = true;
+            }
+            // Weights below 2^-24 of a thread's sum add nothing to it, however many they are, so the sum starts afresh
+            // every kFoldBlocks blocks.
+            const int since = cur.kb - kb0;  // blocks of this part so far
+            if (__builtin_expect((since & (kFoldBlocks - 1)) == 0 && since > 0, 0)) {
+                asm volatile("");
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = rows_sum(l[g][e]);
+                        if (since > kFoldBlocks) v += sh.lsum[quarter][col0 + 8 * g + e];
+                        if (lane < 4) sh.lsum[quarter][col0 + 8 * g + e] = v;
+                        l[g][e] = 0.f;
+                    }
             }
             // `full` of the block's first chunk orders this thread's read of texp
             mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
@@ -873,7 +899,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 bool none = false;
                 if (tid < N) {
                     const float m0 = sh.m[tid];
-                    const float m1 = fmaxf(fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid])), m0);
+                    const float top = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
+                    const float m1 = fmaxf(top - room, m0);
                     none = m1 == -INFINITY;
                     sh.m[tid] = m1;
                     sh.nm[tid] = none ? 0.f : -m1;
@@ -886,6 +913,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     for (int e = 0; e < 2; ++e) {
                         const float alpha = sh.alpha[col0 + 8 * g + e];
                         l[g][e] = l[g][e] * alpha * alpha;
+                        if (since >= kFoldBlocks && lane < 4) sh.lsum[quarter][col0 + 8 * g + e] *= alpha * alpha;
                         nm[g][e] = sh.nm[col0 + 8 * g + e];
                     }
                 if (!first) {
@@ -958,14 +986,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float v = rows_sum(l[g][e]);
-                        if (lane < 4) sh.red[quarter][col0 + 8 * g + e] = v;
+                        float v = rows_sum(l[g][e]);
+                        if (since >= kFoldBlocks) v += sh.lsum[quarter][col0 + 8 * g + e];
+                        if (lane < 4) sh.lsum[quarter][col0 + 8 * g + e] = v;
+                        l[g][e] = 0.f;  // (without this the chunk takes 787 instead of 740 us)
                     }
                 soft_sync();
                 float *part = nullptr;
                 if (!whole) part = a.part + (2 * int64_t(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * N * kPartRow;
                 if (tid < N) {
-                    const float sum = ((sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid])) *
+                    const float sum = ((sh.lsum[0][tid] + sh.lsum[1][tid]) + (sh.lsum[2][tid] + sh.lsum[3][tid])) *
                                       (kExp ? 1.f / float(int64_t(1) << kLift) : 1.f);
                     const float m = sh.m[tid];
                     sh.inv[tid] = whole ? (m == -INFINITY && sum == 0.f ? 0.f : 1.f / sum) : 1.f;
