@@ -74,6 +74,11 @@ constexpr float kStaleMax = 15.f;
 // headroom means fewer moves (4-bit decode / long / chunk 99.8 / 77.3 / 774 us with none, 103 / 82 / 804 with 4, 113 /
 // 91 / 892 with 8, 137 / 112 / 1016 with 12, whatever the length), and a part of up to 64 blocks, as most are, needs none.
 constexpr int kTailBlocks = 6, kMaxHeadroom = 14, kFoldBlocks = 64;
+// The tensor cores round their sums down, so what is summed in TMEM falls short by more the longer it goes on (2^-17 of
+// it after 2,048 blocks, 2^-10 after 16,384, 2 % after 131,072).  Every kFoldOut blocks the outputs so far are added to
+// the part's place in the workspace, which rounds to nearest, and the products start afresh.
+constexpr int kFoldOut = 256;
+static_assert(kFoldOut % kFoldBlocks == 0, "one test finds a block that begins with neither");
 __device__ __forceinline__ float headroom(int blocks) {
     return float(min(max(32 - __clz(max(blocks - 1, 0)) - kTailBlocks, 0), kMaxHeadroom));
 }
@@ -609,16 +614,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             const uint32_t vd = desc_lo(smem_addr(sK), kSubBytes), pd = desc_lo(smem_addr(sP), 16);
             int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
             uint32_t tries = kWaitTries;
+            int since = 0;  // blocks of this part so far
             static_assert(R == 2 * kChunks, "a block's slots alternate between two runs");
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
-                const bool first = left_tile == 0;  // a new tile: a fresh accumulator
-                if (first) {
+                if (left_tile == 0) {  // a new tile
+                    since = 0;
                     left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kSlots>(a, tile).nb, 0) - kb;
                     ++tile;
                     kb = 0;
                 }
                 --left_tile;
+                const bool first = (since++ & (kFoldOut - 1)) == 0;  // a fresh accumulator
                 mbar_wait(smem_addr(&sh.pready[i & 1]), (i >> 1) & 1, tries);
                 tc_fence_after();
                 if (elect_one()) {
@@ -730,6 +737,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         uint32_t tries = kWaitTries;
         int kb0 = 0;
         float room = 0.f;
+        // where a part's sums go that another CTA goes on with or began, or that are too long for TMEM
+        auto part_of = [&](int kb0) { return a.part + (2 * int64_t(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * N * kPartRow; };
 #pragma unroll 1
         for (int i = 0; i < units; ++i, cur.next(a)) {
             const bool first = i == 0 || cur.kb == 0;
@@ -810,6 +819,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         if (lane < 4) sh.lsum[quarter][col0 + 8 * g + e] = v;
                         l[g][e] = 0.f;
                     }
+                if ((since & (kFoldOut - 1)) == 0) {
+                    mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity, tries);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int b = 2 * half; b < 2 * half + 2; ++b)
+#pragma unroll 1
+                        for (int j0 = 0; j0 < N; j0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(trow + b * N + j0, o);
+                            float *to = part_of(kb0) + j0 * kPartRow + b * kChunk + t_row;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j, to += kPartRow)
+                                *to = since > kFoldOut ? *to + __uint_as_float(o[j]) : __uint_as_float(o[j]);
+                        }
+                }
             }
             // `full` of the block's first chunk orders this thread's read of texp
             mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
@@ -931,6 +955,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                             tmem_st16(trow + b * N + j0, o);
                         }
                     tc_wait_st();
+                    if (since >= kFoldOut) {
+#pragma unroll 1
+                        for (int j = 0; j < N; ++j) {
+                            float *to = part_of(kb0) + j * kPartRow + 2 * half * kChunk + t_row;
+                            to[0] = to[0] * sh.alpha[j] * sh.alpha[j];
+                            to[kChunk] = to[kChunk] * sh.alpha[j] * sh.alpha[j];
+                        }
+                    }
                 }
                 weights();
             }
@@ -992,8 +1024,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         l[g][e] = 0.f;  // (without this the chunk takes 787 instead of 740 us)
                     }
                 soft_sync();
-                float *part = nullptr;
-                if (!whole) part = a.part + (2 * int64_t(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * N * kPartRow;
+                float *const part = part_of(kb0);
                 if (tid < N) {
                     const float sum = ((sh.lsum[0][tid] + sh.lsum[1][tid]) + (sh.lsum[2][tid] + sh.lsum[3][tid])) *
                                       (kExp ? 1.f / float(int64_t(1) << kLift) : 1.f);
@@ -1019,6 +1050,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 soft_sync();
                 mbar_wait(smem_addr(&sh.oblk[end.slot]), end.parity, tries);
                 tc_fence_after();
+                if (__builtin_expect(since >= kFoldOut, 0)) {
+#pragma unroll 1
+                    for (int b = 2 * half; b < 2 * half + 2; ++b)
+#pragma unroll 1
+                        for (int j0 = 0; j0 < N; j0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(trow + b * N + j0, o);
+                            const float *from = part + j0 * kPartRow + b * kChunk + t_row;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j, from += kPartRow) o[j] = __float_as_uint(__uint_as_float(o[j]) + *from);
+                            tmem_st16(trow + b * N + j0, o);
+                        }
+                    tc_wait_st();
+                }
                 if (tries) {
 #pragma unroll 1
                     for (int b = 2 * half; b < 2 * half + 2; ++b) {

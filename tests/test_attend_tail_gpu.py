@@ -120,3 +120,69 @@ def test_slots(K, layout, where):
     count = np.bincount(s[s >= 0].numpy(), minlength=PAGES * 64).astype(np.float64)
     for i in (0, 1, 77, many - 1):
         compare(out[i], lse[i], expect(layout, rows, count, d), (where, i))
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [16, 32, 64])
+@pytest.mark.parametrize("n,many", [(313 * 64 - 5, 300), (1 << 20, 160)])
+def test_sums_of_many_equal_weights(K, layout, heads, n, many):
+    """Equal weights are exact, so what the mean is off by is the sums': a CTA that sums most of a sequence, or several,
+    in up to 2^14 blocks.  The tensor cores add 16 tokens at a time and drop what is below 2^-23 of the sum, which is
+    half of the final one on average; over at most 256 blocks that is 256 * 4 * 2^-23 / 2 = 2^-14.  The rest is rounded
+    to nearest (2^-18, with the final division), and a V41 value is off by its decoding."""
+    pool, rows, q, _ = problem(layout, 0.0, 11)
+    table = 1 + torch.arange(-(-n // 64), dtype=torch.int32)[None] % 8
+    out, lse = torch.full((many, heads, 512), float("nan"), device=DEV), torch.full((many, heads), float("nan"), device=DEV)
+    ws = torch.empty(K.attend_workspace(heads), dtype=torch.uint8, device=DEV)
+    K.kvq_attend(layout, 6, q.to(torch.bfloat16).to(DEV).expand(many, heads, 512), torch.from_numpy(pool).to(DEV), PAGES,
+                 table.to(DEV), torch.full((many,), n, dtype=torch.int32, device=DEV), out, ws, scale=0.0,
+                 req=torch.zeros(many, dtype=torch.int32, device=DEV), lse=lse)
+    torch.cuda.synchronize()
+    at = np.arange(n)
+    count = np.bincount(table[0].numpy()[at >> 6] * 64 + (at & 63), minlength=PAGES * 64).astype(np.float64)
+    want = count @ rows / n
+    tol = (2.0 ** -14 + 2.0 ** -18) * (count @ np.abs(rows)) / n
+    if layout == V41:
+        tol = tol + 2.0 ** -25 * (count @ row_power(layout, rows)) / n
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    assert np.abs(lse.double().cpu().numpy() - math.log(n)).max() <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [16, 64])
+def test_maxima_that_move_late(K, layout, heads):
+    """Scores that rise along a part of many blocks, so that sums already put aside are brought to later maxima: the
+    tokens of each quarter of the sequence weigh 2^12 of the quarter before."""
+    n, many = 64 * 1500, 152
+    pool, rows, q, _ = problem(layout, 0.0, 13)
+    x = np.zeros((PAGES * 64, 512), np.float32)
+    g = np.random.default_rng(17)
+    x[:, 32:] = 1 + 0.25 * g.standard_normal((PAGES * 64, 480))
+    for page in range(1, 5):
+        x[page * 64:(page + 1) * 64, :32] = 0.375 * (page - 1)
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    pool = np.zeros(PAGES * 64 * O.bytes_per_token(layout), np.uint8)
+    assert O.store(layout, 6, 0, x.view(torch.int16).numpy().view(np.uint16), np.arange(PAGES * 64), pool) == O.OK
+    rows = decode(layout, 6, pool, np.arange(PAGES * 64))
+    assert all((rows[p * 64:(p + 1) * 64, :32] == 0.375 * (p - 1)).all() for p in range(1, 5))
+    scale = 12 * math.log(2) / (32 * 2 * 0.375)
+    table = (1 + torch.arange(n // 64, dtype=torch.int32) * 4 // (n // 64))[None]
+    out, lse = torch.full((many, heads, 512), float("nan"), device=DEV), torch.full((many, heads), float("nan"), device=DEV)
+    ws = torch.empty(K.attend_workspace(heads), dtype=torch.uint8, device=DEV)
+    K.kvq_attend(layout, 6, q.to(torch.bfloat16).to(DEV).expand(many, heads, 512), torch.from_numpy(pool).to(DEV), PAGES,
+                 table.to(DEV), torch.full((many,), n, dtype=torch.int32, device=DEV), out, ws, scale=scale,
+                 req=torch.zeros(many, dtype=torch.int32, device=DEV), lse=lse)
+    torch.cuda.synchronize()
+    p = np.exp2(12.0 * (np.arange(PAGES * 64) // 64 - 4))
+    p[:64] = p[5 * 64:] = 0
+    count = np.where(p > 0, n / 256, 0.0)
+    l = (p * count).sum()
+    want = (p * count) @ rows / l
+    t = row_power(layout, rows)
+    # weights 2^-11, sums as above, the smallest weights 2^-13 of the largest in all
+    tol = (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -18) * want + 2.0 ** -13 * (p * t).max() * (rows / t[:, None])[p > 0].max(0) / l
+    if layout == V41:
+        tol = tol + 2.0 ** -25 * ((p * count) @ t) / l
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol + 1e-30).all()
+    exact = math.log(l) + 3 * 12 * math.log(2)
+    assert np.abs(lse.double().cpu().numpy() - exact).max() <= 2.0 ** -17 + 2.0 ** -20 * exact
