@@ -1,7 +1,10 @@
 // kvq_attend.cu -- C entry points of the latent attention over the paged V41 /
 // V41_FP4 pool, by page table (kvq_attend) or by selected slots
 // (kvq_attend_slots).
+#include <atomic>
+
 #include "kvq_attend.cuh"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 namespace {
@@ -9,6 +12,10 @@ namespace {
 kvq_status launch_attend(int layout, const AttendArgs &a, bool slots, cudaStream_t s) {
     return layout == KVQ_LAYOUT_V41 ? launch_attend_v41(a, slots, s) : launch_attend_fp4(a, slots, s);
 }
+
+// Tries of the waits inside the kernels: 2^20 take some seconds where nothing happens.
+constexpr uint32_t kMostWaitTries = 1u << 24;
+std::atomic<uint32_t> g_wait_tries{kWaitTries};
 
 constexpr int64_t kMaxLen = int64_t(1) << 30;  // cached tokens of a sequence: positions and block sums fit an int
 
@@ -48,6 +55,10 @@ kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok,
 }  // namespace kvq
 
 using namespace kvq;
+
+extern "C" uint32_t kvq_attend_wait_limit(uint32_t tries) {
+    return g_wait_tries.exchange(tries < kMostWaitTries ? tries : kMostWaitTries, std::memory_order_relaxed);
+}
 
 extern "C" size_t kvq_attend_workspace(int64_t rows) {
     if (rows <= 0) return 0;
@@ -97,6 +108,7 @@ extern "C" kvq_status kvq_attend(kvq_layout layout, int page_bits, const void *q
     a.ws = static_cast<uint8_t *>(workspace);
     a.err = err;
     a.out_bf16 = out_dtype == KVQ_BF16;
+    a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
     return launch_attend(layout, a, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -139,5 +151,6 @@ extern "C" kvq_status kvq_attend_slots(kvq_layout layout, int page_bits, const v
     a.err = err;
     a.slots64 = slot_dtype == KVQ_I64;
     a.out_bf16 = out_dtype == KVQ_BF16;
+    a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
     return launch_attend(layout, a, true, reinterpret_cast<cudaStream_t>(stream));
 }

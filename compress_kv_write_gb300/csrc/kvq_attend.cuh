@@ -29,6 +29,7 @@ struct AttendArgs {
     uint8_t *ws;
     int32_t *err;
     bool slots64, out_bf16;
+    uint32_t wait_tries;  // how often a wait inside the kernel tries before the call gives up
     // set at the launch
     int row_tiles;  // tiles of query rows a sequence
     int2 *join;     // workspace, one a CTA: the tile it began and another CTA went on with (or -1), that tile's last CTA

@@ -98,6 +98,7 @@ template <int N>
 constexpr int kScored = kTmemRing<N> > kChunks ? kTmemRing<N> : kChunks;
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kLookups = 6, kLookupWarps = 2;
+constexpr uint32_t kLookupTries = 16;  // a lookup warp's try is a sleep of 64 ns, a barrier's may take a microsecond
 
 template <int N>
 struct AttendShared {
@@ -475,17 +476,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const uint32_t lane_at = q * (T::kCodeBytes / 32) + chunk * (T::kCodeBytes / kChunks);
         const int scale_at = 4 * chunk + (q >> 1);  // and 2 further for the second half
 
-        // A chunk's codes are loaded a block ahead, from L2, where the lookup warps have sent for them.
-        Raw<L> raw[2][2];  // token, half
+        // A chunk's codes are loaded a block ahead, from L2, where the lookup warps have sent for them.  (A warp that has
+        // given up follows no pointer that may be half written.)
+        Raw<L> raw[2][2] = {};  // token, half
         auto load = [&](int k) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) raw[h][s] = load_raw<L>(sh.code[k][tok0 + 8 * h] + lane_at, s);
         };
-        uint32_t tries = kWaitTries;
+        uint32_t tries = a.wait_tries;
         mbar_wait(smem_addr(&sh.addr[0]), 0, tries);
-        load(0);
+        if (tries) load(0);
         int slot = chunk, kslot = chunk % KR, k = 0;
         int before = (chunk + kScored<N> - KR) % kScored<N>;  // the barrier of the chunk that had this one's TMEM slot
         uint32_t parity = 0, looked = 0;  // `looked`: the phase of the next block's lookup
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.full[slot]));
             if (i + 1 < units) mbar_wait(smem_addr(&sh.addr[kn]), looked, tries);
-            load(kn);
+            if (tries) load(kn);
             slot += kChunks;
             if (slot >= R) {
                 slot -= R;
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
             uint32_t seg = 0;
             int kslot = 0, done = 0;
-            uint32_t tries = kWaitTries;
+            uint32_t tries = a.wait_tries;
             Ring<R> ring;
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             constexpr uint32_t kVHi = desc_hi(1024, kSwizzle128), kPHi = desc_hi(16 * N, kPSwizzle);
             const uint32_t vd = desc_lo(smem_addr(sK), kSubBytes), pd = desc_lo(smem_addr(sP), 16);
             int left_tile = 0, tile = __shfl_sync(0xFFFFFFFFu, sh.start_tile, 0), kb = __shfl_sync(0xFFFFFFFFu, sh.start_kb, 0);
-            uint32_t tries = kWaitTries;
+            uint32_t tries = a.wait_tries;
             int since = 0;  // blocks of this part so far
             static_assert(R == 2 * kChunks, "a block's slots alternate between two runs");
 #pragma unroll 1
@@ -658,6 +660,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             Cursor<N, kSlots> cur(a, sh);
             Index idx[K];
             int t0 = 0, seen = 0;
+            uint32_t tries = a.wait_tries * kLookupTries;
             auto fetch = [&]() {
                 t0 = cur.kb * kTile + mine;
                 seen = cur.left > 0 ? cur.t.seen : 0;
@@ -700,8 +703,16 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     cur.next(a);
                     fetch();
                 }
-                // wait until the entries are free (every reader of block i - kLookups is done)
-                for (int tries = 0; progress < i - (kLookups - 1 - (R + kChunks - 1) / kChunks) && tries < (1 << 22); ++tries) __nanosleep(64);
+                // wait until the entries are free (every reader of block i - kLookups is done); as the other waits, it
+                // gives up once and for all
+                const int need = i - (kLookups - 1 - (R + kChunks - 1) / kChunks);
+                for (uint32_t n = tries; progress < need; --n) {
+                    if (n == 0) {
+                        tries = 0;
+                        break;
+                    }
+                    __nanosleep(64);
+                }
                 const int k = i % kLookups;
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
@@ -716,6 +727,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     fetch();
                 }
             }
+            if (!tries) sh.abort = 1;
         }
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
@@ -734,7 +746,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         float l[G][2], sc[G][2], nm[G][2];
         Ring<R> end;  // the slot of the block's last chunk
         bool unset = false;
-        uint32_t tries = kWaitTries;
+        uint32_t tries = a.wait_tries;
         int kb0 = 0;
         float room = 0.f;
         // where a part's sums go that another CTA goes on with or began, or that are too long for TMEM

@@ -15,9 +15,9 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 
 // Waits until the phase of the given parity has completed, with a bound:
-// `tries` tries (2^20 at first), each of which the hardware may suspend for a
-// while.  (A time-limit operand would make it a sleeping loop, which wakes up
-// late.)  A wait that gives up sets `tries` to 0: the caller's further waits
+// `tries` tries, each of which the hardware may suspend for a while.  (A
+// time-limit operand would make it a sleeping loop, which wakes up late.)
+// A wait that gives up sets `tries` to 0: the caller's further waits
 // then return at once, its loops run through, and the call is reported as
 // failed.  The loop is inside the statement so that the compiler sees no
 // branch, and what follows stays warp-uniform.

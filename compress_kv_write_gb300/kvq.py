@@ -53,6 +53,7 @@ _SIGS = {
     "kvq_dequant_slots": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int,
                                     C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
     "kvq_attend_workspace": (C.c_size_t, [C.c_int64]),
+    "kvq_attend_wait_limit": (C.c_uint32, [C.c_uint32]),
     "kvq_attend": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
                              C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
                              C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
@@ -348,6 +349,14 @@ def kvq_compress_decode(layout, page_bits, ratio, flags, values, scores, state, 
 def attend_workspace(rows):
     """Bytes of workspace for kvq_attend (rows = q_len * heads) or kvq_attend_slots (rows = heads)."""
     return int(lib().kvq_attend_workspace(int(rows)))
+
+
+def attend_wait_limit(tries):
+    """Sets how often a wait inside the attention kernels tries before a later call gives up with DEVERR_WAIT
+    (2^20 by default, at most 2^24; 0: every call gives up) and returns the limit before."""
+    if not 0 <= tries < 1 << 32:
+        raise ValueError("tries must be a 32-bit count")
+    return int(lib().kvq_attend_wait_limit(int(tries)))
 
 
 def _attend_rows(q, out, lse, workspace, err):

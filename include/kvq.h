@@ -208,6 +208,14 @@ kvq_status kvq_dequant_slots(kvq_layout layout, int page_bits,
  * workspaces of their own (captured graphs too, unless they run in turn). */
 size_t kvq_attend_workspace(int64_t rows);
 
+/* How often a wait inside the attention kernels (for another warp's part of
+ * the work) tries before the call gives up with KVQ_DEVERR_WAIT; the default
+ * is 2^20, which takes some seconds, far beyond any wait of a sound call.  Sets
+ * the limit of the process's later calls (at most 2^24; a captured call keeps
+ * the one it was captured with) and returns the one before.  With 0 every call
+ * gives up, which is how a program can test what it does then. */
+uint32_t kvq_attend_wait_limit(uint32_t tries);
+
 /* Latent attention over a paged pool: the reader of the rows that kvq_store
  * and kvq_compress write.  Every head of a query token attends over the same
  * row k[t] (512 values) of a cached token, as key and as value:
