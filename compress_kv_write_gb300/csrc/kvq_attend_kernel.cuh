@@ -333,6 +333,12 @@ __device__ __forceinline__ float rows_sum(float v) {
 // Barrier of the softmax warps; the second form returns whether any of
 // their threads brought true.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The other warps tell that they are done, the softmax warps wait for that.
+__device__ __forceinline__ void done_arrive() {
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"n"(kAttendThreads) : "memory");
+}
+__device__ __forceinline__ void done_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kAttendThreads) : "memory"); }
 __device__ __forceinline__ bool soft_any(bool p) {
     uint32_t r;
     asm volatile(
@@ -561,6 +567,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             k = kn;
         }
         if (!tries) sh.abort = 1;
+        done_arrive();
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------ products
         if (warp == kMmaWarp) {
@@ -729,6 +736,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
             if (!tries) sh.abort = 1;
         }
+        done_arrive();
     } else {
         // ------------------------------------------------------ softmax, queries, outputs
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -1114,16 +1122,38 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             }
         }
         if (!tries) sh.abort = 1;
+        done_sync();
+        if (*const_cast<volatile int *>(&sh.abort)) {  // the same for every thread
+            // A wait gave up: the rows that this CTA worked on are NaN, at once or by way of the join.
+            if (tid == 0) raise_err(a.err, KVQ_DEVERR_WAIT);
+            int tile = sh.start_tile, kb = sh.start_kb;
+#pragma unroll 1
+            for (int left = units; left > 0; ++tile, kb = 0) {
+                const TileInfo t = tile_info<N, kSlots>(a, tile);
+                const int blocks = min(left, t.nb - kb);
+                left -= blocks;
+                if (blocks < t.nb) {
+                    if (tid < N) *reinterpret_cast<float2 *>(part_of(kb) + tid * kPartRow + kD) = make_float2(NAN, NAN);
+                    continue;
+                }
+#pragma unroll 1
+                for (int r = warp; r < N && t.rt * N + r < per; r += kSoftWarps) {
+                    const int row = t.rt * N + r, j = row / a.heads;
+                    const int64_t to = (int64_t(t.seq) * a.q_len + j) * a.out_tok + (row - j * a.heads) * a.out_head;
+                    for (int d = lane; d < kD; d += 32) {
+                        if (a.out_bf16) static_cast<uint16_t *>(a.out)[to + d] = 0x7FFF;
+                        else static_cast<float *>(a.out)[to + d] = NAN;
+                    }
+                    if (a.lse && lane == 0) a.lse[int64_t(t.seq) * per + row] = NAN;
+                }
+            }
+        }
     }
     __syncwarp();
     if (tid == 0) pdl_trigger();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && sh.abort) {
-        raise_err(a.err, KVQ_DEVERR_WAIT);
-        a.join[blockIdx.x] = make_int2(-1, 0);
-    }
     if (warp == kMmaWarp) tmem_dealloc(sh.tmem, kTmemCols);
 }
 

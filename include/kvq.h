@@ -70,8 +70,8 @@ enum {
     KVQ_DEVERR_POS = 2,   /* a RoPE position outside [0, cos_sin_rows) (skipped) */
     KVQ_DEVERR_PAGE = 4,  /* a page-table entry outside [0, pool_pages) (skipped)*/
     KVQ_DEVERR_LOC = 8,   /* a full slot outside the translation table (-> -1)   */
-    KVQ_DEVERR_WAIT = 16, /* an attention kernel gave up a bounded wait: the      */
-                          /* call's outputs are not valid                         */
+    KVQ_DEVERR_WAIT = 16, /* an attention kernel gave up a bounded wait: the rows */
+                          /* and lse that it worked on are NaN                    */
     KVQ_DEVERR_STATE = 32,   /* a request index outside [0, n_state) or a count   */
                              /* outside [0, ratio): that request is skipped; in   */
                              /* kvq_attend a table row outside [0, table_rows)    */

@@ -3,7 +3,8 @@
 With a limit of 0 every wait inside the kernel ends at once, as if its time had
 run out: the warps run through their loops over whatever their buffers hold, all
 at addresses that do not depend on data, wait for the products they issued and
-return.
+return.  What the call should have written is NaN then, so that a caller without
+an error word sees it too.
 """
 import contextlib
 
@@ -68,3 +69,28 @@ def test_other_bits_stay_beside_it(K):
         c.run(K, out=big[:2], kv_len=torch.tensor([70, -1], dtype=torch.int32, device=DEV), err=err)
     assert err.item() == DEVERR_WAIT + 64
     assert (big[2:] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads,q_len,lens", CASES)
+def test_rows_are_nan(K, layout, dtype, heads, q_len, lens):
+    """Whole tiles, tiles that are joined, empty sequences: all of q's rows, and nothing behind them."""
+    c = Paged(layout, 6, lens, heads, q_len, seed=heads)
+    n = len(lens) * q_len
+    big = torch.full((n + 1, heads + 1, 520), 3.0, dtype=dtype, device=DEV)
+    with no_waiting(K):
+        out, lse = c.run(K, out=big[:n, :heads, :512])
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    big[:n, :heads, :512] = 3
+    assert (big == 3).all()
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+def test_rows_by_slots_are_nan(K, layout):
+    pool = make_pool(layout, 6, 512, 3)
+    s = torch.arange(300 * 300, dtype=torch.int32).view(300, 300) % 512
+    s[7] = -1
+    with no_waiting(K):
+        out, lse = run_slots(K, layout, 6, pool, 512, queries(300, 24, 5), s, out=torch.zeros((300, 24, 512), device=DEV))
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
