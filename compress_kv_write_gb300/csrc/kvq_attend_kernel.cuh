@@ -1084,7 +1084,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         }
                     tc_wait_st();
                 }
-                if (tries) {
+                if (__all_sync(0xFFFFFFFFu, tries != 0)) {  // for the warp: loads of TMEM and shuffles follow
 #pragma unroll 1
                     for (int b = 2 * half; b < 2 * half + 2; ++b) {
                         const int d = b * kChunk + t_row;
