@@ -47,19 +47,37 @@ struct NormQuantArgs {
     int64_t codes_stride, scales_stride;
 };
 
-template <bool kBf16>
+// 16 bytes; with kShared of memory that this kernel may write (residual_out may be an input), so not by way of the
+// read-only path.
+template <bool kShared>
+__device__ __forceinline__ uint4 load16(const uint8_t *p) {
+    if constexpr (!kShared) return ld_stream_u4(p);
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
+template <bool kBf16, bool kShared>
 __device__ __forceinline__ void load8(const uint8_t *p, float (&v)[8]) {
+    const uint4 u = load16<kShared>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     if constexpr (kBf16) {
-        const uint4 u = ld_stream_u4(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = bf16_lo(w[i]);
             v[2 * i + 1] = bf16_hi(w[i]);
         }
     } else {
-        const float4 a = ld_f4(reinterpret_cast<const float *>(p)), b = ld_f4(reinterpret_cast<const float *>(p) + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        const uint4 u2 = load16<kShared>(p + 16);
+        const uint32_t w2[4] = {u2.x, u2.y, u2.z, u2.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(w[i]);
+            v[4 + i] = __uint_as_float(w2[i]);
+        }
     }
 }
 
@@ -84,10 +102,10 @@ __global__ void __launch_bounds__(kNqThreads<W>) norm_quant_kernel(const NormQua
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[i][e] = 0.f;
         if (live && p < pieces) {
-            load8<kBf16>(a.x + row * a.x_stride + int64_t(p) * kPieceBytes, z[i]);
+            load8<kBf16, kRes>(a.x + row * a.x_stride + int64_t(p) * kPieceBytes, z[i]);
             if constexpr (kRes) {
                 float r[8];
-                load8<kBf16>(a.res + row * a.res_stride + int64_t(p) * kPieceBytes, r);
+                load8<kBf16, kRes>(a.res + row * a.res_stride + int64_t(p) * kPieceBytes, r);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[i][e] += r[e];
             }
