@@ -181,6 +181,20 @@ kvq_status launch_nq(const NormQuantArgs &a, cudaStream_t s) {
     return launch_pdl(norm_quant_kernel<kBf16, kRes, W, ITER>, dim3(unsigned(blocks)), dim3(kNqThreads<W>), s, a);
 }
 
+// Whether some of n rows of `width` bytes, `as` apart from `a`, share a byte with some of n such rows `bs` apart from
+// `b`; as, bs >= width.
+bool rows_overlap(const void *a_ptr, int64_t as, const void *b_ptr, int64_t bs, int64_t width, int64_t n) {
+    const int64_t a = int64_t(reinterpret_cast<uintptr_t>(a_ptr)), b = int64_t(reinterpret_cast<uintptr_t>(b_ptr));
+    if (a + (n - 1) * as + width <= b || b + (n - 1) * bs + width <= a) return false;
+    // Row i of a against the first row of b that ends behind its start.  With one stride only i - j counts, so the first
+    // and the last row stand for all.
+    for (int64_t i = 0; i < n; i += as == bs && n > 1 ? n - 1 : 1) {
+        const int64_t at = a + i * as, j = at < b + width ? 0 : (at - b - width) / bs + 1;
+        if (j < n && b + j * bs < at + width) return true;
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace kvq
 
@@ -204,6 +218,15 @@ extern "C" kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n
     if (!rows_ok(x, x_row_stride)) return KVQ_ERR_INVALID_ARG;
     if (residual && (!rows_ok(residual, residual_row_stride) || !rows_ok(residual_out, residual_out_row_stride)))
         return KVQ_ERR_INVALID_ARG;
+    if (residual) {  // residual_out is an input, row for row, or apart from it
+        auto clash = [&](const void *in, int64_t stride) {
+            if (in == residual_out && (n == 1 || stride == residual_out_row_stride)) return false;
+            const int64_t width = dim * item;
+            return rows_overlap(residual_out, n == 1 ? width : residual_out_row_stride * item, in,
+                                n == 1 ? width : stride * item, width, n);
+        };
+        if (clash(x, x_row_stride) || clash(residual, residual_row_stride)) return KVQ_ERR_INVALID_ARG;
+    }
     if (!weight || !aligned(weight, 16)) return KVQ_ERR_INVALID_ARG;
     if (!codes || !aligned(codes, 8) || (n > 1 && (codes_stride < dim || codes_stride % 8 != 0)))
         return KVQ_ERR_INVALID_ARG;

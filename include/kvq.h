@@ -293,10 +293,12 @@ kvq_status kvq_attend_slots(kvq_layout layout, int page_bits,
  *   dim           a multiple of 32, at most 16384.
  *   weight        [dim] fp32, 16-B aligned.
  *   residual_out  rows like x's; given exactly when residual is; it may be
- *                 residual itself, or x.
+ *                 residual itself, or x, with that one's row stride; rows
+ *                 that overlap an input's otherwise are refused.
  *   codes         [n, codes_stride] bytes, codes_stride a multiple of 8,
  *                 8-B aligned.
- *   scales        [n, scales_stride] bytes, dim / 32 used a row. */
+ *   scales        [n, scales_stride] bytes, dim / 32 used a row.
+ * codes and scales overlap no other array. */
 kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n, int64_t dim, int64_t x_row_stride,
                           const void *residual, int64_t residual_row_stride,
                           void *residual_out, int64_t residual_out_row_stride,

@@ -45,3 +45,13 @@ def test_placements(K, dtype, n, dim):
     both = x.clone()
     got = run(K, both, w, both, both)                                   # x is the residual too
     assert torch.equal(bits(got[2]), bits((x.float() + x.float()).to(dtype)))
+
+
+def test_overlaps_are_refused(K):
+    buf = torch.zeros((40, 512), dtype=torch.bfloat16, device=DEV)
+    x, w = torch.zeros((8, 512), dtype=torch.bfloat16, device=DEV), torch.ones(512, device=DEV)
+    for r, out in ((buf[:8], buf[1:9]), (buf[0:16:2], buf[0:24:3]), (buf[:8], buf[0:16:2])):
+        with pytest.raises(K.KVQError):
+            run(K, x, w, r, out)
+    run(K, x, w, buf[:8], buf[8:16])
+    run(K, x, w, buf[0:16:2], buf[1:17:2])
