@@ -127,11 +127,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(dev):
+    """The current stream of a device.  torch's raw handle where it has one: a Stream object costs more than the rest
+    of a small call's binding."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _stream(stream):
-    if stream is None:
-        # the raw handle: a Stream object costs more than the rest of a small call's binding
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _idx_dtype(t, name):
@@ -165,7 +169,7 @@ def _err_word(err):
 
 def _on(dev, stream, call):
     """status = call(stream pointer) with `dev` current; the default stream is that device's current one."""
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
     if dev == torch.cuda.current_device():
         return call(s)
     with torch.cuda.device(dev):
