@@ -263,9 +263,13 @@ constexpr int kMinScaleByte = 127 - 40;
 // the sum takes E (2^93 at most, and 2^-89 at least for the token that is the maximum), the outputs E 2^(texp - kLift).
 constexpr int kLift = 32;
 
-// scale 2^(127 - up) 2^lift, within fp32's finite values (a score that is 0 stays 0, whatever its factor).
+// scale 2^(127 - up) 2^lift, within fp32's finite values (a score that is 0 stays 0, whatever its factor).  A query row
+// that is not finite, whose scores are infinite or NaN one and all, has the factor NaN, as all scores of -inf would look
+// like no token seen.
+constexpr uint32_t kUpNotFinite = 268 - 255;
 template <Layout L>
 __device__ __forceinline__ float score_factor(float scale, uint32_t up) {
+    if (up == kUpNotFinite) return NAN;
     const int e = 127 - int(up) + (L == Layout::V41 ? kLift : 0), half = e / 2;  // -127 .. 146
     const float f = scale * __uint_as_float(uint32_t(127 + half) << 23) * __uint_as_float(uint32_t(127 + e - half) << 23);
     return fminf(fmaxf(f, -3.4e38f), 3.4e38f);

@@ -252,7 +252,9 @@ uint32_t kvq_attend_wait_limit(uint32_t tries);
  * The result does not depend on anything but the arguments (no atomics on
  * data).
  * A visible token whose row holds a NaN or an infinity makes the rows that
- * see it NaN, and no others; what masked tokens hold does not matter.
+ * see it NaN, and no others; what masked tokens hold does not matter, nor does
+ * the pool's first row where it is no one's.  A query row that holds a NaN or
+ * an infinity is NaN itself, and its lse, where it sees a token.
  * A bad kv_len (KVQ_DEVERR_LEN) or req (KVQ_DEVERR_STATE) makes the sequence
  * an empty one; a table entry outside [0, pool_pages) (KVQ_DEVERR_PAGE) masks
  * its tokens.  Entries past a sequence's kv_len are not read. */
