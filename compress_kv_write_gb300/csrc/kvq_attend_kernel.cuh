@@ -9,8 +9,8 @@
 // cached rows on the tensor cores' wide side (M = 64 tokens, M = 128 dims) and
 // the query rows on the narrow one (N = 16, 32, 64), so few heads waste no
 // more than their tile's padding.  m_r lags: a block moves it, and rescales O
-// in TMEM, only when a score passes it by kStaleMax, as 2^14 times a weight
-// still fits fp16; after a tile's first block that is rare.
+// in TMEM, only when a weight would pass 2^kStaleMax, which still fits fp16;
+// after a tile's first block that is rare.
 //
 // A block is decoded once for both products: 16 bits a value into shared
 // memory (the A operand of O^T, dims contiguous) and into TMEM (the A operand
@@ -25,22 +25,31 @@
 // ones are packed.  Tiles that a cut passes through leave partial sums, which
 // attend_join_kernel adds in order, so the result does not depend on timing.
 //
-// Rules for N by the rows of a sequence (kvq_attend.cuh): V41, one sequence of
-// 100 tokens / 48 of 1,024 to 8,192 (before the prefetch), in us: 16 heads as 16 rows 9.7 / 39, as 32
-// 10.9 / 45, as 64 13.2 / 60; 32 heads as 32 rows 11.1 / 45, as 64 13.4 / 61;
-// 64 heads as 64 rows 13.5 / 64, as twice 32 11.2 / 77.
+// Rules for N by the rows of a sequence (kvq_attend.cuh), in us, one sequence of
+// 100 tokens / 48 of 1,024 to 8,192 tokens:
+//             V41, as 16    32         64           FP4, as 16    32         64
+//   16 heads  10.2 / 38   11.4 / 45  14.1 / 61      10.1 / 37   11.2 / 43  13.9 / 58
+//   32 heads              11.5 / 45  14.2 / 61                  11.3 / 43  14.0 / 59
+//   64 heads              11.5 / 78  14.4 / 64                  11.4 / 74  14.1 / 61
+// (64 heads as twice 32: shorter where there are two blocks in all, longer from
+// then on.)
 //
-// What bounds it: a block of 64 tokens takes about 2,300 clocks at N = 16 and
-// 3,100 at N = 64 (0.42 PFLOP/s; tensor cores 1,240 and 1,850 of them), and no
-// unit is full.  The rest is the chain of a block: its outputs free the slots
+// What bounds it: a block of 64 tokens takes 2,150 to 2,180 clocks at N = 16,
+// 2,270 (FP4) to 2,400 (V41) at N = 32, 2,810 to 3,060 at N = 64 (152 equal
+// sequences, 40 against 200 blocks, at 2,070 MHz: 0.3, 0.6 and 0.9 PFLOP/s, of
+// which tensor cores need about 1,240 clocks at N = 16 and 1,850 at N = 64), and
+// no unit is full.  The rest is the chain of a block: its outputs free the slots
 // that the block after the next is decoded into (wait 100, codes from L2 to
 // registers, conversions and stores 500, fences 250), then the scores (600 to
 // 1,100), the softmax (1,200 to 1,500) and the outputs (700 to 800); two blocks
-// are under way at a time.  With blocks of 128 tokens 129 x 2,048 slots of 32
-// heads take 65 instead of 55 us and long calls 1 to 4 % longer (a call of two
-// blocks 8.4 instead of 9.8); a ring of three blocks at N = 16, a second code
-// buffer in registers, two score buffers at N = 64 and one wait for a block's
-// four chunks change nothing or cost up to 10 %.
+// are under way at a time.  A tile costs 3.2, 4.7 and 8.8 us besides (queries,
+// first maximum, outputs; 80 blocks a CTA as one tile or as eight), and shares
+// count blocks alone: CTAs that hold many short tiles end last.  With blocks of
+// 128 tokens 129 x 2,048 slots of 32 heads take 65 instead of 55 us and long
+// calls 1 to 4 % longer (a call of two blocks 8.4 instead of 9.8); a ring of
+// three blocks at N = 16, a second code buffer in registers, two score buffers
+// at N = 64 and one wait for a block's four chunks change nothing or cost up to
+// 10 %.
 #pragma once
 
 #include <math.h>
@@ -260,7 +269,7 @@ constexpr int kMinScaleByte = 127 - 40;
 // The weights of the outputs are relative to the running maximum m of score + texp, 2^(x - m); their sum, which has no
 // row in it, takes 2^(x - m - texp).  A row of small power beside one of large power has a weight that fp32 cannot hold
 // in the first and can have as large a share of the second as any, so what is computed is E = 2^(x - m - texp + kLift):
-// the sum takes E (2^93 at most, and 2^-89 at least for the token that is the maximum), the outputs E 2^(texp - kLift).
+// the sum takes E (2^94 at most, and 2^-89 at least for the token that is the maximum), the outputs E 2^(texp - kLift).
 constexpr int kLift = 32;
 
 // scale 2^(127 - up) 2^lift, within fp32's finite values (a score that is 0 stays 0, whatever its factor).  A query row

@@ -248,9 +248,22 @@ uint32_t kvq_attend_wait_limit(uint32_t tries);
  * most 2^-40 of it, and a block whose scale is 2^-32 of the row's largest or
  * less counts as zeros.  (A row whose largest scale is below 2^-40 counts as
  * if it were 2^-40.)  A softmax weight, for V41 times its row's power of two, is
- * rounded to fp16: relative 2^-11, or 2^-25 of the largest where that is more.
- * The result does not depend on anything but the arguments (no atomics on
- * data).
+ * rounded to fp16: relative 2^-11, or, for weights of 2^-14 of the largest and
+ * less, by an amount that all of a CTA's tokens together bring to no more than
+ * 2^-13 of the largest weight (of n > 2^26 tokens, n 2^-39): a long tail of
+ * small weights keeps its share.  The softmax sum takes the weights in fp32.
+ * The tensor cores round their sums down; no more than 256 blocks of 64 tokens
+ * are summed there before they are added to the rest, rounded to nearest.
+ * Scores have to stay within fp32.
+ * The result does not depend on anything but the arguments and the number of
+ * SMs (no atomics on data).
+ * The causal bound moves by one cached row a query token.  Over a pool that
+ * kvq_compress wrote, where a row stands for several tokens, pass every query
+ * token as a sequence of its own (q_len 1, req for the shared table row) with
+ * the kv_len that it sees.
+ * At most 2^20 query tokens a sequence, 1,024 heads and 2^24 query tokens in
+ * all; more, or more blocks of 64 tokens a CTA than an int holds (taken from
+ * table_width, whatever the lengths), is KVQ_ERR_UNSUPPORTED.
  * A visible token whose row holds a NaN or an infinity makes the rows that
  * see it NaN, and no others; what masked tokens hold does not matter, nor does
  * the pool's first row where it is no one's.  A query row that holds a NaN or
