@@ -1,0 +1,467 @@
+// kvq_evict.cu -- eviction from the paged cache by accumulated attention
+// weight: which tokens of a sequence stay (kvq_evict_select), and their rows
+// moved, in order, to pages of their own (kvq_evict_move).
+#include "kvq_launch.cuh"
+
+namespace kvq {
+namespace {
+
+// ---------------------------------------------------------------- selection
+// Of n tokens the first and last few stay anyway; of those between, the m of
+// most weight, among equals the ones that come first.  A weight becomes a
+// 32-bit key of the same order, and the m-th largest key is found digit by
+// digit from the top (11, 11 and 10 bits): a histogram of the digit over the
+// keys that share the digits found so far, and the bin in which the count from
+// the top passes m.  Then every token's fate is known from its key, but for
+// those equal to the m-th: of these the first ones stay.
+//
+// A sequence is a cluster's: its CTAs have equal pieces of it in order, hold
+// their keys in shared memory (one pass over global memory) and add up their
+// histograms there.  Places in the output come from counts: of the CTAs
+// before, of the warps before, and of the lanes before by ballot.
+//
+// Bound by latency: three rounds of clear, count, add up and search, each with
+// barriers of the cluster.
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kSelKeys = 40960;  // keys a CTA can hold; the others are read again
+
+struct SelectArgs {
+    const float *mass;
+    int64_t stride;
+    const int32_t *rows;
+    int64_t n_rows;
+    int64_t width;  // tokens a row of weights has
+    const int32_t *kv_len;
+    int32_t *kept;
+    int64_t kept_stride;
+    int keep, first, last;
+    int32_t *count;
+    int32_t *err;
+    int held;  // keys that a CTA holds
+};
+
+// Larger weight, larger key; zeros are equal, a NaN is above everything.
+__device__ __forceinline__ uint32_t mass_key(float m) {
+    const uint32_t b = __float_as_uint(m);
+    if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+    if (b == 0x80000000u) return 0x80000000u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A 32-bit word at a shared-window address of this CTA, of another CTA of the cluster.
+__device__ __forceinline__ uint32_t lds_of(uint32_t addr, uint32_t rank) {
+    uint32_t at, r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+
+struct SelShared {
+    uint32_t hist[2][kBins];  // by turns, so that a CTA may be counting while another still reads
+    uint32_t warp[kSelWarps];
+    uint32_t gt, eq;          // this CTA's tokens above the m-th key, and equal to it
+    uint32_t bin, above;
+};
+
+// Sum over the warps before this one, of a value that every lane of a warp has; `total`: over all.
+__device__ __forceinline__ uint32_t before_warp(SelShared &sh, uint32_t v, uint32_t &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = v;
+    __syncthreads();
+    const uint32_t of = sh.warp[lane];
+    uint32_t incl = of;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    return __shfl_sync(0xFFFFFFFFu, incl - of, warp);
+}
+
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a, int cluster) {
+    extern __shared__ uint8_t smem[];
+    auto &sh = *reinterpret_cast<SelShared *>(smem);
+    uint32_t *const held = reinterpret_cast<uint32_t *>(smem + sizeof(SelShared));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int seq = int(blockIdx.x) / cluster;
+    const int rank = cluster > 1 ? int(cluster_rank()) : 0;
+    auto sync_all = [&]() {
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
+    };
+    pdl_wait();
+    int64_t n = __ldg(a.kv_len + seq);
+    int64_t row = a.rows ? __ldg(a.rows + seq) : seq;
+    int bits = 0;
+    if (row < 0 || row >= a.n_rows) bits = KVQ_DEVERR_STATE;
+    else if (n < 0 || n > a.width) bits = KVQ_DEVERR_LEN;
+    if (bits) {
+        n = 0;
+        row = 0;
+        if (tid == 0 && rank == 0) raise_err(a.err, bits);
+    }
+    int32_t *const out = a.kept + seq * a.kept_stride;
+    const int count = int(min(n, int64_t(a.keep)));
+    // what does not depend on the weights: the first and the last, or all, and the entries of no token
+    const bool all = n <= a.keep;
+    for (int k = rank * kSelThreads + tid; k < a.keep; k += cluster * kSelThreads) {
+        if (all) out[k] = k < count ? k : -1;
+        else if (k < a.first) out[k] = k;
+        else if (k >= a.keep - a.last) out[k] = int(n) - (a.keep - k);
+    }
+    if (rank == 0 && tid == 0) a.count[seq] = count;
+    const int m = a.keep - a.first - a.last;
+    if (all || m == 0) return;  // the same for the whole cluster
+
+    // this CTA's piece [t0, t1) of the tokens between
+    const int between = int(n) - a.first - a.last;
+    const int per = (between + cluster - 1) / cluster;
+    const int t0 = min(between, rank * per), t1 = min(between, t0 + per), mine = t1 - t0;
+    const float *const from = a.mass + row * a.stride + a.first + t0;
+    const int in_smem = min(mine, a.held);
+    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    constexpr int kBatch = 4;  // loads under way
+    for (int i = tid; i < in_smem; i += kBatch * kSelThreads) {
+        float v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (i + b * kSelThreads < in_smem) v[b] = __ldg(from + i + b * kSelThreads);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (i + b * kSelThreads < in_smem) held[i + b * kSelThreads] = mass_key(v[b]);
+    }
+    pdl_trigger();
+    __syncthreads();
+    auto key = [&](int i) { return i < in_smem ? held[i] : mass_key(__ldg(from + i)); };
+
+    // the m-th largest key, from the top: `prefix` its digits so far, `left` how many of the keys with these digits stay
+    uint32_t prefix = 0, left = uint32_t(m);
+#pragma unroll 1
+    for (int round = 0; round < 3; ++round) {
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, digit = round == 2 ? 1024 : 2048;
+        uint32_t *const hist = sh.hist[round & 1];
+        if (round == 2) {  // its first use is over: every CTA has read it before the last barrier
+            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+        }
+        const uint32_t same = round == 0 ? 0u : 0xFFFFFFFFu << (round == 1 ? 21 : 10);
+        for (int i0 = warp * 32; i0 < mine; i0 += kSelThreads) {
+            const int i = i0 + lane;
+            uint32_t bin = 0xFFFFFFFFu;
+            if (i < mine) {
+                const uint32_t k = key(i);
+                if (((k ^ prefix) & same) == 0) bin = (k >> shift) & (digit - 1);
+            }
+            // many weights are the same (zero): the lanes with the first one's bin count as one
+            const uint32_t some = __ballot_sync(0xFFFFFFFFu, bin != 0xFFFFFFFFu);
+            if (some == 0) continue;
+            const int lead = __ffs(some) - 1;
+            const uint32_t first = __shfl_sync(0xFFFFFFFFu, bin, lead);
+            const uint32_t like = __ballot_sync(0xFFFFFFFFu, bin == first);
+            if (lane == lead) atomicAdd(&hist[first], __popc(like));
+            else if (bin != 0xFFFFFFFFu && bin != first) atomicAdd(&hist[bin], 1u);
+        }
+        sync_all();
+        // thread t has bins digit - 1 - 2 t and the one below (from the top), summed over the cluster
+        uint32_t c0 = 0, c1 = 0;
+        const int top = digit - 1 - 2 * tid;
+        if (top > 0) {
+            if (cluster > 1) {
+                const uint32_t at = smem_addr(hist + top - 1);
+                for (int r = 0; r < cluster; ++r) c1 += lds_of(at, r), c0 += lds_of(at + 4, r);
+            } else {
+                c0 = hist[top], c1 = hist[top - 1];
+            }
+        }
+        uint32_t incl = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        uint32_t total;
+        const uint32_t before = before_warp(sh, __shfl_sync(0xFFFFFFFFu, incl, 31), total) + incl - c0 - c1;
+        if (before < left && before + c0 >= left) {
+            sh.bin = top;
+            sh.above = before;
+        } else if (before + c0 < left && before + c0 + c1 >= left) {
+            sh.bin = top - 1;
+            sh.above = before + c0;
+        }
+        __syncthreads();
+        prefix |= sh.bin << shift;
+        left -= sh.above;
+    }
+
+    // counts: every warp has a piece of the CTA's in order
+    const int wper = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31;
+    const int w0 = min(mine, warp * wper), w1 = min(mine, w0 + wper);
+    uint32_t gt = 0, eq = 0;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const uint32_t k = i0 + lane < w1 ? key(i0 + lane) : 0u;
+        gt += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < w1 && k > prefix));
+        eq += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < w1 && k == prefix));
+    }
+    uint32_t gt_all, eq_all;
+    uint32_t gt_before = before_warp(sh, gt, gt_all);
+    uint32_t eq_before = before_warp(sh, eq, eq_all);
+    if (cluster > 1) {
+        if (tid == 0) {
+            sh.gt = gt_all;
+            sh.eq = eq_all;
+        }
+        cluster_sync();
+        for (int r = 0; r < rank; ++r) {
+            gt_before += lds_of(smem_addr(&sh.gt), r);
+            eq_before += lds_of(smem_addr(&sh.eq), r);
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA's memory may still be read
+    }
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < w1 ? key(i) : 0u;
+        const uint32_t g = __ballot_sync(0xFFFFFFFFu, i < w1 && k > prefix);
+        const uint32_t e = __ballot_sync(0xFFFFFFFFu, i < w1 && k == prefix);
+        const uint32_t low = (1u << lane) - 1;
+        const uint32_t gb = gt_before + __popc(g & low), eb = eq_before + __popc(e & low);
+        const bool stays = ((g >> lane) & 1) || (((e >> lane) & 1) && eb < left);
+        if (stays) out[a.first + gb + min(eb, left)] = a.first + t0 + i;
+        gt_before += __popc(g);
+        eq_before += __popc(e);
+    }
+    if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- the move
+// Row kept[i][k] of sequence i becomes row k of its new pages: codes and scale
+// bytes as they are.  A warp has 8 tokens: eight lanes look up where these lie
+// and shall lie, then all rows' loads are under way before the first store.
+// Bound by memory: rows of 256 or 512 bytes, read and written once.
+constexpr int kMoveThreads = 256, kMoveTok = 8;
+
+struct MoveArgs {
+    uint8_t *pool;
+    int64_t pages;
+    int page_bits;
+    const int32_t *table, *to_table;
+    int64_t table_rows, table_stride, to_stride;
+    int64_t max_len;  // tokens that a row of the table, and of the weights, has
+    const int32_t *req;
+    const int32_t *kept;
+    int64_t kept_stride;
+    int keep;
+    int64_t groups;  // of 8 entries, a sequence
+    int64_t total;   // groups
+    const float *mass;
+    int64_t mass_stride;
+    const int32_t *rows;
+    int64_t n_rows;
+    float *mass_out;
+    int64_t mass_out_stride;
+    int32_t *err;
+};
+
+template <Layout L>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs a) {
+    using T = LayoutTraits<L>;
+    constexpr int kLanes = T::kCodeBytes / 16;           // lanes a code row
+    constexpr int kAtOnce = 32 / kLanes;                 // rows a load has
+    constexpr int kLoads = kMoveTok / kAtOnce;
+    constexpr int kScaleLanes = T::kScaleBytes / 16;     // lanes a scale row
+    const int lane = threadIdx.x & 31;
+    const int64_t group = (int64_t(blockIdx.x) * kMoveThreads + threadIdx.x) >> 5;
+    if (group >= a.total) return;
+    const int64_t seq = group / a.groups;
+    const int k = int(group % a.groups) * kMoveTok + lane;
+    pdl_wait();
+    const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits;
+    const int in_page = (1 << a.page_bits) - 1;
+    int64_t row = seq, mrow = seq;
+    if (a.req) row = __ldg(a.req + seq);
+    if (a.rows) mrow = __ldg(a.rows + seq);
+    int t = -1;
+    if (lane < kMoveTok && k < a.keep) t = __ldg(a.kept + seq * a.kept_stride + k);
+    int bits = 0;
+    if (t != -1 && (row < 0 || row >= a.table_rows || (a.mass && (mrow < 0 || mrow >= a.n_rows)))) bits = KVQ_DEVERR_STATE;
+    else if (t != -1 && (t < 0 || t >= a.max_len)) bits = KVQ_DEVERR_SLOT;
+    bool go = t != -1 && !bits;
+    int64_t from = 0, to = 0;  // pages
+    if (go) {
+        from = __ldg(a.table + row * a.table_stride + (t >> a.page_bits));
+        to = __ldg(a.to_table + seq * a.to_stride + (k >> a.page_bits));
+        if (from < 0 || from >= a.pages || to < 0 || to >= a.pages) {
+            bits = KVQ_DEVERR_PAGE;
+            go = false;
+        }
+    }
+    if (bits) raise_err(a.err, bits);
+    if (go && a.mass) a.mass_out[seq * a.mass_out_stride + k] = __ldg(a.mass + mrow * a.mass_stride + t);
+    const int r0 = t & in_page, r1 = k & in_page;
+    go = go && (from != to || r0 != r1);  // a row that stays where it is
+    // byte offsets of the code rows and of the scale rows
+    const int64_t c0 = from * page_bytes + int64_t(r0) * T::kCodeBytes, c1 = to * page_bytes + int64_t(r1) * T::kCodeBytes;
+    const int64_t area = int64_t(T::kCodeBytes) << a.page_bits;
+    const int64_t s0 = from * page_bytes + area + int64_t(r0) * T::kScaleBytes, s1 = to * page_bytes + area + int64_t(r1) * T::kScaleBytes;
+    const uint32_t live = __ballot_sync(0xFFFFFFFFu, go);
+    uint4 v[kLoads], sc;
+    int64_t at[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int j = i * kAtOnce + lane / kLanes;
+        const int64_t src = __shfl_sync(0xFFFFFFFFu, (long long)c0, j);
+        at[i] = __shfl_sync(0xFFFFFFFFu, (long long)c1, j);
+        if ((live >> j) & 1) v[i] = ld_stream_u4(a.pool + src + (lane % kLanes) * 16);
+    }
+    const int js = lane / kScaleLanes;
+    const int64_t ssrc = __shfl_sync(0xFFFFFFFFu, (long long)s0, js & (kMoveTok - 1));
+    const int64_t sdst = __shfl_sync(0xFFFFFFFFu, (long long)s1, js & (kMoveTok - 1));
+    const bool scales = js < kMoveTok && ((live >> js) & 1);
+    if (scales) sc = ld_stream_u4(a.pool + ssrc + (lane % kScaleLanes) * 16);
+    pdl_trigger();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int j = i * kAtOnce + lane / kLanes;
+        if ((live >> j) & 1) st_u4(a.pool + at[i] + (lane % kLanes) * 16, v[i]);
+    }
+    if (scales) st_u4(a.pool + sdst + (lane % kScaleLanes) * 16, sc);
+}
+
+bool apart(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x + uintptr_t(a_bytes) <= y || y + uintptr_t(b_bytes) <= x;
+}
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxSeqs = int64_t(1) << 20;
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kvq_status kvq_evict_select(const float *mass, int64_t mass_rows, int64_t mass_width, int64_t mass_row_stride,
+                                       const int32_t *rows, const int32_t *kv_len, int64_t n_seq, int64_t keep,
+                                       int64_t first, int64_t last, int32_t *kept, int64_t kept_stride, int32_t *count,
+                                       int32_t *err, struct CUstream_st *stream) {
+    if (n_seq < 0 || mass_rows < 0 || mass_width < 0 || keep < 1 || first < 0 || last < 0) return KVQ_ERR_INVALID_ARG;
+    if (first > keep || last > keep - first) return KVQ_ERR_INVALID_ARG;
+    if (mass_width > kMaxTokens || keep > kMaxTokens || n_seq > kMaxSeqs) return KVQ_ERR_UNSUPPORTED;
+    if (mass_rows > 1 && mass_row_stride < mass_width) return KVQ_ERR_INVALID_ARG;
+    if (err && !aligned(err, 4)) return KVQ_ERR_INVALID_ARG;
+    if (n_seq == 0) return KVQ_OK;
+    if (!rows && n_seq > mass_rows) return KVQ_ERR_INVALID_ARG;
+    if (mass_rows > 0 && mass_width > 0 && (!mass || !aligned(mass, 4))) return KVQ_ERR_INVALID_ARG;
+    if (!kv_len || !aligned(kv_len, 4) || (rows && !aligned(rows, 4))) return KVQ_ERR_INVALID_ARG;
+    if (!kept || !aligned(kept, 4) || (n_seq > 1 && kept_stride < keep) || !count || !aligned(count, 4)) return KVQ_ERR_INVALID_ARG;
+    SelectArgs a = {};
+    a.mass = mass;
+    a.stride = mass_row_stride;
+    a.rows = rows;
+    a.n_rows = mass_rows;
+    a.width = mass_width;
+    a.kv_len = kv_len;
+    a.kept = kept;
+    a.kept_stride = kept_stride;
+    a.keep = int(keep);
+    a.first = int(first);
+    a.last = int(last);
+    a.count = count;
+    a.err = err;
+    // CTAs a sequence: as many as leave each four tokens a thread
+    int cluster = 1;
+    while (cluster < kMaxCluster && mass_width > int64_t(cluster) * 4 * kSelThreads) cluster *= 2;
+    const int64_t per = (mass_width + cluster - 1) / cluster;
+    a.held = int(per < kSelKeys ? per : kSelKeys);
+    int64_t cap = 0;
+    kvq_status st = resident_grid<evict_select_kernel, kSelThreads>(sizeof(SelShared) + kSelKeys * 4, &cap);
+    if (st != KVQ_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(n_seq * cluster));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = sizeof(SelShared) + size_t(a.held) * 4;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return KVQ_ERR_LAUNCH;
+    }
+    return KVQ_OK;
+}
+
+extern "C" kvq_status kvq_evict_move(kvq_layout layout, int page_bits, uint8_t *pool, int64_t pool_pages,
+                                     const int32_t *page_table, int64_t table_rows, int64_t table_width,
+                                     int64_t table_stride, const int32_t *req, const int32_t *new_table,
+                                     int64_t new_width, int64_t new_stride, const int32_t *kept, int64_t n_seq,
+                                     int64_t keep, int64_t kept_stride, const float *mass, int64_t mass_rows,
+                                     int64_t mass_width, int64_t mass_row_stride, const int32_t *rows, float *mass_out,
+                                     int64_t mass_out_stride, int32_t *err, struct CUstream_st *stream) {
+    kvq_status st = check_pool(layout, page_bits, pool, pool_pages > 0 && pool_pages <= (int64_t(1) << 40) ? pool_pages << page_bits : 0);
+    if (st != KVQ_OK) return st;
+    if (n_seq < 0 || keep < 1 || table_rows < 0 || table_width < 0 || table_stride < table_width) return KVQ_ERR_INVALID_ARG;
+    if (keep > kMaxTokens || n_seq > kMaxSeqs || table_width > (kMaxTokens >> page_bits)) return KVQ_ERR_UNSUPPORTED;
+    if (new_width < 0 || (n_seq > 1 && new_stride < new_width) || new_width < ((keep - 1) >> page_bits) + 1) return KVQ_ERR_INVALID_ARG;
+    if (err && !aligned(err, 4)) return KVQ_ERR_INVALID_ARG;
+    if ((mass == nullptr) != (mass_out == nullptr)) return KVQ_ERR_INVALID_ARG;
+    if (!mass && rows) return KVQ_ERR_INVALID_ARG;
+    if (n_seq == 0) return KVQ_OK;
+    if (!req && n_seq > table_rows) return KVQ_ERR_INVALID_ARG;
+    if (table_rows > 0 && table_width > 0 && !page_table) return KVQ_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || (req && !aligned(req, 4)) || !new_table || !aligned(new_table, 4)) return KVQ_ERR_INVALID_ARG;
+    if (!kept || !aligned(kept, 4) || (n_seq > 1 && kept_stride < keep)) return KVQ_ERR_INVALID_ARG;
+    if (mass) {
+        if (mass_rows < 0 || mass_width < 0 || (mass_rows > 1 && mass_row_stride < mass_width)) return KVQ_ERR_INVALID_ARG;
+        if (!aligned(mass, 4) || !aligned(mass_out, 4) || (n_seq > 1 && mass_out_stride < keep)) return KVQ_ERR_INVALID_ARG;
+        if (rows ? !aligned(rows, 4) : n_seq > mass_rows) return KVQ_ERR_INVALID_ARG;
+        const int64_t in = mass_rows > 0 ? ((mass_rows - 1) * mass_row_stride + mass_width) * 4 : 0;
+        if (!apart(mass, in, mass_out, ((n_seq - 1) * mass_out_stride + keep) * 4)) return KVQ_ERR_INVALID_ARG;
+    }
+    MoveArgs a = {};
+    a.pool = pool;
+    a.pages = pool_pages;
+    a.page_bits = page_bits;
+    a.table = page_table;
+    a.to_table = new_table;
+    a.table_rows = table_rows;
+    a.table_stride = table_stride;
+    a.to_stride = new_stride;
+    a.max_len = table_width << page_bits;
+    if (mass && mass_width < a.max_len) a.max_len = mass_width;
+    a.req = req;
+    a.kept = kept;
+    a.kept_stride = kept_stride;
+    a.keep = int(keep);
+    a.groups = (keep + kMoveTok - 1) / kMoveTok;
+    a.total = a.groups * n_seq;
+    a.mass = mass;
+    a.mass_stride = mass_row_stride;
+    a.rows = rows;
+    a.n_rows = mass_rows;
+    a.mass_out = mass_out;
+    a.mass_out_stride = mass_out_stride;
+    a.err = err;
+    const int64_t per = kMoveThreads / 32, blocks = (a.total + per - 1) / per;
+    if (blocks > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return with_layout(layout, [&](auto Lc) {
+        return launch_pdl(evict_move_kernel<decltype(Lc)::value>, dim3(unsigned(blocks)), dim3(kMoveThreads), s, a);
+    });
+}

@@ -1,0 +1,440 @@
+// kvq_rope.cu -- rotary positions outside the store: the table of cosines and
+// sines that kvq_store reads (kvq_rope_table), and the rotation of rows that
+// are not stored, queries before the attention and its outputs after it
+// (kvq_rope).
+#include <math.h>
+
+#include "kvq_launch.cuh"
+
+namespace kvq {
+namespace {
+
+// ---------------------------------------------------------------- table
+// table[p, i] = A cos((first + p) f_i), table[p, h + i] = A sin(...), h = rot / 2.
+//
+// What matters of an angle is its fraction of a turn, and a fraction of a turn
+// times a whole number is exact in integers modulo 2^64: with
+// F = round(2^64 frac(f / 2 pi)) the phase of position p is p F mod 2^64, off
+// by p 2^-65 turns (and by p times the rounding of f / 2 pi, 2^-54 of it).  So
+// the 64-bit floating point that far positions would need, of which this GPU
+// has little (some 2 operations a clock and SM), is spent once a column and
+// CTA; a step of rows is an integer addition.  The top two bits (after half a
+// quarter is added) are the quadrant, the rest an angle within pi / 4 whose
+// sine and cosine are their Taylor series up to x^9 and x^10 (what is left out
+// is below 2^-28 and 2^-32).
+//
+// Bound by the stores: 1,048,576 x 64 in 44 us is 6.1 TB/s.
+constexpr int kTabThreads = 256;
+constexpr int kMaxRot = 1024;
+
+struct TableArgs {
+    const double *freq;
+    int h;
+    int64_t first, rows;
+    float amplitude;
+    float *table;
+};
+
+__device__ __forceinline__ void turn_sincos(uint64_t phase, float &s, float &c) {
+    const uint32_t hi = uint32_t(phase >> 32) + 0x20000000u;
+    const int32_t r = int32_t(hi & 0x3FFFFFFFu) - 0x20000000;  // a 2^32nd of a turn each
+    const float x = float(r) * 1.4629180792671596e-9f;         // 2 pi / 2^32
+    const float y = x * x;
+    float a = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);  // 1 / 9!, 1 / 7!
+    a = fmaf(y, a, 8.3333333e-3f);
+    a = fmaf(y, a, -1.6666667e-1f);
+    const float sx = fmaf(x * y, a, x);
+    float b = fmaf(y, -2.7557319e-7f, 2.4801587e-5f);  // 1 / 10!, 1 / 8!
+    b = fmaf(y, b, -1.3888889e-3f);
+    b = fmaf(y, b, 4.1666667e-2f);
+    b = fmaf(y, b, -0.5f);
+    const float cx = fmaf(y, b, 1.f);
+    const bool odd = hi & 0x40000000u;
+    s = odd ? cx : sx;
+    c = odd ? sx : cx;
+    s = __uint_as_float(__float_as_uint(s) ^ (hi & 0x80000000u));
+    c = __uint_as_float(__float_as_uint(c) ^ ((hi ^ (hi << 1)) & 0x80000000u));
+}
+
+// V columns a thread, the same ones in every row that it writes.
+template <int V>
+__global__ void __launch_bounds__(kTabThreads) rope_table_kernel(const TableArgs a) {
+    __shared__ uint64_t s_step[kMaxRot / 2];  // a column's phase for one position
+    __shared__ float s_amp[kMaxRot / 2];
+    pdl_wait();
+    for (int i = threadIdx.x; i < a.h; i += kTabThreads) {
+        const double t = a.freq[i] * 0.15915494309189535;  // 1 / 2 pi
+        const double f = t - floor(t);
+        s_step[i] = __double2ull_rn(f * 18446744073709551616.0);
+        s_amp[i] = fabs(t) < 4503599627370496.0 ? a.amplitude : NAN;  // no fraction is left of larger ones
+    }
+    __syncthreads();
+    pdl_trigger();
+    const int groups = a.h / V;                       // threads a row
+    const int per = groups < kTabThreads ? kTabThreads / groups : 1;  // rows a CTA has at a time
+    const int r0 = groups < kTabThreads ? threadIdx.x / groups : 0;
+    if (r0 >= per) return;
+    for (int g = groups < kTabThreads ? threadIdx.x % groups : threadIdx.x; g < groups; g += kTabThreads) {
+        uint64_t phase[V], step[V];
+        float amp[V];
+        int64_t row = int64_t(blockIdx.x) * per + r0;
+        const int64_t stride = int64_t(gridDim.x) * per;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            phase[v] = s_step[g * V + v] * uint64_t(a.first + row);
+            step[v] = s_step[g * V + v] * uint64_t(stride);
+            amp[v] = s_amp[g * V + v];
+        }
+        float *to = a.table + row * (2 * a.h) + g * V;
+        for (; row < a.rows; row += stride, to += stride * (2 * a.h)) {
+            float s[V], c[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                turn_sincos(phase[v], s[v], c[v]);
+                s[v] *= amp[v], c[v] *= amp[v];
+                phase[v] += step[v];
+            }
+            if constexpr (V == 4) {
+                *reinterpret_cast<float4 *>(to) = make_float4(c[0], c[1], c[2], c[3]);
+                *reinterpret_cast<float4 *>(to + a.h) = make_float4(s[0], s[1], s[2], s[3]);
+            } else {
+                to[0] = c[0];
+                to[a.h] = s[0];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- rotation
+// (u, v) -> (u c - v s, v c + u s), or with the sine's sign turned the way back
+// (the transpose).  A pair is neighbours (interleaved) or rot / 2 apart
+// (halves).  A row's work is cut into pieces of 16 bytes: pieces that are
+// copied (not where the rows are rotated in place) and pieces that are rotated,
+// with halves two at a time.  A thread has the same piece of several heads of
+// one token, so it reads its cosines and sines once; the heads' loads are all
+// under way before the first is used.
+//
+// Bound by memory: a value is read once and written once, and some 45
+// instructions go to the 32 bytes of a piece.
+constexpr int kRopeThreads = 256, kRopeBatch = 4;
+
+struct RopeArgs {
+    const uint8_t *x;
+    uint8_t *out;
+    int64_t x_tok, x_head, out_tok, out_head;  // bytes
+    int64_t n;
+    int heads, start, rot;  // elements
+    int pieces, front;      // pieces a row has, those of them before the rotated ones
+    int heads_cta, splits;  // heads a CTA has, CTAs a token
+    const float *cos_sin;
+    int64_t rows;
+    const int32_t *pos;
+    int32_t *err;
+    float sign;
+};
+
+// Not by way of the read-only path: the rows may be rotated in place.
+__device__ __forceinline__ uint4 load_row16(const uint8_t *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
+// One element, bf16 or fp32, from / to memory.
+template <bool kBf16>
+__device__ __forceinline__ float load_one(const uint8_t *p) {
+    if constexpr (kBf16) return __uint_as_float(uint32_t(*reinterpret_cast<const volatile uint16_t *>(p)) << 16);
+    else return *reinterpret_cast<const volatile float *>(p);
+}
+template <bool kBf16>
+__device__ __forceinline__ void store_one(uint8_t *p, float v) {
+    if constexpr (kBf16) *reinterpret_cast<uint16_t *>(p) = uint16_t(pack_bf16x2(v, 0.f));
+    else *reinterpret_cast<float *>(p) = v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack16(const uint4 u, float (&v)[kBf16 ? 8 : 4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kBf16) {
+            v[2 * i] = bf16_lo(w[i]);
+            v[2 * i + 1] = bf16_hi(w[i]);
+        } else {
+            v[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack16(const float (&v)[kBf16 ? 8 : 4]) {
+    if constexpr (kBf16)
+        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    else
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+template <bool kBf16, bool kHalf>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+    constexpr int E = kBf16 ? 8 : 4, kItem = kBf16 ? 2 : 4;
+    constexpr int kUse = kHalf ? E : E / 2;  // cosines of a piece
+    const int64_t tok = int64_t(blockIdx.x) / a.splits;
+    const int h0 = int(int64_t(blockIdx.x) % a.splits) * a.heads_cta, h1 = min(a.heads, h0 + a.heads_cta);
+    const int half = a.rot / 2;
+    const int turning = kHalf ? half / E : a.rot / E;  // pieces (of two) that are rotated
+    const int width = min(a.pieces, kRopeThreads), lines = kRopeThreads / width;
+    const int line = threadIdx.x / width;
+    pdl_wait();
+    const int32_t pos = __ldg(a.pos + tok);
+    const bool good = pos >= 0 && pos < a.rows;
+    if (!good) {
+        if (threadIdx.x == 0 && h0 == 0) raise_err(a.err, KVQ_DEVERR_POS);
+        return;
+    }
+    pdl_trigger();
+    if (line >= lines) return;
+    for (int piece = threadIdx.x % width; piece < a.pieces; piece += width) {
+        const bool turns = piece >= a.front && piece < a.front + turning;
+        // the piece's first element: those behind the rotated ones come after all of them
+        const int el = !turns && piece >= a.front ? (piece - turning) * E + a.rot : piece * E + (turns ? a.start - a.front * E : 0);
+        const uint8_t *from = a.x + tok * a.x_tok + int64_t(el) * kItem;
+        uint8_t *to = a.out + tok * a.out_tok + int64_t(el) * kItem;
+        float c[kUse], s[kUse];
+        if (turns) {
+            const float *t = a.cos_sin + int64_t(pos) * a.rot + (piece - a.front) * kUse;
+#pragma unroll
+            for (int i = 0; i < kUse; i += 2) {  // halves of a row need not be 16-byte aligned where rot / 2 is odd
+                const float2 cc = __ldg(reinterpret_cast<const float2 *>(t + i));
+                const float2 ss = __ldg(reinterpret_cast<const float2 *>(t + half + i));
+                c[i] = cc.x, c[i + 1] = cc.y;
+                s[i] = ss.x * a.sign, s[i + 1] = ss.y * a.sign;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUse; ++i) c[i] = 1.f, s[i] = 0.f;
+        }
+        for (int h = h0 + line; h < h1; h += kRopeBatch * lines) {
+            uint4 u[kRopeBatch], w[kHalf ? kRopeBatch : 1];
+#pragma unroll
+            for (int b = 0; b < kRopeBatch; ++b) {
+                const int hb = h + b * lines;
+                if (hb < h1) {
+                    u[b] = load_row16(from + hb * a.x_head);
+                    if constexpr (kHalf) {
+                        if (turns) w[b] = load_row16(from + hb * a.x_head + half * kItem);
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kRopeBatch; ++b) {
+                const int hb = h + b * lines;
+                if (hb >= h1) continue;
+                uint8_t *o = to + hb * a.out_head;
+                if (!turns) {
+                    st_u4(o, u[b]);
+                    continue;
+                }
+                float v[E];
+                unpack16<kBf16>(u[b], v);
+                if constexpr (kHalf) {
+                    float z[E];
+                    unpack16<kBf16>(w[b], z);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const float p = __fsub_rn(__fmul_rn(v[i], c[i]), __fmul_rn(z[i], s[i]));
+                        z[i] = __fadd_rn(__fmul_rn(z[i], c[i]), __fmul_rn(v[i], s[i]));
+                        v[i] = p;
+                    }
+                    st_u4(o, pack16<kBf16>(v));
+                    st_u4(o + half * kItem, pack16<kBf16>(z));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) {
+                        const float p = __fsub_rn(__fmul_rn(v[2 * i], c[i]), __fmul_rn(v[2 * i + 1], s[i]));
+                        v[2 * i + 1] = __fadd_rn(__fmul_rn(v[2 * i + 1], c[i]), __fmul_rn(v[2 * i], s[i]));
+                        v[2 * i] = p;
+                    }
+                    st_u4(o, pack16<kBf16>(v));
+                }
+            }
+        }
+    }
+}
+
+// The same, value by value: rows, heads or rotated parts that do not come in
+// pieces of 16 bytes.  A thread has one pair or one copied value of a head;
+// `pieces` counts these, pairs first.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const RopeArgs a, bool halves) {
+    constexpr int kItem = kBf16 ? 2 : 4;
+    const int64_t tok = int64_t(blockIdx.x) / a.splits;
+    const int h0 = int(int64_t(blockIdx.x) % a.splits) * a.heads_cta, h1 = min(a.heads, h0 + a.heads_cta);
+    const int half = a.rot / 2;
+    pdl_wait();
+    const int32_t pos = __ldg(a.pos + tok);
+    const bool good = pos >= 0 && pos < a.rows;
+    if (!good) {
+        if (threadIdx.x == 0 && h0 == 0) raise_err(a.err, KVQ_DEVERR_POS);
+        return;
+    }
+    pdl_trigger();
+    const float *t = a.cos_sin + int64_t(pos) * a.rot;
+    for (int64_t i = threadIdx.x; i < int64_t(h1 - h0) * a.pieces; i += kRopeThreads) {
+        const int h = h0 + int(i / a.pieces), k = int(i % a.pieces);
+        const uint8_t *from = a.x + tok * a.x_tok + h * a.x_head;
+        uint8_t *to = a.out + tok * a.out_tok + h * a.out_head;
+        if (k >= half) {  // copied
+            const int el = k - half < a.start ? k - half : k - half + a.rot;
+            store_one<kBf16>(to + el * kItem, load_one<kBf16>(from + el * kItem));
+            continue;
+        }
+        const int u = a.start + (halves ? k : 2 * k), v = halves ? u + half : u + 1;
+        const float c = __ldg(t + k), s = __ldg(t + half + k) * a.sign;
+        const float x = load_one<kBf16>(from + u * kItem), y = load_one<kBf16>(from + v * kItem);
+        store_one<kBf16>(to + u * kItem, __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s)));
+        store_one<kBf16>(to + v * kItem, __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s)));
+    }
+}
+
+// Whether rows of `dim` elements, (n, heads) of them, lie apart: one stride spans the other axis.
+bool rows_apart(int64_t n, int64_t heads, int64_t dim, int64_t tok, int64_t head) {
+    if (n > 1 && tok < dim) return false;
+    if (heads > 1 && head < dim) return false;
+    if (n > 1 && heads > 1) {
+        const bool by_token = tok >= head;
+        const int64_t inner = by_token ? head : tok, outer = by_token ? tok : head;
+        if (outer - dim < inner * ((by_token ? heads : n) - 1)) return false;
+    }
+    return true;
+}
+
+// Whether two sets of rows (elements' byte size `item`) certainly share no byte: apart as ranges, or with equal strides
+// beside each other in every pitch.
+bool sets_apart(const void *xp, const void *op, int64_t n, int64_t heads, int64_t dim, int64_t x_tok, int64_t x_head,
+                int64_t o_tok, int64_t o_head, int64_t item) {
+    const int64_t x = int64_t(reinterpret_cast<uintptr_t>(xp)), o = int64_t(reinterpret_cast<uintptr_t>(op));
+    const int64_t xs = ((n - 1) * x_tok + (heads - 1) * x_head + dim) * item;
+    const int64_t os = ((n - 1) * o_tok + (heads - 1) * o_head + dim) * item;
+    if (x + xs <= o || o + os <= x) return true;
+    if ((n > 1 && x_tok != o_tok) || (heads > 1 && x_head != o_head)) return false;
+    const int64_t tok = n > 1 ? x_tok : 0, head = heads > 1 ? x_head : 0;
+    const int64_t pitch = (tok && head ? (tok < head ? tok : head) : tok + head) * item;
+    if (pitch <= 0 || (tok * item) % pitch || (head * item) % pitch) return false;
+    const int64_t off = ((o - x) % pitch + pitch) % pitch;
+    return off >= dim * item && off <= pitch - dim * item;
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, int64_t rows, float amplitude,
+                                     float *table, struct CUstream_st *stream) {
+    if (rot_dim < 2 || rot_dim % 2 || rows < 0 || first < 0) return KVQ_ERR_INVALID_ARG;
+    if (rot_dim > kMaxRot || first + rows > 0x7FFFFFFFll || rows > 0x7FFFFFFFll) return KVQ_ERR_UNSUPPORTED;
+    if (!(amplitude - amplitude == 0.f)) return KVQ_ERR_INVALID_ARG;  // NaN or infinite
+    if (!freq || !aligned(freq, 8)) return KVQ_ERR_INVALID_ARG;
+    if (rows == 0) return KVQ_OK;
+    if (!table || !aligned(table, 16)) return KVQ_ERR_INVALID_ARG;
+    TableArgs a = {};
+    a.freq = freq;
+    a.h = int(rot_dim / 2);
+    a.first = first;
+    a.rows = rows;
+    a.amplitude = amplitude;
+    a.table = table;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // four columns a thread, stored as 16 bytes, where columns come in fours
+    return with_bool(a.h % 4 == 0, [&](auto Vc) {
+        constexpr int V = decltype(Vc)::value ? 4 : 1;
+        int64_t cap = 0;
+        kvq_status st = resident_grid<rope_table_kernel<V>, kTabThreads>(0, &cap);
+        if (st != KVQ_OK) return st;
+        const int64_t groups = a.h / V, per = groups < kTabThreads ? kTabThreads / groups : 1;
+        const int64_t need = (rows + per - 1) / per;
+        return launch_pdl(rope_table_kernel<V>, dim3(unsigned(need < cap ? need : cap)), dim3(kTabThreads), s, a);
+    });
+}
+
+extern "C" kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens, int64_t heads, int64_t dim,
+                               int64_t x_token_stride, int64_t x_head_stride, int64_t rot_start, int64_t rot_dim,
+                               unsigned flags, const float *cos_sin, int64_t cos_sin_rows, const int32_t *pos, void *out,
+                               int64_t out_token_stride, int64_t out_head_stride, int32_t *err,
+                               struct CUstream_st *stream) {
+    if (dtype != KVQ_F32 && dtype != KVQ_BF16) return KVQ_ERR_INVALID_ARG;
+    if (flags & ~unsigned(KVQ_ROPE_HALF | KVQ_ROPE_INVERSE)) return KVQ_ERR_INVALID_ARG;
+    if (n_tokens < 0 || heads < 1 || dim < 2 || cos_sin_rows < 0) return KVQ_ERR_INVALID_ARG;
+    if (rot_dim < 2 || rot_dim % 2 || rot_start < 0 || rot_dim > dim || rot_start > dim - rot_dim) return KVQ_ERR_INVALID_ARG;
+    if (rot_dim > kMaxRot || dim > (1 << 16) || heads > (1 << 16) || n_tokens > (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+    if (err && !aligned(err, 4)) return KVQ_ERR_INVALID_ARG;
+    if (n_tokens == 0) return KVQ_OK;
+    const int64_t item = dtype == KVQ_BF16 ? 2 : 4;
+    if (!x || !out || !aligned(x, item) || !aligned(out, item) || !pos || !aligned(pos, 4)) return KVQ_ERR_INVALID_ARG;
+    if (cos_sin_rows > 0 && (!cos_sin || !aligned(cos_sin, 8))) return KVQ_ERR_INVALID_ARG;
+    if (n_tokens == 1) x_token_stride = out_token_stride = 0;  // the stride of an axis of one element is never used
+    if (heads == 1) x_head_stride = out_head_stride = 0;
+    const int64_t most = int64_t(1) << 40;
+    if (x_token_stride < 0 || x_head_stride < 0 || x_token_stride > most || x_head_stride > most ||
+        out_token_stride > most || out_head_stride > most)
+        return KVQ_ERR_INVALID_ARG;
+    if (!rows_apart(n_tokens, heads, dim, out_token_stride, out_head_stride)) return KVQ_ERR_INVALID_ARG;
+    const bool in_place = x == out && x_token_stride == out_token_stride && x_head_stride == out_head_stride;
+    if (!in_place && !sets_apart(x, out, n_tokens, heads, dim, x_token_stride, x_head_stride, out_token_stride, out_head_stride, item))
+        return KVQ_ERR_INVALID_ARG;
+
+    const bool halves = flags & KVQ_ROPE_HALF;
+    const int64_t E = 16 / item;
+    RopeArgs a = {};
+    a.x = static_cast<const uint8_t *>(x);
+    a.out = static_cast<uint8_t *>(out);
+    a.x_tok = x_token_stride * item;
+    a.x_head = x_head_stride * item;
+    a.out_tok = out_token_stride * item;
+    a.out_head = out_head_stride * item;
+    a.n = n_tokens;
+    a.heads = int(heads);
+    a.start = int(rot_start);
+    a.rot = int(rot_dim);
+    a.cos_sin = cos_sin;
+    a.rows = cos_sin_rows;
+    a.pos = pos;
+    a.err = err;
+    a.sign = (flags & KVQ_ROPE_INVERSE) ? -1.f : 1.f;
+    // 16 bytes at a time where rows, the rotated part and (with halves) its halves begin on such a boundary
+    const bool wide = aligned(x, 16) && aligned(out, 16) && x_token_stride % E == 0 && x_head_stride % E == 0 &&
+                      out_token_stride % E == 0 && out_head_stride % E == 0 && dim % E == 0 && rot_start % E == 0 &&
+                      rot_dim % (halves ? 2 * E : E) == 0;
+    const int64_t pairs = rot_dim / 2;
+    int64_t lines, step;  // heads that a CTA has at a time, and those it has under way
+    if (wide) {
+        const int64_t turning = halves ? pairs / E : rot_dim / E;
+        a.pieces = int(turning + (in_place ? 0 : (dim - rot_dim) / E));
+        a.front = in_place ? 0 : int(rot_start / E);
+        lines = a.pieces < kRopeThreads ? kRopeThreads / a.pieces : 1;
+        step = kRopeBatch * lines;
+    } else {
+        a.pieces = int(pairs + (in_place ? 0 : dim - rot_dim));
+        lines = a.pieces < kRopeThreads ? kRopeThreads / a.pieces : 1;
+        step = lines;
+    }
+    // A CTA has a token's heads; fewer where there are too few tokens to fill the machine.
+    constexpr int64_t kFill = 608;
+    int64_t per = n_tokens >= kFill ? heads : (n_tokens * heads + kFill - 1) / kFill;
+    per = (per + lines - 1) / lines * lines;
+    if (per > lines && per < step) per = step < heads ? step : heads;
+    a.heads_cta = int(per < heads ? per : heads);
+    a.splits = int((heads + a.heads_cta - 1) / a.heads_cta);
+    const int64_t blocks = n_tokens * a.splits;
+    if (blocks > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return with_bool(dtype == KVQ_BF16, [&](auto Bc) {
+        constexpr bool B = decltype(Bc)::value;
+        if (!wide) return launch_pdl(rope_any_kernel<B>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a, halves);
+        return with_bool(halves, [&](auto Hc) {
+            return launch_pdl(rope_kernel<B, decltype(Hc)::value>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a);
+        });
+    });
+}

@@ -19,6 +19,7 @@ V41, V41_FP4 = 1, 2
 F32, BF16 = 0, 1
 I32, I64 = 0, 1
 FLAG_ROPE, FLAG_NORM = 1, 2
+ROPE_HALF, ROPE_INVERSE = 1, 2
 DEVERR_SLOT, DEVERR_POS, DEVERR_PAGE, DEVERR_LOC, DEVERR_WAIT, DEVERR_STATE, DEVERR_LEN = 1, 2, 4, 8, 16, 32, 64
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_LAUNCH = 0, 1, 2, 3, 4
 HEAD_DIM = 512
@@ -65,6 +66,17 @@ _SIGS = {
     "kvq_norm_quant": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
                                  C.c_void_p, C.c_int64, C.c_void_p, C.c_float, C.c_void_p, C.c_int64,
                                  C.c_void_p, C.c_int64, C.c_void_p]),
+    "kvq_rope_table": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_float, C.c_void_p, C.c_void_p]),
+    "kvq_rope": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                           C.c_int64, C.c_uint, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
+                           C.c_void_p, C.c_void_p]),
+    "kvq_evict_select": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64,
+                                   C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                   C.c_void_p]),
+    "kvq_evict_move": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                                 C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int64,
+                                 C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                 C.c_int64, C.c_void_p, C.c_void_p]),
     "kvq_dequant": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
                               C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
 }
@@ -481,3 +493,130 @@ def kvq_norm_quant(x, weight, codes, scales, *, eps=1e-6, residual=None, residua
         residual_out.stride(0) if residual is not None else 0, _ptr(weight), float(eps), _ptr(codes),
         codes.stride(0), _ptr(scales), scales.stride(0), s))
     _check(st, "kvq_norm_quant")
+
+
+def kvq_rope_table(freq, table, *, first=0, amplitude=1.0, stream=None):
+    """table [rows, rot] fp32 <- amplitude * cosines, then sines, of (first + row) * freq (freq [rot / 2] fp64)."""
+    _cuda(freq, "freq", (torch.float64,))
+    _cuda(table, "table", (torch.float32,))
+    _contig1d(freq, "freq")
+    if table.dim() != 2 or table.shape[1] != 2 * freq.numel() or not table.is_contiguous():
+        raise ValueError("table must be contiguous [rows, 2 * freq.numel()]")
+    dev = _same_device(table, freq)
+    st = _on(dev, stream, lambda s: lib().kvq_rope_table(freq.data_ptr(), table.shape[1], int(first), table.shape[0],
+                                                         float(amplitude), table.data_ptr(), s))
+    _check(st, "kvq_rope_table")
+    return table
+
+
+def kvq_rope(x, pos, cos_sin, out, *, start, half=False, inverse=False, err=None, stream=None):
+    """out <- x [tokens, heads, dim] (fp32 / bf16) with dims start .. start + rot - 1 rotated by row pos[token] of cos_sin
+    [rows, rot], interleaved pairs or halves; `inverse` turns them back.  out may be x itself."""
+    _cuda(x, "x", (torch.float32, torch.bfloat16))
+    _cuda(out, "out", (x.dtype,))
+    _cuda(pos, "pos", (torch.int32,))
+    _cuda(cos_sin, "cos_sin", (torch.float32,))
+    shape, xs, os_ = x.shape, x.stride(), out.stride()
+    if len(shape) != 3 or (shape[2] > 1 and xs[2] != 1):
+        raise ValueError("x must be [tokens, heads, dim] with unit inner stride")
+    if out.shape != shape or (shape[2] > 1 and os_[2] != 1):
+        raise ValueError("out must have x's shape and unit inner stride")
+    _contig1d(pos, "pos")
+    if pos.numel() != shape[0]:
+        raise ValueError("pos must hold one position per token")
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous [rows, rot]")
+    rows, rot = cos_sin.shape
+    _err_word(err)
+    dev = _same_device(x, out, pos, cos_sin, err)
+    flags = (ROPE_HALF if half else 0) | (ROPE_INVERSE if inverse else 0)
+    st = _on(dev, stream, lambda s: lib().kvq_rope(
+        x.data_ptr(), BF16 if x.dtype == torch.bfloat16 else F32, shape[0], shape[1], shape[2], xs[0], xs[1], int(start),
+        rot, flags, cos_sin.data_ptr(), rows, pos.data_ptr(), out.data_ptr(), os_[0], os_[1], _ptr(err), s))
+    _check(st, "kvq_rope")
+    return out
+
+
+def _stride0(t):
+    """Row stride of a 2-D tensor; that of a single row is its width."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _matrix(t, name):
+    if t.dim() != 2 or (t.shape[1] > 1 and t.shape[0] and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit inner stride")
+
+
+def _index_rows(t, name, n_seq, table, table_name):
+    """Checks an index of table rows (None: row i for sequence i)."""
+    if t is None:
+        if table.shape[0] < n_seq:
+            raise ValueError(f"{table_name} must hold one row per sequence")
+        return
+    _cuda(t, name, (torch.int32,))
+    _contig1d(t, name)
+    if t.numel() != n_seq:
+        raise ValueError(f"{name} must hold one row per sequence")
+
+
+def kvq_evict_select(mass, kv_len, kept, count, *, first=0, last=0, rows=None, err=None, stream=None):
+    """kept [n_seq, keep] int32 <- the tokens that stay of each sequence, ascending, then -1: the first and last few and,
+    of the others, those of most weight in mass [rows, width] fp32 (row rows[i], or i); count [n_seq] int32 of them."""
+    _cuda(mass, "mass", (torch.float32,))
+    _cuda(kv_len, "kv_len", (torch.int32,))
+    _cuda(kept, "kept", (torch.int32,))
+    _cuda(count, "count", (torch.int32,))
+    _matrix(mass, "mass")
+    _matrix(kept, "kept")
+    _contig1d(kv_len, "kv_len")
+    _contig1d(count, "count")
+    n_seq = kv_len.numel()
+    if kept.shape[0] != n_seq or count.numel() != n_seq:
+        raise ValueError("kept and count must hold one row per sequence")
+    _index_rows(rows, "rows", n_seq, mass, "mass")
+    _err_word(err)
+    dev = _same_device(mass, kv_len, kept, count, rows, err)
+    st = _on(dev, stream, lambda s: lib().kvq_evict_select(
+        mass.data_ptr(), mass.shape[0], mass.shape[1], _stride0(mass), _ptr(rows), kv_len.data_ptr(), n_seq,
+        kept.shape[1], int(first), int(last), kept.data_ptr(), _stride0(kept), count.data_ptr(), _ptr(err), s))
+    _check(st, "kvq_evict_select")
+    return kept, count
+
+
+def kvq_evict_move(layout, page_bits, pool, pool_pages, page_table, new_table, kept, *, req=None, mass=None, rows=None,
+                   mass_out=None, err=None, stream=None):
+    """Moves token kept[i, k] of sequence i (page_table row req[i], or i) to token k of the pages new_table[i], and its
+    weight to mass_out[i, k] where mass and mass_out are given."""
+    _cuda(pool, "pool", (torch.uint8,))
+    _cuda(page_table, "page_table", (torch.int32,))
+    _cuda(new_table, "new_table", (torch.int32,))
+    _cuda(kept, "kept", (torch.int32,))
+    for t, nm in ((page_table, "page_table"), (new_table, "new_table"), (kept, "kept")):
+        _matrix(t, nm)
+    n_seq, keep = kept.shape
+    if new_table.shape[0] != n_seq:
+        raise ValueError("new_table must hold one row per sequence")
+    _index_rows(req, "req", n_seq, page_table, "page_table")
+    if (mass is None) != (mass_out is None):
+        raise ValueError("mass and mass_out come together")
+    if mass is not None:
+        _cuda(mass, "mass", (torch.float32,))
+        _cuda(mass_out, "mass_out", (torch.float32,))
+        _matrix(mass, "mass")
+        _matrix(mass_out, "mass_out")
+        if mass_out.shape[0] != n_seq or mass_out.shape[1] < keep:
+            raise ValueError("mass_out must hold one row of kept weights per sequence")
+        _index_rows(rows, "rows", n_seq, mass, "mass")
+    elif rows is not None:
+        raise ValueError("rows are of mass")
+    if not pool.is_contiguous() or pool.numel() < pool_pages * page_bytes(layout, page_bits):
+        raise ValueError("pool must be contiguous and hold pool_pages pages")
+    _err_word(err)
+    dev = _same_device(pool, page_table, new_table, kept, req, mass, rows, mass_out, err)
+    m_rows, m_width, m_stride = (mass.shape[0], mass.shape[1], _stride0(mass)) if mass is not None else (0, 0, 0)
+    st = _on(dev, stream, lambda s: lib().kvq_evict_move(
+        layout, page_bits, pool.data_ptr(), int(pool_pages), page_table.data_ptr(), page_table.shape[0],
+        page_table.shape[1], _stride0(page_table), _ptr(req), new_table.data_ptr(), new_table.shape[1],
+        _stride0(new_table), kept.data_ptr(), n_seq, keep, _stride0(kept), _ptr(mass), m_rows, m_width, m_stride,
+        _ptr(rows), _ptr(mass_out), _stride0(mass_out) if mass is not None else 0, _ptr(err), s))
+    _check(st, "kvq_evict_move")

@@ -63,6 +63,7 @@ typedef enum { KVQ_LAYOUT_V41 = 1, KVQ_LAYOUT_V41_FP4 = 2 } kvq_layout;
 typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
 typedef enum { KVQ_I32 = 0, KVQ_I64 = 1 } kvq_index_dtype;
 enum { KVQ_FLAG_ROPE = 1, KVQ_FLAG_NORM = 2 };
+enum { KVQ_ROPE_HALF = 1, KVQ_ROPE_INVERSE = 2 }; /* flags of kvq_rope */
 
 /* bits of the device error word */
 enum {
@@ -320,6 +321,87 @@ kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n, int64_t d
                           const float *weight, float eps,
                           uint8_t *codes, int64_t codes_stride, uint8_t *scales, int64_t scales_stride,
                           struct CUstream_st *stream);
+
+/* The table of cosines and sines that kvq_store, the compressors and kvq_rope
+ * read: row r, of rot_dim floats, is amplitude * cos((first + r) * freq[i]),
+ * i = 0 .. rot_dim / 2 - 1, and then as many sines.
+ *   freq      [rot_dim / 2] fp64, radians a position; the frequencies of a
+ *             context that is longer than the model's own are scaled by the
+ *             caller.  One that is not finite, or 2^52 turns and more, makes
+ *             its columns NaN.
+ *   rot_dim   even, at most 1024 (64 for kvq_store).
+ *   first     >= 0; first + rows at most 2^31 - 1.
+ *   table     [rows, rot_dim] fp32, contiguous, 16-B aligned.
+ * Values are off by at most 2^-22 |amplitude|. */
+kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, int64_t rows, float amplitude,
+                          float *table, struct CUstream_st *stream);
+
+/* Rotary positions of rows that are not stored: queries before kvq_attend,
+ * and, with KVQ_ROPE_INVERSE, its output rows, whose rotated dims carry the
+ * cached rows' positions.
+ *   x          [n_tokens, heads, dim] fp32 or bf16 (dtype), strides in
+ *              elements, unit inner stride; a stride of 0 repeats a row.
+ *   rot_start, rot_dim   the rotated dims of a row: an even number, at most
+ *              1024, within dim (at most 65536); the others are copied.
+ *   flags      pairs are neighbours, (start + 2i, start + 2i + 1), or, with
+ *              KVQ_ROPE_HALF, (start + i, start + rot_dim / 2 + i);
+ *              (u, v) -> (u c - v s, v c + u s), or with KVQ_ROPE_INVERSE
+ *              (u c + v s, v c - u s), the transpose (also the gradient).
+ *              fp32, each product and sum rounded, as kvq_store does it.
+ *   cos_sin    [cos_sin_rows, rot_dim] fp32, 8-B aligned: cosines, then sines.
+ *   pos        [n_tokens] int32: row of cos_sin of every head of a token.
+ *   out        dtype; x itself with x's strides (then only the rotated dims
+ *              are read and written), or rows that overlap neither x's nor
+ *              each other.  Sets of rows that share an address range are
+ *              accepted where equal strides keep them beside each other.
+ * A pos outside [0, cos_sin_rows) sets KVQ_DEVERR_POS and leaves the token's
+ * rows of out as they are.  Any alignment and sizes are accepted; rows, parts
+ * and halves that begin on 16 bytes are faster. */
+kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens, int64_t heads, int64_t dim,
+                    int64_t x_token_stride, int64_t x_head_stride, int64_t rot_start, int64_t rot_dim, unsigned flags,
+                    const float *cos_sin, int64_t cos_sin_rows, const int32_t *pos, void *out,
+                    int64_t out_token_stride, int64_t out_head_stride, int32_t *err, struct CUstream_st *stream);
+
+/* Which cached tokens stay when a sequence is cut to `keep`: the first `first`
+ * and the last `last` of it anyway, and of those between the ones of most
+ * weight (kvq_attend_mass); of equal weights the first ones.  A sequence of
+ * at most `keep` tokens stays whole.
+ *   mass       [mass_rows, mass_row_stride] fp32, the first mass_width of a
+ *              row used: a weight for each token.  Zeros of both signs are
+ *              equal, a NaN is above everything.
+ *   rows       [n_seq] int32: row of mass of sequence i (NULL: row i).
+ *   kv_len     [n_seq] int32: tokens of a sequence, at most mass_width.
+ *   keep       >= first + last, at least 1.
+ *   kept       [n_seq, kept_stride] int32: the tokens that stay, ascending,
+ *              then -1 up to `keep`.
+ *   count      [n_seq] int32: how many stay.
+ * A bad kv_len (KVQ_DEVERR_LEN) or row (KVQ_DEVERR_STATE) makes the sequence
+ * an empty one. */
+kvq_status kvq_evict_select(const float *mass, int64_t mass_rows, int64_t mass_width, int64_t mass_row_stride,
+                            const int32_t *rows, const int32_t *kv_len, int64_t n_seq, int64_t keep, int64_t first,
+                            int64_t last, int32_t *kept, int64_t kept_stride, int32_t *count, int32_t *err,
+                            struct CUstream_st *stream);
+
+/* Moves the rows that stay to pages of their own: token kept[i][k] of sequence
+ * i, codes and scales as they are, becomes token k of the pages in row i of
+ * new_table, and its weight mass_out[i][k].  An entry of -1 moves nothing.
+ *   page_table, req   as in kvq_attend.
+ *   new_table  [n_seq, new_stride] int32: pages of this pool, as many as hold
+ *              `keep` tokens (new_width).  A page in it that holds rows of the
+ *              old tables too is fine only where its rows stay where they are
+ *              (the first pages of a sequence whose first tokens all stay):
+ *              otherwise rows may be overwritten before they are read.
+ *   mass, rows as in kvq_evict_select; mass and mass_out NULL: no weights.
+ *   mass_out   [n_seq, mass_out_stride] fp32, apart from mass.
+ * An entry outside the table or the weights sets KVQ_DEVERR_SLOT, a page
+ * outside the pool, old or new, KVQ_DEVERR_PAGE, a bad req or row
+ * KVQ_DEVERR_STATE: the token does not move, and its place stays as it is. */
+kvq_status kvq_evict_move(kvq_layout layout, int page_bits, uint8_t *pool, int64_t pool_pages,
+                          const int32_t *page_table, int64_t table_rows, int64_t table_width, int64_t table_stride,
+                          const int32_t *req, const int32_t *new_table, int64_t new_width, int64_t new_stride,
+                          const int32_t *kept, int64_t n_seq, int64_t keep, int64_t kept_stride, const float *mass,
+                          int64_t mass_rows, int64_t mass_width, int64_t mass_row_stride, const int32_t *rows,
+                          float *mass_out, int64_t mass_out_stride, int32_t *err, struct CUstream_st *stream);
 
 /* Human-readable name of a status. */
 const char *kvq_status_string(kvq_status status);
