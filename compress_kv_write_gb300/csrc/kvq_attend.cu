@@ -1,6 +1,6 @@
 // kvq_attend.cu -- C entry points of the latent attention over the paged V41 /
-// V41_FP4 pool, by page table (kvq_attend) or by selected slots
-// (kvq_attend_slots).
+// V41_FP4 pool, by page table (kvq_attend), with a tree of drafted tokens at its
+// end (kvq_attend_tree), or by selected slots (kvq_attend_slots).
 #include <atomic>
 
 #include "kvq_attend.cuh"
@@ -17,6 +17,7 @@ kvq_status launch_attend(int layout, const AttendArgs &a, bool slots, cudaStream
 constexpr uint32_t kMostWaitTries = 1u << 24;
 std::atomic<uint32_t> g_wait_tries{kWaitTries};
 
+constexpr int64_t kMaxTree = 1024;  // drafted tokens of a sequence, as in kvq_tree_mask
 constexpr int64_t kMaxLen = int64_t(1) << 30;  // cached tokens of a sequence: positions and block sums fit an int
 
 // What both entry points share: layout, pool, query, output and workspace.
@@ -51,6 +52,57 @@ kvq_status check_common(int layout, int page_bits, const void *q, int64_t q_tok,
     return KVQ_OK;
 }
 
+// kvq_attend, and with a mask kvq_attend_tree.
+kvq_status attend_pages(int layout, int page_bits, const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                        int64_t n_seq, int64_t q_len, int64_t heads, const uint8_t *pool, int64_t pool_pages,
+                        const int32_t *page_table, int64_t table_rows, int64_t table_width, int64_t table_stride,
+                        const int32_t *req, const int32_t *kv_len, const uint64_t *mask, bool tree, float scale, void *out,
+                        int out_dtype, int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                        size_t workspace_bytes, int32_t *err, cudaStream_t stream) {
+    kvq_status st = check_common(layout, page_bits, q_bf16, q_token_stride, q_head_stride, n_seq, q_len, heads, pool,
+                                 pool_pages, scale, out, out_dtype, out_token_stride, out_head_stride, lse, workspace,
+                                 workspace_bytes, err);
+    if (st != KVQ_OK || n_seq == 0) return st;
+    if (table_rows < 0 || table_width < 0 || table_stride < table_width) return KVQ_ERR_INVALID_ARG;
+    if (table_rows > 0 && table_width > 0 && !page_table) return KVQ_ERR_INVALID_ARG;
+    if (!aligned(page_table, 4) || (req && !aligned(req, 4))) return KVQ_ERR_INVALID_ARG;
+    if (!kv_len || !aligned(kv_len, 4)) return KVQ_ERR_INVALID_ARG;
+    if (tree && (!mask || !aligned(mask, 8))) return KVQ_ERR_INVALID_ARG;
+    if (!req && n_seq > table_rows) return KVQ_ERR_INVALID_ARG;
+    // no sequence is longer than kMaxLen, however wide the table
+    if (table_width > (kMaxLen >> page_bits)) table_width = kMaxLen >> page_bits;
+
+    AttendArgs a = {};
+    a.q = static_cast<const uint16_t *>(q_bf16);
+    a.q_tok = q_token_stride;
+    a.q_head = q_head_stride;
+    a.n_seq = n_seq;
+    a.q_len = int(q_len);
+    a.heads = int(heads);
+    a.pool = pool;
+    a.pool_limit = pool_pages;
+    a.page_bits = page_bits;
+    a.table = page_table;
+    a.table_rows = table_rows;
+    a.table_stride = table_stride;
+    a.max_len = table_width << page_bits;
+    a.req = req;
+    a.kv_len = kv_len;
+    a.mask = mask;
+    a.mask_words = int((q_len + 63) / 64);
+    a.scale = scale;
+    a.out = out;
+    a.out_tok = out_token_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.ws = static_cast<uint8_t *>(workspace);
+    a.err = err;
+    a.out_bf16 = out_dtype == KVQ_BF16;
+    a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
+    if (tree) return layout == KVQ_LAYOUT_V41 ? launch_attend_tree_v41(a, stream) : launch_attend_tree_fp4(a, stream);
+    return launch_attend(layout, a, false, stream);
+}
+
 }  // namespace
 }  // namespace kvq
 
@@ -72,44 +124,24 @@ extern "C" kvq_status kvq_attend(kvq_layout layout, int page_bits, const void *q
                                  const int32_t *kv_len, float scale, void *out, kvq_dtype out_dtype,
                                  int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
                                  size_t workspace_bytes, int32_t *err, struct CUstream_st *stream) {
-    kvq_status st = check_common(layout, page_bits, q_bf16, q_token_stride, q_head_stride, n_seq, q_len, heads, pool,
-                                 pool_pages, scale, out, out_dtype, out_token_stride, out_head_stride, lse, workspace,
-                                 workspace_bytes, err);
-    if (st != KVQ_OK || n_seq == 0) return st;
-    if (table_rows < 0 || table_width < 0 || table_stride < table_width) return KVQ_ERR_INVALID_ARG;
-    if (table_rows > 0 && table_width > 0 && !page_table) return KVQ_ERR_INVALID_ARG;
-    if (!aligned(page_table, 4) || (req && !aligned(req, 4))) return KVQ_ERR_INVALID_ARG;
-    if (!kv_len || !aligned(kv_len, 4)) return KVQ_ERR_INVALID_ARG;
-    if (!req && n_seq > table_rows) return KVQ_ERR_INVALID_ARG;
-    // no sequence is longer than kMaxLen, however wide the table
-    if (table_width > (kMaxLen >> page_bits)) table_width = kMaxLen >> page_bits;
+    return attend_pages(layout, page_bits, q_bf16, q_token_stride, q_head_stride, n_seq, q_len, heads, pool, pool_pages,
+                        page_table, table_rows, table_width, table_stride, req, kv_len, nullptr, false, scale, out, out_dtype,
+                        out_token_stride, out_head_stride, lse, workspace, workspace_bytes, err,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
 
-    AttendArgs a = {};
-    a.q = static_cast<const uint16_t *>(q_bf16);
-    a.q_tok = q_token_stride;
-    a.q_head = q_head_stride;
-    a.n_seq = n_seq;
-    a.q_len = int(q_len);
-    a.heads = int(heads);
-    a.pool = pool;
-    a.pool_limit = pool_pages;
-    a.page_bits = page_bits;
-    a.table = page_table;
-    a.table_rows = table_rows;
-    a.table_stride = table_stride;
-    a.max_len = table_width << page_bits;
-    a.req = req;
-    a.kv_len = kv_len;
-    a.scale = scale;
-    a.out = out;
-    a.out_tok = out_token_stride;
-    a.out_head = out_head_stride;
-    a.lse = lse;
-    a.ws = static_cast<uint8_t *>(workspace);
-    a.err = err;
-    a.out_bf16 = out_dtype == KVQ_BF16;
-    a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
-    return launch_attend(layout, a, false, reinterpret_cast<cudaStream_t>(stream));
+extern "C" kvq_status kvq_attend_tree(kvq_layout layout, int page_bits, const void *q_bf16, int64_t q_token_stride,
+                                 int64_t q_head_stride, int64_t n_seq, int64_t q_len, int64_t heads,
+                                 const uint8_t *pool, int64_t pool_pages, const int32_t *page_table,
+                                 int64_t table_rows, int64_t table_width, int64_t table_stride, const int32_t *req,
+                                 const int32_t *kv_len, const uint64_t *mask, float scale, void *out, kvq_dtype out_dtype,
+                                 int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                                 size_t workspace_bytes, int32_t *err, struct CUstream_st *stream) {
+    if (q_len > kMaxTree) return KVQ_ERR_UNSUPPORTED;
+    return attend_pages(layout, page_bits, q_bf16, q_token_stride, q_head_stride, n_seq, q_len, heads, pool, pool_pages,
+                        page_table, table_rows, table_width, table_stride, req, kv_len, mask, true, scale, out, out_dtype,
+                        out_token_stride, out_head_stride, lse, workspace, workspace_bytes, err,
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" kvq_status kvq_attend_slots(kvq_layout layout, int page_bits, const void *q_bf16, int64_t q_token_stride,

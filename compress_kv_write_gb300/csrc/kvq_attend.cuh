@@ -6,6 +6,10 @@
 
 namespace kvq {
 
+// How a query row's tokens are given: by pages and a length, causal; by a list of slots; by pages, and for the last q_len
+// tokens by a mask.
+enum : int { kByPages, kBySlots, kByTree };
+
 struct AttendArgs {
     const uint16_t *q;  // bf16
     int64_t q_tok, q_head;
@@ -22,6 +26,8 @@ struct AttendArgs {
     const int32_t *kv_len;
     const void *slots;  // slots
     int64_t slots_stride;
+    const uint64_t *mask;  // tree: mask_words a query token
+    int mask_words;
     float scale;
     void *out;
     int64_t out_tok, out_head;
@@ -54,5 +60,7 @@ __device__ __forceinline__ float attend_lse(float m, float sum) {
 
 kvq_status launch_attend_v41(const AttendArgs &a, bool slots, cudaStream_t s);
 kvq_status launch_attend_fp4(const AttendArgs &a, bool slots, cudaStream_t s);
+kvq_status launch_attend_tree_v41(const AttendArgs &a, cudaStream_t s);
+kvq_status launch_attend_tree_fp4(const AttendArgs &a, cudaStream_t s);
 
 }  // namespace kvq

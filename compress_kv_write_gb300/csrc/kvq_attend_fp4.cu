@@ -3,6 +3,6 @@
 
 namespace kvq {
 kvq_status launch_attend_fp4(const AttendArgs &a, bool slots, cudaStream_t s) {
-    return slots ? launch_attend_layout<Layout::FP4, true>(a, s) : launch_attend_layout<Layout::FP4, false>(a, s);
+    return slots ? launch_attend_layout<Layout::FP4, kBySlots>(a, s) : launch_attend_layout<Layout::FP4, kByPages>(a, s);
 }
 }  // namespace kvq

@@ -119,7 +119,10 @@ struct AttendShared {
     int abort, progress;
     alignas(16) float sc[N], nm[N], m[N], alpha[N], inv[N];
     float red[4][N], lsum[4][N];
-    alignas(16) int vis[N];
+    union {
+        alignas(16) int vis[N];  // tokens that a query row sees; of a tree:
+        uint32_t win[N][2];      // which of a block's tokens it sees
+    };
     int64_t q[N], row[N];  // a query row's element offsets, -1: none
     // What the lookup warps found for a block's tokens, kLookups blocks in turn.
     uint64_t addr[kLookups];                   // full
@@ -140,14 +143,14 @@ struct TileInfo {
     int trow, err;
 };
 
-template <int N, bool kSlots>
+template <int N, int kKind>
 __device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int tile) {
     TileInfo t;
     t.seq = int(uint32_t(tile) / uint32_t(a.row_tiles));
     t.rt = int(uint32_t(tile) % uint32_t(a.row_tiles));
     t.err = 0;
     t.trow = t.seq;
-    if constexpr (kSlots) {
+    if constexpr (kKind == kBySlots) {
         t.len = t.seen = int(a.max_len);
     } else {
         if (a.req) t.trow = __ldg(a.req + t.seq);
@@ -160,7 +163,7 @@ __device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int tile) {
             t.len = 0;
         }
         t.seen = t.len;
-        if (a.q_len > 1) {
+        if (kKind == kByPages && a.q_len > 1) {
             const int64_t per = int64_t(a.q_len) * a.heads;
             const int last = int(min(int64_t(t.rt + 1) * N, per) - 1);
             t.seen = max(0, t.len - (a.q_len - 1 - last / a.heads));
@@ -170,19 +173,31 @@ __device__ __forceinline__ TileInfo tile_info(const AttendArgs &a, int tile) {
     return t;
 }
 
+// Which of the 64 tokens from t0 on a drafted token sees, of a tree that begins at token `base`: all those before it, and
+// of the drafted ones those in its mask.
+__device__ __forceinline__ uint64_t tree_window(const uint64_t *mask, int words, int t0, int base) {
+    const int off = t0 - base;
+    if (off <= -kTile) return ~0ull;
+    if (off < 0) return ((1ull << -off) - 1) | (__ldg(mask) << -off);
+    const int w = off >> 6, sh = off & 63;
+    uint64_t r = w < words ? __ldg(mask + w) >> sh : 0;
+    if (sh && w + 1 < words) r |= __ldg(mask + w + 1) << (64 - sh);
+    return r;
+}
+
 // Walks a CTA's blocks in order.
-template <int N, bool kSlots>
+template <int N, int kKind>
 struct Cursor {
     int tile, kb, left;
     TileInfo t;
     __device__ __forceinline__ Cursor(const AttendArgs &a, const AttendShared<N> &sh)
-        : tile(sh.start_tile), kb(sh.start_kb), left(sh.units), t(tile_info<N, kSlots>(a, tile)) {}
+        : tile(sh.start_tile), kb(sh.start_kb), left(sh.units), t(tile_info<N, kKind>(a, tile)) {}
     __device__ __forceinline__ void next(const AttendArgs &a) {
         --left;
         if (++kb >= t.nb) {
             kb = 0;
             ++tile;
-            if (left > 0) t = tile_info<N, kSlots>(a, tile);
+            if (left > 0) t = tile_info<N, kKind>(a, tile);
         }
     }
 };
@@ -377,9 +392,10 @@ __device__ __forceinline__ void share(int64_t total, int64_t &u0, int64_t &u1) {
     }
 }
 
-template <Layout L, int N, bool kSlots>
+template <Layout L, int N, int kKind>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using T = LayoutTraits<L>;
+    constexpr bool kSlots = kKind == kBySlots, kTree = kKind == kByTree;
     constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
     constexpr int R = kRing;
     constexpr int KR = kTmemRing<N>, kBufs = kScoreBufs<N>;
@@ -436,7 +452,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int t0 = int(min(int64_t(tiles), int64_t(tid) * per)), t1 = int(min(int64_t(tiles), int64_t(t0) + per));
         int64_t mine = 0;
 #pragma unroll 1
-        for (int t = t0; t < t1; ++t) mine += tile_info<N, kSlots>(a, t).nb;
+        for (int t = t0; t < t1; ++t) mine += tile_info<N, kKind>(a, t).nb;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -465,7 +481,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             int t = t0;
 #pragma unroll 1
             for (; t + 1 < t1; ++t) {
-                const int nb = tile_info<N, kSlots>(a, t).nb;
+                const int nb = tile_info<N, kKind>(a, t).nb;
                 if (u0 < at + nb) break;
                 at += nb;
             }
@@ -596,7 +612,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
                 if (left_tile == 0) {  // a new tile: its queries
-                    left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kSlots>(a, tile).nb, 0) - kb;
+                    left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kKind>(a, tile).nb, 0) - kb;
                     ++tile;
                     kb = 0;
                     mbar_wait(smem_addr(&sh.qready), seg & 1, tries);
@@ -642,7 +658,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             for (int i = 0; i < units; ++i) {
                 if (left_tile == 0) {  // a new tile
                     since = 0;
-                    left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kSlots>(a, tile).nb, 0) - kb;
+                    left_tile = __shfl_sync(0xFFFFFFFFu, tile_info<N, kKind>(a, tile).nb, 0) - kb;
                     ++tile;
                     kb = 0;
                 }
@@ -677,7 +693,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             const uint32_t page_bytes = uint32_t(kTokenBytes<L>) << a.page_bits, in_page = (1u << a.page_bits) - 1;
             const uint32_t scale_at = uint32_t(T::kCodeBytes) << a.page_bits;
             volatile int &progress = sh.progress;
-            Cursor<N, kSlots> cur(a, sh);
+            Cursor<N, kKind> cur(a, sh);
             Index idx[K];
             int t0 = 0, seen = 0;
             uint32_t tries = a.wait_tries * kLookupTries;
@@ -762,7 +778,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const float c = a.scale * kLog2e;
         const int per = a.q_len * a.heads;
         const uint32_t trow = (uint32_t(quarter * 32) << 16);
-        Cursor<N, kSlots> cur(a, sh);
+        Cursor<N, kKind> cur(a, sh);
         Ring<R> ring;
         float l[G][2], sc[G][2], nm[G][2];
         Ring<R> end;  // the slot of the block's last chunk
@@ -786,7 +802,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                     const int64_t tok = int64_t(cur.t.seq) * a.q_len + j;
                     sh.q[tid] = row < per ? tok * a.q_tok + head * a.q_head : -1;
                     sh.row[tid] = row < per ? tok * a.out_tok + head * a.out_head : -1;
-                    sh.vis[tid] = kSlots || row >= per ? cur.t.seen : max(0, cur.t.len - (a.q_len - 1 - j));
+                    if constexpr (!kTree) sh.vis[tid] = kSlots || row >= per ? cur.t.seen : max(0, cur.t.len - (a.q_len - 1 - j));
                     sh.m[tid] = -INFINITY;
                     sh.nm[tid] = 0.f;
                 }
@@ -868,6 +884,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                         }
                 }
             }
+            // whether the block holds drafted tokens, and which of them each row sees (a row of no one's: all, so that it
+            // has a maximum).  The block before's windows were read before its last barrier.
+            const int base = kTree ? cur.t.len - a.q_len : 0;
+            const bool of_tree = kTree && (cur.kb + 1) * kTile > base;
+            if (of_tree) {
+                if (tid < N) {
+                    const int row = cur.t.rt * N + tid, j = row / a.heads;
+                    const uint64_t w = row < per ? tree_window(a.mask + (int64_t(cur.t.seq) * a.q_len + j) * a.mask_words,
+                                                               a.mask_words, cur.kb * kTile, base)
+                                                 : ~0ull;
+                    sh.win[tid][0] = uint32_t(w);
+                    sh.win[tid][1] = uint32_t(w >> 32);
+                }
+                soft_sync();
+            }
             // `full` of the block's first chunk orders this thread's read of texp
             mbar_wait(smem_addr(&sh.full[ring.slot]), ring.parity, tries);
             int t_at[2];
@@ -886,7 +917,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 }
             }
             // whether some of the block is masked for some row (the first row of a tile sees least)
-            const bool masked = !__all_sync(0xFFFFFFFFu, have) || int64_t(cur.kb + 1) * kTile > sh.vis[0];
+            const bool masked = !__all_sync(0xFFFFFFFFu, have) || (kTree ? of_tree : int64_t(cur.kb + 1) * kTile > sh.vis[0]);
             mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
             tc_fence_after();
             // x = score in log2 units, plus the row's power of two; -inf where it is masked.  [.][h][e]: token tok + 8 h.
@@ -912,11 +943,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int vis = sh.vis[col0 + 8 * g + e];
+                        // of a tree: the half of the row's window that this warp's 16 tokens lie in
+                        const uint32_t win = !kTree ? 0u : of_tree ? sh.win[col0 + 8 * g + e][quarter >> 1] : 0xFFFFFFFFu;
+                        const int vis = kTree ? 0 : sh.vis[col0 + 8 * g + e];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             odd[h] = odd[h] || !(fabsf(x[g][h][e]) < INFINITY);
-                            if (!(t_at[h] < vis)) x[g][h][e] = -INFINITY;
+                            const bool sees = kTree ? t_at[h] != 0x7FFFFFFF && ((win >> ((tok + 8 * h) & 31)) & 1) : t_at[h] < vis;
+                            if (!sees) x[g][h][e] = -INFINITY;
                         }
                     }
             }
@@ -1142,7 +1176,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             int tile = sh.start_tile, kb = sh.start_kb;
 #pragma unroll 1
             for (int left = units; left > 0; ++tile, kb = 0) {
-                const TileInfo t = tile_info<N, kSlots>(a, tile);
+                const TileInfo t = tile_info<N, kKind>(a, tile);
                 const int blocks = min(left, t.nb - kb);
                 left -= blocks;
                 if (blocks < t.nb) {
@@ -1249,13 +1283,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attend_join_kernel(const __gr
     }
 }
 
-template <Layout L, int N, bool kSlots>
+template <Layout L, int N, int kKind>
 kvq_status launch_attend_n(AttendArgs a, cudaStream_t s) {
     const int64_t per = int64_t(a.q_len) * a.heads;
     a.row_tiles = int((per + N - 1) / N);
     const int64_t tiles = a.n_seq * a.row_tiles;
     int64_t grid = 0;
-    kvq_status st = resident_grid<attend_kernel<L, N, kSlots>, kAttendThreads>(kAttendSmem<N>, &grid);
+    kvq_status st = resident_grid<attend_kernel<L, N, kKind>, kAttendThreads>(kAttendSmem<N>, &grid);
     if (st != KVQ_OK) return st;
     if (grid > kMaxAttendCtas) grid = kMaxAttendCtas;
     const int64_t most = (a.max_len + kTile - 1) / kTile;  // blocks of the longest tile there can be
@@ -1264,17 +1298,17 @@ kvq_status launch_attend_n(AttendArgs a, cudaStream_t s) {
     if (most <= 1 && tiles < grid) grid = tiles;
     a.join = reinterpret_cast<int2 *>(a.ws);
     a.part = reinterpret_cast<float *>(a.ws + kMaxAttendCtas * sizeof(int2));
-    st = launch_pdl_smem(attend_kernel<L, N, kSlots>, dim3(unsigned(grid)), dim3(kAttendThreads), kAttendSmem<N>, s, a);
+    st = launch_pdl_smem(attend_kernel<L, N, kKind>, dim3(unsigned(grid)), dim3(kAttendThreads), kAttendSmem<N>, s, a);
     if (st != KVQ_OK || most <= 1) return st;  // a tile of one block is never split
     return launch_pdl(attend_join_kernel<N>, dim3(unsigned(2 * grid)), dim3(kJoinThreads), s, a, int(grid));
 }
 
-template <Layout L, bool kSlots>
+template <Layout L, int kKind>
 kvq_status launch_attend_layout(const AttendArgs &a, cudaStream_t s) {
     switch (attend_rows(int64_t(a.q_len) * a.heads)) {
-        case 16: return launch_attend_n<L, 16, kSlots>(a, s);
-        case 32: return launch_attend_n<L, 32, kSlots>(a, s);
-        default: return launch_attend_n<L, 64, kSlots>(a, s);
+        case 16: return launch_attend_n<L, 16, kKind>(a, s);
+        case 32: return launch_attend_n<L, 32, kKind>(a, s);
+        default: return launch_attend_n<L, 64, kKind>(a, s);
     }
 }
 

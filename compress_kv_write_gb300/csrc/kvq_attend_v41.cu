@@ -3,6 +3,6 @@
 
 namespace kvq {
 kvq_status launch_attend_v41(const AttendArgs &a, bool slots, cudaStream_t s) {
-    return slots ? launch_attend_layout<Layout::V41, true>(a, s) : launch_attend_layout<Layout::V41, false>(a, s);
+    return slots ? launch_attend_layout<Layout::V41, kBySlots>(a, s) : launch_attend_layout<Layout::V41, kByPages>(a, s);
 }
 }  // namespace kvq

@@ -59,6 +59,12 @@ _SIGS = {
                              C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
                              C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
                              C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "kvq_tree_mask": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                C.c_void_p, C.c_void_p]),
+    "kvq_attend_tree": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                  C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
+                                  C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
     "kvq_attend_slots": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
                                    C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
                                    C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64, C.c_void_p,
@@ -400,13 +406,8 @@ def _attend_rows(q, out, lse, workspace, err):
     return n, h, qs, outs, _same_device(q, out, lse, workspace, err), BF16 if out.dtype == torch.bfloat16 else F32
 
 
-def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, workspace, *, scale, q_len=1,
-               req=None, lse=None, err=None, stream=None):
-    """Latent attention of q [n_seq * q_len, heads, 512] bf16 over the paged pool: out (bf16 or fp32) of q's
-    shape and, if lse [n_seq * q_len, heads] fp32 is given, the natural-log sums.  page_table [rows, width]
-    int32, row req[i] (req None: row i) for sequence i; kv_len [n_seq] int32 cached tokens; query token j of a
-    sequence sees the first kv_len - (q_len - 1 - j).  workspace: attend_workspace(q_len * heads) bytes."""
-    n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+def _paged(layout, page_bits, q, n, q_len, pool, pool_pages, page_table, kv_len, req):
+    """Checks what the calls over pages share; returns the table's (rows, width, row stride) and the sequences."""
     _cuda(pool, "pool", (torch.uint8,))
     _cuda(page_table, "page_table", (torch.int32,))
     _cuda(kv_len, "kv_len", (torch.int32,))
@@ -429,12 +430,71 @@ def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, 
     if not pool.is_contiguous() or pool.numel() < pool_pages * page_bytes(layout, page_bits):
         raise ValueError("pool must be contiguous and hold pool_pages pages")
     _same_device(q, pool, page_table, kv_len, req)
+    return rows, width, ts[0] if rows > 1 else width, n_seq
+
+
+def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, workspace, *, scale, q_len=1,
+               req=None, lse=None, err=None, stream=None):
+    """Latent attention of q [n_seq * q_len, heads, 512] bf16 over the paged pool: out (bf16 or fp32) of q's
+    shape and, if lse [n_seq * q_len, heads] fp32 is given, the natural-log sums.  page_table [rows, width]
+    int32, row req[i] (req None: row i) for sequence i; kv_len [n_seq] int32 cached tokens; query token j of a
+    sequence sees the first kv_len - (q_len - 1 - j).  workspace: attend_workspace(q_len * heads) bytes."""
+    n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+    rows, width, ts, n_seq = _paged(layout, page_bits, q, n, q_len, pool, pool_pages, page_table, kv_len, req)
     st = _on(dev, stream, lambda s: lib().kvq_attend(
         layout, page_bits, _ptr(q), qs[0], qs[1], n_seq, q_len, heads, _ptr(pool), int(pool_pages),
-        _ptr(page_table), rows, width, ts[0] if rows > 1 else width, _ptr(req), _ptr(kv_len),
+        _ptr(page_table), rows, width, ts, _ptr(req), _ptr(kv_len),
         float(scale), _ptr(out), out_dtype, outs[0], outs[1], _ptr(lse), _ptr(workspace),
         workspace.numel(), _ptr(err), s))
     _check(st, "kvq_attend")
+    return out
+
+
+def kvq_tree_mask(parent, mask, *, kv_len=None, pos=None, err=None, stream=None):
+    """mask [n_seq, q_len, ceil(q_len / 64)] int64 <- which drafted tokens each one sees (itself and its ancestors), from
+    parent [n_seq, q_len] int32 (-1: the last token before the tree); pos [n_seq, q_len] int32 <- kv_len - q_len + depth."""
+    _cuda(parent, "parent", (torch.int32,))
+    _cuda(mask, "mask", (torch.int64,))
+    _matrix(parent, "parent")
+    n_seq, q_len = parent.shape
+    if mask.shape != (n_seq, q_len, (q_len + 63) // 64) or not mask.is_contiguous():
+        raise ValueError("mask must be contiguous [n_seq, q_len, ceil(q_len / 64)]")
+    if kv_len is not None:
+        _cuda(kv_len, "kv_len", (torch.int32,))
+        _contig1d(kv_len, "kv_len")
+        if kv_len.numel() != n_seq:
+            raise ValueError("kv_len must hold one length per sequence")
+    if pos is not None:
+        _cuda(pos, "pos", (torch.int32,))
+        if pos.shape != parent.shape or not pos.is_contiguous():
+            raise ValueError("pos must be contiguous [n_seq, q_len]")
+    _err_word(err)
+    dev = _same_device(parent, mask, kv_len, pos, err)
+    st = _on(dev, stream, lambda s: lib().kvq_tree_mask(parent.data_ptr(), n_seq, q_len, _stride0(parent), _ptr(kv_len),
+                                                        mask.data_ptr(), _ptr(pos), _ptr(err), s))
+    _check(st, "kvq_tree_mask")
+    return mask
+
+
+def kvq_attend_tree(layout, page_bits, q, pool, pool_pages, page_table, kv_len, mask, out, workspace, *, scale, req=None,
+                    lse=None, err=None, stream=None):
+    """kvq_attend of a tree of drafted tokens, the last q_len of a sequence's cached tokens: query token j sees all tokens
+    before them and those of them whose bits are set in mask[i, j] ([n_seq, q_len, ceil(q_len / 64)] int64)."""
+    n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
+    _cuda(mask, "mask", (torch.int64,))
+    if mask.dim() != 3 or mask.shape[2] != (mask.shape[1] + 63) // 64 or not mask.is_contiguous():
+        raise ValueError("mask must be contiguous [n_seq, q_len, ceil(q_len / 64)]")
+    q_len = mask.shape[1]
+    rows, width, ts, n_seq = _paged(layout, page_bits, q, n, q_len, pool, pool_pages, page_table, kv_len, req)
+    if mask.shape[0] != n_seq:
+        raise ValueError("mask must hold one tree per sequence")
+    _same_device(q, mask)
+    st = _on(dev, stream, lambda s: lib().kvq_attend_tree(
+        layout, page_bits, _ptr(q), qs[0], qs[1], n_seq, q_len, heads, _ptr(pool), int(pool_pages),
+        _ptr(page_table), rows, width, ts, _ptr(req), _ptr(kv_len), _ptr(mask),
+        float(scale), _ptr(out), out_dtype, outs[0], outs[1], _ptr(lse), _ptr(workspace),
+        workspace.numel(), _ptr(err), s))
+    _check(st, "kvq_attend_tree")
     return out
 
 

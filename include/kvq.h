@@ -282,6 +282,40 @@ kvq_status kvq_attend(kvq_layout layout, int page_bits,
                       float *lse, void *workspace, size_t workspace_bytes,
                       int32_t *err, struct CUstream_st *stream);
 
+/* Masks and positions of trees of drafted tokens, for kvq_attend_tree.
+ *   parent    [n_seq, parent_stride] int32, the first q_len of a row used:
+ *             the token that token j follows, one drafted before it (< j), or
+ *             -1: the sequence's last token before the tree.  Anything else
+ *             counts as -1 and sets KVQ_DEVERR_STATE.  q_len: at most 1024.
+ *   mask      [n_seq, q_len, ceil(q_len / 64)] 64-bit words: bit k % 64 of
+ *             word k / 64 of token j is set where k is j or one of its
+ *             ancestors.
+ *   pos       [n_seq, q_len] int32, or NULL: max(0, kv_len[i] - q_len + depth
+ *             of j), the depth being the number of its ancestors (kv_len NULL:
+ *             the depth alone). */
+kvq_status kvq_tree_mask(const int32_t *parent, int64_t n_seq, int64_t q_len, int64_t parent_stride,
+                         const int32_t *kv_len, uint64_t *mask, int32_t *pos, int32_t *err,
+                         struct CUstream_st *stream);
+
+/* kvq_attend for a tree of drafted tokens, verified in one step: the last
+ * q_len of a sequence's kv_len[i] cached tokens are its query tokens (already
+ * stored, in the order of q), and query token j sees all tokens before them
+ * and, of them, token k where bit k % 64 of word k / 64 of mask[i][j] is set
+ * (its own too).  Any mask is accepted.  Of a sequence with kv_len[i] < q_len
+ * the first q_len - kv_len[i] drafted tokens are not there, whatever the mask.
+ *   mask      [n_seq, q_len, ceil(q_len / 64)] 64-bit words, 8-B aligned.
+ *   q_len     at most 1024.
+ * All else is as in kvq_attend. */
+kvq_status kvq_attend_tree(kvq_layout layout, int page_bits,
+                           const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                           int64_t n_seq, int64_t q_len, int64_t heads,
+                           const uint8_t *pool, int64_t pool_pages,
+                           const int32_t *page_table, int64_t table_rows, int64_t table_width,
+                           int64_t table_stride, const int32_t *req, const int32_t *kv_len, const uint64_t *mask,
+                           float scale, void *out, kvq_dtype out_dtype, int64_t out_token_stride,
+                           int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes,
+                           int32_t *err, struct CUstream_st *stream);
+
 /* kvq_attend over selected tokens: query token i attends over the tokens in
  * slots slots[i * slots_stride + 0 .. n_sel - 1] (int32 or int64), the ones
  * kvq_dequant_slots would gather.  Slot -1 is padding, anywhere in the list;
