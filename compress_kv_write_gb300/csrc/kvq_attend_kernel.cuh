@@ -105,6 +105,11 @@ constexpr int kScoreBufs = N == 64 ? 1 : 2;
 // chunk waited for it).
 template <int N>
 constexpr int kScored = kTmemRing<N> > kChunks ? kTmemRing<N> : kChunks;
+// What a tile costs beside its blocks, in blocks, where shares count it: a tree's rows make many tiles, and those of short
+// sequences among long ones would all be one CTA's (8 trees of 63 tokens, 64 heads, two of the 8 sequences shorter than a
+// block: 1,396 us without, 386 with; 24 trees of 24, 16 heads: 169 and 78).
+template <int N, int kKind>
+constexpr int kTileCost = kKind != kByTree ? 0 : N == 64 ? 6 : N == 32 ? 4 : 3;
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kLookups = 6, kLookupWarps = 2;
 constexpr uint32_t kLookupTries = 16;  // a lookup warp's try is a sleep of 64 ns, a barrier's may take a microsecond
@@ -113,7 +118,7 @@ template <int N>
 struct AttendShared {
     uint64_t full[kRing], oblk[kRing], scored[kScored<N>], sdone[2], sread[2], pready[2], qready, drain[2];
     int64_t scan[kAttendThreads / 32];
-    int64_t total, u0;
+    int64_t total, u0, end_block;
     int units, start_tile, start_kb;
     uint32_t tmem;
     int abort, progress;
@@ -396,6 +401,7 @@ template <Layout L, int N, int kKind>
 __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using T = LayoutTraits<L>;
     constexpr bool kSlots = kKind == kBySlots, kTree = kKind == kByTree;
+    constexpr int kCost = kTileCost<N, kKind>;
     constexpr bool kExp = L == Layout::V41;   // rows carry a power of two
     constexpr int R = kRing;
     constexpr int KR = kTmemRing<N>, kBufs = kScoreBufs<N>;
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
         const int t0 = int(min(int64_t(tiles), int64_t(tid) * per)), t1 = int(min(int64_t(tiles), int64_t(t0) + per));
         int64_t mine = 0;
 #pragma unroll 1
-        for (int t = t0; t < t1; ++t) mine += tile_info<N, kKind>(a, t).nb;
+        for (int t = t0; t < t1; ++t) mine += tile_info<N, kKind>(a, t).nb + kCost;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -477,16 +483,48 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
             sh.units = int(u1 - u0);
         }
         int64_t at = before + incl - mine;
-        if (u0 >= at && u0 < at + mine) {  // one thread
-            int t = t0;
+        if constexpr (kCost == 0) {
+            if (u0 >= at && u0 < at + mine) {  // one thread
+                int t = t0;
 #pragma unroll 1
-            for (; t + 1 < t1; ++t) {
-                const int nb = tile_info<N, kKind>(a, t).nb;
-                if (u0 < at + nb) break;
-                at += nb;
+                for (; t + 1 < t1; ++t) {
+                    const int nb = tile_info<N, kKind>(a, t).nb;
+                    if (u0 < at + nb) break;
+                    at += nb;
+                }
+                sh.start_tile = t;
+                sh.start_kb = int(u0 - at);
             }
-            sh.start_tile = t;
-            sh.start_kb = int(u0 - at);
+        } else {
+            // The shares are of units of which every tile has kCost before its blocks.  A share that ends among these has
+            // no block of the tile, one that begins there has its first.  u0 and `units` count blocks, as without.
+            __syncthreads();
+            const int64_t blocks = total - int64_t(kCost) * tiles;
+            if (tid == 0 && u1 == total) sh.end_block = blocks;
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+                const int64_t u = e ? u1 : u0;
+                if (!(u >= at && u < at + mine)) continue;  // one thread goes on
+                int t = t0;
+                int64_t vs = at;
+#pragma unroll 1
+                for (; t + 1 < t1; ++t) {
+                    const int nb = tile_info<N, kKind>(a, t).nb + kCost;
+                    if (u < vs + nb) break;
+                    vs += nb;
+                }
+                const int kb = int(max(int64_t(0), u - vs - kCost));
+                const int64_t block = vs - int64_t(kCost) * t + kb;
+                if (e) {
+                    sh.end_block = block;
+                } else {
+                    sh.start_tile = t;
+                    sh.start_kb = kb;
+                    sh.u0 = block;
+                }
+            }
+            __syncthreads();
+            if (tid == 0) sh.units = u1 > u0 ? int(sh.end_block - sh.u0) : 0;
         }
     }
     tc_fence_before();
@@ -1108,7 +1146,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) attend_kernel(const __grid_
                 if (tid == 0 && i + 1 == units) {
                     int2 join = make_int2(-1, 0);
                     if (kb0 == 0 && !whole) {  // later CTAs hold the rest of this tile
-                        const int64_t end_unit = sh.u0 + units - 1 + (cur.t.nb - 1 - cur.kb);
+                        const int64_t end_unit = sh.u0 + units - 1 + (cur.t.nb - 1 - cur.kb) + int64_t(kCost) * (cur.tile + 1);
                         const int64_t g = min(int64_t(gridDim.x), sh.total);
                         join = make_int2(cur.tile, int(((end_unit + 1) * g - 1) / sh.total));
                     }
