@@ -7,8 +7,8 @@ kvq_translate_loc, kvq_attend, kvq_norm_quant) and the seeded synthetic input ge
 """
 from .kvq import (  # noqa: F401
     BF16, F32, FLAG_NORM, FLAG_ROPE, I32, I64, V41, V41_FP4, KVQError, attend_wait_limit, attend_workspace, bytes_per_token,
-    ROPE_HALF, ROPE_INVERSE, kvq_attend, kvq_attend_slots, kvq_attend_tree, kvq_evict_move, kvq_evict_select, kvq_norm_quant, kvq_rope,
-    kvq_rope_table, kvq_tree_mask,
+    ROPE_HALF, ROPE_INVERSE, kvq_attend, kvq_attend_mass, kvq_attend_slots, kvq_attend_tree, kvq_evict_move, kvq_evict_select,
+    kvq_norm_quant, kvq_rope, kvq_rope_table, kvq_tree_mask, mass_workspace,
     kvq_compress, kvq_compress_decode, kvq_dequant, kvq_dequant_slots, kvq_store, kvq_translate_loc, lib, page_bytes,
 )
 from .rope import rope_frequencies  # noqa: F401

@@ -98,12 +98,15 @@ kvq_status attend_pages(int layout, int page_bits, const void *q_bf16, int64_t q
     a.ws = static_cast<uint8_t *>(workspace);
     a.err = err;
     a.out_bf16 = out_dtype == KVQ_BF16;
-    a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
+    a.wait_tries = attend_wait_tries();
     if (tree) return layout == KVQ_LAYOUT_V41 ? launch_attend_tree_v41(a, stream) : launch_attend_tree_fp4(a, stream);
     return launch_attend(layout, a, false, stream);
 }
 
 }  // namespace
+
+uint32_t attend_wait_tries() { return g_wait_tries.load(std::memory_order_relaxed); }
+
 }  // namespace kvq
 
 using namespace kvq;
@@ -183,6 +186,6 @@ extern "C" kvq_status kvq_attend_slots(kvq_layout layout, int page_bits, const v
     a.err = err;
     a.slots64 = slot_dtype == KVQ_I64;
     a.out_bf16 = out_dtype == KVQ_BF16;
-    a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
+    a.wait_tries = attend_wait_tries();
     return launch_attend(layout, a, true, reinterpret_cast<cudaStream_t>(stream));
 }

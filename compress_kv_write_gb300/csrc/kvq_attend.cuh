@@ -58,6 +58,9 @@ __device__ __forceinline__ float attend_lse(float m, float sum) {
     return ((m + float(e)) + log2f(__uint_as_float((__float_as_uint(sum) & 0x7FFFFFu) | 0x3F800000u))) * 0.6931471805599453f;
 }
 
+// The limit that kvq_attend_wait_limit sets.
+uint32_t attend_wait_tries();
+
 kvq_status launch_attend_v41(const AttendArgs &a, bool slots, cudaStream_t s);
 kvq_status launch_attend_fp4(const AttendArgs &a, bool slots, cudaStream_t s);
 kvq_status launch_attend_tree_v41(const AttendArgs &a, cudaStream_t s);

@@ -1,0 +1,640 @@
+// kvq_mass_kernel.cuh -- the weight that attention gives each cached token,
+// summed over the query rows that see it.
+//
+// For a tile of N query rows and the cached rows k[t], block after block of
+// 128 tokens:
+//   S[t, r] = sum_d k[t, d] q[r, d]                    (tokens x rows)
+//   mass[t] = sum_r 2^(scale log2(e) S[t, r] - log2(e) lse_r)
+// There is one product and no state between blocks: the softmax's statistics
+// come with the call, a token's sum is one thread's (a TMEM lane), and nothing
+// is joined but the tiles of a sequence with more than 128 query rows.
+//
+// The products are tcgen05 with 128 tokens on the wide side and N = 16, 32, 64
+// or 128 rows on the narrow one.  Codes and scales come by bulk copies, 32
+// tokens a stage, up to 16 stages ahead; a decode warp takes 128 dims of a
+// stage to registers, frees it, and writes fp16 into TMEM as the product's A
+// operand (nothing goes back to shared memory).  A query tile stays in shared
+// memory as long as its blocks last.
+//
+// The numerics are the attention's: queries times a power of two in fp16 (exact
+// down to 2^-28 of a row's largest value), cached rows exact in fp16 (V41:
+// relative to a power of two of their own), fp32 sums.
+#pragma once
+
+#include "kvq_attend_rows.cuh"
+#include "kvq_mass.cuh"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kMTile = 128;  // cached tokens a block
+constexpr int kMStage = 32;  // tokens a stage: a block's share of a TMEM lane quarter
+constexpr int kMChunks = kD / 128;
+// Warps: 0-15 decode (four a quarter of the lanes, a chunk of 128 dims each), 16-23 weights (a lane quarter each; one four
+// for even, one for odd blocks), 24-27 load queries, 28 issues the products, 29 looks up pages and issues the copies.
+constexpr int kMDeq = 16, kMSoft = 8, kMQuery = 4;
+constexpr int kMSoft0 = kMDeq, kMQuery0 = kMSoft0 + kMSoft, kMMma = kMQuery0 + kMQuery, kMLoad = kMMma + 1;
+constexpr int kMThreads = (kMLoad + 1) * 32;
+// What a tile costs beside its blocks (its queries), in blocks, when blocks are shared out.
+constexpr int kMTileCost = 2;
+
+template <Layout L>
+constexpr int kMStageBytes = kMStage * kTokenBytes<L>;
+// Stages: a multiple of four, so that each quarter has slots of its own.
+template <Layout L, int N>
+constexpr int kMStages = (L == Layout::V41 ? 1 : 2) * (N == 128 ? 4 : 8);
+// Chunks that TMEM holds for the products, beside two blocks' scores; four or more, so that a wait for the one that had
+// a slot before is at most one phase off.
+template <int N>
+constexpr int kMRing = N == 128 ? 4 : N == 64 ? 6 : 7;
+
+template <Layout L, int N>
+struct MassShared {
+    static constexpr int S = kMStages<L, N>, KR = kMRing<N>;
+    uint64_t full[S], empty[S];     // a stage's codes are there; are read
+    uint64_t ready[KR], scored[KR]; // a chunk is in TMEM; its products are done
+    uint64_t sdone[2], sread[2];    // a block's scores are done; are read
+    uint64_t tready[4];             // a block's powers of two are there
+    uint64_t qready, qfree, cready[4];
+    uint64_t drain;
+    int64_t scan[2][kMThreads / 32];
+    int64_t u0, u1, b0, b1;
+    int start_tile, start_kb;
+    uint32_t tmem;
+    int abort;
+    uint32_t there[S];              // which of a stage's tokens are
+    int texp[4][kMTile];            // a token's power of two, or kNoToken
+    // of a tile's rows, four tiles in turn: factor, -log2(e) lse, tokens seen; the fewest that one of a warp's rows sees
+    alignas(16) float sc[4][N], nl[4][N];
+    alignas(16) int vis[4][N];
+    int least[4][kMQuery];
+};
+
+template <Layout L, int N>
+constexpr size_t kMassSmem = 1024 + size_t(N) * kD * 2 + size_t(kMStages<L, N>) * kMStageBytes<L> + sizeof(MassShared<L, N>);
+static_assert(kMassSmem<Layout::V41, 16> <= 232448 && kMassSmem<Layout::V41, 32> <= 232448 &&
+                  kMassSmem<Layout::V41, 64> <= 232448 && kMassSmem<Layout::V41, 128> <= 232448 &&
+                  kMassSmem<Layout::FP4, 16> <= 232448 && kMassSmem<Layout::FP4, 64> <= 232448 &&
+                  kMassSmem<Layout::FP4, 128> <= 232448,
+              "227 KB a CTA");
+
+struct MassSeq {
+    int len, err;
+    int64_t trow, mrow;
+};
+
+__device__ __forceinline__ MassSeq mass_seq(const MassArgs &a, int seq) {
+    MassSeq s;
+    s.trow = a.req ? __ldg(a.req + seq) : seq;
+    s.mrow = a.rows ? __ldg(a.rows + seq) : seq;
+    s.len = __ldg(a.kv_len + seq);
+    s.err = 0;
+    if (s.trow < 0 || s.trow >= a.table_rows || s.mrow < 0 || s.mrow >= a.n_rows) s.err = KVQ_DEVERR_STATE;
+    else if (s.len < 0 || s.len > a.max_len) s.err = KVQ_DEVERR_LEN;
+    if (s.err) s.len = 0;
+    return s;
+}
+
+// Walks a CTA's blocks in order; tiles of empty sequences have none.
+struct MassCursor {
+    int tile, kb, left, seq, rt, nb, nth;  // nth: which of this CTA's tiles
+    MassSeq s;
+    __device__ __forceinline__ MassCursor(const MassArgs &a, int start_tile, int start_kb, int units)
+        : tile(start_tile), kb(start_kb), left(units), nth(0) {
+        look(a);
+    }
+    __device__ __forceinline__ void look(const MassArgs &a) {
+        seq = int(uint32_t(tile) / uint32_t(a.row_tiles));
+        rt = int(uint32_t(tile) % uint32_t(a.row_tiles));
+        s = mass_seq(a, seq);
+        nb = (s.len + kMTile - 1) / kMTile;
+    }
+    __device__ __forceinline__ void next(const MassArgs &a) {
+        if (--left <= 0) return;
+        if (++kb < nb) return;
+        next_tile(a);
+    }
+    __device__ __forceinline__ void next_tile(const MassArgs &a) {  // there is one
+        kb = 0;
+        ++nth;
+        do {
+            ++tile;
+            look(a);
+        } while (nb == 0);
+    }
+};
+
+// Where a decoded row lies.  A decode thread has, of tokens r + 8 h (r = lane /
+// 4, h = 0..3) of its warp's 32, the 32 dims (a quant block) from 32 q (q =
+// lane % 4) of its warp's chunk, as vectors v = 0..3 of eight.  In TMEM vector v
+// fills the columns 16 v + 4 i + q, i = 0..3, two dims a column: the contraction
+// runs over the dims in that order, and this is the byte offset in a query
+// tile's shared memory (two 128-byte-swizzled tiles of 32 columns a chunk) of
+// word i of piece g = 0..63 (dims 8 g + 2 i, 8 g + 2 i + 1) of row r.
+template <int N>
+__device__ __forceinline__ uint32_t mass_q_word(int r, int g, int i) {
+    const int b = g >> 4, q = (g >> 2) & 3, v = g & 3;
+    return uint32_t((2 * b + (v >> 1)) * N * 128 + r * 128 + (((4 * (v & 1) + i) ^ (r & 7)) << 4) + q * 4);
+}
+
+template <Layout L, int N>
+__global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constant__ MassArgs a) {
+    using T = LayoutTraits<L>;
+    constexpr int S = kMStages<L, N>, KR = kMRing<N>;
+    constexpr uint32_t kTmemK = 2 * N, kTmemCols = 512;  // scores, then chunks of rows
+    static_assert(kTmemK + 64 * KR <= kTmemCols, "they fit");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
+    uint8_t *const sQ = base, *const sStage = sQ + N * kD * 2;
+    auto &sh = *reinterpret_cast<MassShared<L, N> *>(sStage + S * kMStageBytes<L>);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(smem_addr(&sh.full[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), kMChunks);
+        }
+        for (int i = 0; i < KR; ++i) {
+            mbar_init(smem_addr(&sh.ready[i]), 4);
+            mbar_init(smem_addr(&sh.scored[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.sdone[i]), 1);
+            mbar_init(smem_addr(&sh.sread[i]), 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&sh.tready[i]), 4);
+            mbar_init(smem_addr(&sh.cready[i]), kMQuery);
+        }
+        mbar_init(smem_addr(&sh.qready), kMQuery);
+        mbar_init(smem_addr(&sh.qfree), 1);
+        mbar_init(smem_addr(&sh.drain), 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMMma) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
+    pdl_wait();
+
+    // ---- this CTA's share of all tiles' blocks in order, each tile with kMTileCost units before its blocks
+    const int tiles = int(a.n_seq * a.row_tiles);
+    {
+        const int per = (tiles + kMThreads - 1) / kMThreads;
+        const int t0 = int(min(int64_t(tiles), int64_t(tid) * per)), t1 = int(min(int64_t(tiles), int64_t(t0) + per));
+        auto blocks_of = [&](int t, bool tell) {
+            const MassSeq s = mass_seq(a, int(uint32_t(t) / uint32_t(a.row_tiles)));
+            if (tell && s.err) raise_err(a.err, s.err);
+            return (s.len + kMTile - 1) / kMTile;
+        };
+        int64_t units = 0, blocks = 0;
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t) {
+            const int nb = blocks_of(t, blockIdx.x == 0);
+            blocks += nb;
+            units += nb ? nb + kMTileCost : 0;
+        }
+        int64_t iu = units, ib = blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, (long long)iu, o), w = __shfl_up_sync(0xFFFFFFFFu, (long long)ib, o);
+            if (lane >= o) iu += v, ib += w;
+        }
+        if (lane == 31) sh.scan[0][warp] = iu, sh.scan[1][warp] = ib;
+        __syncthreads();
+        int64_t bu = 0, bb = 0, total = 0, all = 0;
+#pragma unroll 1
+        for (int w = 0; w < kMThreads / 32; ++w) {
+            if (w < warp) bu += sh.scan[0][w], bb += sh.scan[1][w];
+            total += sh.scan[0][w], all += sh.scan[1][w];
+        }
+        int64_t u0, u1;
+        share(total, u0, u1);
+        if (tid == 0) {
+            sh.b0 = sh.b1 = 0;
+            if (u1 > u0 && u1 == total) sh.b1 = all;
+        }
+        __syncthreads();
+        const int64_t at = bu + iu - units, bat = bb + ib - blocks;
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+            const int64_t u = e ? u1 : u0;
+            if (u1 == u0 || !(u >= at && u < at + units)) continue;  // one thread goes on
+            int64_t vs = at, vb = bat;
+            int t = t0;
+#pragma unroll 1
+            for (;; ++t) {
+                const int nb = blocks_of(t, false), w = nb ? nb + kMTileCost : 0;
+                if (u < vs + w) break;
+                vs += w, vb += nb;
+            }
+            const int kb = int(max(int64_t(0), u - vs - kMTileCost));
+            if (e) {
+                sh.b1 = vb + kb;
+            } else {
+                sh.b0 = vb + kb;
+                sh.start_tile = t;
+                sh.start_kb = kb;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int units = int(sh.b1 - sh.b0), start_tile = sh.start_tile, start_kb = sh.start_kb;
+    if (units <= 0) {  // the same for every thread
+        if (warp == kMMma) tmem_dealloc(sh.tmem, kTmemCols);
+        pdl_trigger();
+        return;
+    }
+    const int per = a.q_len * a.heads;  // query rows of a sequence
+    uint32_t tries = a.wait_tries;
+
+    if (warp < kMDeq) {
+        // ------------------------------------------------------ decode
+        const int quarter = warp & 3, chunk = warp >> 2, q = lane & 3, r8 = lane >> 2;
+        const uint32_t tlane = kTmemK + ((32 * quarter) << 16);
+        const uint32_t code_at = r8 * T::kCodeBytes + chunk * (T::kCodeBytes / kMChunks) + q * (T::kCodeBytes / kNBlk);
+        const uint32_t scale_at = kMStage * T::kCodeBytes + r8 * T::kScaleBytes;
+        int slot = quarter, kslot = chunk;
+        uint32_t parity = 0, kparity = 1;  // of the stage; of the chunk that had this one's TMEM slot before
+#pragma unroll 1
+        for (int i = 0; i < units; ++i) {
+            mbar_wait(smem_addr(&sh.full[slot]), parity, tries);
+            const uint32_t stage = smem_addr(sStage) + slot * kMStageBytes<L>;
+            const uint32_t there = sh.there[slot];
+            Raw<L> raw[4][2];  // token, half of the 32 codes
+            int texp[4];
+            uint32_t mul[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t at = stage + code_at + 8 * h * T::kCodeBytes;
+                if constexpr (L == Layout::V41) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 u = lds_u4(at + 16 * j);
+                        raw[h][j].w[0] = u.x, raw[h][j].w[1] = u.y, raw[h][j].w[2] = u.z, raw[h][j].w[3] = u.w;
+                    }
+                } else {
+                    const uint4 u = lds_u4(at);
+                    raw[h][0].w[0] = u.x, raw[h][0].w[1] = u.y, raw[h][1].w[0] = u.z, raw[h][1].w[1] = u.w;
+                }
+                const uint4 sc = lds_u4(stage + scale_at + 8 * h * T::kScaleBytes);
+                texp[h] = row_texp<L>(sc);
+                const uint32_t w = chunk == 0 ? sc.x : chunk == 1 ? sc.y : chunk == 2 ? sc.z : sc.w;
+                mul[h] = block_mul<L>((w >> (8 * q)) & 0xFFu, texp[h]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
+            // a slot in TMEM is free when the products over what it held are done
+            if (i * kMChunks + chunk >= KR) mbar_wait(smem_addr(&sh.scored[kslot]), kparity, tries);
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 4; h += 2)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t v0[4], v1[4];
+                    decode8<L>(raw[h][v >> 1], v & 1, mul[h], v0);
+                    decode8<L>(raw[h + 1][v >> 1], v & 1, mul[h + 1], v1);
+                    tmem_st_16x128b_x4(tlane + (uint32_t(8 * h) << 16) + kslot * 64 + 16 * v, v0, v1);
+                }
+            if (chunk == 0 && q == 0) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int t = 8 * h + r8;
+                    sh.texp[i & 3][32 * quarter + t] = (there >> t) & 1 ? texp[h] : kNoToken;
+                }
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&sh.ready[kslot]));
+                if (chunk == 0) mbar_arrive(smem_addr(&sh.tready[i & 3]));
+            }
+            slot += 4;
+            if (slot >= S) {
+                slot -= S;
+                parity ^= 1;
+            }
+            kslot += kMChunks;
+            if (kslot >= KR) {
+                kslot -= KR;
+                kparity ^= 1;
+            }
+        }
+    } else if (warp < kMQuery0) {
+        // ------------------------------------------------------ weights
+        const int quarter = warp & 3, group = (warp - kMSoft0) >> 2, tok = 32 * quarter + lane;
+        const uint32_t tfrom = (uint32_t(32 * quarter) << 16) + group * N;
+        MassCursor cur(a, start_tile, start_kb, units);
+        int known = -1, least = 0;  // the tile whose rows are known to be there; the fewest tokens that one of them sees
+#pragma unroll 1
+        for (int i = 0; i < units; ++i, cur.next(a)) {
+            if ((i & 1) != group) continue;
+            const int c = cur.nth & 3;
+            if (known != cur.nth) {
+                known = cur.nth;
+                mbar_wait(smem_addr(&sh.cready[c]), (cur.nth >> 2) & 1, tries);
+                least = min(min(sh.least[c][0], sh.least[c][1]), min(sh.least[c][2], sh.least[c][3]));
+            }
+            const int t = cur.kb * kMTile + tok;
+            const bool mine = t < cur.s.len;
+            float before = 0.f;
+            if (a.row_tiles == 1 && a.prev && mine) before = a.prev[cur.s.mrow * a.prev_stride + t];
+            mbar_wait(smem_addr(&sh.tready[i & 3]), (i >> 2) & 1, tries);
+            const int te = sh.texp[i & 3][tok];
+            const bool there = te != kNoToken;
+            const float up = L == Layout::V41 && there ? __uint_as_float(uint32_t(127 + te - kLift) << 23) : 1.f;
+            const bool masked = (cur.kb + 1) * kMTile > least;
+            mbar_wait(smem_addr(&sh.sdone[group]), (i >> 1) & 1, tries);
+            tc_fence_after();
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+            for (int j0 = 0; j0 < N; j0 += 16) {
+                uint32_t x[16];
+                tmem_ld16(tfrom + j0, x);
+                if (j0 + 16 == N) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.sread[group]));
+                }
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 sc = *reinterpret_cast<const float4 *>(&sh.sc[c][j0 + j]);
+                    const float4 nl = *reinterpret_cast<const float4 *>(&sh.nl[c][j0 + j]);
+                    float2 u0 = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                    float2 u1 = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                    if constexpr (L == Layout::V41) {
+                        u0 = fmul2(u0, make_float2(up, up));
+                        u1 = fmul2(u1, make_float2(up, up));
+                    }
+                    u0 = ffma2(u0, make_float2(sc.x, sc.y), make_float2(nl.x, nl.y));
+                    u1 = ffma2(u1, make_float2(sc.z, sc.w), make_float2(nl.z, nl.w));
+                    float2 p0 = make_float2(ex2_approx(u0.x), ex2_approx(u0.y));
+                    float2 p1 = make_float2(ex2_approx(u1.x), ex2_approx(u1.y));
+                    if (masked) {
+                        const int4 vis = *reinterpret_cast<const int4 *>(&sh.vis[c][j0 + j]);
+                        p0 = make_float2(t < vis.x ? p0.x : 0.f, t < vis.y ? p0.y : 0.f);
+                        p1 = make_float2(t < vis.z ? p1.x : 0.f, t < vis.w ? p1.y : 0.f);
+                    }
+                    sum[0] = fadd2(sum[0], p0);
+                    sum[1] = fadd2(sum[1], p1);
+                }
+            }
+            if (mine && tries) {
+                const float2 two = fadd2(sum[0], sum[1]);
+                const float all = there ? two.x + two.y : 0.f;
+                if (a.row_tiles == 1) a.mass[cur.s.mrow * a.mass_stride + t] = a.prev ? fmaf(a.decay, before, all) : all;
+                else a.part[int64_t(cur.tile) * a.part_stride + t] = all;
+            }
+        }
+    } else if (warp < kMMma) {
+        // ------------------------------------------------------ queries
+        const int w = warp - kMQuery0;
+        const uint32_t sq = smem_addr(sQ);
+        const float c = a.scale * kLog2e;
+        constexpr int kBatch = N / kMQuery < 4 ? N / kMQuery : 4;  // rows whose loads are in flight
+        MassCursor cur(a, start_tile, start_kb, units);
+#pragma unroll 1
+        for (;;) {
+            const int slot = cur.nth & 3;
+            int least = 0x7FFFFFFF;
+#pragma unroll 1
+            for (int r0 = w; r0 < N; r0 += kBatch * kMQuery) {
+                uint32_t v[kBatch][8];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int row = cur.rt * N + r0 + b * kMQuery, rc = min(row, per - 1);
+                    const int j = rc / a.heads, head = rc - j * a.heads;
+                    const uint16_t *from = a.q + (int64_t(cur.seq) * a.q_len + j) * a.q_tok + head * a.q_head;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                        if (row < per) u = ld_stream_u4(from + (lane + 32 * h) * 8);
+                        v[b][4 * h] = u.x, v[b][4 * h + 1] = u.y, v[b][4 * h + 2] = u.z, v[b][4 * h + 3] = u.w;
+                    }
+                }
+                // the last tile's queries are free when its products are done
+                if (r0 == w && cur.nth > 0) mbar_wait(smem_addr(&sh.qfree), (cur.nth - 1) & 1, tries);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int r = r0 + b * kMQuery, row = cur.rt * N + r;
+                    // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
+                    uint32_t big = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) big = max(big, max((v[b][e] << 16) & 0x7FFF0000u, v[b][e] & 0x7FFF0000u));
+                    big = __reduce_max_sync(0xFFFFFFFFu, big);
+                    const uint32_t up = min(268u - (big >> 23), 254u);
+                    const float f = __uint_as_float(up << 23);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t h;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[b][e]) * f), "f"(bf16_lo(v[b][e]) * f));
+                        sts_u32(sq + mass_q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
+                    }
+                    if (lane == 0) {
+                        // a row of no one's, and one that saw nothing (lse = -inf), has no weight
+                        const bool real = row < per;
+                        const float l = real ? __ldg(a.lse + int64_t(cur.seq) * per + row) : -INFINITY;
+                        const bool none = l == -INFINITY;
+                        const int j = min(row, per - 1) / a.heads;
+                        const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - j));
+                        sh.sc[slot][r] = none ? 0.f : score_factor<L>(c, up);
+                        sh.nl[slot][r] = none ? -INFINITY : -l * kLog2e;
+                        sh.vis[slot][r] = vis;
+                        if (real) least = min(least, vis);
+                    }
+                }
+            }
+            if (lane == 0) sh.least[slot][w] = least;
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&sh.qready));
+                mbar_arrive(smem_addr(&sh.cready[slot]));
+            }
+            const int blocks = cur.nb - cur.kb;
+            if (cur.left <= blocks) break;
+            cur.left -= blocks;
+            cur.next_tile(a);
+        }
+    } else if (warp == kMMma) {
+        // ------------------------------------------------------ products
+        constexpr uint32_t kIdesc = mma_idesc(kMTile, N, false, false), kHi = desc_hi(1024, kSwizzle128);
+        const uint32_t qd = desc_lo(smem_addr(sQ), 16);
+        MassCursor cur(a, start_tile, start_kb, units);
+        int kslot = 0;
+        uint32_t kparity = 0;
+        bool fresh = true;
+#pragma unroll 1
+        for (int i = 0; i < units; ++i) {
+            if (fresh) mbar_wait(smem_addr(&sh.qready), cur.nth & 1, tries);
+            fresh = cur.kb + 1 == cur.nb;
+            // the score buffer is free when the block before the last has been read
+            if (i >= 2) mbar_wait(smem_addr(&sh.sread[i & 1]), ((i - 2) >> 1) & 1, tries);
+            const uint32_t to = (i & 1) * N;
+#pragma unroll
+            for (int b = 0; b < kMChunks; ++b) {
+                mbar_wait(smem_addr(&sh.ready[kslot]), kparity, tries);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(to, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kHi, kIdesc, b + k > 0);
+                    mma_commit(smem_addr(&sh.scored[kslot]));
+                    if (b == kMChunks - 1) {
+                        mma_commit(smem_addr(&sh.sdone[i & 1]));
+                        if (fresh) mma_commit(smem_addr(&sh.qfree));
+                    }
+                }
+                __syncwarp();
+                if (++kslot == KR) {
+                    kslot = 0;
+                    kparity ^= 1;
+                }
+            }
+            cur.next(a);
+        }
+        if (!tries) sh.abort = 1;
+        tries = kWaitTries;
+        if (elect_one()) mma_commit(smem_addr(&sh.drain));  // nothing may write TMEM once it is freed
+        __syncwarp();
+        mbar_wait(smem_addr(&sh.drain), 0, tries);
+    } else {
+        // ------------------------------------------------------ pages and copies
+        const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits, area = int64_t(T::kCodeBytes) << a.page_bits;
+        const int in_page = (1 << a.page_bits) - 1;
+        const int piece_rows = min(kMStage, 1 << a.page_bits);  // tokens a copy has
+        const int page_of = min(a.page_bits, 7);                // lane l looks up the page of token l << page_of of a block
+        MassCursor cur(a, start_tile, start_kb, units);
+        int64_t entry = -1;
+        auto fetch = [&]() {
+            const int t = cur.kb * kMTile + (lane << page_of);
+            entry = -1;
+            if ((lane << page_of) < kMTile && t < cur.s.len) entry = __ldg(a.table + cur.s.trow * a.table_stride + (t >> a.page_bits));
+        };
+        fetch();
+        int slot = 0, issued = 0;
+        uint32_t parity = 1;
+#pragma unroll 1
+        for (int i = 0; i < units && tries; ++i) {
+            const int64_t page_here = entry;
+            const int t0 = cur.kb * kMTile, len = cur.s.len;
+            if (i + 1 < units) {  // the next block's pages, while this one's stages become free
+                cur.next(a);
+                fetch();
+            }
+#pragma unroll 1
+            for (int st = 0; st < 4; ++st) {
+                if (issued >= S) mbar_wait(smem_addr(&sh.empty[slot]), parity, tries);
+                if (!tries) break;
+                // lane l has the piece from token l * piece_rows of the stage on
+                const int at = lane * piece_rows, t = t0 + st * kMStage + at;
+                const bool has = at < kMStage && t < len;
+                const int64_t page = __shfl_sync(0xFFFFFFFFu, (long long)page_here, ((st * kMStage + min(at, kMStage - 1)) >> page_of) & 31);
+                const bool good = has && page >= 0 && page < a.pool_limit;
+                if (has && !good) raise_err(a.err, KVQ_DEVERR_PAGE);
+                uint32_t mask = 0;
+                if (good) {
+                    const int n = min(piece_rows, len - t);
+                    mask = (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1) << at;
+                }
+                mask = __reduce_or_sync(0xFFFFFFFFu, mask);
+                const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, good)) * piece_rows * kTokenBytes<L>;
+                const uint32_t bar = smem_addr(&sh.full[slot]);
+                if (lane == 0) {
+                    sh.there[slot] = mask;
+                    mbar_arrive_expect(bar, bytes);
+                }
+                __syncwarp();
+                if (good) {
+                    const uint32_t to = smem_addr(sStage) + slot * kMStageBytes<L>;
+                    const uint8_t *from = a.pool + page * page_bytes;
+                    const int row = t & in_page;
+                    bulk_load(to + at * T::kCodeBytes, from + int64_t(row) * T::kCodeBytes, piece_rows * T::kCodeBytes, bar);
+                    bulk_load(to + kMStage * T::kCodeBytes + at * T::kScaleBytes, from + area + int64_t(row) * T::kScaleBytes,
+                              piece_rows * T::kScaleBytes, bar);
+                }
+                ++issued;
+                if (++slot == S) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        if (!tries) sh.abort = 1;
+        // no copy may be under way when the CTA ends: each slot's last one
+        tries = kWaitTries;
+        for (int k = 0; k < S && k < issued; ++k) {
+            const int last = (issued - 1 - k) / S;  // how often the slot was used before
+            mbar_wait(smem_addr(&sh.full[k]), last & 1, tries);
+        }
+        tries = 1;
+    }
+    if (!tries) sh.abort = 1;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) pdl_trigger();
+    if (warp == kMMma) tmem_dealloc(sh.tmem, kTmemCols);
+    if (sh.abort) {  // a wait gave up: the weights that this CTA worked on are NaN, at once or by way of the join
+        if (tid == 0) raise_err(a.err, KVQ_DEVERR_WAIT);
+        MassCursor cur(a, start_tile, start_kb, units);
+#pragma unroll 1
+        for (int i = 0; i < units; ++i, cur.next(a)) {
+            const int t = cur.kb * kMTile + tid;
+            if (tid >= kMTile || t >= cur.s.len) continue;
+            if (a.row_tiles == 1) a.mass[cur.s.mrow * a.mass_stride + t] = NAN;
+            else a.part[int64_t(cur.tile) * a.part_stride + t] = NAN;
+        }
+    }
+}
+
+// Adds the tiles of sequences that have several, in order, and what was before.
+constexpr int kMJoinThreads = 256;
+
+__global__ void __launch_bounds__(kMJoinThreads) mass_join_kernel(const __grid_constant__ MassArgs a) {
+    pdl_wait();
+    const int seq = blockIdx.y;
+    const MassSeq s = mass_seq(a, seq);
+    const float *part = a.part + int64_t(seq) * a.row_tiles * a.part_stride;
+    for (int64_t t = int64_t(blockIdx.x) * kMJoinThreads + threadIdx.x; t < s.len; t += int64_t(gridDim.x) * kMJoinThreads) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < a.row_tiles; ++k) sum += part[k * a.part_stride + t];
+        if (a.prev) sum = fmaf(a.decay, a.prev[s.mrow * a.prev_stride + t], sum);
+        a.mass[s.mrow * a.mass_stride + t] = sum;
+    }
+}
+
+template <Layout L, int N>
+kvq_status launch_mass_n(MassArgs a, cudaStream_t s) {
+    const int64_t per = int64_t(a.q_len) * a.heads;
+    a.row_tiles = int(mass_tiles(per));
+    const int64_t tiles = a.n_seq * a.row_tiles;
+    int64_t grid = 0;
+    kvq_status st = resident_grid<mass_kernel<L, N>, kMThreads>(kMassSmem<L, N>, &grid);
+    if (st != KVQ_OK) return st;
+    if (grid > kMaxAttendCtas) grid = kMaxAttendCtas;
+    const int64_t most = (a.max_len + kMTile - 1) / kMTile;  // blocks of the longest tile there can be
+    if (tiles > 0x7FFFFFFF || tiles * (most ? most : 1) / grid >= 0x7FFFFFFF / 8) return KVQ_ERR_UNSUPPORTED;
+    if (most <= 1 && tiles < grid) grid = tiles;
+    st = launch_pdl_smem(mass_kernel<L, N>, dim3(unsigned(grid)), dim3(kMThreads), kMassSmem<L, N>, s, a);
+    if (st != KVQ_OK || a.row_tiles == 1) return st;
+    const int64_t wide = (a.max_len + kMJoinThreads - 1) / kMJoinThreads;
+    return launch_pdl(mass_join_kernel, dim3(unsigned(wide < 1 ? 1 : wide < 1024 ? wide : 1024), unsigned(a.n_seq)), dim3(kMJoinThreads), s, a);
+}
+
+template <Layout L>
+kvq_status launch_mass_layout(const MassArgs &a, cudaStream_t s) {
+    switch (mass_rows(int64_t(a.q_len) * a.heads)) {
+        case 16: return launch_mass_n<L, 16>(a, s);
+        case 32: return launch_mass_n<L, 32>(a, s);
+        case 64: return launch_mass_n<L, 64>(a, s);
+        default: return launch_mass_n<L, 128>(a, s);
+    }
+}
+
+}  // namespace
+}  // namespace kvq

@@ -1,6 +1,6 @@
 // kvq_tcgen05.cuh -- the sm_103a tensor-core primitives of the attention
-// kernel: bounded mbarrier waits, TMEM allocation and access, shared-memory
-// and instruction descriptors, and the MMA itself.
+// kernels: bounded mbarrier waits, bulk copies, TMEM allocation and access,
+// shared-memory and instruction descriptors, and the MMA itself.
 #pragma once
 
 #include "kvq_device.cuh"
@@ -12,6 +12,17 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrives, and has the phase wait for `bytes` of bulk copies besides.
+__device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Global to shared memory, both 16-byte aligned and `bytes` a multiple of 16; the barrier counts the bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // Waits until the phase of the given parity has completed, with a bound:

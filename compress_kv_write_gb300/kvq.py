@@ -59,6 +59,11 @@ _SIGS = {
                              C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
                              C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_int, C.c_int64, C.c_int64,
                              C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "kvq_mass_workspace": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64]),
+    "kvq_attend_mass": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                  C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                  C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                  C.c_int64, C.c_float, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
     "kvq_tree_mask": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                 C.c_void_p, C.c_void_p]),
     "kvq_attend_tree": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
@@ -617,6 +622,48 @@ def _index_rows(t, name, n_seq, table, table_name):
     _contig1d(t, name)
     if t.numel() != n_seq:
         raise ValueError(f"{name} must hold one row per sequence")
+
+
+def mass_workspace(n_seq, rows, max_len):
+    """Bytes of workspace for kvq_attend_mass: n_seq sequences, rows = q_len * heads, max_len tokens a row of the table (or of
+    the weights, where that is less) can have."""
+    return int(lib().kvq_mass_workspace(int(n_seq), int(rows), int(max_len)))
+
+
+def kvq_attend_mass(layout, page_bits, q, lse, pool, pool_pages, page_table, kv_len, mass, workspace=None, *, scale, q_len=1,
+                    req=None, rows=None, prev=None, decay=1.0, err=None, stream=None):
+    """mass [rows, width] fp32 (row rows[i], or i) <- decay * prev + the weight of each of a sequence's cached tokens in
+    kvq_attend, summed over heads and query tokens; q, pool, page_table, kv_len, scale, q_len, req and lse as in that call.
+    prev may be mass itself, or None: no weights from before.  workspace: mass_workspace(n_seq, q_len * heads, max_len)."""
+    _cuda(q, "q", (torch.bfloat16,))
+    _cuda(lse, "lse", (torch.float32,))
+    _cuda(mass, "mass", (torch.float32,))
+    shape, qs = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or qs[2] != 1:
+        raise ValueError("q must be [tokens, heads, 512] with unit inner stride")
+    if lse.shape != shape[:2] or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous [tokens, heads]")
+    t_rows, width, ts, n_seq = _paged(layout, page_bits, q, shape[0], q_len, pool, pool_pages, page_table, kv_len, req)
+    _matrix(mass, "mass")
+    _index_rows(rows, "rows", n_seq, mass, "mass")
+    if prev is not None:
+        _cuda(prev, "prev", (torch.float32,))
+        _matrix(prev, "prev")
+        if prev.shape != mass.shape:
+            raise ValueError("prev must have mass's shape")
+    if workspace is not None:
+        _cuda(workspace, "workspace", (torch.uint8,))
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _err_word(err)
+    dev = _same_device(q, lse, mass, rows, prev, workspace, err)
+    st = _on(dev, stream, lambda s: lib().kvq_attend_mass(
+        layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, shape[1], lse.data_ptr(), pool.data_ptr(), int(pool_pages),
+        page_table.data_ptr(), t_rows, width, ts, _ptr(req), kv_len.data_ptr(), float(scale), mass.data_ptr(), mass.shape[0],
+        mass.shape[1], _stride0(mass), _ptr(rows), _ptr(prev), _stride0(prev) if prev is not None else 0, float(decay),
+        _ptr(workspace), workspace.numel() if workspace is not None else 0, _ptr(err), s))
+    _check(st, "kvq_attend_mass")
+    return mass
 
 
 def kvq_evict_select(mass, kv_len, kept, count, *, first=0, last=0, rows=None, err=None, stream=None):

@@ -332,6 +332,49 @@ kvq_status kvq_attend_slots(kvq_layout layout, int page_bits,
                             float *lse, void *workspace, size_t workspace_bytes,
                             int32_t *err, struct CUstream_st *stream);
 
+/* Bytes of workspace a kvq_attend_mass call needs: n_seq sequences of `rows`
+ * = q_len * heads query rows over at most max_len tokens (table_width pages of
+ * them, or mass_width where that is less).  0 up to 128 rows, 4 bytes a
+ * sequence, token and 128 rows beyond.  As kvq_attend_workspace otherwise. */
+size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
+
+/* The weight that each cached token gets in kvq_attend, summed over the query
+ * rows that see it (all heads of all q_len query tokens, causal):
+ *   w[t] = sum over these rows of exp(scale * sum_d q[d] k[t][d] - lse[row]),
+ *   mass[t] = decay * prev[t] + w[t], or, where prev is NULL, w[t],
+ * for the tokens t < kv_len[i] of sequence i; what lies behind them in mass
+ * stays as it is.  With prev = mass the weights of one step after another add
+ * up, the older ones worth `decay` as much each step.
+ *   q, pool, page_table, req, kv_len, scale   as in kvq_attend, the call's own.
+ *   lse        [n_seq * q_len, heads] fp32: what kvq_attend left.  A row whose
+ *              lse is -inf has no weight.
+ *   mass       [mass_rows, mass_row_stride] fp32, the first mass_width of a
+ *              row used; row rows[i] (NULL: row i) is sequence i's.  Sequences
+ *              of a call have rows of their own: what two write to one row is
+ *              unspecified.
+ *   prev       rows like mass's, by the same index: mass itself with its
+ *              stride, or apart from it, or NULL.
+ *   n_seq      at most 65535.
+ *   workspace  kvq_mass_workspace bytes, 16-B aligned (NULL where that is 0).
+ * Products, roundings and what counts as nothing are as for kvq_attend's
+ * scores; the exponent is off by 2^-23 (|score| + |lse|) besides.  Sums are
+ * fp32, in one order whatever the lengths (no atomics on data).
+ * A token whose row holds a NaN or an infinity, and a query row that does or
+ * whose lse is NaN, make the weights that they share in NaN, and no others.
+ * A bad kv_len (KVQ_DEVERR_LEN; mass_width is a limit too), req or row
+ * (KVQ_DEVERR_STATE) makes the sequence an empty one; a token behind a bad
+ * table entry (KVQ_DEVERR_PAGE) has w[t] = 0.  A call that gives up a wait
+ * (KVQ_DEVERR_WAIT) leaves NaN in the weights that it worked on. */
+kvq_status kvq_attend_mass(kvq_layout layout, int page_bits,
+                           const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                           int64_t n_seq, int64_t q_len, int64_t heads, const float *lse,
+                           const uint8_t *pool, int64_t pool_pages,
+                           const int32_t *page_table, int64_t table_rows, int64_t table_width,
+                           int64_t table_stride, const int32_t *req, const int32_t *kv_len, float scale,
+                           float *mass, int64_t mass_rows, int64_t mass_width, int64_t mass_row_stride,
+                           const int32_t *rows, const float *prev, int64_t prev_row_stride, float decay,
+                           void *workspace, size_t workspace_bytes, int32_t *err, struct CUstream_st *stream);
+
 /* RMS norm of a row plus its residual, quantised like a V41 row: the input
  * of the projections whose K rows kvq_store takes.
  *   z = x + residual (fp32; residual NULL: z = x), residual_out = z rounded
