@@ -18,7 +18,8 @@
 //
 // The numerics are the attention's: queries times a power of two in fp16 (exact
 // down to 2^-28 of a row's largest value), cached rows exact in fp16 (V41:
-// relative to a power of two of their own), fp32 sums.
+// relative to a power of two of their own), fp32 sums.  What fp32 constants of
+// the exponent leave out is made up for by a factor a row.
 #pragma once
 
 #include "kvq_attend_rows.cuh"
@@ -65,8 +66,9 @@ struct MassShared {
     int abort;
     uint32_t there[S];              // which of a stage's tokens are
     int texp[4][kMTile];            // a token's power of two, or kNoToken
-    // of a tile's rows, four tiles in turn: factor, -log2(e) lse, tokens seen; the fewest that one of a warp's rows sees
-    alignas(16) float sc[4][N], nl[4][N];
+    // of a tile's rows, four tiles in turn: factor, -log2(e) lse, what their roundings leave out, tokens seen; the fewest
+    // that one of a warp's rows sees
+    alignas(16) float sc[4][N], nl[4][N], wf[4][N];
     alignas(16) int vis[4][N];
     int least[4][kMQuery];
 };
@@ -362,6 +364,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 for (int j = 0; j < 16; j += 4) {
                     const float4 sc = *reinterpret_cast<const float4 *>(&sh.sc[c][j0 + j]);
                     const float4 nl = *reinterpret_cast<const float4 *>(&sh.nl[c][j0 + j]);
+                    const float4 wf = *reinterpret_cast<const float4 *>(&sh.wf[c][j0 + j]);
                     float2 u0 = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
                     float2 u1 = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
                     if constexpr (L == Layout::V41) {
@@ -377,8 +380,8 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                         p0 = make_float2(t < vis.x ? p0.x : 0.f, t < vis.y ? p0.y : 0.f);
                         p1 = make_float2(t < vis.z ? p1.x : 0.f, t < vis.w ? p1.y : 0.f);
                     }
-                    sum[0] = fadd2(sum[0], p0);
-                    sum[1] = fadd2(sum[1], p1);
+                    sum[0] = ffma2(p0, make_float2(wf.x, wf.y), sum[0]);
+                    sum[1] = ffma2(p1, make_float2(wf.z, wf.w), sum[1]);
                 }
             }
             if (mine && tries) {
@@ -392,13 +395,23 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         // ------------------------------------------------------ queries
         const int w = warp - kMQuery0;
         const uint32_t sq = smem_addr(sQ);
-        const float c = a.scale * kLog2e;
+        // A weight is 2^(S c + n) with c = scale log2(e) and n = -log2(e) lse, whose roundings to fp32 would be up to 2^-24
+        // (|S c| + |n|) of the exponent.  S c is about -n wherever a weight counts, so a row's weights are taken times
+        // 2^((n - fl(n)) - n (c / fl(c) - 1)).
+        constexpr double kLog2e64 = 1.4426950408889634;
+        const double c64 = double(a.scale) * kLog2e64;
+        const float c = float(c64);
+        const double c_off = c != 0.f ? c64 / double(c) - 1.0 : 0.0;
         constexpr int kBatch = N / kMQuery < 4 ? N / kMQuery : 4;  // rows whose loads are in flight
         MassCursor cur(a, start_tile, start_kb, units);
 #pragma unroll 1
         for (;;) {
             const int slot = cur.nth & 3;
-            int least = 0x7FFFFFFF;
+            // lane l has the constants of the warp's l-th row
+            const int row_l = cur.rt * N + w + lane * kMQuery;
+            const bool real = lane < N / kMQuery && row_l < per;
+            const float lse = real ? __ldg(a.lse + int64_t(cur.seq) * per + row_l) : -INFINITY;
+            uint32_t up_l = 254;
 #pragma unroll 1
             for (int r0 = w; r0 < N; r0 += kBatch * kMQuery) {
                 uint32_t v[kBatch][8];
@@ -418,7 +431,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 if (r0 == w && cur.nth > 0) mbar_wait(smem_addr(&sh.qfree), (cur.nth - 1) & 1, tries);
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
-                    const int r = r0 + b * kMQuery, row = cur.rt * N + r;
+                    const int r = r0 + b * kMQuery;
                     // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
                     uint32_t big = 0;
 #pragma unroll
@@ -432,20 +445,22 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[b][e]) * f), "f"(bf16_lo(v[b][e]) * f));
                         sts_u32(sq + mass_q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
                     }
-                    if (lane == 0) {
-                        // a row of no one's, and one that saw nothing (lse = -inf), has no weight
-                        const bool real = row < per;
-                        const float l = real ? __ldg(a.lse + int64_t(cur.seq) * per + row) : -INFINITY;
-                        const bool none = l == -INFINITY;
-                        const int j = min(row, per - 1) / a.heads;
-                        const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - j));
-                        sh.sc[slot][r] = none ? 0.f : score_factor<L>(c, up);
-                        sh.nl[slot][r] = none ? -INFINITY : -l * kLog2e;
-                        sh.vis[slot][r] = vis;
-                        if (real) least = min(least, vis);
-                    }
+                    if (lane == r / kMQuery) up_l = up;
                 }
             }
+            // a row of no one's, and one that saw nothing (lse = -inf), has no weight
+            const bool none = lse == -INFINITY;
+            const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - row_l / a.heads));
+            if (lane < N / kMQuery) {
+                const int r = w + lane * kMQuery;
+                sh.sc[slot][r] = none ? 0.f : score_factor<L>(c, up_l);
+                const double n64 = -double(lse) * kLog2e64;
+                const float n = float(n64);
+                sh.nl[slot][r] = none ? -INFINITY : n;
+                sh.wf[slot][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(float((n64 - double(n)) - n64 * c_off));
+                sh.vis[slot][r] = vis;
+            }
+            const int least = __reduce_min_sync(0xFFFFFFFFu, real ? vis : 0x7FFFFFFF);
             if (lane == 0) sh.least[slot][w] = least;
             fence_proxy_async();
             __syncwarp();
@@ -503,64 +518,68 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         mbar_wait(smem_addr(&sh.drain), 0, tries);
     } else {
         // ------------------------------------------------------ pages and copies
+        // A block's four stages go out together: lane l has the piece of piece_rows tokens from token l * piece_rows of the
+        // block on, the first lane of a stage waits for its slot and arms its barrier.  (Stage after stage took 780 clocks
+        // each, all of them this warp's latencies: 16 heads, 4 bits, 1.70 us a block.)
         const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits, area = int64_t(T::kCodeBytes) << a.page_bits;
         const int in_page = (1 << a.page_bits) - 1;
-        const int piece_rows = min(kMStage, 1 << a.page_bits);  // tokens a copy has
-        const int page_of = min(a.page_bits, 7);                // lane l looks up the page of token l << page_of of a block
+        const int piece_bits = min(5, a.page_bits), piece_rows = 1 << piece_bits;
+        const int at = lane << piece_bits;                   // of the block
+        const int st = (at >> 5) & 3, off = at & 31;         // stage, token of the stage
+        const bool lead = at < kMTile && off == 0;
         MassCursor cur(a, start_tile, start_kb, units);
         int64_t entry = -1;
         auto fetch = [&]() {
-            const int t = cur.kb * kMTile + (lane << page_of);
+            const int t = cur.kb * kMTile + at;
             entry = -1;
-            if ((lane << page_of) < kMTile && t < cur.s.len) entry = __ldg(a.table + cur.s.trow * a.table_stride + (t >> a.page_bits));
+            if (at < kMTile && t < cur.s.len) entry = __ldg(a.table + cur.s.trow * a.table_stride + (t >> a.page_bits));
         };
         fetch();
-        int slot = 0, issued = 0;
+        int slot = st, issued = 0;
         uint32_t parity = 1;
 #pragma unroll 1
-        for (int i = 0; i < units && tries; ++i) {
-            const int64_t page_here = entry;
-            const int t0 = cur.kb * kMTile, len = cur.s.len;
+        for (int i = 0; i < units; ++i) {
+            const int64_t page = entry;
+            const int t = cur.kb * kMTile + at, len = cur.s.len;
             if (i + 1 < units) {  // the next block's pages, while this one's stages become free
                 cur.next(a);
                 fetch();
             }
-#pragma unroll 1
-            for (int st = 0; st < 4; ++st) {
-                if (issued >= S) mbar_wait(smem_addr(&sh.empty[slot]), parity, tries);
-                if (!tries) break;
-                // lane l has the piece from token l * piece_rows of the stage on
-                const int at = lane * piece_rows, t = t0 + st * kMStage + at;
-                const bool has = at < kMStage && t < len;
-                const int64_t page = __shfl_sync(0xFFFFFFFFu, (long long)page_here, ((st * kMStage + min(at, kMStage - 1)) >> page_of) & 31);
-                const bool good = has && page >= 0 && page < a.pool_limit;
-                if (has && !good) raise_err(a.err, KVQ_DEVERR_PAGE);
-                uint32_t mask = 0;
-                if (good) {
-                    const int n = min(piece_rows, len - t);
-                    mask = (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1) << at;
-                }
-                mask = __reduce_or_sync(0xFFFFFFFFu, mask);
-                const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, good)) * piece_rows * kTokenBytes<L>;
-                const uint32_t bar = smem_addr(&sh.full[slot]);
-                if (lane == 0) {
-                    sh.there[slot] = mask;
-                    mbar_arrive_expect(bar, bytes);
-                }
-                __syncwarp();
-                if (good) {
-                    const uint32_t to = smem_addr(sStage) + slot * kMStageBytes<L>;
-                    const uint8_t *from = a.pool + page * page_bytes;
-                    const int row = t & in_page;
-                    bulk_load(to + at * T::kCodeBytes, from + int64_t(row) * T::kCodeBytes, piece_rows * T::kCodeBytes, bar);
-                    bulk_load(to + kMStage * T::kCodeBytes + at * T::kScaleBytes, from + area + int64_t(row) * T::kScaleBytes,
-                              piece_rows * T::kScaleBytes, bar);
-                }
-                ++issued;
-                if (++slot == S) {
-                    slot = 0;
-                    parity ^= 1;
-                }
+            const bool has = at < kMTile && t < len, good = has && page >= 0 && page < a.pool_limit;
+            if (has && !good) raise_err(a.err, KVQ_DEVERR_PAGE);
+            uint32_t mask = 0, bytes = good ? piece_rows * kTokenBytes<L> : 0;
+            if (good) {
+                const int n = min(piece_rows, len - t);
+                mask = (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1) << off;
+            }
+            for (int o = 1; o < (32 >> piece_bits); o <<= 1) {  // over a stage's lanes
+                mask |= __shfl_xor_sync(0xFFFFFFFFu, mask, o);
+                bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, o);
+            }
+            const uint32_t bar = smem_addr(&sh.full[slot]);
+            if (lead && i * 4 >= S) mbar_wait(smem_addr(&sh.empty[slot]), parity, tries);
+            if (__any_sync(0xFFFFFFFFu, tries == 0)) {
+                tries = 0;
+                break;
+            }
+            if (lead) {
+                sh.there[slot] = mask;
+                mbar_arrive_expect(bar, bytes);
+            }
+            __syncwarp();
+            if (good) {
+                const uint32_t to = smem_addr(sStage) + slot * kMStageBytes<L>;
+                const uint8_t *from = a.pool + page * page_bytes;
+                const int row = t & in_page;
+                bulk_load(to + off * T::kCodeBytes, from + int64_t(row) * T::kCodeBytes, piece_rows * T::kCodeBytes, bar);
+                bulk_load(to + kMStage * T::kCodeBytes + off * T::kScaleBytes, from + area + int64_t(row) * T::kScaleBytes,
+                          piece_rows * T::kScaleBytes, bar);
+            }
+            issued += 4;
+            slot += 4;
+            if (slot >= S) {
+                slot -= S;
+                parity ^= 1;
             }
         }
         if (!tries) sh.abort = 1;

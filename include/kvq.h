@@ -357,7 +357,7 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  *   n_seq      at most 65535.
  *   workspace  kvq_mass_workspace bytes, 16-B aligned (NULL where that is 0).
  * Products, roundings and what counts as nothing are as for kvq_attend's
- * scores; the exponent is off by 2^-23 (|score| + |lse|) besides.  Sums are
+ * scores; the exponent's own roundings are relative to score - lse.  Sums are
  * fp32, in one order whatever the lengths (no atomics on data).
  * A token whose row holds a NaN or an infinity, and a query row that does or
  * whose lse is NaN, make the weights that they share in NaN, and no others.
