@@ -20,7 +20,12 @@ struct MassArgs {
     const int32_t *req;
     const int32_t *kv_len;
     const float *lse;
-    float scale;
+    // A weight is 2^(S c + n) with c = scale log2(e) and n = -log2(e) lse, whose roundings to fp32 would be up to 2^-24 (|S c|
+    // + |n|) of the exponent.  S c is about -n wherever a weight counts, so a row's weights are taken times 2^((n - fl(n)) - n
+    // c_off), c_off being the relative error of fl(c).  The tensor cores drop what is below two bits behind fp32's last in
+    // each of a score's 32 sums, which leaves S short by 1.375 (V41) or 0.875 (V41_FP4) times 2^-23 of it on average where the
+    // terms are of a kind (measured on rows ~ N(0, 1) with outliers); c_off makes up for that too.
+    float c, c_off;
     float *mass;
     int64_t mass_stride;
     const float *prev;

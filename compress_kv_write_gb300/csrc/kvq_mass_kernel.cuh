@@ -33,7 +33,7 @@ constexpr int kMTile = 128;  // cached tokens a block
 constexpr int kMStage = 32;  // tokens a stage: a block's share of a TMEM lane quarter
 constexpr int kMChunks = kD / 128;
 // Warps: 0-15 decode (four a quarter of the lanes, a chunk of 128 dims each), 16-23 weights (a lane quarter each; one four
-// for even, one for odd blocks), 24-27 load queries, 28 issues the products, 29 looks up pages and issues the copies.
+// for even, one for odd blocks), 24-27 load queries (the first tile's: the decode warps), 28 issues the products, 29 looks up pages and issues the copies.
 constexpr int kMDeq = 16, kMSoft = 8, kMQuery = 4;
 constexpr int kMSoft0 = kMDeq, kMQuery0 = kMSoft0 + kMSoft, kMMma = kMQuery0 + kMQuery, kMLoad = kMMma + 1;
 constexpr int kMThreads = (kMLoad + 1) * 32;
@@ -59,8 +59,8 @@ struct MassShared {
     uint64_t tready[4];             // a block's powers of two are there
     uint64_t qready, qfree, cready[4];
     uint64_t drain;
-    int64_t scan[2][kMThreads / 32];
-    int64_t u0, u1, b0, b1;
+    uint32_t scan[2][kMThreads / 32];
+    int b0, b1;                     // this CTA's blocks, counted over all tiles
     int start_tile, start_kb;
     uint32_t tmem;
     int abort;
@@ -70,7 +70,7 @@ struct MassShared {
     // that one of a warp's rows sees
     alignas(16) float sc[4][N], nl[4][N], wf[4][N];
     alignas(16) int vis[4][N];
-    int least[4][kMQuery];
+    int least[4][kMDeq];
 };
 
 template <Layout L, int N>
@@ -140,6 +140,96 @@ __device__ __forceinline__ uint32_t mass_q_word(int r, int g, int i) {
     return uint32_t((2 * b + (v >> 1)) * N * 128 + r * 128 + (((4 * (v & 1) + i) ^ (r & 7)) << 4) + q * 4);
 }
 
+// Warp w of W loads its rows of a tile's queries (w, w + W, ..) and their constants.
+template <Layout L, int N, int W>
+__device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N> &sh, uint32_t sq, const MassCursor &cur, int w,
+                                             int lane, uint32_t &tries) {
+    constexpr int kRows = N / W, kBatch = kRows < 4 ? kRows : 4;  // a warp's rows; those whose loads are in flight
+    static_assert(N % W == 0 && W % 4 == 0, "a warp's rows are w + 4 k, k of one parity a batch entry");
+    const int per = a.q_len * a.heads, slot = cur.nth & 3;
+    // lane l has the constants of the warp's l-th row
+    const int row_l = cur.rt * N + w + lane * W;
+    const bool real = lane < kRows && row_l < per;
+    const float lse = real ? __ldg(a.lse + int64_t(cur.seq) * per + row_l) : -INFINITY;
+    uint32_t up_l = 254;
+    auto row_of = [&](int row) {
+        const int j = row / a.heads, head = row - j * a.heads;
+        return a.q + (int64_t(cur.seq) * a.q_len + j) * a.q_tok + head * a.q_head;
+    };
+    if constexpr (kRows > kBatch) {
+        // all rows are sent for at once
+#pragma unroll 1
+        for (int k = lane >> 3; k < kRows; k += 4) {
+            const int row = cur.rt * N + w + k * W;
+            if (row < per) prefetch_l2(row_of(row) + (lane & 7) * 64);
+        }
+    }
+    // byte offsets of a lane's words within a row (see mass_q_word); of its second piece, 32 further, 4 N 128 more
+    uint32_t word[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) word[i] = sq + mass_q_word<N>(w & 7, lane, i) - (w & 7) * 128;
+#pragma unroll 1
+    for (int k0 = 0; k0 < kRows; k0 += kBatch) {
+        uint32_t v[kBatch][8];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int row = cur.rt * N + w + (k0 + b) * W;
+            const uint16_t *from = row_of(min(row, per - 1));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (row < per) u = ld_stream_u4(from + (lane + 32 * h) * 8);
+                v[b][4 * h] = u.x, v[b][4 * h + 1] = u.y, v[b][4 * h + 2] = u.z, v[b][4 * h + 3] = u.w;
+            }
+        }
+        // the last tile's queries are free when its products are done
+        if (k0 == 0 && cur.nth > 0) mbar_wait(smem_addr(&sh.qfree), (cur.nth - 1) & 1, tries);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + b;
+            // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
+            uint32_t big = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = max(big, max((v[b][e] << 16) & 0x7FFF0000u, v[b][e] & 0x7FFF0000u));
+            big = __reduce_max_sync(0xFFFFFFFFu, big);
+            const uint32_t up = min(268u - (big >> 23), 254u);
+            const float f = __uint_as_float(up << 23);
+            // the row's number modulo 8 is w's, and with four warps that plus four in every other row
+            const uint32_t flip = W == 4 && (b & 1) ? 64u : 0u, at = (w + k * W) * 128;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                uint32_t h;
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[b][e]) * f), "f"(bf16_lo(v[b][e]) * f));
+                sts_u32((word[e & 3] ^ flip) + at + (e >> 2) * (4 * N * 128), h);
+            }
+            if (lane == k) up_l = up;
+        }
+    }
+    // a row of no one's, and one that saw nothing (lse = -inf), has no weight
+    const bool none = lse == -INFINITY;
+    const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - row_l / a.heads));
+    if (lane < kRows) {
+        const int r = w + lane * W;
+        // n = -log2(e) lse in two parts, log2(e) in two as well
+        const float n = -lse * kLog2e;
+        const float rest = fmaf(-lse, kLog2e, -n) - lse * 1.9259629e-8f;
+        sh.sc[slot][r] = none ? 0.f : score_factor<L>(a.c, up_l);
+        sh.nl[slot][r] = none ? -INFINITY : n;
+        sh.wf[slot][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(rest - n * a.c_off);
+        sh.vis[slot][r] = vis;
+    }
+    const int least = __reduce_min_sync(0xFFFFFFFFu, real ? vis : 0x7FFFFFFF);
+    // the barriers count 16 arrivals, and the least number of tokens seen is looked for in 16 places, whoever loads
+    constexpr int kTimes = kMDeq / W;
+    if (lane < kTimes) sh.least[slot][w * kTimes + lane] = least;
+    fence_proxy_async();
+    __syncwarp();
+    if (lane < kTimes) {
+        mbar_arrive(smem_addr(&sh.qready));
+        mbar_arrive(smem_addr(&sh.cready[slot]));
+    }
+}
+
 template <Layout L, int N>
 __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constant__ MassArgs a) {
     using T = LayoutTraits<L>;
@@ -167,9 +257,9 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_addr(&sh.tready[i]), 4);
-            mbar_init(smem_addr(&sh.cready[i]), kMQuery);
+            mbar_init(smem_addr(&sh.cready[i]), kMDeq);
         }
-        mbar_init(smem_addr(&sh.qready), kMQuery);
+        mbar_init(smem_addr(&sh.qready), kMDeq);
         mbar_init(smem_addr(&sh.qfree), 1);
         mbar_init(smem_addr(&sh.drain), 1);
         sh.abort = 0;
@@ -181,78 +271,77 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
     // ---- this CTA's share of all tiles' blocks in order, each tile with kMTileCost units before its blocks
     const int tiles = int(a.n_seq * a.row_tiles);
     {
-        const int per = (tiles + kMThreads - 1) / kMThreads;
-        const int t0 = int(min(int64_t(tiles), int64_t(tid) * per)), t1 = int(min(int64_t(tiles), int64_t(t0) + per));
+        const int each = (tiles + kMThreads - 1) / kMThreads;
+        const int t0 = min(tiles, tid * each), t1 = min(tiles, t0 + each);
         auto blocks_of = [&](int t, bool tell) {
             const MassSeq s = mass_seq(a, int(uint32_t(t) / uint32_t(a.row_tiles)));
             if (tell && s.err) raise_err(a.err, s.err);
-            return (s.len + kMTile - 1) / kMTile;
+            return uint32_t(s.len + kMTile - 1) / kMTile;
         };
-        int64_t units = 0, blocks = 0;
+        uint32_t units = 0, blocks = 0;
 #pragma unroll 1
         for (int t = t0; t < t1; ++t) {
-            const int nb = blocks_of(t, blockIdx.x == 0);
+            const uint32_t nb = blocks_of(t, blockIdx.x == 0);
             blocks += nb;
             units += nb ? nb + kMTileCost : 0;
         }
-        int64_t iu = units, ib = blocks;
+        uint32_t iu = units, ib = blocks;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, (long long)iu, o), w = __shfl_up_sync(0xFFFFFFFFu, (long long)ib, o);
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, iu, o), w = __shfl_up_sync(0xFFFFFFFFu, ib, o);
             if (lane >= o) iu += v, ib += w;
         }
         if (lane == 31) sh.scan[0][warp] = iu, sh.scan[1][warp] = ib;
+        if (tid == 0) sh.b0 = sh.b1 = 0;
         __syncthreads();
-        int64_t bu = 0, bb = 0, total = 0, all = 0;
-#pragma unroll 1
-        for (int w = 0; w < kMThreads / 32; ++w) {
-            if (w < warp) bu += sh.scan[0][w], bb += sh.scan[1][w];
-            total += sh.scan[0][w], all += sh.scan[1][w];
-        }
+        // every warp sums the warps' totals: lane w has those of warp w
+        const uint32_t wu = lane < kMThreads / 32 ? sh.scan[0][lane] : 0, wb = lane < kMThreads / 32 ? sh.scan[1][lane] : 0;
+        const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, wu), all = __reduce_add_sync(0xFFFFFFFFu, wb);
+        const uint32_t at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wu : 0) + iu - units;
+        const uint32_t bat = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wb : 0) + ib - blocks;
         int64_t u0, u1;
         share(total, u0, u1);
-        if (tid == 0) {
-            sh.b0 = sh.b1 = 0;
-            if (u1 > u0 && u1 == total) sh.b1 = all;
-        }
-        __syncthreads();
-        const int64_t at = bu + iu - units, bat = bb + ib - blocks;
+        if (tid == 0 && u1 > u0 && u1 == total) sh.b1 = int(all);
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            const int64_t u = e ? u1 : u0;
-            if (u1 == u0 || !(u >= at && u < at + units)) continue;  // one thread goes on
-            int64_t vs = at, vb = bat;
+            const uint32_t u = uint32_t(e ? u1 : u0);
+            if (u1 == u0 || u < at || u - at >= units) continue;  // one thread goes on
+            uint32_t vs = at, vb = bat;
             int t = t0;
 #pragma unroll 1
             for (;; ++t) {
-                const int nb = blocks_of(t, false), w = nb ? nb + kMTileCost : 0;
-                if (u < vs + w) break;
+                const uint32_t nb = blocks_of(t, false), w = nb ? nb + kMTileCost : 0;
+                if (u - vs < w) break;
                 vs += w, vb += nb;
             }
-            const int kb = int(max(int64_t(0), u - vs - kMTileCost));
+            const uint32_t kb = u - vs > kMTileCost ? u - vs - kMTileCost : 0;
             if (e) {
-                sh.b1 = vb + kb;
+                sh.b1 = int(vb + kb);
             } else {
-                sh.b0 = vb + kb;
+                sh.b0 = int(vb + kb);
                 sh.start_tile = t;
-                sh.start_kb = kb;
+                sh.start_kb = int(kb);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int units = int(sh.b1 - sh.b0), start_tile = sh.start_tile, start_kb = sh.start_kb;
+    const int units = sh.b1 - sh.b0, start_tile = sh.start_tile, start_kb = sh.start_kb;
     if (units <= 0) {  // the same for every thread
         if (warp == kMMma) tmem_dealloc(sh.tmem, kTmemCols);
         pdl_trigger();
         return;
     }
-    const int per = a.q_len * a.heads;  // query rows of a sequence
     uint32_t tries = a.wait_tries;
 
     if (warp < kMDeq) {
         // ------------------------------------------------------ decode
+        // The first tile's queries: these warps have nothing else to do until the first codes come.
+        {
+            MassCursor cur(a, start_tile, start_kb, units);
+            mass_queries<L, N, kMDeq>(a, sh, smem_addr(sQ), cur, warp, lane, tries);
+        }
         const int quarter = warp & 3, chunk = warp >> 2, q = lane & 3, r8 = lane >> 2;
         const uint32_t tlane = kTmemK + ((32 * quarter) << 16);
         const uint32_t code_at = r8 * T::kCodeBytes + chunk * (T::kCodeBytes / kMChunks) + q * (T::kCodeBytes / kNBlk);
@@ -337,7 +426,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             if (known != cur.nth) {
                 known = cur.nth;
                 mbar_wait(smem_addr(&sh.cready[c]), (cur.nth >> 2) & 1, tries);
-                least = min(min(sh.least[c][0], sh.least[c][1]), min(sh.least[c][2], sh.least[c][3]));
+                least = __reduce_min_sync(0xFFFFFFFFu, sh.least[c][lane & (kMDeq - 1)]);
             }
             const int t = cur.kb * kMTile + tok;
             const bool mine = t < cur.s.len;
@@ -351,15 +440,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             mbar_wait(smem_addr(&sh.sdone[group]), (i >> 1) & 1, tries);
             tc_fence_after();
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-            for (int j0 = 0; j0 < N; j0 += 16) {
-                uint32_t x[16];
-                tmem_ld16(tfrom + j0, x);
-                if (j0 + 16 == N) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.sread[group]));
-                }
+            auto add = [&](const uint32_t (&x)[16], int j0) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 sc = *reinterpret_cast<const float4 *>(&sh.sc[c][j0 + j]);
@@ -383,6 +464,27 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                     sum[0] = ffma2(p0, make_float2(wf.x, wf.y), sum[0]);
                     sum[1] = ffma2(p1, make_float2(wf.z, wf.w), sum[1]);
                 }
+            };
+            auto done = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.sread[group]));
+            };
+            // 16 columns are summed while the next 16 come
+            uint32_t x0[16], x1[16];
+            tmem_ld16_begin(tfrom, x0);
+#pragma unroll 1
+            for (int j0 = 0; j0 < N; j0 += 32) {
+                tmem_ld16_end(x0);
+                if (j0 + 16 < N) tmem_ld16_begin(tfrom + j0 + 16, x1);
+                else done();
+                add(x0, j0);
+                if (j0 + 16 < N) {
+                    tmem_ld16_end(x1);
+                    if (j0 + 32 < N) tmem_ld16_begin(tfrom + j0 + 32, x0);
+                    else done();
+                    add(x1, j0 + 16);
+                }
             }
             if (mine && tries) {
                 const float2 two = fadd2(sum[0], sum[1]);
@@ -392,86 +494,15 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             }
         }
     } else if (warp < kMMma) {
-        // ------------------------------------------------------ queries
-        const int w = warp - kMQuery0;
-        const uint32_t sq = smem_addr(sQ);
-        // A weight is 2^(S c + n) with c = scale log2(e) and n = -log2(e) lse, whose roundings to fp32 would be up to 2^-24
-        // (|S c| + |n|) of the exponent.  S c is about -n wherever a weight counts, so a row's weights are taken times
-        // 2^((n - fl(n)) - n (c / fl(c) - 1)).
-        constexpr double kLog2e64 = 1.4426950408889634;
-        const double c64 = double(a.scale) * kLog2e64;
-        const float c = float(c64);
-        const double c_off = c != 0.f ? c64 / double(c) - 1.0 : 0.0;
-        constexpr int kBatch = N / kMQuery < 4 ? N / kMQuery : 4;  // rows whose loads are in flight
+        // ------------------------------------------------------ queries of the tiles after the first
         MassCursor cur(a, start_tile, start_kb, units);
 #pragma unroll 1
         for (;;) {
-            const int slot = cur.nth & 3;
-            // lane l has the constants of the warp's l-th row
-            const int row_l = cur.rt * N + w + lane * kMQuery;
-            const bool real = lane < N / kMQuery && row_l < per;
-            const float lse = real ? __ldg(a.lse + int64_t(cur.seq) * per + row_l) : -INFINITY;
-            uint32_t up_l = 254;
-#pragma unroll 1
-            for (int r0 = w; r0 < N; r0 += kBatch * kMQuery) {
-                uint32_t v[kBatch][8];
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int row = cur.rt * N + r0 + b * kMQuery, rc = min(row, per - 1);
-                    const int j = rc / a.heads, head = rc - j * a.heads;
-                    const uint16_t *from = a.q + (int64_t(cur.seq) * a.q_len + j) * a.q_tok + head * a.q_head;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < per) u = ld_stream_u4(from + (lane + 32 * h) * 8);
-                        v[b][4 * h] = u.x, v[b][4 * h + 1] = u.y, v[b][4 * h + 2] = u.z, v[b][4 * h + 3] = u.w;
-                    }
-                }
-                // the last tile's queries are free when its products are done
-                if (r0 == w && cur.nth > 0) mbar_wait(smem_addr(&sh.qfree), (cur.nth - 1) & 1, tries);
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int r = r0 + b * kMQuery;
-                    // fp16: the row times a power of two that brings its largest magnitude to [2^14, 2^15)
-                    uint32_t big = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) big = max(big, max((v[b][e] << 16) & 0x7FFF0000u, v[b][e] & 0x7FFF0000u));
-                    big = __reduce_max_sync(0xFFFFFFFFu, big);
-                    const uint32_t up = min(268u - (big >> 23), 254u);
-                    const float f = __uint_as_float(up << 23);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t h;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[b][e]) * f), "f"(bf16_lo(v[b][e]) * f));
-                        sts_u32(sq + mass_q_word<N>(r, lane + 32 * (e >> 2), e & 3), h);
-                    }
-                    if (lane == r / kMQuery) up_l = up;
-                }
-            }
-            // a row of no one's, and one that saw nothing (lse = -inf), has no weight
-            const bool none = lse == -INFINITY;
-            const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - row_l / a.heads));
-            if (lane < N / kMQuery) {
-                const int r = w + lane * kMQuery;
-                sh.sc[slot][r] = none ? 0.f : score_factor<L>(c, up_l);
-                const double n64 = -double(lse) * kLog2e64;
-                const float n = float(n64);
-                sh.nl[slot][r] = none ? -INFINITY : n;
-                sh.wf[slot][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(float((n64 - double(n)) - n64 * c_off));
-                sh.vis[slot][r] = vis;
-            }
-            const int least = __reduce_min_sync(0xFFFFFFFFu, real ? vis : 0x7FFFFFFF);
-            if (lane == 0) sh.least[slot][w] = least;
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_addr(&sh.qready));
-                mbar_arrive(smem_addr(&sh.cready[slot]));
-            }
             const int blocks = cur.nb - cur.kb;
             if (cur.left <= blocks) break;
             cur.left -= blocks;
             cur.next_tile(a);
+            mass_queries<L, N, kMQuery>(a, sh, smem_addr(sQ), cur, warp - kMQuery0, lane, tries);
         }
     } else if (warp == kMMma) {
         // ------------------------------------------------------ products
@@ -637,7 +668,7 @@ kvq_status launch_mass_n(MassArgs a, cudaStream_t s) {
     if (st != KVQ_OK) return st;
     if (grid > kMaxAttendCtas) grid = kMaxAttendCtas;
     const int64_t most = (a.max_len + kMTile - 1) / kMTile;  // blocks of the longest tile there can be
-    if (tiles > 0x7FFFFFFF || tiles * (most ? most : 1) / grid >= 0x7FFFFFFF / 8) return KVQ_ERR_UNSUPPORTED;
+    if (tiles > 0x7FFFFFFF / (most + kMTileCost)) return KVQ_ERR_UNSUPPORTED;  // units fit an int
     if (most <= 1 && tiles < grid) grid = tiles;
     st = launch_pdl_smem(mass_kernel<L, N>, dim3(unsigned(grid)), dim3(kMThreads), kMassSmem<L, N>, s, a);
     if (st != KVQ_OK || a.row_tiles == 1) return st;

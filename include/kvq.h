@@ -354,7 +354,9 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  *              unspecified.
  *   prev       rows like mass's, by the same index: mass itself with its
  *              stride, or apart from it, or NULL.
- *   n_seq      at most 65535.
+ *   n_seq      at most 65535; sequences times 128 query rows times 128 tokens
+ *              of the table's width (of mass_width where that is less), each
+ *              rounded up, below 2^31: more is KVQ_ERR_UNSUPPORTED.
  *   workspace  kvq_mass_workspace bytes, 16-B aligned (NULL where that is 0).
  * Products, roundings and what counts as nothing are as for kvq_attend's
  * scores; the exponent's own roundings are relative to score - lse.  Sums are
