@@ -32,8 +32,9 @@ namespace {
 constexpr int kMTile = 128;  // cached tokens a block
 constexpr int kMStage = 32;  // tokens a stage: a block's share of a TMEM lane quarter
 constexpr int kMChunks = kD / 128;
-// Warps: 0-15 decode (four a quarter of the lanes, a chunk of 128 dims each), 16-23 weights (a lane quarter each; one four
-// for even, one for odd blocks), 24-27 load queries (the first tile's: the decode warps), 28 issues the products, 29 looks up pages and issues the copies.
+// Warps: 0-15 decode (four a quarter of the lanes, a chunk of 128 dims each), 16-23 weights (a lane quarter and half of the
+// rows each; with all rows of every other block a score buffer was free later: 4 bits, 128 rows, 1.77 instead of XX us a
+// block), 24-27 load queries (the first tile's: the decode warps), 28 issues the products, 29 looks up pages and issues the copies.
 constexpr int kMDeq = 16, kMSoft = 8, kMQuery = 4;
 constexpr int kMSoft0 = kMDeq, kMQuery0 = kMSoft0 + kMSoft, kMMma = kMQuery0 + kMQuery, kMLoad = kMMma + 1;
 constexpr int kMThreads = (kMLoad + 1) * 32;
@@ -66,6 +67,7 @@ struct MassShared {
     int abort;
     uint32_t there[S];              // which of a stage's tokens are
     int texp[4][kMTile];            // a token's power of two, or kNoToken
+    float other[2][kMTile];         // a token's weights of the second half of the rows
     // of a tile's rows, four tiles in turn: factor, -log2(e) lse, what their roundings leave out, tokens seen; the fewest
     // that one of a warp's rows sees
     alignas(16) float sc[4][N], nl[4][N], wf[4][N];
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.sdone[i]), 1);
-            mbar_init(smem_addr(&sh.sread[i]), 4);
+            mbar_init(smem_addr(&sh.sread[i]), kMSoft);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_addr(&sh.tready[i]), 4);
@@ -415,13 +417,14 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         }
     } else if (warp < kMQuery0) {
         // ------------------------------------------------------ weights
-        const int quarter = warp & 3, group = (warp - kMSoft0) >> 2, tok = 32 * quarter + lane;
-        const uint32_t tfrom = (uint32_t(32 * quarter) << 16) + group * N;
+        // A warp has 32 tokens, a lane each, and half of the rows; the warp with the first half adds the other's sums.
+        constexpr int NC = N / 2, NL = NC < 16 ? NC : 16;  // a warp's columns; those of a load
+        const int quarter = warp & 3, half = (warp - kMSoft0) >> 2, tok = 32 * quarter + lane, c0 = half * NC;
+        const uint32_t tfrom = (uint32_t(32 * quarter) << 16) + c0;
         MassCursor cur(a, start_tile, start_kb, units);
         int known = -1, least = 0;  // the tile whose rows are known to be there; the fewest tokens that one of them sees
 #pragma unroll 1
         for (int i = 0; i < units; ++i, cur.next(a)) {
-            if ((i & 1) != group) continue;
             const int c = cur.nth & 3;
             if (known != cur.nth) {
                 known = cur.nth;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 least = __reduce_min_sync(0xFFFFFFFFu, sh.least[c][lane & (kMDeq - 1)]);
             }
             const int t = cur.kb * kMTile + tok;
-            const bool mine = t < cur.s.len;
+            const bool mine = half == 0 && t < cur.s.len;
             float before = 0.f;
             if (a.row_tiles == 1 && a.prev && mine) before = a.prev[cur.s.mrow * a.prev_stride + t];
             mbar_wait(smem_addr(&sh.tready[i & 3]), (i >> 2) & 1, tries);
@@ -437,15 +440,25 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             const bool there = te != kNoToken;
             const float up = L == Layout::V41 && there ? __uint_as_float(uint32_t(127 + te - kLift) << 23) : 1.f;
             const bool masked = (cur.kb + 1) * kMTile > least;
-            mbar_wait(smem_addr(&sh.sdone[group]), (i >> 1) & 1, tries);
+            mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
             tc_fence_after();
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            auto add = [&](const uint32_t (&x)[16], int j0) {
+#pragma unroll 1
+            for (int j0 = 0; j0 < NC; j0 += NL) {
+                uint32_t x[NL];
+                if constexpr (NL == 16) tmem_ld16(tfrom + (i & 1) * N + j0, x);
+                else tmem_ld8(tfrom + (i & 1) * N + j0, x);
+                if (j0 + NL == NC) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.sread[i & 1]));
+                }
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 sc = *reinterpret_cast<const float4 *>(&sh.sc[c][j0 + j]);
-                    const float4 nl = *reinterpret_cast<const float4 *>(&sh.nl[c][j0 + j]);
-                    const float4 wf = *reinterpret_cast<const float4 *>(&sh.wf[c][j0 + j]);
+                for (int j = 0; j < NL; j += 4) {
+                    const int r = c0 + j0 + j;
+                    const float4 sc = *reinterpret_cast<const float4 *>(&sh.sc[c][r]);
+                    const float4 nl = *reinterpret_cast<const float4 *>(&sh.nl[c][r]);
+                    const float4 wf = *reinterpret_cast<const float4 *>(&sh.wf[c][r]);
                     float2 u0 = make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
                     float2 u1 = make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
                     if constexpr (L == Layout::V41) {
@@ -457,38 +470,20 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                     float2 p0 = make_float2(ex2_approx(u0.x), ex2_approx(u0.y));
                     float2 p1 = make_float2(ex2_approx(u1.x), ex2_approx(u1.y));
                     if (masked) {
-                        const int4 vis = *reinterpret_cast<const int4 *>(&sh.vis[c][j0 + j]);
+                        const int4 vis = *reinterpret_cast<const int4 *>(&sh.vis[c][r]);
                         p0 = make_float2(t < vis.x ? p0.x : 0.f, t < vis.y ? p0.y : 0.f);
                         p1 = make_float2(t < vis.z ? p1.x : 0.f, t < vis.w ? p1.y : 0.f);
                     }
                     sum[0] = ffma2(p0, make_float2(wf.x, wf.y), sum[0]);
                     sum[1] = ffma2(p1, make_float2(wf.z, wf.w), sum[1]);
                 }
-            };
-            auto done = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.sread[group]));
-            };
-            // 16 columns are summed while the next 16 come
-            uint32_t x0[16], x1[16];
-            tmem_ld16_begin(tfrom, x0);
-#pragma unroll 1
-            for (int j0 = 0; j0 < N; j0 += 32) {
-                tmem_ld16_end(x0);
-                if (j0 + 16 < N) tmem_ld16_begin(tfrom + j0 + 16, x1);
-                else done();
-                add(x0, j0);
-                if (j0 + 16 < N) {
-                    tmem_ld16_end(x1);
-                    if (j0 + 32 < N) tmem_ld16_begin(tfrom + j0 + 32, x0);
-                    else done();
-                    add(x1, j0 + 16);
-                }
             }
+            const float2 two = fadd2(sum[0], sum[1]);
+            float all = two.x + two.y;
+            if (half == 1) sh.other[i & 1][tok] = all;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");  // the quarter's two warps
             if (mine && tries) {
-                const float2 two = fadd2(sum[0], sum[1]);
-                const float all = there ? two.x + two.y : 0.f;
+                all = there ? all + sh.other[i & 1][tok] : 0.f;
                 if (a.row_tiles == 1) a.mass[cur.s.mrow * a.mass_stride + t] = a.prev ? fmaf(a.decay, before, all) : all;
                 else a.part[int64_t(cur.tile) * a.part_stride + t] = all;
             }
