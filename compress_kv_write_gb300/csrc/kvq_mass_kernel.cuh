@@ -34,9 +34,10 @@ constexpr int kMStage = 32;  // tokens a stage: a block's share of a TMEM lane q
 constexpr int kMChunks = kD / 128;
 // Warps: 0-15 decode (four a quarter of the lanes, a chunk of 128 dims each), 16-23 weights (a lane quarter and half of the
 // rows each; with all rows of every other block a score buffer was free later: 4 bits, 128 rows, 1.77 instead of XX us a
-// block), 24-27 load queries (the first tile's: the decode warps), 28 issues the products, 29 looks up pages and issues the copies.
-constexpr int kMDeq = 16, kMSoft = 8, kMQuery = 4;
-constexpr int kMSoft0 = kMDeq, kMQuery0 = kMSoft0 + kMSoft, kMMma = kMQuery0 + kMQuery, kMLoad = kMMma + 1;
+// block), 24 issues the products, 25 looks up pages and issues the copies.  The decode warps load a tile's queries too: at its
+// start they have nothing else to do (four warps for that alone took 13 us for 128 rows, and 8 registers of every thread).
+constexpr int kMDeq = 16, kMSoft = 8;
+constexpr int kMSoft0 = kMDeq, kMMma = kMSoft0 + kMSoft, kMLoad = kMMma + 1;
 constexpr int kMThreads = (kMLoad + 1) * 32;
 // What a tile costs beside its blocks (its queries), in blocks, when blocks are shared out.
 constexpr int kMTileCost = 2;
@@ -142,30 +143,18 @@ __device__ __forceinline__ uint32_t mass_q_word(int r, int g, int i) {
     return uint32_t((2 * b + (v >> 1)) * N * 128 + r * 128 + (((4 * (v & 1) + i) ^ (r & 7)) << 4) + q * 4);
 }
 
-// Warp w of W loads its rows of a tile's queries (w, w + W, ..) and their constants.
-template <Layout L, int N, int W>
+// Decode warp w loads its rows of a tile's queries (w, w + 16, ..) and their constants.
+template <Layout L, int N>
 __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N> &sh, uint32_t sq, const MassCursor &cur, int w,
                                              int lane, uint32_t &tries) {
-    constexpr int kRows = N / W, kBatch = kRows < 4 ? kRows : 4;  // a warp's rows; those whose loads are in flight
-    static_assert(N % W == 0 && W % 4 == 0, "a warp's rows are w + 4 k, k of one parity a batch entry");
+    constexpr int kRows = N / kMDeq, kBatch = kRows < 4 ? kRows : 4;  // a warp's rows; those whose loads are in flight
+    static_assert(N % kMDeq == 0 && kMDeq % 8 == 0, "a warp's rows are equal modulo 8");
     const int per = a.q_len * a.heads, slot = cur.nth & 3;
     // lane l has the constants of the warp's l-th row
-    const int row_l = cur.rt * N + w + lane * W;
+    const int row_l = cur.rt * N + w + lane * kMDeq;
     const bool real = lane < kRows && row_l < per;
     const float lse = real ? __ldg(a.lse + int64_t(cur.seq) * per + row_l) : -INFINITY;
     uint32_t up_l = 254;
-    auto row_of = [&](int row) {
-        const int j = row / a.heads, head = row - j * a.heads;
-        return a.q + (int64_t(cur.seq) * a.q_len + j) * a.q_tok + head * a.q_head;
-    };
-    if constexpr (kRows > kBatch) {
-        // all rows are sent for at once
-#pragma unroll 1
-        for (int k = lane >> 3; k < kRows; k += 4) {
-            const int row = cur.rt * N + w + k * W;
-            if (row < per) prefetch_l2(row_of(row) + (lane & 7) * 64);
-        }
-    }
     // byte offsets of a lane's words within a row (see mass_q_word); of its second piece, 32 further, 4 N 128 more
     uint32_t word[4];
 #pragma unroll
@@ -175,8 +164,9 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
         uint32_t v[kBatch][8];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int row = cur.rt * N + w + (k0 + b) * W;
-            const uint16_t *from = row_of(min(row, per - 1));
+            const int row = cur.rt * N + w + (k0 + b) * kMDeq, rc = min(row, per - 1);
+            const int j = rc / a.heads, head = rc - j * a.heads;
+            const uint16_t *from = a.q + (int64_t(cur.seq) * a.q_len + j) * a.q_tok + head * a.q_head;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 u = make_uint4(0u, 0u, 0u, 0u);
@@ -196,13 +186,11 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
             big = __reduce_max_sync(0xFFFFFFFFu, big);
             const uint32_t up = min(268u - (big >> 23), 254u);
             const float f = __uint_as_float(up << 23);
-            // the row's number modulo 8 is w's, and with four warps that plus four in every other row
-            const uint32_t flip = W == 4 && (b & 1) ? 64u : 0u, at = (w + k * W) * 128;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 uint32_t h;
                 asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(bf16_hi(v[b][e]) * f), "f"(bf16_lo(v[b][e]) * f));
-                sts_u32((word[e & 3] ^ flip) + at + (e >> 2) * (4 * N * 128), h);
+                sts_u32(word[e & 3] + (w + k * kMDeq) * 128 + (e >> 2) * (4 * N * 128), h);
             }
             if (lane == k) up_l = up;
         }
@@ -211,7 +199,7 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
     const bool none = lse == -INFINITY;
     const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - row_l / a.heads));
     if (lane < kRows) {
-        const int r = w + lane * W;
+        const int r = w + lane * kMDeq;
         // n = -log2(e) lse in two parts, log2(e) in two as well
         const float n = -lse * kLog2e;
         const float rest = fmaf(-lse, kLog2e, -n) - lse * 1.9259629e-8f;
@@ -221,12 +209,10 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
         sh.vis[slot][r] = vis;
     }
     const int least = __reduce_min_sync(0xFFFFFFFFu, real ? vis : 0x7FFFFFFF);
-    // the barriers count 16 arrivals, and the least number of tokens seen is looked for in 16 places, whoever loads
-    constexpr int kTimes = kMDeq / W;
-    if (lane < kTimes) sh.least[slot][w * kTimes + lane] = least;
+    if (lane == 0) sh.least[slot][w] = least;
     fence_proxy_async();
     __syncwarp();
-    if (lane < kTimes) {
+    if (lane == 0) {
         mbar_arrive(smem_addr(&sh.qready));
         mbar_arrive(smem_addr(&sh.cready[slot]));
     }
@@ -339,19 +325,20 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
 
     if (warp < kMDeq) {
         // ------------------------------------------------------ decode
-        // The first tile's queries: these warps have nothing else to do until the first codes come.
-        {
-            MassCursor cur(a, start_tile, start_kb, units);
-            mass_queries<L, N, kMDeq>(a, sh, smem_addr(sQ), cur, warp, lane, tries);
-        }
         const int quarter = warp & 3, chunk = warp >> 2, q = lane & 3, r8 = lane >> 2;
         const uint32_t tlane = kTmemK + ((32 * quarter) << 16);
         const uint32_t code_at = r8 * T::kCodeBytes + chunk * (T::kCodeBytes / kMChunks) + q * (T::kCodeBytes / kNBlk);
         const uint32_t scale_at = kMStage * T::kCodeBytes + r8 * T::kScaleBytes;
         int slot = quarter, kslot = chunk;
         uint32_t parity = 0, kparity = 1;  // of the stage; of the chunk that had this one's TMEM slot before
+        MassCursor cur(a, start_tile, start_kb, units);
+        int known = -1;  // the tile whose queries are loaded
 #pragma unroll 1
-        for (int i = 0; i < units; ++i) {
+        for (int i = 0; i < units; ++i, cur.next(a)) {
+            if (known != cur.nth) {
+                known = cur.nth;
+                mass_queries<L, N>(a, sh, smem_addr(sQ), cur, warp, lane, tries);
+            }
             mbar_wait(smem_addr(&sh.full[slot]), parity, tries);
             const uint32_t stage = smem_addr(sStage) + slot * kMStageBytes<L>;
             const uint32_t there = sh.there[slot];
@@ -415,7 +402,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 kparity ^= 1;
             }
         }
-    } else if (warp < kMQuery0) {
+    } else if (warp < kMMma) {
         // ------------------------------------------------------ weights
         // A warp has 32 tokens, a lane each, and half of the rows; the warp with the first half adds the other's sums.
         constexpr int NC = N / 2, NL = NC < 16 ? NC : 16;  // a warp's columns; those of a load
@@ -487,17 +474,6 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 if (a.row_tiles == 1) a.mass[cur.s.mrow * a.mass_stride + t] = a.prev ? fmaf(a.decay, before, all) : all;
                 else a.part[int64_t(cur.tile) * a.part_stride + t] = all;
             }
-        }
-    } else if (warp < kMMma) {
-        // ------------------------------------------------------ queries of the tiles after the first
-        MassCursor cur(a, start_tile, start_kb, units);
-#pragma unroll 1
-        for (;;) {
-            const int blocks = cur.nb - cur.kb;
-            if (cur.left <= blocks) break;
-            cur.left -= blocks;
-            cur.next_tile(a);
-            mass_queries<L, N, kMQuery>(a, sh, smem_addr(sQ), cur, warp - kMQuery0, lane, tries);
         }
     } else if (warp == kMMma) {
         // ------------------------------------------------------ products
