@@ -12,20 +12,23 @@ namespace {
 // 32-bit key of the same order, and the m-th largest key is found digit by
 // digit from the top (11, 11 and 10 bits): a histogram of the digit over the
 // keys that share the digits found so far, and the bin in which the count from
-// the top passes m.  Then every token's fate is known from its key, but for
-// those equal to the m-th: of these the first ones stay.
+// the top reaches m.  A bin all of whose keys stay ends the search.  Then every
+// token's fate is known from its key, but for those equal to the m-th: of these
+// the first ones stay.
 //
-// A sequence is a cluster's: its CTAs have equal pieces of it in order, hold
-// their keys in shared memory (one pass over global memory) and add up their
-// histograms there.  Places in the output come from counts: of the CTAs
-// before, of the warps before, and of the lanes before by ballot.
+// A sequence is a CTA's, or with many tokens a cluster's: its CTAs have equal
+// pieces of it in order, hold their keys in shared memory (one pass over global
+// memory), add their filled bins to the first CTA's and read back what it
+// found.  Places in the output come from counts: of the CTAs before, of the
+// warps before, and of the lanes before by ballot.
 //
-// Bound by latency: three rounds of clear, count, add up and search, each with
-// barriers of the cluster.
+// Bound by latency: rounds of clear, count and search, each with barriers.
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kSelKeys = 40960;  // keys a CTA can hold; the others are read again
+// Tokens up to which a CTA works alone, and that it has at least in a cluster.
+constexpr int64_t kSelAlone = 16384;
 
 struct SelectArgs {
     const float *mass;
@@ -58,7 +61,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A 32-bit word at a shared-window address of this CTA, of another CTA of the cluster.
+// Adds to a 32-bit word at a shared-window address of this CTA, in another CTA of the cluster.
+__device__ __forceinline__ void adds_of(uint32_t addr, uint32_t rank, uint32_t v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+// Such a word's value.
 __device__ __forceinline__ uint32_t lds_of(uint32_t addr, uint32_t rank) {
     uint32_t at, r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
@@ -67,10 +76,10 @@ __device__ __forceinline__ uint32_t lds_of(uint32_t addr, uint32_t rank) {
 }
 
 struct SelShared {
-    uint32_t hist[2][kBins];  // by turns, so that a CTA may be counting while another still reads
+    uint32_t hist[2][kBins];  // by turns, so that a CTA may be counting while the first one still reads
     uint32_t warp[kSelWarps];
     uint32_t gt, eq;          // this CTA's tokens above the m-th key, and equal to it
-    uint32_t bin, above;
+    uint32_t bin, above, in;  // the bin that was found, the keys above it and in it
 };
 
 // Sum over the warps before this one, of a value that every lane of a warp has; `total`: over all.
@@ -97,10 +106,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = int(blockIdx.x) / cluster;
     const int rank = cluster > 1 ? int(cluster_rank()) : 0;
-    auto sync_all = [&]() {
-        if (cluster > 1) cluster_sync();
-        else __syncthreads();
-    };
     pdl_wait();
     int64_t n = __ldg(a.kv_len + seq);
     int64_t row = a.rows ? __ldg(a.rows + seq) : seq;
@@ -143,7 +148,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
             if (i + b * kSelThreads < in_smem) held[i + b * kSelThreads] = mass_key(v[b]);
     }
     pdl_trigger();
-    __syncthreads();
+    if (cluster > 1) cluster_sync();  // the first CTA's bins are clear
+    else __syncthreads();
     auto key = [&](int i) { return i < in_smem ? held[i] : mass_key(__ldg(from + i)); };
 
     // the m-th largest key, from the top: `prefix` its digits so far, `left` how many of the keys with these digits stay
@@ -152,11 +158,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     for (int round = 0; round < 3; ++round) {
         const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, digit = round == 2 ? 1024 : 2048;
         uint32_t *const hist = sh.hist[round & 1];
-        if (round == 2) {  // its first use is over: every CTA has read it before the last barrier
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-        }
         const uint32_t same = round == 0 ? 0u : 0xFFFFFFFFu << (round == 1 ? 21 : 10);
+#pragma unroll 2
         for (int i0 = warp * 32; i0 < mine; i0 += kSelThreads) {
             const int i = i0 + lane;
             uint32_t bin = 0xFFFFFFFFu;
@@ -173,36 +176,48 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
             if (lane == lead) atomicAdd(&hist[first], __popc(like));
             else if (bin != 0xFFFFFFFFu && bin != first) atomicAdd(&hist[bin], 1u);
         }
-        sync_all();
-        // thread t has bins digit - 1 - 2 t and the one below (from the top), summed over the cluster
-        uint32_t c0 = 0, c1 = 0;
-        const int top = digit - 1 - 2 * tid;
-        if (top > 0) {
-            if (cluster > 1) {
-                const uint32_t at = smem_addr(hist + top - 1);
-                for (int r = 0; r < cluster; ++r) c1 += lds_of(at, r), c0 += lds_of(at + 4, r);
-            } else {
-                c0 = hist[top], c1 = hist[top - 1];
-            }
-        }
-        uint32_t incl = c0 + c1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        uint32_t total;
-        const uint32_t before = before_warp(sh, __shfl_sync(0xFFFFFFFFu, incl, 31), total) + incl - c0 - c1;
-        if (before < left && before + c0 >= left) {
-            sh.bin = top;
-            sh.above = before;
-        } else if (before + c0 < left && before + c0 + c1 >= left) {
-            sh.bin = top - 1;
-            sh.above = before + c0;
-        }
         __syncthreads();
-        prefix |= sh.bin << shift;
-        left -= sh.above;
+        // thread t has bins digit - 1 - 2 t and the one below (from the top)
+        const int top = digit - 1 - 2 * tid;
+        uint32_t c0 = top > 0 ? hist[top] : 0, c1 = top > 0 ? hist[top - 1] : 0;
+        if (cluster > 1) {
+            if (rank > 0) {
+                if (c0) adds_of(smem_addr(hist + top), 0, c0);
+                if (c1) adds_of(smem_addr(hist + top - 1), 0, c1);
+            }
+            cluster_sync();
+            if (rank == 0 && top > 0) c0 = hist[top], c1 = hist[top - 1];
+        }
+        if (rank == 0) {
+            uint32_t incl = c0 + c1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            uint32_t total;
+            const uint32_t before = before_warp(sh, __shfl_sync(0xFFFFFFFFu, incl, 31), total) + incl - c0 - c1;
+            if (before < left && before + c0 >= left) sh.bin = top, sh.above = before, sh.in = c0;
+            else if (before + c0 < left && before + c0 + c1 >= left) sh.bin = top - 1, sh.above = before + c0, sh.in = c1;
+        }
+        if (round == 0) {  // for the third round; the first CTA's is read until here
+            if (cluster > 1) cluster_sync();
+            else __syncthreads();
+            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+        } else {
+            if (cluster > 1) cluster_sync();
+            else __syncthreads();
+        }
+        const uint32_t bin = cluster > 1 ? lds_of(smem_addr(&sh.bin), 0) : sh.bin;
+        const uint32_t above = cluster > 1 ? lds_of(smem_addr(&sh.above), 0) : sh.above;
+        const uint32_t in = cluster > 1 ? lds_of(smem_addr(&sh.in), 0) : sh.in;
+        prefix |= bin << shift;
+        left -= above;
+        if (in == left) {  // all of them stay: they are above a key of their lowest, less one (no key is that low)
+            prefix -= 1;
+            left = 0;
+            break;
+        }
     }
 
     // counts: every warp has a piece of the CTA's in order
@@ -246,10 +261,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 
 // ---------------------------------------------------------------- the move
 // Row kept[i][k] of sequence i becomes row k of its new pages: codes and scale
-// bytes as they are.  A warp has 8 tokens: eight lanes look up where these lie
-// and shall lie, then all rows' loads are under way before the first store.
-// Bound by memory: rows of 256 or 512 bytes, read and written once.
-constexpr int kMoveThreads = 256, kMoveTok = 8;
+// bytes as they are.  A warp has 8 (V41) or 16 (V41_FP4) tokens: as many lanes
+// look up where these lie and shall lie, then all rows' loads (8 a lane) are
+// under way before the first store.  Bound by memory: rows of 256 or 512 bytes,
+// read and written once.
+constexpr int kMoveThreads = 256;
+template <Layout L>
+constexpr int kMoveTok = L == Layout::V41 ? 8 : 16;
 
 struct MoveArgs {
     uint8_t *pool;
@@ -262,7 +280,7 @@ struct MoveArgs {
     const int32_t *kept;
     int64_t kept_stride;
     int keep;
-    int64_t groups;  // of 8 entries, a sequence
+    int64_t groups;  // warps a sequence
     int64_t total;   // groups
     const float *mass;
     int64_t mass_stride;
@@ -276,15 +294,16 @@ struct MoveArgs {
 template <Layout L>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs a) {
     using T = LayoutTraits<L>;
+    constexpr int kTok = kMoveTok<L>;
     constexpr int kLanes = T::kCodeBytes / 16;           // lanes a code row
     constexpr int kAtOnce = 32 / kLanes;                 // rows a load has
-    constexpr int kLoads = kMoveTok / kAtOnce;
+    constexpr int kLoads = kTok / kAtOnce;
     constexpr int kScaleLanes = T::kScaleBytes / 16;     // lanes a scale row
     const int lane = threadIdx.x & 31;
     const int64_t group = (int64_t(blockIdx.x) * kMoveThreads + threadIdx.x) >> 5;
     if (group >= a.total) return;
     const int64_t seq = group / a.groups;
-    const int k = int(group % a.groups) * kMoveTok + lane;
+    const int k = int(group % a.groups) * kTok + lane;
     pdl_wait();
     const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits;
     const int in_page = (1 << a.page_bits) - 1;
@@ -292,7 +311,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
     if (a.req) row = __ldg(a.req + seq);
     if (a.rows) mrow = __ldg(a.rows + seq);
     int t = -1;
-    if (lane < kMoveTok && k < a.keep) t = __ldg(a.kept + seq * a.kept_stride + k);
+    if (lane < kTok && k < a.keep) t = __ldg(a.kept + seq * a.kept_stride + k);
     int bits = 0;
     if (t != -1 && (row < 0 || row >= a.table_rows || (a.mass && (mrow < 0 || mrow >= a.n_rows)))) bits = KVQ_DEVERR_STATE;
     else if (t != -1 && (t < 0 || t >= a.max_len)) bits = KVQ_DEVERR_SLOT;
@@ -325,9 +344,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
         if ((live >> j) & 1) v[i] = ld_stream_u4(a.pool + src + (lane % kLanes) * 16);
     }
     const int js = lane / kScaleLanes;
-    const int64_t ssrc = __shfl_sync(0xFFFFFFFFu, (long long)s0, js & (kMoveTok - 1));
-    const int64_t sdst = __shfl_sync(0xFFFFFFFFu, (long long)s1, js & (kMoveTok - 1));
-    const bool scales = js < kMoveTok && ((live >> js) & 1);
+    const int64_t ssrc = __shfl_sync(0xFFFFFFFFu, (long long)s0, js & (kTok - 1));
+    const int64_t sdst = __shfl_sync(0xFFFFFFFFu, (long long)s1, js & (kTok - 1));
+    const bool scales = js < kTok && ((live >> js) & 1);
     if (scales) sc = ld_stream_u4(a.pool + ssrc + (lane % kScaleLanes) * 16);
     pdl_trigger();
 #pragma unroll
@@ -379,9 +398,8 @@ extern "C" kvq_status kvq_evict_select(const float *mass, int64_t mass_rows, int
     a.last = int(last);
     a.count = count;
     a.err = err;
-    // CTAs a sequence: as many as leave each four tokens a thread
     int cluster = 1;
-    while (cluster < kMaxCluster && mass_width > int64_t(cluster) * 4 * kSelThreads) cluster *= 2;
+    while (cluster < kMaxCluster && mass_width > cluster * kSelAlone) cluster *= 2;
     const int64_t per = (mass_width + cluster - 1) / cluster;
     a.held = int(per < kSelKeys ? per : kSelKeys);
     int64_t cap = 0;
@@ -449,8 +467,6 @@ extern "C" kvq_status kvq_evict_move(kvq_layout layout, int page_bits, uint8_t *
     a.kept = kept;
     a.kept_stride = kept_stride;
     a.keep = int(keep);
-    a.groups = (keep + kMoveTok - 1) / kMoveTok;
-    a.total = a.groups * n_seq;
     a.mass = mass;
     a.mass_stride = mass_row_stride;
     a.rows = rows;
@@ -458,10 +474,13 @@ extern "C" kvq_status kvq_evict_move(kvq_layout layout, int page_bits, uint8_t *
     a.mass_out = mass_out;
     a.mass_out_stride = mass_out_stride;
     a.err = err;
-    const int64_t per = kMoveThreads / 32, blocks = (a.total + per - 1) / per;
-    if (blocks > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_layout(layout, [&](auto Lc) {
+        constexpr int kTok = kMoveTok<decltype(Lc)::value>;
+        a.groups = (keep + kTok - 1) / kTok;
+        a.total = a.groups * n_seq;
+        const int64_t per = kMoveThreads / 32, blocks = (a.total + per - 1) / per;
+        if (blocks > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
         return launch_pdl(evict_move_kernel<decltype(Lc)::value>, dim3(unsigned(blocks)), dim3(kMoveThreads), s, a);
     });
 }
