@@ -17,18 +17,22 @@ namespace {
 // the first ones stay.
 //
 // A sequence is a CTA's, or with many tokens a cluster's: its CTAs have equal
-// pieces of it in order, hold their keys in shared memory (one pass over global
-// memory), add their filled bins to the first CTA's and read back what it
-// found.  Places in the output come from counts: of the CTAs before, of the
-// warps before, and of the lanes before by ballot.
+// pieces of it in order, and their warps equal pieces of those.  A thread holds
+// up to 16 keys in registers (one pass over global memory); what a cluster of
+// eight cannot hold that way is in shared memory or read again.  CTAs add their
+// filled bins to the first one's and read back what it found.  Places in the
+// output come from counts: of the CTAs before, of the warps before, and of the
+// lanes before by ballot.
 //
-// Bound by latency: rounds of clear, count and search, each with barriers.
+// Bound by latency and by the instructions a key takes in one or a few SMs:
+// some five a round.  (Keys in shared memory and ballots to add up equal bins,
+// which the hardware's counting increments do by themselves, took 60 a round.)
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kSelKeys = 40960;  // keys a CTA can hold; the others are read again
-// Tokens up to which a CTA works alone, and that it has at least in a cluster.
-constexpr int64_t kSelAlone = 16384;
+constexpr int kSelRegs = 16;                              // keys a thread holds
+constexpr int kSelPiece = kSelThreads * kSelRegs;         // tokens that a CTA holds so
+constexpr int kSelKeys = 40960;                           // and in shared memory
 
 struct SelectArgs {
     const float *mass;
@@ -42,7 +46,7 @@ struct SelectArgs {
     int keep, first, last;
     int32_t *count;
     int32_t *err;
-    int held;  // keys that a CTA holds
+    int held;  // keys that a CTA holds in shared memory
 };
 
 // Larger weight, larger key; zeros are equal, a NaN is above everything.
@@ -77,28 +81,23 @@ __device__ __forceinline__ uint32_t lds_of(uint32_t addr, uint32_t rank) {
 
 struct SelShared {
     uint32_t hist[2][kBins];  // by turns, so that a CTA may be counting while the first one still reads
-    uint32_t warp[kSelWarps];
+    uint32_t warp[2][kSelWarps];
     uint32_t gt, eq;          // this CTA's tokens above the m-th key, and equal to it
     uint32_t bin, above, in;  // the bin that was found, the keys above it and in it
 };
 
-// Sum over the warps before this one, of a value that every lane of a warp has; `total`: over all.
-__device__ __forceinline__ uint32_t before_warp(SelShared &sh, uint32_t v, uint32_t &total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) sh.warp[warp] = v;
-    __syncthreads();
-    const uint32_t of = sh.warp[lane];
-    uint32_t incl = of;
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {  // inclusive
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += u;
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
     }
-    total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-    return __shfl_sync(0xFFFFFFFFu, incl - of, warp);
+    return v;
 }
 
+// kRegs keys a thread in registers; 0: keys in shared memory, or read again.
+template <int kRegs>
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a, int cluster) {
     extern __shared__ uint8_t smem[];
     auto &sh = *reinterpret_cast<SelShared *>(smem);
@@ -106,6 +105,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int seq = int(blockIdx.x) / cluster;
     const int rank = cluster > 1 ? int(cluster_rank()) : 0;
+    auto sync_all = [&]() {
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
+    };
+    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
     pdl_wait();
     int64_t n = __ldg(a.kv_len + seq);
     int64_t row = a.rows ? __ldg(a.rows + seq) : seq;
@@ -118,39 +122,56 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         if (tid == 0 && rank == 0) raise_err(a.err, bits);
     }
     int32_t *const out = a.kept + seq * a.kept_stride;
-    const int count = int(min(n, int64_t(a.keep)));
-    // what does not depend on the weights: the first and the last, or all, and the entries of no token
     const bool all = n <= a.keep;
+    const int m = a.keep - a.first - a.last;
+
+    // this CTA's piece of the tokens between, and this warp's: a multiple of 32 tokens from w0 on
+    const int between = all || m == 0 ? 0 : int(n) - a.first - a.last;
+    const int per = (between + cluster - 1) / cluster;
+    const int t0 = min(between, rank * per), mine = min(between, t0 + per) - t0;
+    const float *const from = a.mass + row * a.stride + a.first + t0;
+    const int steps = (mine + kSelThreads - 1) / kSelThreads, w0 = warp * steps * 32;
+    const int in_smem = kRegs ? 0 : min(mine, a.held);
+    uint32_t keys[kRegs ? kRegs : 1];
+    if constexpr (kRegs > 0) {
+        float v[kRegs];
+#pragma unroll
+        for (int j = 0; j < kRegs; ++j) {
+            const int i = w0 + j * 32 + lane;
+            v[j] = j < steps && i < mine ? __ldg(from + i) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kRegs; ++j) keys[j] = j < steps && w0 + j * 32 + lane < mine ? mass_key(v[j]) : 0u;
+    } else {
+        for (int i = tid; i < in_smem; i += kSelThreads) held[i] = mass_key(__ldg(from + i));
+    }
+    pdl_trigger();
+
+    // what does not depend on the weights: the first and the last, or all, and the entries of no token
+    const int count = int(min(n, int64_t(a.keep)));
     for (int k = rank * kSelThreads + tid; k < a.keep; k += cluster * kSelThreads) {
         if (all) out[k] = k < count ? k : -1;
         else if (k < a.first) out[k] = k;
         else if (k >= a.keep - a.last) out[k] = int(n) - (a.keep - k);
     }
     if (rank == 0 && tid == 0) a.count[seq] = count;
-    const int m = a.keep - a.first - a.last;
-    if (all || m == 0) return;  // the same for the whole cluster
+    if (between == 0) return;  // the same for the whole cluster
+    sync_all();  // bins are clear, keys are there
 
-    // this CTA's piece [t0, t1) of the tokens between
-    const int between = int(n) - a.first - a.last;
-    const int per = (between + cluster - 1) / cluster;
-    const int t0 = min(between, rank * per), t1 = min(between, t0 + per), mine = t1 - t0;
-    const float *const from = a.mass + row * a.stride + a.first + t0;
-    const int in_smem = min(mine, a.held);
-    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-    constexpr int kBatch = 4;  // loads under way
-    for (int i = tid; i < in_smem; i += kBatch * kSelThreads) {
-        float v[kBatch];
+    // The warp's tokens in order, 32 at a time: f(token, key), key 0 (lower than any weight's) for none.
+    auto for_each = [&](auto &&f) {
+        if constexpr (kRegs > 0) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (i + b * kSelThreads < in_smem) v[b] = __ldg(from + i + b * kSelThreads);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (i + b * kSelThreads < in_smem) held[i + b * kSelThreads] = mass_key(v[b]);
-    }
-    pdl_trigger();
-    if (cluster > 1) cluster_sync();  // the first CTA's bins are clear
-    else __syncthreads();
-    auto key = [&](int i) { return i < in_smem ? held[i] : mass_key(__ldg(from + i)); };
+            for (int j = 0; j < kRegs; ++j)
+                if (j < steps) f(w0 + j * 32 + lane, keys[j]);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < steps; ++j) {
+                const int i = w0 + j * 32 + lane;
+                f(i, i >= mine ? 0u : i < in_smem ? held[i] : mass_key(__ldg(from + i)));
+            }
+        }
+    };
 
     // the m-th largest key, from the top: `prefix` its digits so far, `left` how many of the keys with these digits stay
     uint32_t prefix = 0, left = uint32_t(m);
@@ -159,23 +180,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, digit = round == 2 ? 1024 : 2048;
         uint32_t *const hist = sh.hist[round & 1];
         const uint32_t same = round == 0 ? 0u : 0xFFFFFFFFu << (round == 1 ? 21 : 10);
-#pragma unroll 2
-        for (int i0 = warp * 32; i0 < mine; i0 += kSelThreads) {
-            const int i = i0 + lane;
-            uint32_t bin = 0xFFFFFFFFu;
-            if (i < mine) {
-                const uint32_t k = key(i);
-                if (((k ^ prefix) & same) == 0) bin = (k >> shift) & (digit - 1);
-            }
-            // many weights are the same (zero): the lanes with the first one's bin count as one
-            const uint32_t some = __ballot_sync(0xFFFFFFFFu, bin != 0xFFFFFFFFu);
-            if (some == 0) continue;
-            const int lead = __ffs(some) - 1;
-            const uint32_t first = __shfl_sync(0xFFFFFFFFu, bin, lead);
-            const uint32_t like = __ballot_sync(0xFFFFFFFFu, bin == first);
-            if (lane == lead) atomicAdd(&hist[first], __popc(like));
-            else if (bin != 0xFFFFFFFFu && bin != first) atomicAdd(&hist[bin], 1u);
-        }
+        for_each([&](int, uint32_t k) {
+            if (k && ((k ^ prefix) & same) == 0) atomicAdd(&hist[(k >> shift) & (digit - 1)], 1u);
+        });
         __syncthreads();
         // thread t has bins digit - 1 - 2 t and the one below (from the top)
         const int top = digit - 1 - 2 * tid;
@@ -189,25 +196,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
             if (rank == 0 && top > 0) c0 = hist[top], c1 = hist[top - 1];
         }
         if (rank == 0) {
-            uint32_t incl = c0 + c1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += u;
+            const uint32_t of_warp = __reduce_add_sync(0xFFFFFFFFu, c0 + c1);
+            if (lane == 0) sh.warp[0][warp] = of_warp;
+            __syncthreads();
+            const uint32_t upto = warp_scan(sh.warp[0][lane]);
+            const uint32_t here = __shfl_sync(0xFFFFFFFFu, upto, warp), before_warp = here - of_warp;
+            if (before_warp < left && here >= left) {  // one warp has the bin
+                const uint32_t before = before_warp + warp_scan(c0 + c1) - c0 - c1;
+                if (before < left && before + c0 >= left) sh.bin = top, sh.above = before, sh.in = c0;
+                else if (before + c0 < left && before + c0 + c1 >= left) sh.bin = top - 1, sh.above = before + c0, sh.in = c1;
             }
-            uint32_t total;
-            const uint32_t before = before_warp(sh, __shfl_sync(0xFFFFFFFFu, incl, 31), total) + incl - c0 - c1;
-            if (before < left && before + c0 >= left) sh.bin = top, sh.above = before, sh.in = c0;
-            else if (before + c0 < left && before + c0 + c1 >= left) sh.bin = top - 1, sh.above = before + c0, sh.in = c1;
         }
-        if (round == 0) {  // for the third round; the first CTA's is read until here
-            if (cluster > 1) cluster_sync();
-            else __syncthreads();
+        sync_all();
+        if (round == 0)  // for the third round; the first CTA's was read until here
             for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-        } else {
-            if (cluster > 1) cluster_sync();
-            else __syncthreads();
-        }
         const uint32_t bin = cluster > 1 ? lds_of(smem_addr(&sh.bin), 0) : sh.bin;
         const uint32_t above = cluster > 1 ? lds_of(smem_addr(&sh.above), 0) : sh.above;
         const uint32_t in = cluster > 1 ? lds_of(smem_addr(&sh.in), 0) : sh.in;
@@ -220,22 +222,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         }
     }
 
-    // counts: every warp has a piece of the CTA's in order
-    const int wper = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int w0 = min(mine, warp * wper), w1 = min(mine, w0 + wper);
+    // counts of what is above and equal, of the warps and of the CTAs before
     uint32_t gt = 0, eq = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const uint32_t k = i0 + lane < w1 ? key(i0 + lane) : 0u;
-        gt += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < w1 && k > prefix));
-        eq += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < w1 && k == prefix));
-    }
-    uint32_t gt_all, eq_all;
-    uint32_t gt_before = before_warp(sh, gt, gt_all);
-    uint32_t eq_before = before_warp(sh, eq, eq_all);
+    for_each([&](int, uint32_t k) {
+        gt += k > prefix;
+        eq += k == prefix;
+    });
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    __syncthreads();
+    if (lane == 0) sh.warp[0][warp] = gt, sh.warp[1][warp] = eq;
+    __syncthreads();
+    const uint32_t gt_upto = warp_scan(sh.warp[0][lane]), eq_upto = warp_scan(sh.warp[1][lane]);
+    uint32_t gt_before = __shfl_sync(0xFFFFFFFFu, gt_upto, warp) - gt, eq_before = __shfl_sync(0xFFFFFFFFu, eq_upto, warp) - eq;
     if (cluster > 1) {
-        if (tid == 0) {
-            sh.gt = gt_all;
-            sh.eq = eq_all;
+        if (tid == 31) {
+            sh.gt = gt_upto;
+            sh.eq = eq_upto;
         }
         cluster_sync();
         for (int r = 0; r < rank; ++r) {
@@ -244,19 +247,42 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
         }
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA's memory may still be read
     }
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < w1 ? key(i) : 0u;
-        const uint32_t g = __ballot_sync(0xFFFFFFFFu, i < w1 && k > prefix);
-        const uint32_t e = __ballot_sync(0xFFFFFFFFu, i < w1 && k == prefix);
+    for_each([&](int i, uint32_t k) {
+        const uint32_t g = __ballot_sync(0xFFFFFFFFu, k > prefix), e = __ballot_sync(0xFFFFFFFFu, k == prefix);
         const uint32_t low = (1u << lane) - 1;
         const uint32_t gb = gt_before + __popc(g & low), eb = eq_before + __popc(e & low);
-        const bool stays = ((g >> lane) & 1) || (((e >> lane) & 1) && eb < left);
-        if (stays) out[a.first + gb + min(eb, left)] = a.first + t0 + i;
+        if (k > prefix || (k == prefix && eb < left)) out[a.first + gb + min(eb, left)] = a.first + t0 + i;
         gt_before += __popc(g);
         eq_before += __popc(e);
-    }
+    });
     if (cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int kRegs>
+kvq_status launch_select(SelectArgs a, int64_t n_seq, int cluster, cudaStream_t s) {
+    const int64_t per = (a.width + cluster - 1) / cluster;
+    a.held = kRegs ? 0 : int(per < kSelKeys ? per : kSelKeys);
+    int64_t cap = 0;
+    kvq_status st = resident_grid<evict_select_kernel<kRegs>, kSelThreads>(sizeof(SelShared) + (kRegs ? 0 : kSelKeys * 4), &cap);
+    if (st != KVQ_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(n_seq * cluster));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = sizeof(SelShared) + size_t(a.held) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel<kRegs>, a, cluster) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return KVQ_ERR_LAUNCH;
+    }
+    return KVQ_OK;
 }
 
 // ---------------------------------------------------------------- the move
@@ -398,31 +424,12 @@ extern "C" kvq_status kvq_evict_select(const float *mass, int64_t mass_rows, int
     a.last = int(last);
     a.count = count;
     a.err = err;
+    // as many CTAs a sequence as hold its keys in registers
     int cluster = 1;
-    while (cluster < kMaxCluster && mass_width > cluster * kSelAlone) cluster *= 2;
-    const int64_t per = (mass_width + cluster - 1) / cluster;
-    a.held = int(per < kSelKeys ? per : kSelKeys);
-    int64_t cap = 0;
-    kvq_status st = resident_grid<evict_select_kernel, kSelThreads>(sizeof(SelShared) + kSelKeys * 4, &cap);
-    if (st != KVQ_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(n_seq * cluster));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = sizeof(SelShared) + size_t(a.held) * 4;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cluster) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return KVQ_ERR_LAUNCH;
-    }
-    return KVQ_OK;
+    while (cluster < kMaxCluster && mass_width > int64_t(cluster) * kSelPiece) cluster *= 2;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (mass_width <= int64_t(cluster) * kSelPiece) return launch_select<kSelRegs>(a, n_seq, cluster, s);
+    return launch_select<0>(a, n_seq, cluster, s);
 }
 
 extern "C" kvq_status kvq_evict_move(kvq_layout layout, int page_bits, uint8_t *pool, int64_t pool_pages,
