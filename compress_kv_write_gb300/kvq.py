@@ -199,6 +199,76 @@ def _on(dev, stream, call):
         return call(s)
 
 
+def _current_device():
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return get() if get is not None else torch.cuda.current_device()
+
+
+def _run(name, dev, stream, *args):
+    """The C call `name` with `dev` current, on the stream given or that device's current one (the last argument)."""
+    f = getattr(lib(), name)
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == _current_device():
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, s)
+    if st != OK:
+        raise KVQError(st, name)
+
+
+def _at(t, name, dtype, dev=None):
+    """The device index of a CUDA tensor of this type (on device `dev`)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    d = t.get_device()
+    if d < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if dev is not None and d != dev:
+        raise ValueError(f"every tensor must be on cuda:{dev}, got {name} on {t.device}")
+    return d
+
+
+def _vec(t, name, dtype, dev, n):
+    """Address of a contiguous 1-D tensor of n elements; None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _at(t, name, dtype, dev)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D tensor of {n}")
+    return t.data_ptr()
+
+
+def _mat(t, name, dtype, dev):
+    """(address, rows, width, row stride) of a 2-D tensor with unit inner stride; the stride of a single row is its width."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:  # _at, which says why, costs a call
+        _at(t, name, dtype, dev)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D with unit inner stride")
+    rows, width = shape
+    stride = width
+    if not t.is_contiguous():
+        strides = t.stride()
+        if width > 1 and strides[1] != 1:
+            raise ValueError(f"{name} must be 2-D with unit inner stride")
+        if rows > 1:
+            stride = strides[0]
+    return t.data_ptr(), rows, width, stride
+
+
+def _err(err, dev):
+    if err is None:
+        return None
+    _at(err, "err", torch.int32, dev)
+    if err.numel() < 1:
+        raise ValueError("err must hold one int32")
+    return err.data_ptr()
+
+
 # ------------------------------------------------------------------ entry points
 
 def kvq_translate_loc(full_loc, full_to_swa, out, n=None, err=None, stream=None):
@@ -388,9 +458,10 @@ def attend_wait_limit(tries):
 
 def _attend_rows(q, out, lse, workspace, err):
     """Checks what both attention calls share; returns (tokens, heads, strides of q and out, device, out dtype)."""
-    _cuda(q, "q", (torch.bfloat16,))
-    _cuda(out, "out", (torch.bfloat16, torch.float32))
-    _cuda(workspace, "workspace", (torch.uint8,))
+    dev = _at(q, "q", torch.bfloat16)
+    bf16 = isinstance(out, torch.Tensor) and out.dtype is torch.bfloat16
+    _at(out, "out", torch.bfloat16 if bf16 else torch.float32, dev)
+    _at(workspace, "workspace", torch.uint8, dev)
     shape, qs, outs = q.shape, q.stride(), out.stride()
     if len(shape) != 3 or shape[2] != HEAD_DIM or qs[2] != 1:
         raise ValueError("q must be [tokens, heads, 512] with unit inner stride")
@@ -404,38 +475,30 @@ def _attend_rows(q, out, lse, workspace, err):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if lse is not None:
-        _cuda(lse, "lse", (torch.float32,))
-        if lse.shape != shape[:2] or not lse.is_contiguous():
+        _at(lse, "lse", torch.float32, dev)
+        if lse.shape != (n, h) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous [tokens, heads]")
-    _err_word(err)
-    return n, h, qs, outs, _same_device(q, out, lse, workspace, err), BF16 if out.dtype == torch.bfloat16 else F32
+    _err(err, dev)
+    return n, h, qs, outs, dev, BF16 if bf16 else F32
 
 
-def _paged(layout, page_bits, q, n, q_len, pool, pool_pages, page_table, kv_len, req):
-    """Checks what the calls over pages share; returns the table's (rows, width, row stride) and the sequences."""
-    _cuda(pool, "pool", (torch.uint8,))
-    _cuda(page_table, "page_table", (torch.int32,))
-    _cuda(kv_len, "kv_len", (torch.int32,))
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [rows, width] with unit inner stride")
-    (rows, width), ts = page_table.shape, page_table.stride()
-    if rows and width > 1 and ts[1] != 1:
-        raise ValueError("page_table must be [rows, width] with unit inner stride")
-    _contig1d(kv_len, "kv_len")
-    n_seq = kv_len.numel()
+def _paged(layout, page_bits, dev, n, q_len, pool, pool_pages, page_table, kv_len, req):
+    """Checks what the calls over pages share; returns the addresses of pool, table, req and kv_len, the table's rows, width
+    and row stride, and the sequences."""
+    _at(pool, "pool", torch.uint8, dev)
+    table, rows, width, stride = _mat(page_table, "page_table", torch.int32, dev)
+    _at(kv_len, "kv_len", torch.int32, dev)
+    if len(kv_len.shape) != 1 or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be a contiguous 1-D tensor")
+    n_seq = kv_len.shape[0]
     if q_len < 1 or n != n_seq * q_len:
         raise ValueError("q must hold q_len rows per entry of kv_len")
-    if req is not None:
-        _cuda(req, "req", (torch.int32,))
-        _contig1d(req, "req")
-        if req.numel() != n_seq:
-            raise ValueError("req must hold one table row per sequence")
-    elif rows < n_seq:
+    req = _vec(req, "req", torch.int32, dev, n_seq)
+    if req is None and rows < n_seq:
         raise ValueError("page_table must hold one row per sequence")
     if not pool.is_contiguous() or pool.numel() < pool_pages * page_bytes(layout, page_bits):
         raise ValueError("pool must be contiguous and hold pool_pages pages")
-    _same_device(q, pool, page_table, kv_len, req)
-    return rows, width, ts[0] if rows > 1 else width, n_seq
+    return pool.data_ptr(), table, req, kv_len.data_ptr(), rows, width, stride, n_seq
 
 
 def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, workspace, *, scale, q_len=1,
@@ -445,39 +508,28 @@ def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, 
     int32, row req[i] (req None: row i) for sequence i; kv_len [n_seq] int32 cached tokens; query token j of a
     sequence sees the first kv_len - (q_len - 1 - j).  workspace: attend_workspace(q_len * heads) bytes."""
     n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
-    rows, width, ts, n_seq = _paged(layout, page_bits, q, n, q_len, pool, pool_pages, page_table, kv_len, req)
-    st = _on(dev, stream, lambda s: lib().kvq_attend(
-        layout, page_bits, _ptr(q), qs[0], qs[1], n_seq, q_len, heads, _ptr(pool), int(pool_pages),
-        _ptr(page_table), rows, width, ts, _ptr(req), _ptr(kv_len),
-        float(scale), _ptr(out), out_dtype, outs[0], outs[1], _ptr(lse), _ptr(workspace),
-        workspace.numel(), _ptr(err), s))
-    _check(st, "kvq_attend")
+    pool, table, req, kv_len, rows, width, ts, n_seq = _paged(layout, page_bits, dev, n, q_len, pool, pool_pages, page_table,
+                                                              kv_len, req)
+    _run("kvq_attend", dev, stream, layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, heads, pool, int(pool_pages),
+         table, rows, width, ts, req, kv_len, float(scale), out.data_ptr(), out_dtype, outs[0], outs[1], _ptr(lse),
+         workspace.data_ptr(), workspace.numel(), _ptr(err))
     return out
 
 
 def kvq_tree_mask(parent, mask, *, kv_len=None, pos=None, err=None, stream=None):
     """mask [n_seq, q_len, ceil(q_len / 64)] int64 <- which drafted tokens each one sees (itself and its ancestors), from
     parent [n_seq, q_len] int32 (-1: the last token before the tree); pos [n_seq, q_len] int32 <- kv_len - q_len + depth."""
-    _cuda(parent, "parent", (torch.int32,))
-    _cuda(mask, "mask", (torch.int64,))
-    _matrix(parent, "parent")
-    n_seq, q_len = parent.shape
+    dev = _at(parent, "parent", torch.int32)
+    parent_ptr, n_seq, q_len, stride = _mat(parent, "parent", torch.int32, dev)
+    _at(mask, "mask", torch.int64, dev)
     if mask.shape != (n_seq, q_len, (q_len + 63) // 64) or not mask.is_contiguous():
         raise ValueError("mask must be contiguous [n_seq, q_len, ceil(q_len / 64)]")
-    if kv_len is not None:
-        _cuda(kv_len, "kv_len", (torch.int32,))
-        _contig1d(kv_len, "kv_len")
-        if kv_len.numel() != n_seq:
-            raise ValueError("kv_len must hold one length per sequence")
     if pos is not None:
-        _cuda(pos, "pos", (torch.int32,))
-        if pos.shape != parent.shape or not pos.is_contiguous():
+        _at(pos, "pos", torch.int32, dev)
+        if pos.shape != (n_seq, q_len) or not pos.is_contiguous():
             raise ValueError("pos must be contiguous [n_seq, q_len]")
-    _err_word(err)
-    dev = _same_device(parent, mask, kv_len, pos, err)
-    st = _on(dev, stream, lambda s: lib().kvq_tree_mask(parent.data_ptr(), n_seq, q_len, _stride0(parent), _ptr(kv_len),
-                                                        mask.data_ptr(), _ptr(pos), _ptr(err), s))
-    _check(st, "kvq_tree_mask")
+    _run("kvq_tree_mask", dev, stream, parent_ptr, n_seq, q_len, stride, _vec(kv_len, "kv_len", torch.int32, dev, n_seq),
+         mask.data_ptr(), _ptr(pos), _err(err, dev))
     return mask
 
 
@@ -486,20 +538,18 @@ def kvq_attend_tree(layout, page_bits, q, pool, pool_pages, page_table, kv_len, 
     """kvq_attend of a tree of drafted tokens, the last q_len of a sequence's cached tokens: query token j sees all tokens
     before them and those of them whose bits are set in mask[i, j] ([n_seq, q_len, ceil(q_len / 64)] int64)."""
     n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
-    _cuda(mask, "mask", (torch.int64,))
-    if mask.dim() != 3 or mask.shape[2] != (mask.shape[1] + 63) // 64 or not mask.is_contiguous():
+    _at(mask, "mask", torch.int64, dev)
+    shape = mask.shape
+    if len(shape) != 3 or shape[2] != (shape[1] + 63) // 64 or not mask.is_contiguous():
         raise ValueError("mask must be contiguous [n_seq, q_len, ceil(q_len / 64)]")
-    q_len = mask.shape[1]
-    rows, width, ts, n_seq = _paged(layout, page_bits, q, n, q_len, pool, pool_pages, page_table, kv_len, req)
-    if mask.shape[0] != n_seq:
+    q_len = shape[1]
+    pool, table, req, kv_len, rows, width, ts, n_seq = _paged(layout, page_bits, dev, n, q_len, pool, pool_pages, page_table,
+                                                              kv_len, req)
+    if shape[0] != n_seq:
         raise ValueError("mask must hold one tree per sequence")
-    _same_device(q, mask)
-    st = _on(dev, stream, lambda s: lib().kvq_attend_tree(
-        layout, page_bits, _ptr(q), qs[0], qs[1], n_seq, q_len, heads, _ptr(pool), int(pool_pages),
-        _ptr(page_table), rows, width, ts, _ptr(req), _ptr(kv_len), _ptr(mask),
-        float(scale), _ptr(out), out_dtype, outs[0], outs[1], _ptr(lse), _ptr(workspace),
-        workspace.numel(), _ptr(err), s))
-    _check(st, "kvq_attend_tree")
+    _run("kvq_attend_tree", dev, stream, layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, heads, pool,
+         int(pool_pages), table, rows, width, ts, req, kv_len, mask.data_ptr(), float(scale), out.data_ptr(), out_dtype, outs[0],
+         outs[1], _ptr(lse), workspace.data_ptr(), workspace.numel(), _ptr(err))
     return out
 
 
@@ -562,66 +612,35 @@ def kvq_norm_quant(x, weight, codes, scales, *, eps=1e-6, residual=None, residua
 
 def kvq_rope_table(freq, table, *, first=0, amplitude=1.0, stream=None):
     """table [rows, rot] fp32 <- amplitude * cosines, then sines, of (first + row) * freq (freq [rot / 2] fp64)."""
-    _cuda(freq, "freq", (torch.float64,))
-    _cuda(table, "table", (torch.float32,))
-    _contig1d(freq, "freq")
-    if table.dim() != 2 or table.shape[1] != 2 * freq.numel() or not table.is_contiguous():
-        raise ValueError("table must be contiguous [rows, 2 * freq.numel()]")
-    dev = _same_device(table, freq)
-    st = _on(dev, stream, lambda s: lib().kvq_rope_table(freq.data_ptr(), table.shape[1], int(first), table.shape[0],
-                                                         float(amplitude), table.data_ptr(), s))
-    _check(st, "kvq_rope_table")
+    dev = _at(freq, "freq", torch.float64)
+    to, rows, rot, stride = _mat(table, "table", torch.float32, dev)
+    if stride != rot:
+        raise ValueError("table must be contiguous [rows, rot]")
+    _run("kvq_rope_table", dev, stream, _vec(freq, "freq", torch.float64, dev, rot // 2), rot, int(first), rows,
+         float(amplitude), to)
     return table
 
 
 def kvq_rope(x, pos, cos_sin, out, *, start, half=False, inverse=False, err=None, stream=None):
     """out <- x [tokens, heads, dim] (fp32 / bf16) with dims start .. start + rot - 1 rotated by row pos[token] of cos_sin
     [rows, rot], interleaved pairs or halves; `inverse` turns them back.  out may be x itself."""
-    _cuda(x, "x", (torch.float32, torch.bfloat16))
-    _cuda(out, "out", (x.dtype,))
-    _cuda(pos, "pos", (torch.int32,))
-    _cuda(cos_sin, "cos_sin", (torch.float32,))
-    shape, xs, os_ = x.shape, x.stride(), out.stride()
+    bf16 = isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    dev = _at(x, "x", dtype)
+    _at(out, "out", dtype, dev)
+    shape, xs, outs = x.shape, x.stride(), out.stride()
     if len(shape) != 3 or (shape[2] > 1 and xs[2] != 1):
         raise ValueError("x must be [tokens, heads, dim] with unit inner stride")
-    if out.shape != shape or (shape[2] > 1 and os_[2] != 1):
+    if out.shape != shape or (shape[2] > 1 and outs[2] != 1):
         raise ValueError("out must have x's shape and unit inner stride")
-    _contig1d(pos, "pos")
-    if pos.numel() != shape[0]:
-        raise ValueError("pos must hold one position per token")
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    table, rows, rot, stride = _mat(cos_sin, "cos_sin", torch.float32, dev)
+    if stride != rot:
         raise ValueError("cos_sin must be contiguous [rows, rot]")
-    rows, rot = cos_sin.shape
-    _err_word(err)
-    dev = _same_device(x, out, pos, cos_sin, err)
     flags = (ROPE_HALF if half else 0) | (ROPE_INVERSE if inverse else 0)
-    st = _on(dev, stream, lambda s: lib().kvq_rope(
-        x.data_ptr(), BF16 if x.dtype == torch.bfloat16 else F32, shape[0], shape[1], shape[2], xs[0], xs[1], int(start),
-        rot, flags, cos_sin.data_ptr(), rows, pos.data_ptr(), out.data_ptr(), os_[0], os_[1], _ptr(err), s))
-    _check(st, "kvq_rope")
+    _run("kvq_rope", dev, stream, x.data_ptr(), BF16 if bf16 else F32, shape[0], shape[1], shape[2], xs[0], xs[1], int(start),
+         rot, flags, table, rows, _vec(pos, "pos", torch.int32, dev, shape[0]), out.data_ptr(), outs[0], outs[1],
+         _err(err, dev))
     return out
-
-
-def _stride0(t):
-    """Row stride of a 2-D tensor; that of a single row is its width."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _matrix(t, name):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.shape[0] and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit inner stride")
-
-
-def _index_rows(t, name, n_seq, table, table_name):
-    """Checks an index of table rows (None: row i for sequence i)."""
-    if t is None:
-        if table.shape[0] < n_seq:
-            raise ValueError(f"{table_name} must hold one row per sequence")
-        return
-    _cuda(t, name, (torch.int32,))
-    _contig1d(t, name)
-    if t.numel() != n_seq:
-        raise ValueError(f"{name} must hold one row per sequence")
 
 
 def mass_workspace(n_seq, rows, max_len):
@@ -635,58 +654,48 @@ def kvq_attend_mass(layout, page_bits, q, lse, pool, pool_pages, page_table, kv_
     """mass [rows, width] fp32 (row rows[i], or i) <- decay * prev + the weight of each of a sequence's cached tokens in
     kvq_attend, summed over heads and query tokens; q, pool, page_table, kv_len, scale, q_len, req and lse as in that call.
     prev may be mass itself, or None: no weights from before.  workspace: mass_workspace(n_seq, q_len * heads, max_len)."""
-    _cuda(q, "q", (torch.bfloat16,))
-    _cuda(lse, "lse", (torch.float32,))
-    _cuda(mass, "mass", (torch.float32,))
+    dev = _at(q, "q", torch.bfloat16)
     shape, qs = q.shape, q.stride()
     if len(shape) != 3 or shape[2] != HEAD_DIM or qs[2] != 1:
         raise ValueError("q must be [tokens, heads, 512] with unit inner stride")
-    if lse.shape != shape[:2] or not lse.is_contiguous():
+    n, heads, _ = shape
+    _at(lse, "lse", torch.float32, dev)
+    if lse.shape != (n, heads) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous [tokens, heads]")
-    t_rows, width, ts, n_seq = _paged(layout, page_bits, q, shape[0], q_len, pool, pool_pages, page_table, kv_len, req)
-    _matrix(mass, "mass")
-    _index_rows(rows, "rows", n_seq, mass, "mass")
+    pool, table, req, kv_len, t_rows, width, ts, n_seq = _paged(layout, page_bits, dev, n, q_len, pool, pool_pages, page_table,
+                                                                kv_len, req)
+    to, m_rows, m_width, m_stride = _mat(mass, "mass", torch.float32, dev)
+    rows = _vec(rows, "rows", torch.int32, dev, n_seq)
+    if rows is None and m_rows < n_seq:
+        raise ValueError("mass must hold one row per sequence")
+    before = p_stride = None
     if prev is not None:
-        _cuda(prev, "prev", (torch.float32,))
-        _matrix(prev, "prev")
-        if prev.shape != mass.shape:
+        before, p_rows, p_width, p_stride = _mat(prev, "prev", torch.float32, dev)
+        if p_rows != m_rows or p_width != m_width:
             raise ValueError("prev must have mass's shape")
+    ws = size = 0
     if workspace is not None:
-        _cuda(workspace, "workspace", (torch.uint8,))
+        _at(workspace, "workspace", torch.uint8, dev)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    _err_word(err)
-    dev = _same_device(q, lse, mass, rows, prev, workspace, err)
-    st = _on(dev, stream, lambda s: lib().kvq_attend_mass(
-        layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, shape[1], lse.data_ptr(), pool.data_ptr(), int(pool_pages),
-        page_table.data_ptr(), t_rows, width, ts, _ptr(req), kv_len.data_ptr(), float(scale), mass.data_ptr(), mass.shape[0],
-        mass.shape[1], _stride0(mass), _ptr(rows), _ptr(prev), _stride0(prev) if prev is not None else 0, float(decay),
-        _ptr(workspace), workspace.numel() if workspace is not None else 0, _ptr(err), s))
-    _check(st, "kvq_attend_mass")
+        ws, size = workspace.data_ptr(), workspace.numel()
+    _run("kvq_attend_mass", dev, stream, layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, heads, lse.data_ptr(), pool,
+         int(pool_pages), table, t_rows, width, ts, req, kv_len, float(scale), to, m_rows, m_width, m_stride, rows, before,
+         p_stride or 0, float(decay), ws, size, _err(err, dev))
     return mass
 
 
 def kvq_evict_select(mass, kv_len, kept, count, *, first=0, last=0, rows=None, err=None, stream=None):
     """kept [n_seq, keep] int32 <- the tokens that stay of each sequence, ascending, then -1: the first and last few and,
     of the others, those of most weight in mass [rows, width] fp32 (row rows[i], or i); count [n_seq] int32 of them."""
-    _cuda(mass, "mass", (torch.float32,))
-    _cuda(kv_len, "kv_len", (torch.int32,))
-    _cuda(kept, "kept", (torch.int32,))
-    _cuda(count, "count", (torch.int32,))
-    _matrix(mass, "mass")
-    _matrix(kept, "kept")
-    _contig1d(kv_len, "kv_len")
-    _contig1d(count, "count")
-    n_seq = kv_len.numel()
-    if kept.shape[0] != n_seq or count.numel() != n_seq:
-        raise ValueError("kept and count must hold one row per sequence")
-    _index_rows(rows, "rows", n_seq, mass, "mass")
-    _err_word(err)
-    dev = _same_device(mass, kv_len, kept, count, rows, err)
-    st = _on(dev, stream, lambda s: lib().kvq_evict_select(
-        mass.data_ptr(), mass.shape[0], mass.shape[1], _stride0(mass), _ptr(rows), kv_len.data_ptr(), n_seq,
-        kept.shape[1], int(first), int(last), kept.data_ptr(), _stride0(kept), count.data_ptr(), _ptr(err), s))
-    _check(st, "kvq_evict_select")
+    dev = _at(mass, "mass", torch.float32)
+    of, m_rows, m_width, m_stride = _mat(mass, "mass", torch.float32, dev)
+    to, n_seq, keep, k_stride = _mat(kept, "kept", torch.int32, dev)
+    rows = _vec(rows, "rows", torch.int32, dev, n_seq)
+    if rows is None and m_rows < n_seq:
+        raise ValueError("mass must hold one row per sequence")
+    _run("kvq_evict_select", dev, stream, of, m_rows, m_width, m_stride, rows, _vec(kv_len, "kv_len", torch.int32, dev, n_seq),
+         n_seq, keep, int(first), int(last), to, k_stride, _vec(count, "count", torch.int32, dev, n_seq), _err(err, dev))
     return kept, count
 
 
@@ -694,36 +703,30 @@ def kvq_evict_move(layout, page_bits, pool, pool_pages, page_table, new_table, k
                    mass_out=None, err=None, stream=None):
     """Moves token kept[i, k] of sequence i (page_table row req[i], or i) to token k of the pages new_table[i], and its
     weight to mass_out[i, k] where mass and mass_out are given."""
-    _cuda(pool, "pool", (torch.uint8,))
-    _cuda(page_table, "page_table", (torch.int32,))
-    _cuda(new_table, "new_table", (torch.int32,))
-    _cuda(kept, "kept", (torch.int32,))
-    for t, nm in ((page_table, "page_table"), (new_table, "new_table"), (kept, "kept")):
-        _matrix(t, nm)
-    n_seq, keep = kept.shape
-    if new_table.shape[0] != n_seq:
+    dev = _at(pool, "pool", torch.uint8)
+    table, t_rows, t_width, t_stride = _mat(page_table, "page_table", torch.int32, dev)
+    new, n_rows, n_width, n_stride = _mat(new_table, "new_table", torch.int32, dev)
+    of, n_seq, keep, k_stride = _mat(kept, "kept", torch.int32, dev)
+    if n_rows != n_seq:
         raise ValueError("new_table must hold one row per sequence")
-    _index_rows(req, "req", n_seq, page_table, "page_table")
+    req = _vec(req, "req", torch.int32, dev, n_seq)
+    if req is None and t_rows < n_seq:
+        raise ValueError("page_table must hold one row per sequence")
     if (mass is None) != (mass_out is None):
         raise ValueError("mass and mass_out come together")
+    weights, m_rows, m_width, m_stride, w_out, o_stride = None, 0, 0, 0, None, 0
+    rows = _vec(rows, "rows", torch.int32, dev, n_seq)
     if mass is not None:
-        _cuda(mass, "mass", (torch.float32,))
-        _cuda(mass_out, "mass_out", (torch.float32,))
-        _matrix(mass, "mass")
-        _matrix(mass_out, "mass_out")
-        if mass_out.shape[0] != n_seq or mass_out.shape[1] < keep:
+        weights, m_rows, m_width, m_stride = _mat(mass, "mass", torch.float32, dev)
+        w_out, o_rows, o_width, o_stride = _mat(mass_out, "mass_out", torch.float32, dev)
+        if o_rows != n_seq or o_width < keep:
             raise ValueError("mass_out must hold one row of kept weights per sequence")
-        _index_rows(rows, "rows", n_seq, mass, "mass")
+        if rows is None and m_rows < n_seq:
+            raise ValueError("mass must hold one row per sequence")
     elif rows is not None:
         raise ValueError("rows are of mass")
     if not pool.is_contiguous() or pool.numel() < pool_pages * page_bytes(layout, page_bits):
         raise ValueError("pool must be contiguous and hold pool_pages pages")
-    _err_word(err)
-    dev = _same_device(pool, page_table, new_table, kept, req, mass, rows, mass_out, err)
-    m_rows, m_width, m_stride = (mass.shape[0], mass.shape[1], _stride0(mass)) if mass is not None else (0, 0, 0)
-    st = _on(dev, stream, lambda s: lib().kvq_evict_move(
-        layout, page_bits, pool.data_ptr(), int(pool_pages), page_table.data_ptr(), page_table.shape[0],
-        page_table.shape[1], _stride0(page_table), _ptr(req), new_table.data_ptr(), new_table.shape[1],
-        _stride0(new_table), kept.data_ptr(), n_seq, keep, _stride0(kept), _ptr(mass), m_rows, m_width, m_stride,
-        _ptr(rows), _ptr(mass_out), _stride0(mass_out) if mass is not None else 0, _ptr(err), s))
-    _check(st, "kvq_evict_move")
+    _run("kvq_evict_move", dev, stream, layout, page_bits, pool.data_ptr(), int(pool_pages), table, t_rows, t_width, t_stride, req,
+         new, n_width, n_stride, of, n_seq, keep, k_stride, weights, m_rows, m_width, m_stride, rows, w_out, o_stride,
+         _err(err, dev))
