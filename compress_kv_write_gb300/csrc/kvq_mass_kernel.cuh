@@ -536,6 +536,8 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             entry = -1;
             if (at < kMTile && t < cur.s.len) entry = __ldg(a.table + cur.s.trow * a.table_stride + (t >> a.page_bits));
         };
+        // Where the queries leave room for one block's stages, the next block is sent for to L2.
+        constexpr bool kAhead = S == 4;
         fetch();
         int slot = st, issued = 0;
         uint32_t parity = 1;
@@ -576,6 +578,14 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 bulk_load(to + off * T::kCodeBytes, from + int64_t(row) * T::kCodeBytes, piece_rows * T::kCodeBytes, bar);
                 bulk_load(to + kMStage * T::kCodeBytes + off * T::kScaleBytes, from + area + int64_t(row) * T::kScaleBytes,
                           piece_rows * T::kScaleBytes, bar);
+            }
+            if constexpr (kAhead) {
+                const int ta = cur.kb * kMTile + at;
+                if (i + 1 < units && at < kMTile && ta < cur.s.len && entry >= 0 && entry < a.pool_limit) {
+                    const uint8_t *from = a.pool + entry * page_bytes;
+                    prefetch_l2_bulk(from + int64_t(ta & in_page) * T::kCodeBytes, piece_rows * T::kCodeBytes);
+                    prefetch_l2_bulk(from + area + int64_t(ta & in_page) * T::kScaleBytes, piece_rows * T::kScaleBytes);
+                }
             }
             issued += 4;
             slot += 4;
