@@ -10,10 +10,10 @@
 // is joined but the tiles of a sequence with more than 128 query rows.
 //
 // The products are tcgen05 with 128 tokens on the wide side and N = 16, 32, 64
-// or 128 rows on the narrow one.  Codes and scales come by bulk copies, 32
-// tokens a stage, up to 16 stages ahead; a decode warp takes 128 dims of a
-// stage to registers, frees it, and writes fp16 into TMEM as the product's A
-// operand (nothing goes back to shared memory).  A query tile stays in shared
+// or 128 rows on the narrow one.  Codes and scales come by bulk copies, pages or
+// what a block has of them, up to four blocks ahead; a decode warp takes 128
+// dims of 32 tokens to registers, frees the block, and writes fp16 into TMEM as
+// the product's A operand (nothing goes back to shared memory).  A query tile stays in shared
 // memory as long as its blocks last.
 //
 // The numerics are the attention's: queries times a power of two in fp16 (exact
@@ -30,7 +30,6 @@ namespace kvq {
 namespace {
 
 constexpr int kMTile = 128;  // cached tokens a block
-constexpr int kMStage = 32;  // tokens a stage: a block's share of a TMEM lane quarter
 constexpr int kMChunks = kD / 128;
 // Warps: 0-15 decode (four a quarter of the lanes, a chunk of 128 dims each), 16-23 weights (a lane quarter and half of the
 // rows each; with all rows of every other block a score buffer was free later: 4 bits, 128 rows, 1.77 instead of XX us a
@@ -42,11 +41,11 @@ constexpr int kMThreads = (kMLoad + 1) * 32;
 // What a tile costs beside its blocks (its queries), in blocks, when blocks are shared out.
 constexpr int kMTileCost = 2;
 
+// Blocks whose codes and scales shared memory holds.
 template <Layout L>
-constexpr int kMStageBytes = kMStage * kTokenBytes<L>;
-// Stages: a multiple of four, so that each quarter has slots of its own.
+constexpr int kMStageBytes = kMTile * kTokenBytes<L>;
 template <Layout L, int N>
-constexpr int kMStages = (L == Layout::V41 ? 1 : 2) * (N == 128 ? 4 : 8);
+constexpr int kMStages = (L == Layout::V41 ? 1 : 2) * (N == 128 ? 1 : 2);
 // Chunks that TMEM holds for the products, beside two blocks' scores; four or more, so that a wait for the one that had
 // a slot before is at most one phase off.
 template <int N>
@@ -55,7 +54,7 @@ constexpr int kMRing = N == 128 ? 4 : N == 64 ? 6 : 7;
 template <Layout L, int N>
 struct MassShared {
     static constexpr int S = kMStages<L, N>, KR = kMRing<N>;
-    uint64_t full[S], empty[S];     // a stage's codes are there; are read
+    uint64_t full[S], empty[S];     // a block's codes are there; are read
     uint64_t ready[KR], scored[KR]; // a chunk is in TMEM; its products are done
     uint64_t sdone[2], sread[2];    // a block's scores are done; are read
     uint64_t tready[4];             // a block's powers of two are there
@@ -66,7 +65,7 @@ struct MassShared {
     int start_tile, start_kb;
     uint32_t tmem;
     int abort;
-    uint32_t there[S];              // which of a stage's tokens are
+    uint32_t pieces[S];             // which of a block's copies there are
     int texp[4][kMTile];            // a token's power of two, or kNoToken
     float other[2][kMTile];         // a token's weights of the second half of the rows
     // of a tile's rows, four tiles in turn: factor, -log2(e) lse, what their roundings leave out, tokens seen; the fewest
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), kMChunks);
+            mbar_init(smem_addr(&sh.empty[i]), kMDeq);
         }
         for (int i = 0; i < KR; ++i) {
             mbar_init(smem_addr(&sh.ready[i]), 4);
@@ -327,10 +326,11 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         // ------------------------------------------------------ decode
         const int quarter = warp & 3, chunk = warp >> 2, q = lane & 3, r8 = lane >> 2;
         const uint32_t tlane = kTmemK + ((32 * quarter) << 16);
-        const uint32_t code_at = r8 * T::kCodeBytes + chunk * (T::kCodeBytes / kMChunks) + q * (T::kCodeBytes / kNBlk);
-        const uint32_t scale_at = kMStage * T::kCodeBytes + r8 * T::kScaleBytes;
-        int slot = quarter, kslot = chunk;
-        uint32_t parity = 0, kparity = 1;  // of the stage; of the chunk that had this one's TMEM slot before
+        const uint32_t code_at = (32 * quarter + r8) * T::kCodeBytes + chunk * (T::kCodeBytes / kMChunks) + q * (T::kCodeBytes / kNBlk);
+        const uint32_t scale_at = kMTile * T::kCodeBytes + (32 * quarter + r8) * T::kScaleBytes;
+        const int piece_bits = min(7, a.page_bits);
+        int slot = 0, kslot = chunk;
+        uint32_t parity = 0, kparity = 1;  // of the block; of the chunk that had this one's TMEM slot before
         MassCursor cur(a, start_tile, start_kb, units);
         int known = -1;  // the tile whose queries are loaded
 #pragma unroll 1
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             }
             mbar_wait(smem_addr(&sh.full[slot]), parity, tries);
             const uint32_t stage = smem_addr(sStage) + slot * kMStageBytes<L>;
-            const uint32_t there = sh.there[slot];
+            const uint32_t pieces = sh.pieces[slot];
             Raw<L> raw[4][2];  // token, half of the 32 codes
             int texp[4];
             uint32_t mul[4];
@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             if (chunk == 0 && q == 0) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const int t = 8 * h + r8;
-                    sh.texp[i & 3][32 * quarter + t] = (there >> t) & 1 ? texp[h] : kNoToken;
+                    const int t = 32 * quarter + 8 * h + r8;
+                    const bool there = cur.kb * kMTile + t < cur.s.len && ((pieces >> (t >> piece_bits)) & 1);
+                    sh.texp[i & 3][t] = there ? texp[h] : kNoToken;
                 }
             }
             tc_wait_st();
@@ -391,9 +392,8 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 mbar_arrive(smem_addr(&sh.ready[kslot]));
                 if (chunk == 0) mbar_arrive(smem_addr(&sh.tready[i & 3]));
             }
-            slot += 4;
-            if (slot >= S) {
-                slot -= S;
+            if (++slot == S) {
+                slot = 0;
                 parity ^= 1;
             }
             kslot += kMChunks;
@@ -520,15 +520,12 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         mbar_wait(smem_addr(&sh.drain), 0, tries);
     } else {
         // ------------------------------------------------------ pages and copies
-        // A block's four stages go out together: lane l has the piece of piece_rows tokens from token l * piece_rows of the
-        // block on, the first lane of a stage waits for its slot and arms its barrier.  (Stage after stage took 780 clocks
-        // each, all of them this warp's latencies: 16 heads, 4 bits, 1.70 us a block.)
+        // Lane l has the piece of piece_rows tokens from token l * piece_rows of the block on: a page, or what the block has of
+        // it.  (32 tokens a copy and a barrier: 780 clocks each, all of them this warp's latencies.)
         const int64_t page_bytes = int64_t(kTokenBytes<L>) << a.page_bits, area = int64_t(T::kCodeBytes) << a.page_bits;
         const int in_page = (1 << a.page_bits) - 1;
-        const int piece_bits = min(5, a.page_bits), piece_rows = 1 << piece_bits;
-        const int at = lane << piece_bits;                   // of the block
-        const int st = (at >> 5) & 3, off = at & 31;         // stage, token of the stage
-        const bool lead = at < kMTile && off == 0;
+        const int piece_bits = min(7, a.page_bits), piece_rows = 1 << piece_bits;
+        const int at = lane << piece_bits;  // of the block
         MassCursor cur(a, start_tile, start_kb, units);
         int64_t entry = -1;
         auto fetch = [&]() {
@@ -536,47 +533,35 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             entry = -1;
             if (at < kMTile && t < cur.s.len) entry = __ldg(a.table + cur.s.trow * a.table_stride + (t >> a.page_bits));
         };
-        // Where the queries leave room for one block's stages, the next block is sent for to L2.
-        constexpr bool kAhead = S == 4;
+        // Where the queries leave room for one block, the next one is sent for to L2.
+        constexpr bool kAhead = S == 1;
         fetch();
-        int slot = st, issued = 0;
+        int slot = 0, issued = 0;
         uint32_t parity = 1;
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
             const int64_t page = entry;
-            const int t = cur.kb * kMTile + at, len = cur.s.len;
-            if (i + 1 < units) {  // the next block's pages, while this one's stages become free
+            const int t = cur.kb * kMTile + at;
+            const bool has = at < kMTile && t < cur.s.len, good = has && page >= 0 && page < a.pool_limit;
+            if (i + 1 < units) {  // the next block's pages, while this one's place becomes free
                 cur.next(a);
                 fetch();
             }
-            const bool has = at < kMTile && t < len, good = has && page >= 0 && page < a.pool_limit;
             if (has && !good) raise_err(a.err, KVQ_DEVERR_PAGE);
-            uint32_t mask = 0, bytes = good ? piece_rows * kTokenBytes<L> : 0;
-            if (good) {
-                const int n = min(piece_rows, len - t);
-                mask = (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1) << off;
-            }
-            for (int o = 1; o < (32 >> piece_bits); o <<= 1) {  // over a stage's lanes
-                mask |= __shfl_xor_sync(0xFFFFFFFFu, mask, o);
-                bytes += __shfl_xor_sync(0xFFFFFFFFu, bytes, o);
-            }
-            const uint32_t bar = smem_addr(&sh.full[slot]);
-            if (lead && i * 4 >= S) mbar_wait(smem_addr(&sh.empty[slot]), parity, tries);
-            if (__any_sync(0xFFFFFFFFu, tries == 0)) {
-                tries = 0;
-                break;
-            }
-            if (lead) {
-                sh.there[slot] = mask;
-                mbar_arrive_expect(bar, bytes);
+            const uint32_t pieces = __ballot_sync(0xFFFFFFFFu, good), bar = smem_addr(&sh.full[slot]);
+            if (i >= S) mbar_wait(smem_addr(&sh.empty[slot]), parity, tries);
+            if (!tries) break;
+            if (lane == 0) {
+                sh.pieces[slot] = pieces;
+                mbar_arrive_expect(bar, __popc(pieces) * piece_rows * kTokenBytes<L>);
             }
             __syncwarp();
             if (good) {
                 const uint32_t to = smem_addr(sStage) + slot * kMStageBytes<L>;
                 const uint8_t *from = a.pool + page * page_bytes;
                 const int row = t & in_page;
-                bulk_load(to + off * T::kCodeBytes, from + int64_t(row) * T::kCodeBytes, piece_rows * T::kCodeBytes, bar);
-                bulk_load(to + kMStage * T::kCodeBytes + off * T::kScaleBytes, from + area + int64_t(row) * T::kScaleBytes,
+                bulk_load(to + at * T::kCodeBytes, from + int64_t(row) * T::kCodeBytes, piece_rows * T::kCodeBytes, bar);
+                bulk_load(to + kMTile * T::kCodeBytes + at * T::kScaleBytes, from + area + int64_t(row) * T::kScaleBytes,
                           piece_rows * T::kScaleBytes, bar);
             }
             if constexpr (kAhead) {
@@ -587,10 +572,9 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                     prefetch_l2_bulk(from + area + int64_t(ta & in_page) * T::kScaleBytes, piece_rows * T::kScaleBytes);
                 }
             }
-            issued += 4;
-            slot += 4;
-            if (slot >= S) {
-                slot -= S;
+            ++issued;
+            if (++slot == S) {
+                slot = 0;
                 parity ^= 1;
             }
         }
