@@ -6,6 +6,7 @@ namespace kvq {
 namespace {
 
 constexpr int64_t kMaxLen = int64_t(1) << 30;  // cached tokens of a sequence
+constexpr int64_t kMaxTree = 1024;             // drafted tokens of a sequence, as in kvq_tree_mask
 
 // Bytes of `rows` rows of `width` floats.
 int64_t span(int64_t rows, int64_t width, int64_t stride) { return rows > 0 ? ((rows - 1) * stride + width) * 4 : 0; }
@@ -24,7 +25,7 @@ extern "C" kvq_status kvq_attend_mass(kvq_layout layout, int page_bits, const vo
                                       int64_t q_head_stride, int64_t n_seq, int64_t q_len, int64_t heads, const float *lse,
                                       const uint8_t *pool, int64_t pool_pages, const int32_t *page_table,
                                       int64_t table_rows, int64_t table_width, int64_t table_stride, const int32_t *req,
-                                      const int32_t *kv_len, float scale, float *mass, int64_t mass_row_count,
+                                      const int32_t *kv_len, const uint64_t *mask, float scale, float *mass, int64_t mass_row_count,
                                       int64_t mass_width, int64_t mass_row_stride, const int32_t *rows, const float *prev,
                                       int64_t prev_row_stride, float decay, void *workspace, size_t workspace_bytes,
                                       int32_t *err, struct CUstream_st *stream) {
@@ -34,6 +35,8 @@ extern "C" kvq_status kvq_attend_mass(kvq_layout layout, int page_bits, const vo
     if (n_seq < 0 || q_len < 1 || heads < 1 || mass_row_count < 0 || mass_width < 0) return KVQ_ERR_INVALID_ARG;
     if (q_len > (int64_t(1) << 20) || heads > (int64_t(1) << 10) || n_seq > 0xFFFF || n_seq * q_len > (int64_t(1) << 24))
         return KVQ_ERR_UNSUPPORTED;
+    if (mask && q_len > kMaxTree) return KVQ_ERR_UNSUPPORTED;
+    if (!aligned(mask, 8)) return KVQ_ERR_INVALID_ARG;
     if (!(scale - scale == 0.f) || (prev && !(decay - decay == 0.f))) return KVQ_ERR_INVALID_ARG;  // NaN or infinite
     if (!pool || !aligned(pool, 16) || pool_pages <= 0) return KVQ_ERR_INVALID_ARG;
     if (err && !aligned(err, 4)) return KVQ_ERR_INVALID_ARG;
@@ -78,6 +81,8 @@ extern "C" kvq_status kvq_attend_mass(kvq_layout layout, int page_bits, const vo
     a.max_len = max_len;
     a.req = req;
     a.kv_len = kv_len;
+    a.mask = mask;
+    a.mask_words = int((q_len + 63) / 64);
     a.lse = lse;
     const double c = double(scale) * 1.4426950408889634;
     a.c = float(c);

@@ -19,6 +19,8 @@ struct MassArgs {
     int64_t max_len;  // tokens that a row of the table, and of the weights, has
     const int32_t *req;
     const int32_t *kv_len;
+    const uint64_t *mask;  // tree: mask_words a query token; or NULL
+    int mask_words;
     const float *lse;
     // A weight is 2^(S c + n) with c = scale log2(e) and n = -log2(e) lse, whose roundings to fp32 would be up to 2^-24 (|S c|
     // + |n|) of the exponent.  S c is about -n wherever a weight counts, so a row's weights are taken times 2^((n - fl(n)) - n

@@ -72,6 +72,7 @@ struct MassShared {
     // that one of a warp's rows sees
     alignas(16) float sc[4][N], nl[4][N], wf[4][N];
     alignas(16) int vis[4][N];
+    int words[4][N];                // where a row's mask begins, of a tree; -1: it sees no drafted token
     int least[4][kMDeq];
 };
 
@@ -196,9 +197,11 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
     }
     // a row of no one's, and one that saw nothing (lse = -inf), has no weight
     const bool none = lse == -INFINITY;
-    const int vis = none ? 0 : max(0, cur.s.len - (a.q_len - 1 - row_l / a.heads));
+    const int j_l = row_l / a.heads;
+    const int vis = none ? 0 : max(0, cur.s.len - (a.mask ? a.q_len : a.q_len - 1 - j_l));
     if (lane < kRows) {
         const int r = w + lane * kMDeq;
+        sh.words[slot][r] = none || !a.mask ? -1 : (cur.seq * a.q_len + j_l) * a.mask_words;
         // n = -log2(e) lse in two parts, log2(e) in two as well
         const float n = -lse * kLog2e;
         const float rest = fmaf(-lse, kLog2e, -n) - lse * 1.9259629e-8f;
@@ -427,6 +430,14 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             const bool there = te != kNoToken;
             const float up = L == Layout::V41 && there ? __uint_as_float(uint32_t(127 + te - kLift) << 23) : 1.f;
             const bool masked = (cur.kb + 1) * kMTile > least;
+            // whether row r, of the tile, sees this thread's token: it is one of the first `vis`, or drafted and in its mask
+            const int drafted = t - (cur.s.len - a.q_len);
+            auto sees = [&](int r, int vis) {
+                if (t < vis) return true;
+                if (!a.mask || drafted < 0 || drafted >= a.q_len) return false;
+                const int at = sh.words[c][r];
+                return at >= 0 && ((__ldg(a.mask + at + (drafted >> 6)) >> (drafted & 63)) & 1) != 0;
+            };
             mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
             tc_fence_after();
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -458,8 +469,8 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                     float2 p1 = make_float2(ex2_approx(u1.x), ex2_approx(u1.y));
                     if (masked) {
                         const int4 vis = *reinterpret_cast<const int4 *>(&sh.vis[c][r]);
-                        p0 = make_float2(t < vis.x ? p0.x : 0.f, t < vis.y ? p0.y : 0.f);
-                        p1 = make_float2(t < vis.z ? p1.x : 0.f, t < vis.w ? p1.y : 0.f);
+                        p0 = make_float2(sees(r, vis.x) ? p0.x : 0.f, sees(r + 1, vis.y) ? p0.y : 0.f);
+                        p1 = make_float2(sees(r + 2, vis.z) ? p1.x : 0.f, sees(r + 3, vis.w) ? p1.y : 0.f);
                     }
                     sum[0] = ffma2(p0, make_float2(wf.x, wf.y), sum[0]);
                     sum[1] = ffma2(p1, make_float2(wf.z, wf.w), sum[1]);

@@ -62,8 +62,8 @@ _SIGS = {
     "kvq_mass_workspace": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64]),
     "kvq_attend_mass": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
                                   C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
-                                  C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
-                                  C.c_int64, C.c_float, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+                                  C.c_void_p, C.c_void_p, C.c_float, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                  C.c_void_p, C.c_int64, C.c_float, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
     "kvq_tree_mask": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
                                 C.c_void_p, C.c_void_p]),
     "kvq_attend_tree": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
@@ -533,19 +533,24 @@ def kvq_tree_mask(parent, mask, *, kv_len=None, pos=None, err=None, stream=None)
     return mask
 
 
+def _tree_words(mask, dev):
+    """Checks a tree's masks; returns the drafted tokens of a sequence."""
+    _at(mask, "mask", torch.int64, dev)
+    shape = mask.shape
+    if len(shape) != 3 or shape[2] != (shape[1] + 63) // 64 or not mask.is_contiguous():
+        raise ValueError("mask must be contiguous [n_seq, q_len, ceil(q_len / 64)]")
+    return shape[1]
+
+
 def kvq_attend_tree(layout, page_bits, q, pool, pool_pages, page_table, kv_len, mask, out, workspace, *, scale, req=None,
                     lse=None, err=None, stream=None):
     """kvq_attend of a tree of drafted tokens, the last q_len of a sequence's cached tokens: query token j sees all tokens
     before them and those of them whose bits are set in mask[i, j] ([n_seq, q_len, ceil(q_len / 64)] int64)."""
     n, heads, qs, outs, dev, out_dtype = _attend_rows(q, out, lse, workspace, err)
-    _at(mask, "mask", torch.int64, dev)
-    shape = mask.shape
-    if len(shape) != 3 or shape[2] != (shape[1] + 63) // 64 or not mask.is_contiguous():
-        raise ValueError("mask must be contiguous [n_seq, q_len, ceil(q_len / 64)]")
-    q_len = shape[1]
+    q_len = _tree_words(mask, dev)
     pool, table, req, kv_len, rows, width, ts, n_seq = _paged(layout, page_bits, dev, n, q_len, pool, pool_pages, page_table,
                                                               kv_len, req)
-    if shape[0] != n_seq:
+    if mask.shape[0] != n_seq:
         raise ValueError("mask must hold one tree per sequence")
     _run("kvq_attend_tree", dev, stream, layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, heads, pool,
          int(pool_pages), table, rows, width, ts, req, kv_len, mask.data_ptr(), float(scale), out.data_ptr(), out_dtype, outs[0],
@@ -650,10 +655,11 @@ def mass_workspace(n_seq, rows, max_len):
 
 
 def kvq_attend_mass(layout, page_bits, q, lse, pool, pool_pages, page_table, kv_len, mass, workspace=None, *, scale, q_len=1,
-                    req=None, rows=None, prev=None, decay=1.0, err=None, stream=None):
+                    mask=None, req=None, rows=None, prev=None, decay=1.0, err=None, stream=None):
     """mass [rows, width] fp32 (row rows[i], or i) <- decay * prev + the weight of each of a sequence's cached tokens in
-    kvq_attend, summed over heads and query tokens; q, pool, page_table, kv_len, scale, q_len, req and lse as in that call.
-    prev may be mass itself, or None: no weights from before.  workspace: mass_workspace(n_seq, q_len * heads, max_len)."""
+    kvq_attend, or with mask in kvq_attend_tree, summed over heads and query tokens; q, pool, page_table, kv_len, scale, q_len
+    (with mask: mask.shape[1]), req and lse as in that call.  prev may be mass itself, or None: no weights from before.
+    workspace: mass_workspace(n_seq, q_len * heads, max_len)."""
     dev = _at(q, "q", torch.bfloat16)
     shape, qs = q.shape, q.stride()
     if len(shape) != 3 or shape[2] != HEAD_DIM or qs[2] != 1:
@@ -662,8 +668,12 @@ def kvq_attend_mass(layout, page_bits, q, lse, pool, pool_pages, page_table, kv_
     _at(lse, "lse", torch.float32, dev)
     if lse.shape != (n, heads) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous [tokens, heads]")
+    if mask is not None:
+        q_len = _tree_words(mask, dev)
     pool, table, req, kv_len, t_rows, width, ts, n_seq = _paged(layout, page_bits, dev, n, q_len, pool, pool_pages, page_table,
                                                                 kv_len, req)
+    if mask is not None and mask.shape[0] != n_seq:
+        raise ValueError("mask must hold one tree per sequence")
     to, m_rows, m_width, m_stride = _mat(mass, "mass", torch.float32, dev)
     rows = _vec(rows, "rows", torch.int32, dev, n_seq)
     if rows is None and m_rows < n_seq:
@@ -680,8 +690,8 @@ def kvq_attend_mass(layout, page_bits, q, lse, pool, pool_pages, page_table, kv_
             raise ValueError("workspace must be contiguous")
         ws, size = workspace.data_ptr(), workspace.numel()
     _run("kvq_attend_mass", dev, stream, layout, page_bits, q.data_ptr(), qs[0], qs[1], n_seq, q_len, heads, lse.data_ptr(), pool,
-         int(pool_pages), table, t_rows, width, ts, req, kv_len, float(scale), to, m_rows, m_width, m_stride, rows, before,
-         p_stride or 0, float(decay), ws, size, _err(err, dev))
+         int(pool_pages), table, t_rows, width, ts, req, kv_len, _ptr(mask), float(scale), to, m_rows, m_width, m_stride, rows,
+         before, p_stride or 0, float(decay), ws, size, _err(err, dev))
     return mass
 
 

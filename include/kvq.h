@@ -338,16 +338,18 @@ kvq_status kvq_attend_slots(kvq_layout layout, int page_bits,
  * sequence, token and 128 rows beyond.  As kvq_attend_workspace otherwise. */
 size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
 
-/* The weight that each cached token gets in kvq_attend, summed over the query
- * rows that see it (all heads of all q_len query tokens, causal):
+/* The weight that each cached token gets in kvq_attend, or with a mask in
+ * kvq_attend_tree, summed over the query rows that see it (all heads of all
+ * q_len query tokens):
  *   w[t] = sum over these rows of exp(scale * sum_d q[d] k[t][d] - lse[row]),
  *   mass[t] = decay * prev[t] + w[t], or, where prev is NULL, w[t],
  * for the tokens t < kv_len[i] of sequence i; what lies behind them in mass
  * stays as it is.  With prev = mass the weights of one step after another add
  * up, the older ones worth `decay` as much each step.
  *   q, pool, page_table, req, kv_len, scale   as in kvq_attend, the call's own.
- *   lse        [n_seq * q_len, heads] fp32: what kvq_attend left.  A row whose
- *              lse is -inf has no weight.
+ *   lse        [n_seq * q_len, heads] fp32: what the attention left.  A row
+ *              whose lse is -inf has no weight.
+ *   mask       as in kvq_attend_tree (q_len at most 1024), or NULL: causal.
  *   mass       [mass_rows, mass_row_stride] fp32, the first mass_width of a
  *              row used; row rows[i] (NULL: row i) is sequence i's.  Sequences
  *              of a call have rows of their own: what two write to one row is
@@ -372,8 +374,8 @@ kvq_status kvq_attend_mass(kvq_layout layout, int page_bits,
                            int64_t n_seq, int64_t q_len, int64_t heads, const float *lse,
                            const uint8_t *pool, int64_t pool_pages,
                            const int32_t *page_table, int64_t table_rows, int64_t table_width,
-                           int64_t table_stride, const int32_t *req, const int32_t *kv_len, float scale,
-                           float *mass, int64_t mass_rows, int64_t mass_width, int64_t mass_row_stride,
+                           int64_t table_stride, const int32_t *req, const int32_t *kv_len, const uint64_t *mask,
+                           float scale, float *mass, int64_t mass_rows, int64_t mass_width, int64_t mass_row_stride,
                            const int32_t *rows, const float *prev, int64_t prev_row_stride, float decay,
                            void *workspace, size_t workspace_bytes, int32_t *err, struct CUstream_st *stream);
 

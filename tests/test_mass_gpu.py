@@ -76,7 +76,8 @@ class Mass(Paged):
             got.append((total, tol + 1e-36))
         return got
 
-    def run(self, K, lse, mass=None, prev=None, decay=1.0, rows=None, req=None, table=None, kv_len=None, q=None, err=None, ws=None):
+    def run(self, K, lse, mass=None, prev=None, decay=1.0, rows=None, req=None, table=None, kv_len=None, q=None, err=None, ws=None,
+            mask=None):
         width = self.width << self.pb
         if mass is None:
             mass = torch.full((len(self.lens), width), -7.0, device=DEV)
@@ -87,7 +88,7 @@ class Mass(Paged):
             ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
         K.kvq_attend_mass(self.layout, self.pb, self.q.to(DEV) if q is None else q, lse.to(DEV), torch.from_numpy(self.pool).to(DEV),
                           self.pages, table, kv_len, mass, ws, scale=self.scale, q_len=self.q_len, req=req, rows=rows, prev=prev,
-                          decay=decay, err=err)
+                          decay=decay, mask=mask, err=err)
         torch.cuda.synchronize()
         return mass
 
@@ -355,6 +356,34 @@ def test_captured(K, heads, q_len):
         check(mass, lens, c.want(l), lens)
 
 
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads,q_len,lens", [(4, 7, [7, 100, 0, 130, 3]), (2, 63, [63, 64, 127, 200]), (3, 70, [70, 133, 400]),
+                                              (64, 5, [69, 300])])
+def test_trees(K, layout, heads, q_len, lens):
+    """With a tree's masks, any mask among them, and the lse that kvq_attend_tree leaves."""
+    from test_tree_gpu import Tree
+    rng = np.random.default_rng(heads)
+    for sees in (None, [[np.flatnonzero(rng.random(q_len) < (0.3 if j % 4 else 0.0)).tolist() for j in range(q_len)] for _ in lens]):
+        c = Tree(layout, 6, lens, heads, q_len, seed=5, sees=sees)
+        out, lse = c.run(K)
+        mass = torch.full((len(lens), c.width * 64), -7.0, device=DEV)
+        ws = torch.full((K.mass_workspace(len(lens), q_len * heads, c.width * 64),), 0xFF, dtype=torch.uint8, device=DEV)
+        K.kvq_attend_mass(layout, 6, c.q.to(DEV), lse, torch.from_numpy(c.pool).to(DEV), c.pages, torch.from_numpy(c.table).to(DEV),
+                          torch.tensor(lens, dtype=torch.int32, device=DEV), mass, ws, scale=c.scale, mask=c.mask.to(DEV))
+        q, l = c.q.double().numpy(), lse.cpu().double().numpy()
+        want = []
+        for i, n in enumerate(lens):
+            rows = decode(layout, 6, c.pool, c.slots(i, n)) if n else np.zeros((0, 512))
+            total, tol = np.zeros(n), np.zeros(n)
+            for j in range(q_len):
+                t = np.array(c.seen(i, j) if n else [], np.int64)
+                p, d = weights(layout, q[i * q_len + j], l[i * q_len + j], rows[t], c.scale)
+                total[t] += p.sum(0)
+                tol[t] += d.sum(0)
+            want.append((total, tol + q_len * heads * 2.0 ** -24 * total + 1e-36))
+        check(mass, lens, want, sees is None)
+
+
 def test_a_wait_that_gives_up(K):
     """With a limit of 0 every wait gives up: the weights are NaN and the error word says so; the next call is sound."""
     for heads, q_len in ((16, 1), (64, 3)):
@@ -380,7 +409,9 @@ def test_binding_refuses(K):
     m = torch.zeros((2, 64), device=DEV)
     for bad in (dict(mass=m[:1]), dict(mass=m.double()), dict(mass=m[0]), dict(prev=m[:, :32]), dict(prev=m.double()),
                 dict(rows=torch.zeros(1, dtype=torch.int32, device=DEV)), dict(err=m), dict(q=c.q.to(DEV).float()),
-                dict(kv_len=torch.zeros(3, dtype=torch.int32, device=DEV)), dict(ws=m)):
+                dict(kv_len=torch.zeros(3, dtype=torch.int32, device=DEV)), dict(ws=m), dict(mask=m),
+                dict(mask=torch.zeros((1, 1, 1), dtype=torch.int64, device=DEV)),
+                dict(mask=torch.zeros((2, 2, 1), dtype=torch.int64, device=DEV))):
         with pytest.raises((TypeError, ValueError)):
             c.run(K, lse, **({"mass": torch.zeros((2, 64), device=DEV)} | bad))
     with pytest.raises((TypeError, ValueError)):

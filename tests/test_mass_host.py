@@ -23,17 +23,17 @@ def test_workspace(L):
 
 
 def _mass(L, layout=1, pb=6, q=A, q_tok=8192, q_head=512, n_seq=4, q_len=1, heads=16, lse=A, pool=A, pages=8, table=A, trows=4,
-          width=2, stride=2, req=None, kv_len=A, scale=0.04, mass=A, mrows=4, mwidth=128, mstride=128, rows=None, prev=None,
+          width=2, stride=2, req=None, kv_len=A, mask=None, scale=0.04, mass=A, mrows=4, mwidth=128, mstride=128, rows=None, prev=None,
           pstride=0, decay=1.0, ws=None, ws_bytes=0, err=None):
     return L.kvq_attend_mass(layout, pb, q, q_tok, q_head, n_seq, q_len, heads, lse, pool, pages, table, trows, width, stride,
-                             req, kv_len, scale, mass, mrows, mwidth, mstride, rows, prev, pstride, decay, ws, ws_bytes, err, None)
+                             req, kv_len, mask, scale, mass, mrows, mwidth, mstride, rows, prev, pstride, decay, ws, ws_bytes, err, None)
 
 
 @pytest.mark.parametrize("bad,status", [
     (dict(layout=0), 1), (dict(layout=3), 1), (dict(pb=0), 1), (dict(pb=17), 1), (dict(pb=5), 2), (dict(q=None), 1),
     (dict(q=A + 8), 1), (dict(q_tok=-8), 1), (dict(q_tok=516), 1), (dict(q_head=4), 1), (dict(n_seq=-1), 1), (dict(q_len=0), 1),
     (dict(heads=0), 1), (dict(heads=1025), 2), (dict(n_seq=65536, trows=65536, mrows=65536), 2),
-    (dict(n_seq=1 << 12, q_len=1 << 13), 2), (dict(lse=None), 1), (dict(lse=A + 2), 1), (dict(pool=None), 1), (dict(pool=A + 4), 1),
+    (dict(n_seq=1 << 12, q_len=1 << 13), 2), (dict(mask=A + 4), 1), (dict(mask=A, q_len=1025), 2), (dict(lse=None), 1), (dict(lse=A + 2), 1), (dict(pool=None), 1), (dict(pool=A + 4), 1),
     (dict(pages=0), 1), (dict(table=None), 1), (dict(table=A + 2), 1), (dict(trows=-1), 1), (dict(trows=3), 1), (dict(width=-1), 1),
     (dict(stride=1), 1), (dict(req=A + 1), 1), (dict(kv_len=None), 1), (dict(kv_len=A + 2), 1), (dict(scale=NAN), 1),
     (dict(scale=INF), 1), (dict(mass=None), 1), (dict(mass=A + 2), 1), (dict(mrows=3), 1), (dict(mrows=-1), 1), (dict(mwidth=-1), 1),
