@@ -199,15 +199,15 @@ def _on(dev, stream, call):
         return call(s)
 
 
-def _current_device():
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return get() if get is not None else torch.cuda.current_device()
+# What every call asks torch for, its private form where this torch has that: the public ones cost more than a call's checks.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _raw_stream
 
 
 def _run(name, dev, stream, *args):
     """The C call `name` with `dev` current, on the stream given or that device's current one (the last argument)."""
     f = getattr(lib(), name)
-    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    s = _current_raw(dev) if stream is None else stream.cuda_stream
     if dev == _current_device():
         st = f(*args, s)
     else:
