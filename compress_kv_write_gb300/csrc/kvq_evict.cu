@@ -27,6 +27,8 @@ namespace {
 // Bound by latency and by the instructions a key takes in one or a few SMs:
 // some five a round.  (Keys in shared memory and ballots to add up equal bins,
 // which the hardware's counting increments do by themselves, took 60 a round.)
+// One sequence of 4,097 tokens 5.9 us, 32 of up to 24,577 10.7, one of 131,072
+// 15.4, one of 400,000 (by way of shared memory) 81.
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
@@ -297,7 +299,8 @@ kvq_status launch_select(SelectArgs a, int64_t n_seq, int cluster, cudaStream_t 
 // bytes as they are.  A warp has 8 (V41) or 16 (V41_FP4) tokens: as many lanes
 // look up where these lie and shall lie, then all rows' loads (8 a lane) are
 // under way before the first store.  Bound by memory: rows of 256 or 512 bytes,
-// read and written once.
+// read and written once: 224 MB of V41 rows in 38 us = 5.9 TB/s (with 4 tokens a
+// warp 39.8, with more warps an SM 40.0), 2,048 V41_FP4 rows in 3.0 (2.5).
 constexpr int kMoveThreads = 256;
 template <Layout L>
 constexpr int kMoveTok = L == Layout::V41 ? 8 : 16;

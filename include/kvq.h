@@ -3,7 +3,9 @@
  * DeepSeek-V4-style serving: block quantisation of new K rows into a paged
  * pool (optionally pooled by a ratio-r softmax compressor, RMS-normalised and
  * rotated), the once-per-step full->SWA slot translation, and the paged
- * dequant back to a bf16 workspace.
+ * dequant back to a bf16 workspace; and of what a decode step does around it:
+ * attention over the pool (also of a tree of drafted tokens), the weight that
+ * it gives each token and eviction by it, rotary positions, and the norm.
  *
  * Sources (page title, section):
  *  [P1] "[sglang] DeepSeek V4.1 Paged KV Cache: V41 and FP4 formats"
@@ -75,7 +77,8 @@ enum {
                           /* and lse that it worked on are NaN                    */
     KVQ_DEVERR_STATE = 32,   /* a request index outside [0, n_state) or a count   */
                              /* outside [0, ratio): that request is skipped; in   */
-                             /* kvq_attend a table row outside [0, table_rows)    */
+                             /* the calls over pages a row outside its table; in  */
+                             /* kvq_tree_mask a parent that is no earlier token   */
     KVQ_DEVERR_LEN = 64      /* a kv_len outside [0, table_width pages] or above  */
                              /* 2^30 (the sequence counts as empty)               */
 };
@@ -436,8 +439,8 @@ kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, in
  *              each other.  Sets of rows that share an address range are
  *              accepted where equal strides keep them beside each other.
  * A pos outside [0, cos_sin_rows) sets KVQ_DEVERR_POS and leaves the token's
- * rows of out as they are.  Any alignment and sizes are accepted; rows, parts
- * and halves that begin on 16 bytes are faster. */
+ * rows of out as they are.  Rows, parts and halves that begin on 16 bytes are
+ * faster.  out overlaps neither cos_sin nor pos. */
 kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens, int64_t heads, int64_t dim,
                     int64_t x_token_stride, int64_t x_head_stride, int64_t rot_start, int64_t rot_dim, unsigned flags,
                     const float *cos_sin, int64_t cos_sin_rows, const int32_t *pos, void *out,
@@ -471,7 +474,8 @@ kvq_status kvq_evict_select(const float *mass, int64_t mass_rows, int64_t mass_w
  *              `keep` tokens (new_width).  A page in it that holds rows of the
  *              old tables too is fine only where its rows stay where they are
  *              (the first pages of a sequence whose first tokens all stay):
- *              otherwise rows may be overwritten before they are read.
+ *              otherwise rows may be overwritten before they are read.  No
+ *              page is in two places of it that tokens move to.
  *   mass, rows as in kvq_evict_select; mass and mass_out NULL: no weights.
  *   mass_out   [n_seq, mass_out_stride] fp32, apart from mass.
  * An entry outside the table or the weights sets KVQ_DEVERR_SLOT, a page
