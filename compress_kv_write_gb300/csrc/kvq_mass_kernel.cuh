@@ -99,8 +99,8 @@ template <Layout L, int N>
 constexpr size_t kMassSmem = 1024 + size_t(N) * kD * 2 + size_t(kMStages<L, N>) * kMStageBytes<L> + sizeof(MassShared<L, N>);
 static_assert(kMassSmem<Layout::V41, 16> <= 232448 && kMassSmem<Layout::V41, 32> <= 232448 &&
                   kMassSmem<Layout::V41, 64> <= 232448 && kMassSmem<Layout::V41, 128> <= 232448 &&
-                  kMassSmem<Layout::FP4, 16> <= 232448 && kMassSmem<Layout::FP4, 64> <= 232448 &&
-                  kMassSmem<Layout::FP4, 128> <= 232448,
+                  kMassSmem<Layout::FP4, 16> <= 232448 && kMassSmem<Layout::FP4, 32> <= 232448 &&
+                  kMassSmem<Layout::FP4, 64> <= 232448 && kMassSmem<Layout::FP4, 128> <= 232448,
               "227 KB a CTA");
 
 struct MassSeq {
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 mul[h] = block_mul<L>((w >> (8 * q)) & 0xFFu, texp[h]);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.empty[slot]));
+            // (once the wait for it has given up its copy may be under way: then nothing is copied over it)
+            if (lane == 0 && tries) mbar_arrive(smem_addr(&sh.empty[slot]));
             // a slot in TMEM is free when the products over what it held are done
             if (i * kMChunks + chunk >= KR) mbar_wait(smem_addr(&sh.scored[kslot]), kparity, tries);
             tc_fence_after();
@@ -492,7 +493,9 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                         sum[1] = ffma2(p[1], make_float2(wf.z, wf.w), sum[1]);
                     }
                 }
-            } else {  // a tile's last block or two, in a loop of their own: the roles share the instruction cache (1.39 us a block, 1.61 in one)
+            } else {
+                // A tile's last block or two, in a loop of their own: the roles share the instruction cache (128 rows over
+                // 4-bit slots 1.39 us a block, with masks in the other loop 1.61).
 #pragma unroll 1
                 for (int j0 = 0; j0 < NC; j0 += 4) {
                     uint32_t x[4];
@@ -596,7 +599,10 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             if (has && !good) raise_err(a.err, KVQ_DEVERR_PAGE);
             const uint32_t pieces = __ballot_sync(0xFFFFFFFFu, good), bar = smem_addr(&sh.full[slot]);
             if (i >= S) mbar_wait(smem_addr(&sh.empty[slot]), parity, tries);
-            if (!tries) break;
+            if (__any_sync(0xFFFFFFFFu, tries == 0)) {  // the warp's decision
+                tries = 0;
+                break;
+            }
             if (lane == 0) {
                 sh.pieces[slot] = pieces;
                 mbar_arrive_expect(bar, __popc(pieces) * piece_rows * kTokenBytes<L>);

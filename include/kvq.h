@@ -212,8 +212,8 @@ kvq_status kvq_dequant_slots(kvq_layout layout, int page_bits,
  * workspaces of their own (captured graphs too, unless they run in turn). */
 size_t kvq_attend_workspace(int64_t rows);
 
-/* How often a wait inside the attention kernels (for another warp's part of
- * the work) tries before the call gives up with KVQ_DEVERR_WAIT; the default
+/* How often a wait inside the kernels of kvq_attend, kvq_attend_slots,
+ * kvq_attend_tree and kvq_attend_mass (for another warp's part of the work) tries before the call gives up with KVQ_DEVERR_WAIT; the default
  * is 2^20, which takes some seconds, far beyond any wait of a sound call.  Sets
  * the limit of the process's later calls (at most 2^24; a captured call keeps
  * the one it was captured with) and returns the one before.  With 0 every call

@@ -403,6 +403,30 @@ def test_a_wait_that_gives_up(K):
         assert err.item() == 0
 
 
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads,q_len", [(16, 1), (128, 1), (64, 3)])
+def test_a_few_tries(K, layout, heads, q_len):
+    """With a few tries some waits give up and some do not: the call ends, and a weight is right or, where the error word
+    says so, NaN."""
+    c = Mass(layout, 6, [3000, 30, 0, 900], heads, q_len=q_len, seed=43)
+    lse = c.lses()
+    want = c.want(lse)
+    for limit in (1, 2, 5, 20, 100):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        before = K.attend_wait_limit(limit)
+        try:
+            got = c.run(K, lse, err=err)
+        finally:
+            K.attend_wait_limit(before)
+        assert err.item() in (0, 16)
+        if err.item() == 0:
+            check(got, c.lens, want, limit)
+        for i, (total, tol) in enumerate(want):
+            row = got[i, :c.lens[i]].cpu().double().numpy()
+            assert (np.isnan(row) | (np.abs(row - total) <= tol)).all() and (got[i, c.lens[i]:] == -7).all()
+    check(c.run(K, lse), c.lens, want, "after")
+
+
 def test_binding_refuses(K):
     c = Mass(V41, 6, [20, 9], 4, seed=47)
     lse = c.lses()

@@ -265,6 +265,26 @@ def test_tree_captured(K):
         check(out, lse, c.want(), seed)
 
 
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads,q_len,lens", [(16, 1, [70]), (4, 8, [5000, 0, 9]), (64, 3, [700, 64, 9000])])
+def test_a_wait_that_gives_up(K, layout, heads, q_len, lens):
+    """With a limit of 0 every wait gives up: all rows are NaN, nothing behind them is written, and the next call is right."""
+    c = Tree(layout, 6, lens, heads, q_len, seed=31)
+    n = len(lens) * q_len
+    big = torch.full((n + 1, heads, 512), 3.0, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    before = K.attend_wait_limit(0)
+    try:
+        out, lse = c.run(K, out=big[:n], err=err)
+    finally:
+        K.attend_wait_limit(before)
+    assert err.item() == 16 and out.isnan().all() and lse.isnan().all() and (big[n] == 3).all()
+    err.zero_()
+    out, lse = c.run(K, err=err)
+    assert err.item() == 0
+    check(out, lse, c.want(), "after")
+
+
 def test_binding_refuses(K):
     c = Tree(V41, 6, [20, 9], 4, 3, seed=29)
     m = c.mask
