@@ -218,6 +218,35 @@ def test_select_and_move_captured(K):
         assert np.array_equal(d.cpu().numpy(), moved(pool, V41, 6, 32, table.numpy(), new.numpy(), want))
 
 
+@pytest.mark.parametrize("width", [20000, 100000, 200000])
+def test_select_captured_in_clusters(K, width):
+    """Sequences that a cluster's CTAs share, in a graph, replayed over other weights and lengths."""
+    keep = width // 3
+    mass, lens = torch.zeros((2, width), device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    kept, count = torch.zeros((2, keep), dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        K.kvq_evict_select(mass, lens, kept, count, first=3, last=50)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.kvq_evict_select(mass, lens, kept, count, first=3, last=50)
+    for seed, ls in ((1, [width, width // 2]), (2, [keep, width - 1])):
+        m = weights("zeros", 2, width, seed)
+        mass.copy_(m)
+        lens.copy_(torch.tensor(ls))
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, n in enumerate(ls):
+            if n <= keep:
+                want = np.arange(n)
+            else:
+                free = np.argsort(-m[i, 3:n - 50].numpy(), kind="stable")[:keep - 53] + 3
+                want = np.concatenate((np.arange(3), np.sort(free), np.arange(n - 50, n)))
+            assert count[i] == want.size and np.array_equal(kept[i, :want.size].cpu().numpy(), want)
+
+
 def test_binding_refuses(K):
     mass, lens = torch.zeros((2, 64), device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
     kept, count = torch.zeros((2, 8), dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)

@@ -206,3 +206,42 @@ def test_other_streams(K):
     side.synchronize()
     assert torch.equal(mask.cpu(), c.mask) and torch.equal(out, want) and torch.equal(l2, lse)
     assert count.tolist() == [40, 40] and abs(mass.double().sum().item() - 2 * 48) < 1e-2
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+def test_two_streams_at_once(K, layout):
+    """Calls with buffers and workspaces of their own, under way on two streams together: the results of one at a time."""
+    probs = [Tree(layout, 6, lens, heads, q_len, seed=heads) for lens, heads, q_len in (([3000, 90, 7], 16, 5), ([700, 0, 1500], 64, 3))]
+    runs = []
+    for c in probs:
+        n, rows, width = len(c.lens), c.q_len * c.heads, c.width * 64
+        runs.append(dict(c=c, q=c.q.to(DEV), pool=torch.from_numpy(c.pool).to(DEV), table=torch.from_numpy(c.table).to(DEV),
+                         kv=torch.tensor(c.lens, dtype=torch.int32, device=DEV), mask=c.mask.to(DEV), out=torch.empty_like(c.q, device=DEV),
+                         lse=torch.empty(c.q.shape[:2], device=DEV), mass=torch.zeros((n, width), device=DEV),
+                         kept=torch.zeros((n, 200), dtype=torch.int32, device=DEV), count=torch.zeros(n, dtype=torch.int32, device=DEV),
+                         ws=torch.empty(K.attend_workspace(rows), dtype=torch.uint8, device=DEV),
+                         ws2=torch.empty(K.mass_workspace(n, rows, width), dtype=torch.uint8, device=DEV), stream=torch.cuda.Stream()))
+
+    def go(r, stream):
+        c = r["c"]
+        K.kvq_attend_tree(layout, 6, r["q"], r["pool"], c.pages, r["table"], r["kv"], r["mask"], r["out"], r["ws"], scale=c.scale,
+                          lse=r["lse"], stream=stream)
+        K.kvq_attend_mass(layout, 6, r["q"], r["lse"], r["pool"], c.pages, r["table"], r["kv"], r["mass"], r["ws2"], scale=c.scale,
+                          mask=r["mask"], stream=stream)
+        K.kvq_evict_select(r["mass"], r["kv"], r["kept"], r["count"], last=9, stream=stream)
+
+    alone = []
+    for r in runs:
+        go(r, None)
+        torch.cuda.synchronize()
+        alone.append([r[k].clone() for k in ("out", "lse", "mass", "kept", "count")])
+        for k in ("out", "lse", "mass", "kept", "count"):
+            r[k].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r in runs:
+            go(r, r["stream"])
+    torch.cuda.synchronize()
+    for r, want in zip(runs, alone):
+        for k, w in zip(("out", "lse", "mass", "kept", "count"), want):
+            assert torch.equal(r[k], w), k
