@@ -28,11 +28,11 @@ namespace {
 // some five a round.  (Keys in shared memory and ballots to add up equal bins,
 // which the hardware's counting increments do by themselves, took 60 a round.)
 // One sequence of 4,097 tokens 5.9 us, 32 of up to 24,577 10.7, one of 131,072
-// 15.4, one of 400,000 (by way of shared memory) 81.
+// 15.4 to 17; by way of shared memory one of 400,000 51, a million 114.
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kSelKeys = 40960;  // keys that a CTA can hold in shared memory
+constexpr int kSelKeys = 52224;  // keys that a CTA can hold in shared memory (204 KB)
 
 struct SelectArgs {
     const float *mass;
@@ -166,14 +166,22 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
             for (int j = 0; j < kRegs; ++j)
                 if (j < steps) f(w0 + j * 32 + lane, keys[j]);
         } else {
-            constexpr int kBatch = 8;  // loads under way
+            constexpr int kBatch = 16;  // loads under way
 #pragma unroll 1
             for (int j0 = 0; j0 < steps; j0 += kBatch) {
                 uint32_t k[kBatch];
+                if (w0 + j0 * 32 >= in_smem) {
+                    float v[kBatch];
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int i = w0 + (j0 + b) * 32 + lane;
-                    k[b] = j0 + b >= steps || i >= mine ? 0u : i < in_smem ? held[i] : mass_key(__ldg(from + i));
+                    for (int b = 0; b < kBatch; ++b) v[b] = __ldg(from + min(w0 + (j0 + b) * 32 + lane, mine - 1));
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) k[b] = w0 + (j0 + b) * 32 + lane < mine ? mass_key(v[b]) : 0u;
+                } else {
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int i = w0 + (j0 + b) * 32 + lane;
+                        k[b] = i >= mine ? 0u : i < in_smem ? held[i] : mass_key(__ldg(from + i));
+                    }
                 }
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b)
