@@ -108,15 +108,16 @@ __global__ void __launch_bounds__(kTabThreads) rope_table_kernel(const TableArgs
 // ---------------------------------------------------------------- rotation
 // (u, v) -> (u c - v s, v c + u s), or with the sine's sign turned the way back
 // (the transpose).  A pair is neighbours (interleaved) or rot / 2 apart
-// (halves).  A row's work is cut into pieces of 16 bytes: pieces that are
-// copied (not where the rows are rotated in place) and pieces that are rotated,
-// with halves two at a time.  A thread has the same piece of several heads of
-// one token, so it reads its cosines and sines once; the heads' loads are all
+// (halves).  A row's work is cut into pieces of 16 or 8 bytes: first those that
+// are rotated, with halves two at a time, then those that are copied (none where
+// the rows are rotated in place).  A thread has the same piece of several heads
+// of one token, so it reads its cosines and sines once; the heads' loads are all
 // under way before the first is used.
 //
 // Bound by memory: a value is read once and written once, and some 45
 // instructions go to the 32 bytes of a piece.  8,191 tokens of 64 heads, bf16
-// rows of 512 (1.08 GB): 159 us = 6.75 TB/s; one token of 16 heads: 1.9 us.
+// rows of 512 (1.08 GB): 160 us = 6.7 TB/s; one token of 16 heads: 2.0 us.
+// (Rotated and copied pieces one after the other instead of side by side: 179.)
 constexpr int kRopeThreads = 256, kRopeBatch = 4;
 
 struct RopeArgs {
@@ -125,7 +126,7 @@ struct RopeArgs {
     int64_t x_tok, x_head, out_tok, out_head;  // bytes
     int64_t n;
     int heads, start, rot;  // elements
-    int pieces, front;      // pieces a row has, those of them before the rotated ones
+    int turning, copied;    // a row's pieces that are rotated, those that are copied (value by value: pairs, values)
     int heads_cta, splits;  // heads a CTA has, CTAs a token
     const float *cos_sin;
     int64_t rows;
@@ -134,14 +135,22 @@ struct RopeArgs {
     float sign;
 };
 
-// Not by way of the read-only path: the rows may be rotated in place.
-__device__ __forceinline__ uint4 load_row16(const uint8_t *p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-    return r;
+// W words.  Not by way of the read-only path: the rows may be rotated in place.
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&r)[W]) {
+    if constexpr (W == 4) {
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p) : "memory");
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&r)[W]) {
+    if constexpr (W == 4) st_u4(p, make_uint4(r[0], r[1], r[2], r[3]));
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(r[0], r[1]);
 }
 
 // One element, bf16 or fp32, from / to memory.
@@ -156,11 +165,10 @@ __device__ __forceinline__ void store_one(uint8_t *p, float v) {
     else *reinterpret_cast<float *>(p) = v;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void unpack16(const uint4 u, float (&v)[kBf16 ? 8 : 4]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+template <bool kBf16, int W>
+__device__ __forceinline__ void unpack(const uint32_t (&w)[W], float (&v)[kBf16 ? 2 * W : W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
         if constexpr (kBf16) {
             v[2 * i] = bf16_lo(w[i]);
             v[2 * i + 1] = bf16_hi(w[i]);
@@ -169,24 +177,23 @@ __device__ __forceinline__ void unpack16(const uint4 u, float (&v)[kBf16 ? 8 : 4
         }
     }
 }
-template <bool kBf16>
-__device__ __forceinline__ uint4 pack16(const float (&v)[kBf16 ? 8 : 4]) {
-    if constexpr (kBf16)
-        return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    else
-        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+template <bool kBf16, int W>
+__device__ __forceinline__ void pack(const float (&v)[kBf16 ? 2 * W : W], uint32_t (&w)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        if constexpr (kBf16) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        else w[i] = __float_as_uint(v[i]);
+    }
 }
 
-template <bool kBf16, bool kHalf>
+// Pieces of W words.
+template <bool kBf16, bool kHalf, int W>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
-    constexpr int E = kBf16 ? 8 : 4, kItem = kBf16 ? 2 : 4;
+    constexpr int kItem = kBf16 ? 2 : 4, E = 4 * W / kItem;
     constexpr int kUse = kHalf ? E : E / 2;  // cosines of a piece
     const int64_t tok = int64_t(blockIdx.x) / a.splits;
     const int h0 = int(int64_t(blockIdx.x) % a.splits) * a.heads_cta, h1 = min(a.heads, h0 + a.heads_cta);
     const int half = a.rot / 2;
-    const int turning = kHalf ? half / E : a.rot / E;  // pieces (of two) that are rotated
-    const int width = min(a.pieces, kRopeThreads), lines = kRopeThreads / width;
-    const int line = threadIdx.x / width;
     pdl_wait();
     const int32_t pos = __ldg(a.pos + tok);
     const bool good = pos >= 0 && pos < a.rows;
@@ -195,36 +202,43 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
         return;
     }
     pdl_trigger();
+    const int pieces = a.turning + a.copied, width = min(pieces, kRopeThreads), lines = kRopeThreads / width;
+    const int line = threadIdx.x / width;
     if (line >= lines) return;
-    for (int piece = threadIdx.x % width; piece < a.pieces; piece += width) {
-        const bool turns = piece >= a.front && piece < a.front + turning;
-        // the piece's first element: those behind the rotated ones come after all of them
-        const int el = !turns && piece >= a.front ? (piece - turning) * E + a.rot : piece * E + (turns ? a.start - a.front * E : 0);
+    for (int piece = threadIdx.x % width; piece < pieces; piece += width) {
+        const bool turns = piece < a.turning;
+        const int at = (turns ? piece : piece - a.turning) * E;
+        const int el = turns ? a.start + at : at < a.start ? at : at + a.rot;  // the piece's first element
         const uint8_t *from = a.x + tok * a.x_tok + int64_t(el) * kItem;
         uint8_t *to = a.out + tok * a.out_tok + int64_t(el) * kItem;
         float c[kUse], s[kUse];
         if (turns) {
-            const float *t = a.cos_sin + int64_t(pos) * a.rot + (piece - a.front) * kUse;
+            const float *t = a.cos_sin + int64_t(pos) * a.rot + piece * kUse;
+            if constexpr (kUse % 2 == 0) {
 #pragma unroll
-            for (int i = 0; i < kUse; i += 2) {  // halves of a row need not be 16-byte aligned where rot / 2 is odd
-                const float2 cc = __ldg(reinterpret_cast<const float2 *>(t + i));
-                const float2 ss = __ldg(reinterpret_cast<const float2 *>(t + half + i));
-                c[i] = cc.x, c[i + 1] = cc.y;
-                s[i] = ss.x * a.sign, s[i + 1] = ss.y * a.sign;
+                for (int i = 0; i < kUse; i += 2) {  // halves of a table row need not be 16-byte aligned
+                    const float2 cc = __ldg(reinterpret_cast<const float2 *>(t + i));
+                    const float2 ss = __ldg(reinterpret_cast<const float2 *>(t + half + i));
+                    c[i] = cc.x, c[i + 1] = cc.y;
+                    s[i] = ss.x * a.sign, s[i + 1] = ss.y * a.sign;
+                }
+            } else {
+                c[0] = __ldg(t);
+                s[0] = __ldg(t + half) * a.sign;
             }
         } else {
 #pragma unroll
             for (int i = 0; i < kUse; ++i) c[i] = 1.f, s[i] = 0.f;
         }
         for (int h = h0 + line; h < h1; h += kRopeBatch * lines) {
-            uint4 u[kRopeBatch], w[kHalf ? kRopeBatch : 1];
+            uint32_t u[kRopeBatch][W], w[kHalf ? kRopeBatch : 1][W];
 #pragma unroll
             for (int b = 0; b < kRopeBatch; ++b) {
                 const int hb = h + b * lines;
                 if (hb < h1) {
-                    u[b] = load_row16(from + hb * a.x_head);
+                    load_words<W>(from + hb * a.x_head, u[b]);
                     if constexpr (kHalf) {
-                        if (turns) w[b] = load_row16(from + hb * a.x_head + half * kItem);
+                        if (turns) load_words<W>(from + hb * a.x_head + half * kItem, w[b]);
                     }
                 }
             }
@@ -234,22 +248,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
                 if (hb >= h1) continue;
                 uint8_t *o = to + hb * a.out_head;
                 if (!turns) {
-                    st_u4(o, u[b]);
+                    store_words<W>(o, u[b]);
                     continue;
                 }
                 float v[E];
-                unpack16<kBf16>(u[b], v);
+                unpack<kBf16, W>(u[b], v);
                 if constexpr (kHalf) {
                     float z[E];
-                    unpack16<kBf16>(w[b], z);
+                    unpack<kBf16, W>(w[b], z);
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
                         const float p = __fsub_rn(__fmul_rn(v[i], c[i]), __fmul_rn(z[i], s[i]));
                         z[i] = __fadd_rn(__fmul_rn(z[i], c[i]), __fmul_rn(v[i], s[i]));
                         v[i] = p;
                     }
-                    st_u4(o, pack16<kBf16>(v));
-                    st_u4(o + half * kItem, pack16<kBf16>(z));
+                    pack<kBf16, W>(z, w[b]);
+                    store_words<W>(o + half * kItem, w[b]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < E / 2; ++i) {
@@ -257,16 +271,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
                         v[2 * i + 1] = __fadd_rn(__fmul_rn(v[2 * i + 1], c[i]), __fmul_rn(v[2 * i], s[i]));
                         v[2 * i] = p;
                     }
-                    st_u4(o, pack16<kBf16>(v));
                 }
+                pack<kBf16, W>(v, u[b]);
+                store_words<W>(o, u[b]);
             }
         }
     }
 }
 
 // The same, value by value: rows, heads or rotated parts that do not come in
-// pieces of 16 bytes.  A thread has one pair or one copied value of a head;
-// `pieces` counts these, pairs first.
+// pieces of 8 bytes.  A thread has one pair or one copied value of a head.
 template <bool kBf16>
 __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const RopeArgs a, bool halves) {
     constexpr int kItem = kBf16 ? 2 : 4;
@@ -282,8 +296,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const RopeArgs a
     }
     pdl_trigger();
     const float *t = a.cos_sin + int64_t(pos) * a.rot;
-    for (int64_t i = threadIdx.x; i < int64_t(h1 - h0) * a.pieces; i += kRopeThreads) {
-        const int h = h0 + int(i / a.pieces), k = int(i % a.pieces);
+    const int pieces = a.turning + a.copied;
+    for (int64_t i = threadIdx.x; i < int64_t(h1 - h0) * pieces; i += kRopeThreads) {
+        const int h = h0 + int(i / pieces), k = int(i % pieces);
         const uint8_t *from = a.x + tok * a.x_tok + h * a.x_head;
         uint8_t *to = a.out + tok * a.out_tok + h * a.out_head;
         if (k >= half) {  // copied
@@ -387,7 +402,6 @@ extern "C" kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens,
         return KVQ_ERR_INVALID_ARG;
 
     const bool halves = flags & KVQ_ROPE_HALF;
-    const int64_t E = 16 / item;
     RopeArgs a = {};
     a.x = static_cast<const uint8_t *>(x);
     a.out = static_cast<uint8_t *>(out);
@@ -404,23 +418,22 @@ extern "C" kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens,
     a.pos = pos;
     a.err = err;
     a.sign = (flags & KVQ_ROPE_INVERSE) ? -1.f : 1.f;
-    // 16 bytes at a time where rows, the rotated part and (with halves) its halves begin on such a boundary
-    const bool wide = aligned(x, 16) && aligned(out, 16) && x_token_stride % E == 0 && x_head_stride % E == 0 &&
-                      out_token_stride % E == 0 && out_head_stride % E == 0 && dim % E == 0 && rot_start % E == 0 &&
-                      rot_dim % (halves ? 2 * E : E) == 0;
-    const int64_t pairs = rot_dim / 2;
-    int64_t lines, step;  // heads that a CTA has at a time, and those it has under way
-    if (wide) {
-        const int64_t turning = halves ? pairs / E : rot_dim / E;
-        a.pieces = int(turning + (in_place ? 0 : (dim - rot_dim) / E));
-        a.front = in_place ? 0 : int(rot_start / E);
-        lines = a.pieces < kRopeThreads ? kRopeThreads / a.pieces : 1;
-        step = kRopeBatch * lines;
-    } else {
-        a.pieces = int(pairs + (in_place ? 0 : dim - rot_dim));
-        lines = a.pieces < kRopeThreads ? kRopeThreads / a.pieces : 1;
-        step = lines;
-    }
+    // 16 or 8 bytes at a time where rows, the rotated part and (with halves) its halves begin and end on such a boundary.
+    // Halves of bf16 rows go by 8 (a piece is two places of a row, and twice as many cosines in registers cost more than
+    // shorter loads: 8,000 x 64 rows of 128, 64 rotated, 54.5 us by 8, 62.2 by 16; fp32, 8,000 x 30 of 336, 125 and 117).
+    auto fits = [&](int64_t bytes) {
+        const int64_t E = bytes / item;
+        return aligned(x, bytes) && aligned(out, bytes) && x_token_stride % E == 0 && x_head_stride % E == 0 &&
+               out_token_stride % E == 0 && out_head_stride % E == 0 && dim % E == 0 && rot_start % E == 0 &&
+               rot_dim % (halves ? 2 * E : E) == 0;
+    };
+    const int words = fits(16) && !(halves && dtype == KVQ_BF16) ? 4 : fits(8) ? 2 : 0;
+    const int64_t E = words ? words * 4 / item : 1;
+    a.turning = int(words && !halves ? rot_dim / E : rot_dim / 2 / E);
+    a.copied = int(in_place ? 0 : (dim - rot_dim) / E);
+    // heads that a CTA has at a time, and those it has under way
+    const int64_t pieces = int64_t(a.turning) + a.copied;
+    const int64_t lines = pieces < kRopeThreads ? kRopeThreads / pieces : 1, step = words ? kRopeBatch * lines : lines;
     // A CTA has a token's heads; fewer where there are too few tokens to fill the machine.
     constexpr int64_t kFill = 608;
     int64_t per = n_tokens >= kFill ? heads : (n_tokens * heads + kFill - 1) / kFill;
@@ -433,9 +446,13 @@ extern "C" kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens,
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return with_bool(dtype == KVQ_BF16, [&](auto Bc) {
         constexpr bool B = decltype(Bc)::value;
-        if (!wide) return launch_pdl(rope_any_kernel<B>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a, halves);
+        if (!words) return launch_pdl(rope_any_kernel<B>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a, halves);
         return with_bool(halves, [&](auto Hc) {
-            return launch_pdl(rope_kernel<B, decltype(Hc)::value>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a);
+            constexpr bool H = decltype(Hc)::value;
+            if constexpr (!(B && H)) {
+                if (words == 4) return launch_pdl(rope_kernel<B, H, 4>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a);
+            }
+            return launch_pdl(rope_kernel<B, H, 2>, dim3(unsigned(blocks)), dim3(kRopeThreads), s, a);
         });
     });
 }

@@ -439,8 +439,8 @@ kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, in
  *              each other.  Sets of rows that share an address range are
  *              accepted where equal strides keep them beside each other.
  * A pos outside [0, cos_sin_rows) sets KVQ_DEVERR_POS and leaves the token's
- * rows of out as they are.  Rows, parts and halves that begin on 16 bytes are
- * faster.  out overlaps neither cos_sin nor pos. */
+ * rows of out as they are.  Rows, parts and halves that begin on 16 (halves of
+ * bf16: 8) bytes are faster.  out overlaps neither cos_sin nor pos. */
 kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens, int64_t heads, int64_t dim,
                     int64_t x_token_stride, int64_t x_head_stride, int64_t rot_start, int64_t rot_dim, unsigned flags,
                     const float *cos_sin, int64_t cos_sin_rows, const int32_t *pos, void *out,

@@ -67,7 +67,8 @@ def problem(n, heads, dim, rot, dtype, seed):
 @pytest.mark.parametrize("n,heads,dim,start,rot", [
     (1, 1, 64, 0, 64), (1, 16, 512, 448, 64), (3, 5, 512, 448, 64), (700, 3, 128, 0, 64), (2, 128, 512, 448, 64),
     (5, 7, 192, 32, 96), (4, 3, 66, 2, 62), (3, 2, 7, 1, 6), (2, 9, 2, 0, 2), (1, 130, 40, 0, 16), (2, 2, 4096, 1000, 1024),
-    (2, 3, 24, 8, 16), (1, 1, 8200, 4, 20), (9, 1, 512, 0, 512)])
+    (2, 3, 24, 8, 16), (1, 1, 8200, 4, 20), (9, 1, 512, 0, 512), (6, 5, 128, 88, 40), (3, 4, 44, 4, 24), (2, 3, 20, 2, 12),
+    (5, 300, 36, 0, 36), (2, 2, 6000, 0, 8)])
 def test_rope(K, dtype, half, inverse, n, heads, dim, start, rot):
     x, pos, table = problem(n, heads, dim, rot, dtype, n * 31 + dim)
     want = turned(x, pos, table, start, half, inverse)
