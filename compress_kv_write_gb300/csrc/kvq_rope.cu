@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(kTabThreads) rope_table_kernel(const TableArgs
 //
 // Bound by memory: a value is read once and written once, and some 45
 // instructions go to the 32 bytes of a piece.  8,191 tokens of 64 heads, bf16
-// rows of 512 (1.08 GB): 160 us = 6.7 TB/s; one token of 16 heads: 2.0 us.
-// (Rotated and copied pieces one after the other instead of side by side: 179.)
+// rows of 512 (1.08 GB): 159 us = 6.8 TB/s; one token of 16 heads: 1.8 us.
+// (A thread's first rows requested after its position instead of before it:
+// 161 and 1.9.  Rotated and copied pieces one after the other: 179.)
 constexpr int kRopeThreads = 256, kRopeBatch = 4;
 
 struct RopeArgs {
@@ -194,7 +195,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     const int64_t tok = int64_t(blockIdx.x) / a.splits;
     const int h0 = int(int64_t(blockIdx.x) % a.splits) * a.heads_cta, h1 = min(a.heads, h0 + a.heads_cta);
     const int half = a.rot / 2;
+    const int pieces = a.turning + a.copied, width = min(pieces, kRopeThreads), lines = kRopeThreads / width;
+    const int line = threadIdx.x / width;
+    if (line >= lines) return;
+    uint32_t u[kRopeBatch][W], w[kHalf ? kRopeBatch : 1][W];
+    // a piece's first element
+    auto element = [&](int piece) {
+        if (piece < a.turning) return a.start + piece * E;
+        const int at = (piece - a.turning) * E;
+        return at < a.start ? at : at + a.rot;
+    };
+    auto load = [&](int piece, int h) {
+        const uint8_t *from = a.x + tok * a.x_tok + int64_t(element(piece)) * kItem;
+#pragma unroll
+        for (int b = 0; b < kRopeBatch; ++b) {
+            const int hb = h + b * lines;
+            if (hb < h1) {
+                load_words<W>(from + hb * a.x_head, u[b]);
+                if constexpr (kHalf) {
+                    if (piece < a.turning) load_words<W>(from + hb * a.x_head + half * kItem, w[b]);
+                }
+            }
+        }
+    };
+    int piece = threadIdx.x % width;
     pdl_wait();
+    load(piece, h0 + line);  // while the position and its row of the table come
+    bool loaded = true;
     const int32_t pos = __ldg(a.pos + tok);
     const bool good = pos >= 0 && pos < a.rows;
     if (!good) {
@@ -202,15 +229,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
         return;
     }
     pdl_trigger();
-    const int pieces = a.turning + a.copied, width = min(pieces, kRopeThreads), lines = kRopeThreads / width;
-    const int line = threadIdx.x / width;
-    if (line >= lines) return;
-    for (int piece = threadIdx.x % width; piece < pieces; piece += width) {
+    for (; piece < pieces; piece += width) {
         const bool turns = piece < a.turning;
-        const int at = (turns ? piece : piece - a.turning) * E;
-        const int el = turns ? a.start + at : at < a.start ? at : at + a.rot;  // the piece's first element
-        const uint8_t *from = a.x + tok * a.x_tok + int64_t(el) * kItem;
-        uint8_t *to = a.out + tok * a.out_tok + int64_t(el) * kItem;
+        uint8_t *to = a.out + tok * a.out_tok + int64_t(element(piece)) * kItem;
         float c[kUse], s[kUse];
         if (turns) {
             const float *t = a.cos_sin + int64_t(pos) * a.rot + piece * kUse;
@@ -231,17 +252,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
             for (int i = 0; i < kUse; ++i) c[i] = 1.f, s[i] = 0.f;
         }
         for (int h = h0 + line; h < h1; h += kRopeBatch * lines) {
-            uint32_t u[kRopeBatch][W], w[kHalf ? kRopeBatch : 1][W];
-#pragma unroll
-            for (int b = 0; b < kRopeBatch; ++b) {
-                const int hb = h + b * lines;
-                if (hb < h1) {
-                    load_words<W>(from + hb * a.x_head, u[b]);
-                    if constexpr (kHalf) {
-                        if (turns) load_words<W>(from + hb * a.x_head + half * kItem, w[b]);
-                    }
-                }
-            }
+            if (!loaded) load(piece, h);
+            loaded = false;
 #pragma unroll
             for (int b = 0; b < kRopeBatch; ++b) {
                 const int hb = h + b * lines;
@@ -420,7 +432,7 @@ extern "C" kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens,
     a.sign = (flags & KVQ_ROPE_INVERSE) ? -1.f : 1.f;
     // 16 or 8 bytes at a time where rows, the rotated part and (with halves) its halves begin and end on such a boundary.
     // Halves of bf16 rows go by 8 (a piece is two places of a row, and twice as many cosines in registers cost more than
-    // shorter loads: 8,000 x 64 rows of 128, 64 rotated, 54.5 us by 8, 62.2 by 16; fp32, 8,000 x 30 of 336, 125 and 117).
+    // shorter loads: 8,000 x 64 rows of 128, 64 rotated, 51.6 us by 8, 59.6 by 16; fp32, 8,000 x 30 of 336, 125 and 117).
     auto fits = [&](int64_t bytes) {
         const int64_t E = bytes / item;
         return aligned(x, bytes) && aligned(out, bytes) && x_token_stride % E == 0 && x_head_stride % E == 0 &&
