@@ -362,7 +362,7 @@ using namespace kvq;
 extern "C" kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, int64_t rows, float amplitude,
                                      float *table, struct CUstream_st *stream) {
     if (rot_dim < 2 || rot_dim % 2 || rows < 0 || first < 0) return KVQ_ERR_INVALID_ARG;
-    if (rot_dim > kMaxRot || first + rows > 0x7FFFFFFFll || rows > 0x7FFFFFFFll) return KVQ_ERR_UNSUPPORTED;
+    if (rot_dim > kMaxRot || rows > 0x7FFFFFFFll || first > 0x7FFFFFFFll - rows) return KVQ_ERR_UNSUPPORTED;
     if (!(amplitude - amplitude == 0.f)) return KVQ_ERR_INVALID_ARG;  // NaN or infinite
     if (!freq || !aligned(freq, 8)) return KVQ_ERR_INVALID_ARG;
     if (rows == 0) return KVQ_OK;
@@ -404,9 +404,9 @@ extern "C" kvq_status kvq_rope(const void *x, kvq_dtype dtype, int64_t n_tokens,
     if (cos_sin_rows > 0 && (!cos_sin || !aligned(cos_sin, 8))) return KVQ_ERR_INVALID_ARG;
     if (n_tokens == 1) x_token_stride = out_token_stride = 0;  // the stride of an axis of one element is never used
     if (heads == 1) x_head_stride = out_head_stride = 0;
-    const int64_t most = int64_t(1) << 40;
-    if (x_token_stride < 0 || x_head_stride < 0 || x_token_stride > most || x_head_stride > most ||
-        out_token_stride > most || out_head_stride > most)
+    const int64_t most = int64_t(1) << 58;  // elements that an axis spans: sums of bytes fit 64 bits
+    if (x_token_stride < 0 || x_head_stride < 0 || x_token_stride > most / n_tokens || x_head_stride > most / heads ||
+        out_token_stride > most / n_tokens || out_head_stride > most / heads)
         return KVQ_ERR_INVALID_ARG;
     if (!rows_apart(n_tokens, heads, dim, out_token_stride, out_head_stride)) return KVQ_ERR_INVALID_ARG;
     const bool in_place = x == out && x_token_stride == out_token_stride && x_head_stride == out_head_stride;

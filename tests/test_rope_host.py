@@ -76,3 +76,10 @@ BIG = 1 << 30
     (dict(n=0, x=None, out=None, pos=None), 0)])
 def test_rope_on_the_host(L, bad, status):
     assert _rope(L, **bad) == status, bad
+
+
+def test_sizes_past_64_bits_are_refused(L):
+    assert _table(L, first=2 ** 63 - 1, rows=1) == 2
+    assert _table(L, first=2 ** 62, rows=2 ** 62) == 2
+    assert _rope(L, n=2 ** 31, xt=2 ** 40, out=BIG, ot=2 ** 40) == 1
+    assert _rope(L, n=2, heads=2 ** 16, xt=512, xh=2 ** 60, out=BIG) == 1
