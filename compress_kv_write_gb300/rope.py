@@ -13,7 +13,8 @@ def rope_frequencies(rot, base=10000.0, *, factor=1.0, how="blend", original=409
     how="base"    the base grown to base * factor ** (rot / (rot - 2)): the slowest frequency is divided by the factor, the
                   fastest stays (rot > 2)
     how="blend"   what turns `fast` times or more within the original context stays, what turns `slow` times or less is
-                  divided by the factor, in between the two are mixed, linearly in the pair's index (the YaRN method)
+                  divided by the factor, in between the two are mixed, linearly in the pair's index, from the first border
+                  rounded down (at least 0) to the second rounded up (at most rot - 1): the YaRN method
     """
     if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
         raise ValueError("rot must be even and positive, base positive and factor at least 1")
@@ -33,6 +34,6 @@ def rope_frequencies(rot, base=10000.0, *, factor=1.0, how="blend", original=409
         raise ValueError("blend takes original > 0, fast > slow > 0 and base > 1")
     # the (fractional) index of the pair that turns `n` times within the original context
     at = lambda n: rot * math.log(original / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
-    first, last = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot // 2 - 1)
+    first, last = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot - 1)
     mix = ((i - first) / max(last - first, 1e-3)).clamp(0, 1)
     return freq * (1 - mix) + freq / factor * mix
