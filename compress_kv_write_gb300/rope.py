@@ -34,6 +34,8 @@ def rope_frequencies(rot, base=10000.0, *, factor=1.0, how="blend", original=409
         raise ValueError("blend takes original > 0, fast > slow > 0 and base > 1")
     # the (fractional) index of the pair that turns `n` times within the original context
     at = lambda n: rot * math.log(original / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
+    if at(slow) <= 0:  # not even the fastest pair turns more than `slow` times
+        return freq / factor
     first, last = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), rot - 1)
     mix = ((i - first) / max(last - first, 1e-3)).clamp(0, 1)
     return freq * (1 - mix) + freq / factor * mix

@@ -36,3 +36,11 @@ def test_last_pair_by_hand():
     assert math.isclose(got, 10000.0 ** (-62 / 64) * 41 / 104, rel_tol=1e-12)
     # every pair turns 32 times and more: nothing changes
     assert torch.equal(rope_frequencies(8, factor=4, original=2 ** 26)[:4], rope_frequencies(8))
+
+
+@pytest.mark.parametrize("original,slow,fast", [(4, 1, 32), (6, 1, 32), (100, 16, 32), (1, 1, 2)])
+def test_no_pair_turns_so_often(original, slow, fast):
+    """The fastest pair turns original / (2 pi) times: where that is not more than `slow`, every pair is divided."""
+    got = rope_frequencies(64, factor=4, original=original, slow=slow, fast=fast)
+    assert original / (2 * math.pi) <= slow
+    assert torch.allclose(got, rope_frequencies(64) / 4, rtol=1e-12, atol=0)
