@@ -15,15 +15,16 @@ namespace {
 // What matters of an angle is its fraction of a turn, and a fraction of a turn
 // times a whole number is exact in integers modulo 2^64: with
 // F = round(2^64 frac(f / 2 pi)) the phase of position p is p F mod 2^64, off
-// by p 2^-65 turns (and by p times the rounding of f / 2 pi, 2^-54 of it).  So
-// the 64-bit floating point that far positions would need, of which this GPU
-// has little (some 2 operations a clock and SM), is spent once a column and
-// CTA; a step of rows is an integer addition.  The top two bits (after half a
-// quarter is added) are the quadrant, the rest an angle within pi / 4 whose
-// sine and cosine are their Taylor series up to x^9 and x^10 (what is left out
-// is below 2^-28 and 2^-32).
+// by p 2^-65 turns, less than 2^-34 at every position.  F comes from f's 53 bits
+// times 126 bits of 1 / 2 pi, in integers too: of a product of doubles, off by
+// 2^-53 of itself, far positions of fast pairs show the error (10^-4 at position
+// 10^6 of a million radians each).  A step of rows is an integer addition.  The
+// top two bits (after half a quarter is added) are the quadrant, the rest an
+// angle within pi / 4 whose sine and cosine are their Taylor series up to x^9
+// and x^10 (what is left out is below 2^-28 and 2^-32).
 //
-// Bound by the stores: 1,048,576 x 64 in 42 us is 6.4 TB/s.
+// Bound by the stores: 1,048,576 x 64 in 42.7 us is 6.3 TB/s; 8,192 x 64 in 2.4 us
+// (with F by doubles 42.0 and 2.3).
 constexpr int kTabThreads = 256;
 constexpr int kMaxRot = 1024;
 
@@ -34,6 +35,23 @@ struct TableArgs {
     float amplitude;
     float *table;
 };
+
+// 2^64 frac(f / 2 pi), rounded, for |f| < 2^55.
+__device__ __forceinline__ uint64_t turn_step(double f) {
+    constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;  // 2^128 / 2 pi
+    const uint64_t bits = uint64_t(__double_as_longlong(f));
+    const int e = int(bits >> 52) & 0x7FF;
+    const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e ? 1ull << 52 : 0ull);  // |f| = m 2^(max(e, 1) - 1075)
+    const int right = 64 + 1075 - max(e, 1);                                   // of the product with 2^128 / 2 pi
+    const uint64_t p0 = m * kLo, up = __umul64hi(m, kLo), mid = m * kHi;
+    const uint64_t p1 = up + mid, p2 = __umul64hi(m, kHi) + (p1 < mid ? 1 : 0);
+    if (right >= 192 || right < 62) return 0;  // nothing is left of it; out of range
+    const int w = right >> 6, r = right & 63;
+    const uint64_t a0 = w == 0 ? p0 : w == 1 ? p1 : p2, a1 = w == 0 ? p1 : w == 1 ? p2 : 0;
+    const uint64_t below = r ? a0 : w == 1 ? p0 : p1;  // the word that the bit to round by is in
+    const uint64_t v = (r ? (a0 >> r) | (a1 << (64 - r)) : a0) + ((below >> ((right - 1) & 63)) & 1);
+    return bits >> 63 ? 0 - v : v;
+}
 
 __device__ __forceinline__ void turn_sincos(uint64_t phase, float &s, float &c) {
     const uint32_t hi = uint32_t(phase >> 32) + 0x20000000u;
@@ -63,10 +81,10 @@ __global__ void __launch_bounds__(kTabThreads) rope_table_kernel(const TableArgs
     __shared__ float s_amp[kMaxRot / 2];
     pdl_wait();
     for (int i = threadIdx.x; i < a.h; i += kTabThreads) {
-        const double t = a.freq[i] * 0.15915494309189535;  // 1 / 2 pi
-        const double f = t - floor(t);
-        s_step[i] = __double2ull_rn(f * 18446744073709551616.0);
-        s_amp[i] = fabs(t) < 4503599627370496.0 ? a.amplitude : NAN;  // no fraction is left of larger ones
+        const double f = a.freq[i];
+        const bool fine = fabs(f) * 0.15915494309189535 < 4503599627370496.0;  // turns; a double has no fraction of more
+        s_step[i] = fine ? turn_step(f) : 0;
+        s_amp[i] = fine ? a.amplitude : NAN;
     }
     __syncthreads();
     pdl_trigger();

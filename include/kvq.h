@@ -416,7 +416,8 @@ kvq_status kvq_norm_quant(const void *x, kvq_dtype x_dtype, int64_t n, int64_t d
  *   rot_dim   even, at most 1024 (64 for kvq_store).
  *   first     >= 0; first + rows at most 2^31 - 1.
  *   table     [rows, rot_dim] fp32, contiguous, 16-B aligned.
- * Values are off by at most 2^-22 |amplitude|. */
+ * Values are off by at most 2^-22 |amplitude|, at every position and for every
+ * finite frequency below that limit: the phase is held modulo 2^64 of a turn. */
 kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, int64_t rows, float amplitude,
                           float *table, struct CUstream_st *stream);
 
