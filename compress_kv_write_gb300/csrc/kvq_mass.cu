@@ -86,7 +86,7 @@ extern "C" kvq_status kvq_attend_mass(kvq_layout layout, int page_bits, const vo
     a.lse = lse;
     const double c = double(scale) * 1.4426950408889634;
     a.c = float(c);
-    a.c_off = float((a.c != 0.f ? c / double(a.c) - 1.0 : 0.0) + (layout == KVQ_LAYOUT_V41 ? 1.375 : 0.875) / (1 << 23));
+    a.c_off = float(a.c != 0.f ? c / double(a.c) - 1.0 : 0.0);
     a.mass = mass;
     a.mass_stride = mass_row_stride;
     a.prev = prev;

@@ -364,8 +364,11 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  *              rounded up, below 2^31: more is KVQ_ERR_UNSUPPORTED.
  *   workspace  kvq_mass_workspace bytes, 16-B aligned (NULL where that is 0).
  * Products, roundings and what counts as nothing are as for kvq_attend's
- * scores; the exponent's own roundings are relative to score - lse.  Sums are
- * fp32, in one order whatever the lengths (no atomics on data).
+ * scores: a score is off by what its 32 fp32 sums on the tensor cores drop
+ * (some 2^-23 of it where its terms are of a kind, nothing where
+ * they sum exactly; the lse that the attention leaves is of the same scores).
+ * The exponent's own roundings are relative to score - lse.  Sums are fp32, in
+ * one order whatever the lengths (no atomics on data).
  * A token whose row holds a NaN or an infinity, and a query row that does or
  * whose lse is NaN, make the weights that they share in NaN, and no others.
  * A bad kv_len (KVQ_DEVERR_LEN; mass_width is a limit too), req or row

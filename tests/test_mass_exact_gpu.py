@@ -1,0 +1,81 @@
+"""kvq_attend_mass where the scores' products sum exactly, so that a weight is off by its exponent's own roundings alone.
+
+A row has two dims that a query sees, of power-of-two and 6 * power-of-two values, and a query two that are not zero: a score
+s is two products whose sum has no more than 24 bits, and lse is one of the scores.  exp(s - lse) is off by
+* 2^-23 |s - lse| in the exponent: log2(e) scale and log2(e) lse rounded to fp32 (2^-24 of s and of lse; their difference is
+  what is left once both are made up for), and the sum of the two products rounded (2^-24 of it);
+* 2^-20 relative: two hardware exponentials of 2^-22 and their product, and the sum over the heads.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from test_attend_gpu import DEV, FP4, V41, K, decode  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+SMALL = [0.0, 1.5, -3.0, 6.0, -12.0, -0.75, 0.375]   # dim 40 of the tokens: 6 * 2^j
+
+
+def pool_of(layout, large, small):
+    """numpy pool, one slot a token: dim 5 holds large[t] (a power of two), dim 6, which no query sees, 1.5 of it (6 * 2^j, so
+    that a V41_FP4 block's scale is exact), dim 40, in a block of its own, small[t]."""
+    n = -(-len(large) // 64) * 64
+    x = torch.zeros((n, 512))
+    x[:len(large), 5] = torch.tensor(large)
+    x[:len(large), 6] = 1.5 * x[:len(large), 5].abs()
+    x[:len(large), 40] = torch.tensor(small)
+    pool = np.zeros(n * O.bytes_per_token(layout), np.uint8)
+    assert O.store(layout, 6, 0, x.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16), np.arange(n), pool) == O.OK
+    rows = decode(layout, 6, pool, np.arange(len(large)))
+    assert (rows == x[:len(large)].double().numpy()).all()      # nothing was rounded
+    return pool, rows
+
+
+def run(K, layout, pool, n, q, lse, scale):
+    mass = torch.full((1, n + 1), -7.0, device=DEV)
+    K.kvq_attend_mass(layout, 6, q.to(DEV), lse.to(DEV), torch.from_numpy(pool).to(DEV), -(-n // 64),
+                      torch.arange(-(-n // 64), dtype=torch.int32, device=DEV)[None], torch.tensor([n], dtype=torch.int32, device=DEV),
+                      mass, scale=scale)
+    assert mass[0, n] == -7
+    return mass[0, :n].cpu().double().numpy()
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [1, 16, 20, 64, 128])
+@pytest.mark.parametrize("scale", [1.0, 0.7, 512 ** -0.5, -0.3])
+@pytest.mark.parametrize("power", [0, 3, 5, 9, 12])
+def test_exponent(K, layout, heads, scale, power):
+    scale = float(np.float32(scale))
+    small = [SMALL[t % len(SMALL)] for t in range(150)]
+    large = [32.0] * 150
+    pool, rows = pool_of(layout, large, small)
+    q = torch.zeros((1, heads, 512))
+    q[0, :, 5] = torch.tensor([2.0 ** max(power - h % 4, 0) for h in range(heads)])
+    q[0, :, 40] = 1.0
+    s = q[0].double().numpy() @ rows.T * scale
+    lse = torch.from_numpy(s[:, 0]).float()[None]
+    # dim 40 is 0 in token 0: its score is a power of two times the scale, its weight 1
+    assert (lse[0].double().numpy() == s[:, 0]).all()
+    got = run(K, layout, pool, 150, q.to(torch.bfloat16), lse, scale)
+    d = s - s[:, :1]
+    want = np.exp(d)
+    tol = (want * np.expm1(2.0 ** -23 * np.abs(d) + 2.0 ** -20)).sum(0) + heads * 2.0 ** -24 * want.sum(0)
+    assert (np.abs(got - want.sum(0)) <= tol).all(), (np.abs(got - want.sum(0)) / tol).max()
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("lse", [-3.0, 0.0, 11.5129, 20.0, 60.0])
+def test_flat(K, layout, lse):
+    """Scores of zero, whatever lse is."""
+    pool, rows = pool_of(layout, [4.0] * 70, [0.0] * 70)
+    q = torch.zeros((1, 16, 512))
+    q[0, :, 100] = 3.0
+    lse = torch.full((1, 16), lse)
+    got = run(K, layout, pool, 70, q.to(torch.bfloat16), lse, 0.125)
+    l = lse[0].double().numpy()
+    want = np.exp(-l).sum()
+    tol = want * (math.expm1(2.0 ** -23 * abs(l[0]) + 2.0 ** -20) + 16 * 2.0 ** -24)
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
