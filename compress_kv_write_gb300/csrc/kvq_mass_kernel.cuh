@@ -226,7 +226,9 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
         const float rest = fmaf(-lse, kLog2e, -n) - lse * 1.9259629e-8f;
         sh.sc[slot][r] = none ? 0.f : score_factor<L>(a.c, up_l);
         sh.nl[slot][r] = none ? -INFINITY : n;
-        sh.wf[slot][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(rest - n * a.c_off);
+        // (up to |lse| = 2^28 within 2^64; beyond, where fp32 no longer tells weights apart, it stays finite and above zero, so
+        // that no weight is NaN)
+        sh.wf[slot][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(fminf(fmaxf(rest - n * a.c_off, -64.f), 64.f));
         sh.vis[slot][r] = vis;
     }
     const int least = __reduce_min_sync(0xFFFFFFFFu, real ? vis : 0x7FFFFFFF);

@@ -367,8 +367,9 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  * scores: a score is off by what its 32 fp32 sums on the tensor cores drop
  * (some 2^-23 of it where its terms are of a kind, nothing where
  * they sum exactly; the lse that the attention leaves is of the same scores).
- * The exponent's own roundings are relative to score - lse.  Sums are fp32, in
- * one order whatever the lengths (no atomics on data).
+ * The exponent's own roundings are relative to score - lse up to |lse| = 2^28;
+ * beyond, where fp32 hardly tells one weight from another, none is NaN for it.
+ * Sums are fp32, in one order whatever the lengths (no atomics on data).
  * A token whose row holds a NaN or an infinity, and a query row that does or
  * whose lse is NaN, make the weights that they share in NaN, and no others.
  * A bad kv_len (KVQ_DEVERR_LEN; mass_width is a limit too), req or row

@@ -79,3 +79,26 @@ def test_flat(K, layout, lse):
     want = np.exp(-l).sum()
     tol = want * (math.expm1(2.0 ** -23 * abs(l[0]) + 2.0 ** -20) + 16 * 2.0 ** -24)
     assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [1, 64, 128])
+@pytest.mark.parametrize("scale", [1.0, 0.7, -0.3, 0.9, 1.1])
+@pytest.mark.parametrize("power", [24, 29, 34, 60])
+def test_scores_that_fp32_cannot_tell_apart(K, layout, heads, scale, power):
+    """|lse| of 2^24 to 2^60, where a unit in its last place is 2 and more: no weight is NaN, a token far below lse has none, and up
+    to 2^28 the token whose score lse is has 1, within 2^-20 and what the second-order terms, 2^-46 of lse, come to."""
+    scale = float(np.float32(scale))
+    top = 32.0 if layout == FP4 else 2.0 ** 20
+    pool, rows = pool_of(layout, [top, -top, top / 2, top / 4] * 20, [0.0] * 80)
+    q = torch.zeros((1, heads, 512))
+    q[0, :, 5] = 2.0 ** power / top
+    s = q[0].double().numpy() @ rows.T * scale
+    for at in range(4):
+        lse = torch.from_numpy(s[:, at]).float()[None]
+        assert (lse[0].double().numpy() == s[:, at]).all()
+        got = run(K, layout, pool, 80, q.to(torch.bfloat16), lse, scale)
+        assert not np.isnan(got).any() and (got >= 0).all()
+        assert (got[s[0] < s[0, at]] == 0).all()
+        if power <= 28:
+            assert (np.abs(got[s[0] == s[0, at]] - heads) <= heads * (2.0 ** -20 + heads * 2.0 ** -24 + abs(s[0, at]) * 2.0 ** -46)).all()
