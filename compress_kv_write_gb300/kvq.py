@@ -628,7 +628,8 @@ def kvq_rope_table(freq, table, *, first=0, amplitude=1.0, stream=None):
 
 def kvq_rope(x, pos, cos_sin, out, *, start, half=False, inverse=False, err=None, stream=None):
     """out <- x [tokens, heads, dim] (fp32 / bf16) with dims start .. start + rot - 1 rotated by row pos[token] of cos_sin
-    [rows, rot], interleaved pairs or halves; `inverse` turns them back.  out may be x itself."""
+    [rows, rot], interleaved pairs or halves; with `inverse` by the transpose, which turns back what a table of amplitude 1
+    turned (what one of amplitude A turned, a table of 1 / A does: with the same one A * A stays).  out may be x itself."""
     bf16 = isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16
     dtype = torch.bfloat16 if bf16 else torch.float32
     dev = _at(x, "x", dtype)

@@ -427,7 +427,8 @@ kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, in
 
 /* Rotary positions of rows that are not stored: queries before kvq_attend,
  * and, with KVQ_ROPE_INVERSE, its output rows, whose rotated dims carry the
- * cached rows' positions.
+ * cached rows' positions (turned back by the query's, they carry those relative
+ * to it).
  *   x          [n_tokens, heads, dim] fp32 or bf16 (dtype), strides in
  *              elements, unit inner stride; a stride of 0 repeats a row.
  *   rot_start, rot_dim   the rotated dims of a row: an even number, at most
@@ -436,6 +437,10 @@ kvq_status kvq_rope_table(const double *freq, int64_t rot_dim, int64_t first, in
  *              KVQ_ROPE_HALF, (start + i, start + rot_dim / 2 + i);
  *              (u, v) -> (u c - v s, v c + u s), or with KVQ_ROPE_INVERSE
  *              (u c + v s, v c - u s), the transpose (also the gradient).
+ *              The transpose undoes the turn where the table's amplitude is 1.
+ *              What a table of amplitude A turned is undone with one of 1 / A;
+ *              with its own table it comes back times A * A, as do the rotated
+ *              dims of outputs over rows that were stored with amplitude A.
  *              fp32, each product and sum rounded, as kvq_store does it.
  *   cos_sin    [cos_sin_rows, rot_dim] fp32, 8-B aligned: cosines, then sines.
  *   pos        [n_tokens] int32: row of cos_sin of every head of a token.
