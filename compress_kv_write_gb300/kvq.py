@@ -518,7 +518,8 @@ def kvq_attend(layout, page_bits, q, pool, pool_pages, page_table, kv_len, out, 
 
 def kvq_tree_mask(parent, mask, *, kv_len=None, pos=None, err=None, stream=None):
     """mask [n_seq, q_len, ceil(q_len / 64)] int64 <- which drafted tokens each one sees (itself and its ancestors), from
-    parent [n_seq, q_len] int32 (-1: the last token before the tree); pos [n_seq, q_len] int32 <- kv_len - q_len + depth."""
+    parent [n_seq, q_len] int32 (-1: the last token before the tree); pos [n_seq, q_len] int32 <- kv_len - q_len + depth, with
+    the kv_len that a sequence has, or had it not been cut (kvq_evict_move) would have: positions go on where they were."""
     dev = _at(parent, "parent", torch.int32)
     parent_ptr, n_seq, q_len, stride = _mat(parent, "parent", torch.int32, dev)
     _at(mask, "mask", torch.int64, dev)
@@ -713,7 +714,8 @@ def kvq_evict_select(mass, kv_len, kept, count, *, first=0, last=0, rows=None, e
 def kvq_evict_move(layout, page_bits, pool, pool_pages, page_table, new_table, kept, *, req=None, mass=None, rows=None,
                    mass_out=None, err=None, stream=None):
     """Moves token kept[i, k] of sequence i (page_table row req[i], or i) to token k of the pages new_table[i], and its
-    weight to mass_out[i, k] where mass and mass_out are given."""
+    weight to mass_out[i, k] where mass and mass_out are given.  Rows keep the rotation of the positions that they had: later
+    tokens' positions go on from the length without the cut, the calls over pages take the cut one."""
     dev = _at(pool, "pool", torch.uint8)
     table, t_rows, t_width, t_stride = _mat(page_table, "page_table", torch.int32, dev)
     new, n_rows, n_width, n_stride = _mat(new_table, "new_table", torch.int32, dev)

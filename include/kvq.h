@@ -295,7 +295,12 @@ kvq_status kvq_attend(kvq_layout layout, int page_bits,
  *             ancestors.
  *   pos       [n_seq, q_len] int32, or NULL: max(0, kv_len[i] - q_len + depth
  *             of j), the depth being the number of its ancestors (kv_len NULL:
- *             the depth alone). */
+ *             the depth alone).
+ *   kv_len    [n_seq] int32, or NULL: here a length in positions, the drafted
+ *             tokens included.  Of a cache that was cut (kvq_evict_move) that
+ *             is what the sequence would have without the cut: with the cut
+ *             length, which the attention takes, drafted tokens would be placed
+ *             before keys that they follow. */
 kvq_status kvq_tree_mask(const int32_t *parent, int64_t n_seq, int64_t q_len, int64_t parent_stride,
                          const int32_t *kv_len, uint64_t *mask, int32_t *pos, int32_t *err,
                          struct CUstream_st *stream);
@@ -348,7 +353,8 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  *   mass[t] = decay * prev[t] + w[t], or, where prev is NULL, w[t],
  * for the tokens t < kv_len[i] of sequence i; what lies behind them in mass
  * stays as it is.  With prev = mass the weights of one step after another add
- * up, the older ones worth `decay` as much each step.
+ * up, the older ones worth `decay` as much each step (a token that is new in
+ * the cache has a 0 in prev).
  *   q, pool, page_table, req, kv_len, scale   as in kvq_attend, the call's own.
  *   lse        [n_seq * q_len, heads] fp32: what the attention left.  A row
  *              whose lse is -inf has no weight.
@@ -490,7 +496,11 @@ kvq_status kvq_evict_select(const float *mass, int64_t mass_rows, int64_t mass_w
  *   mass_out   [n_seq, mass_out_stride] fp32, apart from mass.
  * An entry outside the table or the weights sets KVQ_DEVERR_SLOT, a page
  * outside the pool, old or new, KVQ_DEVERR_PAGE, a bad req or row
- * KVQ_DEVERR_STATE: the token does not move, and its place stays as it is. */
+ * KVQ_DEVERR_STATE: the token does not move, and its place stays as it is.
+ * The rows keep the rotation of the positions that they had.  From then on the
+ * caller has two lengths of a sequence: `count` and what is stored behind it,
+ * for the calls over pages, and the one without the cut, for positions
+ * (kvq_tree_mask, kvq_rope, kvq_store). */
 kvq_status kvq_evict_move(kvq_layout layout, int page_bits, uint8_t *pool, int64_t pool_pages,
                           const int32_t *page_table, int64_t table_rows, int64_t table_width, int64_t table_stride,
                           const int32_t *req, const int32_t *new_table, int64_t new_width, int64_t new_stride,
