@@ -84,6 +84,7 @@ extern "C" kvq_status kvq_attend_mass(kvq_layout layout, int page_bits, const vo
     a.mask = mask;
     a.mask_words = int((q_len + 63) / 64);
     a.lse = lse;
+    a.scale = scale;
     const double c = double(scale) * 1.4426950408889634;
     a.c = float(c);
     a.c_off = float(a.c != 0.f ? c / double(a.c) - 1.0 : 0.0);

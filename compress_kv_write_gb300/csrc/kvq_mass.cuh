@@ -25,10 +25,9 @@ struct MassArgs {
     // A weight is 2^(S c + n) with c = scale log2(e) and n = -log2(e) lse, whose roundings to fp32 would be up to 2^-24 (|S c|
     // + |n|) of the exponent.  S c is about -n wherever a weight counts, so a row's weights are taken times 2^((n - fl(n)) - n
     // c_off), c_off being the relative error of fl(c): what is left is relative to S c + n.  What the tensor cores drop of S
-    // (behind two bits more than fp32 has, in each of its 32 sums) stays out of it: how much that is depends on the row.  (The
-    // mean of N(0, 1) rows, 1.375 or 0.875 times 2^-23 of S, made up for here, left weights of such rows off by 0.1 to 1.0 instead
-    // of 0.2 to 2.4 times 10^-6, but those of rows whose products sum exactly by 1.6 10^-4 at a score of 1,000 instead of 10^-7.)
-    float c, c_off;
+    // is kept small (kvq_mass_kernel.cuh) but not made up for: how much it is depends on the row.  (Its mean over N(0, 1) rows added
+    // here left rows whose products sum exactly off by 1.6 10^-4 at a score of 1,000.)
+    float c, c_off, scale;
     float *mass;
     int64_t mass_stride;
     const float *prev;

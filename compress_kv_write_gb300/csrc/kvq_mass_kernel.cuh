@@ -18,8 +18,9 @@
 //
 // The numerics are the attention's: queries times a power of two in fp16 (exact
 // down to 2^-28 of a row's largest value), cached rows exact in fp16 (V41:
-// relative to a power of two of their own), fp32 sums.  What fp32 constants of
-// the exponent leave out is made up for by a factor a row.
+// relative to a power of two of their own), fp32 sums, here kept short (kMParts,
+// kMShift).  What fp32 constants of the exponent leave out is made up for by a
+// factor a row.
 //
 // Rules for N by the rows of a sequence (kvq_mass.cuh), in us, one sequence of
 // 100 tokens / 48 of 1,024 to 8,192 / 152 of 4,096:
@@ -65,10 +66,29 @@ template <Layout L>
 constexpr int kMStageBytes = kMTile * kTokenBytes<L>;
 template <Layout L, int N>
 constexpr int kMStages = (L == Layout::V41 ? 1 : 2) * (N == 128 ? 1 : 2);
+// The tensor cores take a score's 512 products 16 at a time and round the sum so far towards zero each time, so a score falls
+// short by more the larger the sums on its way are (2^-24 of each, on average; 1.0 to 1.7 10^-7 of the scores that count).  Up
+// to 32 rows TMEM holds a score as four sums, a chunk each (17 rows and more over 4-bit slots 4 % longer than as one, else 1 %).
+// Beyond, half of a number near the row's largest scores is taken off after a quarter and after three quarters, so that the
+// sums of scores that count stay near zero on the way and at the end (64 rows 1 to 4 % longer than without, 128 rows 0 to 2 %;
+// two sums 3 and 28 %, for as much of the error as four steps instead of two, 1 to 9 %).
+template <int N>
+constexpr int kMParts = N <= 32 ? 4 : 1;
+template <int N>
+constexpr bool kMShift = N > 32;
 // Chunks that TMEM holds for the products, beside two blocks' scores; four or more, so that a wait for the one that had
 // a slot before is at most one phase off.
 template <int N>
-constexpr int kMRing = N == 128 ? 4 : N == 64 ? 6 : 7;
+constexpr int kMRing = (512 - 2 * kMParts<N> * N) / 64;
+// What is taken off is 2 16 a b: 16 columns of an A operand with a factor a of the token's, and of a B operand with b of the
+// row's.  V41: a = 2^-texp, in the sum's own unit, where fp16 holds it (other tokens' scores are as they are).
+constexpr float kMStep = 32.f;
+template <Layout L>
+constexpr float kMFactor = L == Layout::V41 ? 1.f : 16.f;
+constexpr int kMTexpMin = -15, kMTexpMax = 14;
+template <Layout L, int N>
+constexpr int kMFactors = !kMShift<N> ? 0 : L == Layout::V41 ? 2 : 1;  // blocks in turn; the same for all
+constexpr int kMFactorBytes = kMTile * 32;
 
 template <Layout L, int N>
 struct MassShared {
@@ -87,16 +107,19 @@ struct MassShared {
     uint32_t pieces[S];             // which of a block's copies there are
     int texp[4][kMTile];            // a token's power of two, or kNoToken
     float other[2][kMTile];         // a token's weights of the second half of the rows
-    // of a tile's rows, four tiles in turn: factor, -log2(e) lse, what their roundings leave out, tokens seen; the fewest
-    // that one of a warp's rows sees
-    alignas(16) float sc[4][N], nl[4][N], wf[4][N];
+    // of a tile's rows, four tiles in turn: factor, -log2(e) lse (less what is taken off a score), what their roundings leave
+    // out, tokens seen; the fewest that one of a warp's rows sees
+    // (for tokens whose scores are as they are behind those for the others)
+    static constexpr int kSets = L == Layout::V41 && kMShift<N> ? 8 : 4;
+    alignas(16) float sc[4][N], nl[kSets][N], wf[kSets][N];
     alignas(16) int vis[4][N];
     int words[4][N];                // where a row's mask begins, of a tree; -1: it sees no drafted token
     int least[4][kMDeq];
 };
 
 template <Layout L, int N>
-constexpr size_t kMassSmem = 1024 + size_t(N) * kD * 2 + size_t(kMStages<L, N>) * kMStageBytes<L> + sizeof(MassShared<L, N>);
+constexpr size_t kMassSmem = 1024 + size_t(N) * kD * 2 + size_t(kMStages<L, N>) * kMStageBytes<L> + kMFactors<L, N> * kMFactorBytes +
+                             (kMShift<N> ? N * 32 : 0) + sizeof(MassShared<L, N>);
 static_assert(kMassSmem<Layout::V41, 16> <= 232448 && kMassSmem<Layout::V41, 32> <= 232448 &&
                   kMassSmem<Layout::V41, 64> <= 232448 && kMassSmem<Layout::V41, 128> <= 232448 &&
                   kMassSmem<Layout::FP4, 16> <= 232448 && kMassSmem<Layout::FP4, 32> <= 232448 &&
@@ -164,8 +187,8 @@ __device__ __forceinline__ uint32_t mass_q_word(int r, int g, int i) {
 
 // Decode warp w loads its rows of a tile's queries (w, w + 16, ..) and their constants.
 template <Layout L, int N>
-__device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N> &sh, uint32_t sq, const MassCursor &cur, int w,
-                                             int lane, uint32_t &tries) {
+__device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N> &sh, uint32_t sq, uint32_t sb, const MassCursor &cur,
+                                             int w, int lane, uint32_t &tries) {
     constexpr int kRows = N / kMDeq, kBatch = kRows < 4 ? kRows : 4;  // a warp's rows; those whose loads are in flight
     static_assert(N % kMDeq == 0 && kMDeq % 8 == 0, "a warp's rows are equal modulo 8");
     const int per = a.q_len * a.heads, slot = cur.nth & 3;
@@ -221,14 +244,43 @@ __device__ __forceinline__ void mass_queries(const MassArgs &a, MassShared<L, N>
     if (lane < kRows) {
         const int r = w + lane * kMDeq;
         sh.words[slot][r] = none || !a.mask ? -1 : (cur.seq * a.q_len + j_l) * a.mask_words;
-        // n = -log2(e) lse in two parts, log2(e) in two as well
-        const float n = -lse * kLog2e;
-        const float rest = fmaf(-lse, kLog2e, -n) - lse * 1.9259629e-8f;
+        // n = -log2(e) l in two parts, l = lse (less what is taken off the scores) and log2(e) in two as well
+        auto constants = [&](int set, float l, float l_lo) {
+            const float n = -l * kLog2e;
+            const float rest = fmaf(-l, kLog2e, -n) - l * 1.9259629e-8f - l_lo * kLog2e;
+            sh.nl[set][r] = none ? -INFINITY : n;
+            // (up to |lse| = 2^28 within 2^64; beyond, where fp32 no longer tells weights apart, it stays finite and above zero,
+            // so that no weight is NaN)
+            sh.wf[set][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(fminf(fmaxf(rest - n * a.c_off, -64.f), 64.f));
+        };
         sh.sc[slot][r] = none ? 0.f : score_factor<L>(a.c, up_l);
-        sh.nl[slot][r] = none ? -INFINITY : n;
-        // (up to |lse| = 2^28 within 2^64; beyond, where fp32 no longer tells weights apart, it stays finite and above zero, so
-        // that no weight is NaN)
-        sh.wf[slot][r] = !(fabsf(n) < INFINITY) ? 1.f : ex2_approx(fminf(fmaxf(rest - n * a.c_off, -64.f), 64.f));
+        float l = lse, l_lo = 0.f;
+        if constexpr (kMShift<N>) {
+            if constexpr (sh.kSets == 8) constants(4 + slot, lse, 0.f);
+            // Half way between lse, near which the scores of a peaked row count, and lse - ln(tokens), where all are of a flat
+            // one; in fp16, so that sums of few bits stay sums of few bits.
+            uint32_t b16 = 0;
+            if (!none && up_l >= 40 && up_l <= 214) {
+                const float unit = kMStep * kMFactor<L> * __uint_as_float((254 - up_l) << 23);  // of a score, a unit of b
+                const float b = (lse - 0.5f * __logf(float(max(vis, 1)))) / a.scale / unit;
+                uint32_t h;
+                asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(fminf(fmaxf(b, -61440.f), 61440.f)));
+                float m;
+                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(m) : "r"(h));
+                m *= unit;
+                const float p = a.scale * m, p_lo = fmaf(a.scale, m, -p);
+                if (fabsf(b) < INFINITY && fabsf(p) < 1e30f) {
+                    l = lse - p;
+                    const float t = l - lse;
+                    l_lo = ((lse - (l - t)) - (p + t)) - p_lo;
+                    b16 = h ^ 0x80008000u;
+                }
+            }
+            const uint32_t four[4] = {b16, b16, b16, b16}, to = sb + r * 32;
+            sts_u4(to, four);
+            sts_u4(to + 16, four);
+        }
+        constants(slot, l, l_lo);
         sh.vis[slot][r] = vis;
     }
     const int least = __reduce_min_sync(0xFFFFFFFFu, real ? vis : 0x7FFFFFFF);
@@ -245,12 +297,15 @@ template <Layout L, int N>
 __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constant__ MassArgs a) {
     using T = LayoutTraits<L>;
     constexpr int S = kMStages<L, N>, KR = kMRing<N>;
-    constexpr uint32_t kTmemK = 2 * N, kTmemCols = 512;  // scores, then chunks of rows
-    static_assert(kTmemK + 64 * KR <= kTmemCols, "they fit");
+    constexpr int G = kMParts<N>;
+    constexpr bool kShift = kMShift<N>, kTokens = kShift && L == Layout::V41;  // a factor for each token
+    constexpr uint32_t kTmemK = 2 * G * N, kTmemCols = 512;  // scores, then chunks of rows
+    static_assert(KR >= 4 && kTmemK + 64 * KR <= kTmemCols, "they fit");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + (-(uintptr_t(smem_addr(smem_raw))) & 1023);
-    uint8_t *const sQ = base, *const sStage = sQ + N * kD * 2;
-    auto &sh = *reinterpret_cast<MassShared<L, N> *>(sStage + S * kMStageBytes<L>);
+    uint8_t *const sQ = base, *const sStage = sQ + N * kD * 2, *const sA = sStage + S * kMStageBytes<L>;
+    uint8_t *const sB = sA + kMFactors<L, N> * kMFactorBytes;
+    auto &sh = *reinterpret_cast<MassShared<L, N> *>(sB + (kMShift<N> ? N * 32 : 0));
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
@@ -277,6 +332,11 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMMma) tmem_alloc(smem_addr(&sh.tmem), kTmemCols);
+    if constexpr (kShift && !kTokens) {
+        static_assert(kMFactor<Layout::FP4> == 16.f, "0x4C00");
+        for (int i = tid; i < kMFactorBytes / 4; i += kMThreads) reinterpret_cast<uint32_t *>(sA)[i] = 0x4C004C00u;
+        fence_proxy_async();
+    }
     pdl_wait();
 
     // ---- this CTA's share of all tiles' blocks in order, each tile with kMTileCost units before its blocks
@@ -361,7 +421,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         for (int i = 0; i < units; ++i, cur.next(a)) {
             if (known != cur.nth) {
                 known = cur.nth;
-                mass_queries<L, N>(a, sh, smem_addr(sQ), cur, warp, lane, tries);
+                mass_queries<L, N>(a, sh, smem_addr(sQ), smem_addr(sB), cur, warp, lane, tries);
             }
             mbar_wait(smem_addr(&sh.full[slot]), parity, tries);
             const uint32_t stage = smem_addr(sStage) + slot * kMStageBytes<L>;
@@ -450,6 +510,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             mbar_wait(smem_addr(&sh.tready[i & 3]), (i >> 2) & 1, tries);
             const int te = sh.texp[i & 3][tok];
             const bool there = te != kNoToken;
+            const int set = !kTokens || (te >= kMTexpMin && te <= kMTexpMax) ? c : 4 + c;
             const float up = L == Layout::V41 && there ? __uint_as_float(uint32_t(127 + te - kLift) << 23) : 1.f;
             const bool masked = (cur.kb + 1) * kMTile > least;
             // whether row r, of the tile, sees this thread's token: it is one of the first `vis`, or drafted and in its mask
@@ -463,12 +524,11 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             mbar_wait(smem_addr(&sh.sdone[i & 1]), (i >> 1) & 1, tries);
             tc_fence_after();
             // 2^(exponent) of four rows from r on, and their factors
-            auto weigh = [&](uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, int r, float2 (&p)[2], float4 &wf) {
+            auto weigh = [&](float x0, float x1, float x2, float x3, int r, float2 (&p)[2], float4 &wf) {
                 const float4 sc = *reinterpret_cast<const float4 *>(&sh.sc[c][r]);
-                const float4 nl = *reinterpret_cast<const float4 *>(&sh.nl[c][r]);
-                wf = *reinterpret_cast<const float4 *>(&sh.wf[c][r]);
-                float2 u0 = make_float2(__uint_as_float(x0), __uint_as_float(x1));
-                float2 u1 = make_float2(__uint_as_float(x2), __uint_as_float(x3));
+                const float4 nl = *reinterpret_cast<const float4 *>(&sh.nl[set][r]);
+                wf = *reinterpret_cast<const float4 *>(&sh.wf[set][r]);
+                float2 u0 = make_float2(x0, x1), u1 = make_float2(x2, x3);
                 if constexpr (L == Layout::V41) {
                     u0 = fmul2(u0, make_float2(up, up));
                     u1 = fmul2(u1, make_float2(up, up));
@@ -479,13 +539,23 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 p[1] = make_float2(ex2_approx(u1.x), ex2_approx(u1.y));
             };
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const uint32_t at = tfrom + (i & 1) * N;
+            const uint32_t at = tfrom + (i & 1) * (G * N);
             if (!masked) {
 #pragma unroll 1
                 for (int j0 = 0; j0 < NC; j0 += NL) {
-                    uint32_t x[NL];
-                    if constexpr (NL == 16) tmem_ld16(at + j0, x);
-                    else tmem_ld8(at + j0, x);
+                    float x[NL];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        uint32_t y[NL];
+                        if constexpr (NL == 16) tmem_ld16(at + g * N + j0, y);
+                        else tmem_ld8(at + g * N + j0, y);
+#pragma unroll
+                        for (int j = 0; j < NL; j += 2) {
+                            float2 v = make_float2(__uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                            if (g) v = fadd2(make_float2(x[j], x[j + 1]), v);
+                            x[j] = v.x, x[j + 1] = v.y;
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < NL; j += 4) {
                         float2 p[2];
@@ -500,8 +570,14 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 // 4-bit slots 1.39 us a block, with masks in the other loop 1.61).
 #pragma unroll 1
                 for (int j0 = 0; j0 < NC; j0 += 4) {
-                    uint32_t x[4];
-                    tmem_ld4(at + j0, x);
+                    float x[4];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        uint32_t y[4];
+                        tmem_ld4(at + g * N + j0, y);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] = g ? x[j] + __uint_as_float(y[j]) : __uint_as_float(y[j]);
+                    }
                     const int r = c0 + j0;
                     const int4 vis = *reinterpret_cast<const int4 *>(&sh.vis[c][r]);
                     float2 p[2];
@@ -530,6 +606,9 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
         // ------------------------------------------------------ products
         constexpr uint32_t kIdesc = mma_idesc(kMTile, N, false, false), kHi = desc_hi(1024, kSwizzle128);
         const uint32_t qd = desc_lo(smem_addr(sQ), 16);
+        constexpr uint32_t kHi32 = desc_hi(256, kSwizzle32);  // of rows of 16 equal columns
+        const uint32_t ad = desc_lo(smem_addr(sA), 16), bd = desc_lo(smem_addr(sB), 16);
+        static_assert(!kShift || G == 1, "one sum");
         MassCursor cur(a, start_tile, start_kb, units);
         int kslot = 0;
         uint32_t kparity = 0;
@@ -540,7 +619,7 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
             fresh = cur.kb + 1 == cur.nb;
             // the score buffer is free when the block before the last has been read
             if (i >= 2) mbar_wait(smem_addr(&sh.sread[i & 1]), ((i - 2) >> 1) & 1, tries);
-            const uint32_t to = (i & 1) * N;
+            const uint32_t to = (i & 1) * (G * N), factors = ad + (kTokens ? (i & 1) * (kMFactorBytes >> 4) : 0);
 #pragma unroll
             for (int b = 0; b < kMChunks; ++b) {
                 mbar_wait(smem_addr(&sh.ready[kslot]), kparity, tries);
@@ -548,8 +627,16 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                 if (elect_one()) {
                     const uint32_t at = qd + ((2 * b * N * 128) >> 4), from = kTmemK + kslot * 64;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(to, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kHi, kIdesc, b + k > 0);
+                    for (int k = 0; k < 8; ++k) {
+                        if constexpr (kShift) {
+                            if (b == 1 && k == 0) mma_ss(to, factors, kHi32, bd, kHi32, kIdesc, true);
+                        }
+                        mma_ts(to + b * G / kMChunks * N, from + 8 * k, at + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), kHi, kIdesc,
+                               b % (kMChunks / G) + k > 0);
+                        if constexpr (kShift) {
+                            if (b == 2 && k == 7) mma_ss(to, factors, kHi32, bd, kHi32, kIdesc, true);
+                        }
+                    }
                     mma_commit(smem_addr(&sh.scored[kslot]));
                     if (b == kMChunks - 1) {
                         mma_commit(smem_addr(&sh.sdone[i & 1]));
@@ -557,6 +644,23 @@ __global__ void __launch_bounds__(kMThreads, 1) mass_kernel(const __grid_constan
                     }
                 }
                 __syncwarp();
+                if constexpr (kTokens) {
+                    // The tokens' factors, while the first chunk's products run.  (That this chunk is there tells that the first
+                    // three chunks of two blocks ago are done, which took the factors that were in this place.)
+                    if (b == 0) {
+                        mbar_wait(smem_addr(&sh.tready[i & 3]), (i >> 2) & 1, tries);
+#pragma unroll
+                        for (int t = lane; t < kMTile; t += 32) {
+                            const int te = sh.texp[i & 3][t];
+                            const uint32_t f = te >= kMTexpMin && te <= kMTexpMax ? uint32_t(15 - te) * 0x04000400u : 0u;  // 2^-te
+                            const uint32_t four[4] = {f, f, f, f}, at = smem_addr(sA) + (i & 1) * kMFactorBytes + t * 32;
+                            sts_u4(at, four);
+                            sts_u4(at + 16, four);
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
+                }
                 if (++kslot == KR) {
                     kslot = 0;
                     kparity ^= 1;

@@ -369,10 +369,11 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  *              of the table's width (of mass_width where that is less), each
  *              rounded up, below 2^31: more is KVQ_ERR_UNSUPPORTED.
  *   workspace  kvq_mass_workspace bytes, 16-B aligned (NULL where that is 0).
- * Products, roundings and what counts as nothing are as for kvq_attend's
- * scores: a score is off by what its 32 fp32 sums on the tensor cores drop
- * (some 2^-23 of it where its terms are of a kind, nothing where
- * they sum exactly; the lse that the attention leaves is of the same scores).
+ * Products and what counts as nothing are as for kvq_attend's scores.  The
+ * tensor cores round a score's sums towards zero; they are kept short (a score
+ * of up to 32 rows in four sums; of more rows, less a number near the scores
+ * that count), which leaves weights short by some 2^-24 of lse where a row's
+ * products are of a kind, and by nothing where they sum exactly.
  * The exponent's own roundings are relative to score - lse up to |lse| = 2^28;
  * beyond, where fp32 hardly tells one weight from another, none is NaN for it.
  * Sums are fp32, in one order whatever the lengths (no atomics on data).

@@ -14,6 +14,7 @@ import torch
 
 import oracle as O
 from test_attend_gpu import DEV, FP4, V41, K, decode  # noqa: F401
+from test_mass_gpu import Mass, check
 
 pytestmark = pytest.mark.gpu
 SMALL = [0.0, 1.5, -3.0, 6.0, -12.0, -0.75, 0.375]   # dim 40 of the tokens: 6 * 2^j
@@ -102,3 +103,18 @@ def test_scores_that_fp32_cannot_tell_apart(K, layout, heads, scale, power):
         assert (got[s[0] < s[0, at]] == 0).all()
         if power <= 28:
             assert (np.abs(got[s[0] == s[0, at]] - heads) <= heads * (2.0 ** -20 + heads * 2.0 ** -24 + abs(s[0, at]) * 2.0 ** -46)).all()
+
+
+@pytest.mark.parametrize("heads,q_len", [(16, 1), (32, 1), (64, 1), (128, 1), (64, 3)])
+@pytest.mark.parametrize("e", [-30, -8, 10, 13, 20, 60, 100])
+def test_rows_of_other_powers(K, heads, q_len, e):
+    """V41 rows far from one beside rows near it, every other token's, queries that bring the large ones' scores back."""
+    c = Mass(V41, 6, [200, 333], heads, q_len=q_len, seed=29)
+    pool = c.pool.reshape(c.pages, -1)
+    scales = pool[:, 64 * 512:].reshape(c.pages, 64, 16).astype(np.int32)
+    scales[:, ::2] = np.clip(scales[:, ::2] + e, 0, 254)
+    pool[:, 64 * 512:] = scales.astype(np.uint8).reshape(c.pages, -1)
+    if e > 0:
+        c.q = (c.q.double() * 2.0 ** -e).to(torch.bfloat16)
+    lse = c.lses()
+    check(c.run(K, lse), c.lens, c.want(lse), e)
