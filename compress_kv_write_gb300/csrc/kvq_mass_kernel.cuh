@@ -23,23 +23,24 @@
 // factor a row.
 //
 // Rules for N by the rows of a sequence (kvq_mass.cuh), in us, one sequence of
-// 100 tokens / 48 of 1,024 to 8,192 / 152 of 4,096:
+// 100 tokens / 48 of 1,024 to 8,192 in even steps / 152 of 4,096:
 //              as 16              32                 64                 128
-//   16 heads V41  6.7/22.8/57.4   7.4/23.1/58.0      8.8/25.2/60.9      11.7/31.1/71.2
-//            FP4  6.5/18.6/41.6   7.2/19.0/42.9      8.5/20.5/46.0      11.1/24.6/50.3
-//   64 heads V41                                     9.3/25.9/62.5      12.3/33.9/74.8
-//            FP4                                     8.9/21.6/47.9      11.5/26.0/52.1
-//  128 heads V41                            twice:  11.2/44.0/122      12.9/35.7/76.0
-//            FP4                                    10.7/36.7/93.2      11.8/28.1/55.1
+//   16 heads V41  6.9/26.8/57.4   7.6/27.8/58.4      9.3/30.0/61.3      12.4/37.1/71.6
+//            FP4  6.7/21.6/42.2   7.5/22.6/44.9      8.8/24.4/46.9      11.3/28.6/51.9
+//   64 heads V41                                     9.5/31.2/62.7      12.9/39.9/75.0
+//            FP4                                     9.1/25.2/48.5      11.6/30.0/53.5
+//  128 heads V41                            twice:  11.4/53.7/123       13.6/41.3/76.5
+//            FP4                                    10.7/43.0/94.3      12.0/31.5/56.0
 //
-// What bounds it: a block of 128 tokens takes 1.54 us (V41, up to 64 rows), what
-// its 67.6 KB take from memory; 1.07 to 1.20 us (FP4; memory alone would be
-// 0.79), where issue slots are 57 to 71 % full and the decode warps' work is most
-// of that (without the conversions 0.93); 1.93 (V41) and 1.39 us (FP4) with 128
-// rows, whose products alone take 2,048 clocks, 1.05 us: the queries leave
-// shared memory for one (V41) or two blocks, and a block's weights take 2,700
-// clocks.  A call costs 6 to 14 us besides: launch, shares (3,400 clocks),
-// queries, the first block's way through all roles (8,000) and the last one's.
+// What bounds it: a block of 128 tokens takes 1.53 to 1.55 us (V41, up to 32
+// rows), what its 67.6 KB take from memory; 1.08 to 1.22 us (FP4, up to 64 rows;
+// memory alone would be 0.79), where issue slots are 57 to 71 % full and the
+// decode warps' work is most of that (without the conversions 0.93); 1.62 us (V41,
+// 64 rows), 1.91 (V41) and 1.40 us (FP4) with 128 rows, whose products alone take
+// 2,048 clocks, 1.05 us: the queries leave shared memory for one (V41) or two
+// blocks, and a block's weights take 2,700 clocks.  A call costs 6 to 15 us
+// besides: launch, shares (3,400 clocks), queries, the first block's way through
+// all roles (8,000) and the last one's.
 #pragma once
 
 #include "kvq_attend_rows.cuh"

@@ -213,8 +213,9 @@ kvq_status kvq_dequant_slots(kvq_layout layout, int page_bits,
 size_t kvq_attend_workspace(int64_t rows);
 
 /* How often a wait inside the kernels of kvq_attend, kvq_attend_slots,
- * kvq_attend_tree and kvq_attend_mass (for another warp's part of the work) tries before the call gives up with KVQ_DEVERR_WAIT; the default
- * is 2^20, which takes some seconds, far beyond any wait of a sound call.  Sets
+ * kvq_attend_tree and kvq_attend_mass (for another warp's part of the work)
+ * tries before the call gives up with KVQ_DEVERR_WAIT; the default is 2^20,
+ * which takes some seconds, far beyond any wait of a sound call.  Sets
  * the limit of the process's later calls (at most 2^24; a captured call keeps
  * the one it was captured with) and returns the one before.  With 0 every call
  * gives up, which is how a program can test what it does then. */
@@ -313,7 +314,10 @@ kvq_status kvq_tree_mask(const int32_t *parent, int64_t n_seq, int64_t q_len, in
  * the first q_len - kv_len[i] drafted tokens are not there, whatever the mask.
  *   mask      [n_seq, q_len, ceil(q_len / 64)] 64-bit words, 8-B aligned.
  *   q_len     at most 1024.
- * All else is as in kvq_attend. */
+ * All else is as in kvq_attend, among it that a softmax weight is rounded to
+ * fp16 for the outputs' products (not for their sum and lse).  fp32 outputs are
+ * off by some 2^-12 of their scale for it; bf16 ones are a neighbouring value of
+ * what fp32 weights give in 2 to 6 places of a hundred, and no further off. */
 kvq_status kvq_attend_tree(kvq_layout layout, int page_bits,
                            const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
                            int64_t n_seq, int64_t q_len, int64_t heads,
@@ -365,9 +369,10 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  *              unspecified.
  *   prev       rows like mass's, by the same index: mass itself with its
  *              stride, or apart from it, or NULL.
- *   n_seq      at most 65535; sequences times 128 query rows times 128 tokens
- *              of the table's width (of mass_width where that is less), each
- *              rounded up, below 2^31: more is KVQ_ERR_UNSUPPORTED.
+ *   n_seq      at most 65535; with T = n_seq * ceil(q_len * heads / 128) and B
+ *              = ceil(tokens of the table's width, or mass_width where that is
+ *              less, / 128): T * (B + 2) below 2^31, above it the call is
+ *              KVQ_ERR_UNSUPPORTED.
  *   workspace  kvq_mass_workspace bytes, 16-B aligned (NULL where that is 0).
  * Products and what counts as nothing are as for kvq_attend's scores.  The
  * tensor cores round a score's sums towards zero; they are kept short (a score

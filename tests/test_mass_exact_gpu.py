@@ -118,3 +118,25 @@ def test_rows_of_other_powers(K, heads, q_len, e):
         c.q = (c.q.double() * 2.0 ** -e).to(torch.bfloat16)
     lse = c.lses()
     check(c.run(K, lse), c.lens, c.want(lse), e)
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+@pytest.mark.parametrize("scale", [0.125, 0.0, -0.0, 1e-38, 1e30])
+def test_rows_without_scores(K, layout, heads, scale):
+    """Queries of zeros, scales of zero and near it, lse infinite, of the largest size or absent, rows beside plain ones."""
+    scale = float(np.float32(scale))
+    pool, rows = pool_of(layout, [4.0, -8.0, 16.0] * 30, [0.0, 1.5, -3.0] * 30)
+    q = torch.zeros((1, heads, 512))
+    q[0, ::2, 5] = 0.5 if scale < 1 else 2.0 ** -110
+    lse = torch.full((1, heads), 1.25)
+    lse[0, 1], lse[0, 2], lse[0, 3], lse[0, 4] = math.inf, -math.inf, 3e38, 80.0
+    s = q[0].double().numpy() @ rows.T * scale
+    l = lse[0].double().numpy()[:, None]
+    with np.errstate(over="ignore"):
+        p = np.where(np.isneginf(l), 0.0, np.exp(s - l))
+    got = run(K, layout, pool, 90, q.to(torch.bfloat16), lse, scale)
+    tol = np.where(p > 0, p * np.expm1(2.0 ** -23 * np.where(np.isinf(l), 0, np.minimum(np.abs(s - l), 1e3)) + 2.0 ** -20) + 2.0 ** -126, 0)
+    assert (np.abs(got - p.sum(0)) <= tol.sum(0) + heads * 2.0 ** -24 * p.sum(0)).all()
+    lse[0, 5] = math.nan
+    assert np.isnan(run(K, layout, pool, 90, q.to(torch.bfloat16), lse, scale)).all()
