@@ -140,3 +140,46 @@ def test_rows_without_scores(K, layout, heads, scale):
     assert (np.abs(got - p.sum(0)) <= tol.sum(0) + heads * 2.0 ** -24 * p.sum(0)).all()
     lse[0, 5] = math.nan
     assert np.isnan(run(K, layout, pool, 90, q.to(torch.bfloat16), lse, scale)).all()
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads", [20, 64])
+def test_few_tries(K, layout, heads):
+    """Waits that give up, for the tiles of 32 and 64 rows: the call ends, weights are right or, where the error word says so, NaN."""
+    c = Mass(layout, 6, [3000, 30, 0, 900], heads, seed=43)
+    lse = c.lses()
+    want = c.want(lse)
+    for limit in (0, 1, 3, 10, 50, 200):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        before = K.attend_wait_limit(limit)
+        try:
+            got = c.run(K, lse, err=err)
+        finally:
+            K.attend_wait_limit(before)
+        assert err.item() in (0, 16)
+        if err.item() == 0:
+            check(got, c.lens, want, limit)
+        for i, (total, tol) in enumerate(want):
+            row = got[i, :c.lens[i]].cpu().double().numpy()
+            assert (np.isnan(row) | (np.abs(row - total) <= tol)).all() and (got[i, c.lens[i]:] == -7).all()
+    check(c.run(K, lse), c.lens, want, "after")
+
+
+@pytest.mark.parametrize("layout", [V41, FP4])
+@pytest.mark.parametrize("heads,q_len", [(16, 1), (32, 1), (64, 1), (128, 1), (64, 6)])
+def test_tiles_of_one_block(K, layout, heads, q_len):
+    """Many tiles of one block and a few of more, so that a CTA's tiles, with constants of their own, follow each other closely: every
+    sequence as in a call of its own, bit for bit."""
+    lens = [1 + (37 * i) % 128 if i % 5 else 129 + 53 * i % 400 for i in range(400 if q_len == 1 else 150)]
+    c = Mass(layout, 6, lens, heads, q_len=q_len, seed=61)
+    # rows of a sequence have scores, and sums, of a size of their own
+    size = torch.tensor([2.0 ** (i % 7 - 3) for i in range(len(lens))]).repeat_interleave(q_len)[:, None, None]
+    c.q = (c.q.float() * size).to(torch.bfloat16)
+    lse = c.lses()   # (with scores to 100 above some other number, weights pass fp32)
+    got = c.run(K, lse)
+    check(got, c.lens, c.want(lse), "all")
+    whole_q, whole_table = c.q, c.table
+    for i in (0, 1, 5, 77, 149):
+        c.q, c.table, c.lens = whole_q[i * q_len:(i + 1) * q_len], whole_table[i:i + 1], lens[i:i + 1]
+        one = c.run(K, lse[i * q_len:(i + 1) * q_len])
+        assert torch.equal(one[0, :lens[i]], got[i, :lens[i]])
