@@ -377,8 +377,8 @@ size_t kvq_mass_workspace(int64_t n_seq, int64_t rows, int64_t max_len);
  * Products and what counts as nothing are as for kvq_attend's scores.  The
  * tensor cores round a score's sums towards zero; they are kept short (a score
  * of up to 32 rows in four sums; of more rows, less a number near the scores
- * that count), which leaves weights short by some 2^-24 of lse where a row's
- * products are of a kind, and by nothing where they sum exactly.
+ * that count), which leaves weights off by some 2^-24 of lse, and by nothing
+ * where a row's products sum exactly.
  * The exponent's own roundings are relative to score - lse up to |lse| = 2^28;
  * beyond, where fp32 hardly tells one weight from another, none is NaN for it.
  * Sums are fp32, in one order whatever the lengths (no atomics on data).
